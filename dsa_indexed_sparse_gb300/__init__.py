@@ -20,7 +20,10 @@ LIB_PATH = os.path.join(_HERE, "libdsa.so")
 DSA_OK = 0
 STATUS_NAMES = {0: "DSA_OK", 1: "DSA_ERR_INVALID_ARG", 2: "DSA_ERR_UNSUPPORTED", 3: "DSA_ERR_WORKSPACE",
                 4: "DSA_ERR_CUDA", 5: "DSA_ERR_TIMEOUT", 6: "DSA_ERR_DEVICE_CHECK"}
-DSA_F32, DSA_BF16, DSA_E4M3, DSA_MXFP8_E4M3, DSA_E4M3_T128 = 0, 1, 2, 3, 4
+DSA_F32, DSA_BF16, DSA_E4M3, DSA_MXFP8_E4M3, DSA_E4M3_T128, DSA_E2M1 = 0, 1, 2, 3, 4, 5
+E2M1_ROW_BYTES = 432                # a DSA_E2M1 latent row
+ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 EXPORTED = ("dsa_abi_version", "dsa_status_string", "dsa_last_error", "dsa_last_plan",
             "dsa_indexer_scores", "dsa_topk", "dsa_sparse_mla_attn_workspace_size",
@@ -28,7 +31,8 @@ EXPORTED = ("dsa_abi_version", "dsa_status_string", "dsa_last_error", "dsa_last_
             "dsa_decode_step_static_ws", "dsa_index_cache_append", "dsa_index_cache_append_mx",
             "dsa_latent_cache_append", "dsa_debug_withhold_arrival",
             "dsa_indexer_prolog_workspace_size", "dsa_indexer_prolog",
-            "dsa_check_status")
+            "dsa_rope_turns", "dsa_rope", "dsa_latent_cache_append_rope", "dsa_index_cache_append_rope",
+            "dsa_latent_cache_read", "dsa_check_status")
 STATIC_WORKSPACE_BYTES = 32 << 20   # DSA_STATIC_WORKSPACE_BYTES
 
 
@@ -56,6 +60,11 @@ class PrologDesc(ctypes.Structure):
                 ("D_I", ctypes.c_int32), ("x", ctypes.c_void_p), ("x_q", ctypes.c_void_p), ("w_q", ctypes.c_void_p),
                 ("w_k", ctypes.c_void_p), ("w_w", ctypes.c_void_p), ("gamma", ctypes.c_void_p),
                 ("beta", ctypes.c_void_p)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("d_rot", ctypes.c_int32), ("layout", ctypes.c_int), ("turns", ctypes.c_void_p),
+                ("magnitude", ctypes.c_float)]
 
 
 class DSAError(RuntimeError):
@@ -87,6 +96,13 @@ def _load() -> ctypes.CDLL:
         "dsa_debug_withhold_arrival": (C, [ctypes.c_int32, ctypes.c_uint64]),
         "dsa_indexer_prolog_workspace_size": (ctypes.c_size_t, [P, P]),
         "dsa_indexer_prolog": (C, [P, P, P, P, P, P, P, P, ctypes.c_size_t, P]),
+        "dsa_rope_turns": (C, [ctypes.c_int32, ctypes.c_double, C, ctypes.c_double, ctypes.c_double,
+                               ctypes.c_double, ctypes.c_double, P, P]),
+        "dsa_rope": (C, [P, ctypes.c_int32, ctypes.c_int32, P, C, P, ctypes.c_int64, ctypes.c_int64, P,
+                         ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, P]),
+        "dsa_latent_cache_append_rope": (C, [P, P, P, P, ctypes.c_int64, P, ctypes.c_int64, P, P]),
+        "dsa_index_cache_append_rope": (C, [P, P, ctypes.c_int32, ctypes.c_int32, C, C, P, ctypes.c_int64, P, P, P]),
+        "dsa_latent_cache_read": (C, [P, P, P, C, P, ctypes.c_int64, P]),
         "dsa_check_status": (C, [P]),
     }
     for name, (res, args) in sig.items():
@@ -127,6 +143,15 @@ def _stream(stream) -> int:
     if stream is None:
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _rows(t: torch.Tensor, name: str) -> int:
+    """Data pointer of a tensor whose values are contiguous along its last dim, on the current GPU."""
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device, not on {t.device}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last dim of {name} must be contiguous")
+    return t.data_ptr()
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -228,6 +253,61 @@ class Prolog(_CachedDesc):
                           _ptr(self.beta))
 
 
+@dataclasses.dataclass
+class Rope(_CachedDesc):
+    """A rotation's frequencies, kept on the device; see dsa_rope_desc_t.  `make`
+    computes them."""
+    d_rot: int
+    turns: torch.Tensor                # int64 [d_rot / 2]: turns per position in units of 2**-64 (unsigned)
+    magnitude: float = 1.0
+    layout: str = "interleaved"
+
+    @classmethod
+    def make(cls, d_rot: int, theta: float = 10000.0, layout: str = "interleaved", scaling: str = "none",
+             factor: float = 1.0, original_ctx: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+             magnitude: Optional[float] = None, device="cuda") -> "Rope":
+        """scaling: "none", "linear", "ntk" or "yarn" (with factor; "yarn" also
+        original_ctx and the betas).  magnitude overrides the factor on cosine and
+        sine (1, or YaRN's 0.1 ln(factor) + 1)."""
+        if layout not in ROPE_LAYOUTS or scaling not in ROPE_SCALINGS:
+            raise ValueError(f"layout must be one of {list(ROPE_LAYOUTS)}, scaling one of {list(ROPE_SCALINGS)}")
+        host = (ctypes.c_uint64 * (max(int(d_rot), 0) // 2))()
+        mag = ctypes.c_float()
+        _check(_lib.dsa_rope_turns(d_rot, theta, ROPE_SCALINGS[scaling], factor, original_ctx, beta_fast, beta_slow,
+                                   host, ctypes.byref(mag)))
+        turns = torch.tensor([ctypes.c_int64(v).value for v in host], dtype=torch.int64, device=device)
+        return cls(d_rot, turns, mag.value if magnitude is None else float(magnitude), layout)
+
+    def _build_desc(self) -> RopeDesc:
+        if self.turns.dtype != torch.int64 or self.turns.numel() != self.d_rot // 2:
+            raise ValueError("turns must be int64 [d_rot / 2]")
+        if not self.turns.is_contiguous():
+            raise ValueError("turns must be contiguous")
+        return RopeDesc(self.d_rot, ROPE_LAYOUTS[self.layout], _rows(self.turns, "turns"), self.magnitude)
+
+
+def rope(plan: Rope, pos: torch.Tensor, x: torch.Tensor, out: torch.Tensor, inverse: bool = False,
+         stream=None) -> torch.Tensor:
+    """Rotates x [T, H, d_rot] (or [T, d_rot]; bf16 or fp32) by the positions pos
+    (int32 [T]) into out, of the same shape and type.  Both may be strided views
+    whose last dim is contiguous: q[..., 512:] rotates that part of a head.  out is
+    x (in place) or shares no value with it.  inverse: the transposed matrix -- the
+    gradient of the rotation."""
+    d = plan.desc()
+    shape = x.shape
+    if len(shape) not in (2, 3) or shape[-1] != d.d_rot or out.shape != shape:
+        raise ValueError("x and out must be [T, H, d_rot] or [T, d_rot]")
+    if out.dtype != x.dtype or x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("x and out must both be bfloat16 or float32")
+    if pos.dtype != torch.int32 or pos.shape != shape[:1] or not pos.is_contiguous():
+        raise ValueError("pos must be contiguous int32 [T]")
+    xs, os_ = x.stride(), out.stride()
+    H, xh, oh = (shape[1], xs[1], os_[1]) if len(shape) == 3 else (1, 0, 0)
+    _check(_lib.dsa_rope(ctypes.byref(d), shape[0], H, _rows(pos, "pos"), DSA_F32 if x.dtype == torch.float32 else DSA_BF16,
+                         _rows(x, "x"), xs[0], xh, _rows(out, "out"), os_[0], oh, 1 if inverse else 0, _stream(stream)))
+    return out
+
+
 def indexer_prolog_workspace_size(seq: Seq, pro: Prolog) -> int:
     s, d = seq.desc(), pro.desc()
     return _lib.dsa_indexer_prolog_workspace_size(ctypes.byref(s), ctypes.byref(d))
@@ -316,6 +396,51 @@ def latent_cache_append(seq: Seq, mla: Mla, kv_new: torch.Tensor, stream=None) -
     s, m = seq.desc(), mla.desc()
     _check(_lib.dsa_latent_cache_append(ctypes.byref(s), ctypes.byref(m), _ptr(kv_new), _ptr(mla.kv_cache),
                                         _stream(stream)))
+
+
+def latent_cache_append_rope(seq: Seq, mla: Mla, plan: Rope, latent: torch.Tensor, k_rope: torch.Tensor,
+                             stream=None) -> None:
+    """Writes the new tokens' latent rows latent [T, d_latent] and k_rope
+    [T, d_rope] (bf16, or fp32 for an fp32 cache; row-strided views are fine) into
+    mla.kv_cache, with k_rope rotated by the tokens' positions on the way."""
+    s, m, r = seq.desc(), mla.desc(), plan.desc()
+    want = torch.float32 if m.dtype == DSA_F32 else torch.bfloat16
+    if latent.dtype != want or k_rope.dtype != want:
+        raise ValueError(f"latent and k_rope must be {want} for this cache")
+    if latent.shape != (s.T, m.d_latent) or k_rope.shape != (s.T, m.d_rope):
+        raise ValueError("latent must be [T, d_latent] and k_rope [T, d_rope]")
+    _check(_lib.dsa_latent_cache_append_rope(ctypes.byref(s), ctypes.byref(m), ctypes.byref(r),
+                                             _rows(latent, "latent"), latent.stride(0), _rows(k_rope, "k_rope"),
+                                             k_rope.stride(0), m.kv_cache, _stream(stream)))
+
+
+def index_cache_append_rope(seq: Seq, plan: Rope, k_new: torch.Tensor, k_cache: torch.Tensor, k_scale: torch.Tensor,
+                            offset: int = 0, stream=None, mx: bool = False) -> None:
+    """index_cache_append with dims [offset, offset + d_rot) of every new key
+    rotated by the token's position before it is quantised (k_new may be a
+    row-strided view)."""
+    s, r = seq.desc(), plan.desc()
+    if k_new.dim() != 2 or k_new.shape[0] != s.T:
+        raise ValueError("k_new must be [T, D_I]")
+    _check(_lib.dsa_index_cache_append_rope(ctypes.byref(s), ctypes.byref(r), k_new.shape[1], offset,
+                                            _dtype_code(k_new), DSA_MXFP8_E4M3 if mx else DSA_E4M3,
+                                            _rows(k_new, "k_new"), k_new.stride(0), _ptr(k_cache), _ptr(k_scale),
+                                            _stream(stream)))
+
+
+def latent_cache_read(seq: Seq, mla: Mla, out: torch.Tensor, stream=None) -> torch.Tensor:
+    """The latent rows of the positions of seq (q_seq, q_pos) in mla.kv_cache as the
+    values they stand for: out [T, d_latent + d_rope], bf16 or fp32 (a row-strided
+    view is fine)."""
+    s, m = seq.desc(), mla.desc()
+    if out.shape != (s.T, m.d_latent + m.d_rope):
+        raise ValueError("out must be [T, d_latent + d_rope]")
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out must be bfloat16 or float32")
+    _check(_lib.dsa_latent_cache_read(ctypes.byref(s), ctypes.byref(m), m.kv_cache,
+                                      DSA_F32 if out.dtype == torch.float32 else DSA_BF16, _rows(out, "out"),
+                                      out.stride(0), _stream(stream)))
+    return out
 
 
 def debug_withhold_arrival(enable: bool, wait_limit_ns: int = 2_000_000) -> None:

@@ -13,6 +13,7 @@
 #include "dsa.h"
 #include "dsa_device.cuh"
 #include "dsa_internal.h"
+#include "rope.cuh"
 
 namespace {
 
@@ -123,6 +124,13 @@ dsa_status_t check_mla_shape(const dsa_mla_desc_t* m, int32_t K, dsa::MlaArgs* a
         return fail(DSA_ERR_UNSUPPORTED, "FP8 latent rows are defined for 512 + 64 dims only");
       kind = dsa::MlaKind::kFP8Tile;
       min_row = 656;
+      break;
+    case DSA_E2M1:
+      if (m->d_latent != 512 || m->d_rope != 64)
+        return fail(DSA_ERR_UNSUPPORTED, "4-bit latent rows are defined for 512 + 64 dims only");
+      if (m->row_bytes % 16 != 0) return fail(DSA_ERR_INVALID_ARG, "row_bytes of 4-bit rows must be a multiple of 16");
+      kind = dsa::MlaKind::kE2M1;
+      min_row = 432;
       break;
     default: return fail(DSA_ERR_UNSUPPORTED, "unknown MLA cache dtype");
   }
@@ -519,7 +527,7 @@ dsa_status_t dsa_latent_cache_append(const dsa_seq_desc_t* seq, const dsa_mla_de
     dsa_status_t st = check_seq(seq, &s);
     if (st != DSA_OK) return st;
     if ((st = check_mla_shape(mla, 1, &a)) != DSA_OK) return st;
-    if (a.kind != dsa::MlaKind::kFP8Row && a.kind != dsa::MlaKind::kFP8Tile) {
+    if (a.kind == dsa::MlaKind::kF32 || a.kind == dsa::MlaKind::kBF16) {
       const int64_t row_in = static_cast<int64_t>(a.d_latent + a.d_rope) * (a.kind == dsa::MlaKind::kF32 ? 4 : 2);
       if (row_in % 16 != 0 || a.row_bytes % 16 != 0)
         return fail(DSA_ERR_UNSUPPORTED, "latent append copies 16-byte vectors: row and row_bytes must be multiples of 16");
@@ -532,8 +540,212 @@ dsa_status_t dsa_latent_cache_append(const dsa_seq_desc_t* seq, const dsa_mla_de
     dsa::LaunchEnv env;
     if ((st = make_env(stream, &env)) != DSA_OK) return st;
     std::string plan;
-    cudaError_t e = dsa::launch_latent_append(s, a, kv_new, kv_cache, env, &plan);
+    cudaError_t e;
+    if (a.kind == dsa::MlaKind::kE2M1)   // packed rows: the rope part follows the latent part
+      e = dsa::launch_latent_write(s, a, dsa::RopeArgs{nullptr, 64, false, 1.f}, kv_new, 1152,
+                                   static_cast<const char*>(kv_new) + 1024, 1152, kv_cache, env, &plan);
+    else
+      e = dsa::launch_latent_append(s, a, kv_new, kv_cache, env, &plan);
     if (e != cudaSuccess) return cuda_fail(e, "latent append launch");
+    g_last_plan = plan;
+    return DSA_OK;
+  } catch (...) {
+    return fail(DSA_ERR_CUDA, "unexpected host exception");
+  }
+}
+
+namespace {
+
+// Row sizes that the copying kernels move in 16-byte vectors: whole rows, and with
+// `parts` the latent and the rope part each.
+dsa_status_t check_copied_rows(const dsa::MlaArgs& a, bool parts) {
+  const int64_t es = a.kind == dsa::MlaKind::kF32 ? 4 : 2;
+  if (a.kind == dsa::MlaKind::kF32 || a.kind == dsa::MlaKind::kBF16) {
+    if ((static_cast<int64_t>(a.d_latent) + a.d_rope) * es % 16 != 0 || a.row_bytes % 16 != 0)
+      return fail(DSA_ERR_UNSUPPORTED, "cache rows and row_bytes must be multiples of 16 bytes");
+    if (parts && a.d_latent * es % 16 != 0)
+      return fail(DSA_ERR_UNSUPPORTED, "latent and rope part must be multiples of 16 bytes");
+  } else if (a.row_bytes % 16 != 0) {
+    return fail(DSA_ERR_INVALID_ARG, "row_bytes must be a multiple of 16");
+  }
+  return DSA_OK;
+}
+
+dsa_status_t check_rope(const dsa_rope_desc_t* r, bool used, dsa::RopeArgs* out) {
+  if (!r) return fail(DSA_ERR_INVALID_ARG, "rope descriptor is NULL");
+  if (r->d_rot < 2 || r->d_rot > 512 || r->d_rot % 2 != 0)
+    return fail(DSA_ERR_UNSUPPORTED, "d_rot must be even and in [2, 512]");
+  if (r->layout != DSA_ROPE_INTERLEAVED && r->layout != DSA_ROPE_HALF)
+    return fail(DSA_ERR_INVALID_ARG, "unknown rope layout");
+  if (used && !r->turns) return fail(DSA_ERR_INVALID_ARG, "rope turns must be non-NULL");
+  if (reinterpret_cast<uintptr_t>(r->turns) % 8 != 0) return fail(DSA_ERR_INVALID_ARG, "rope turns must be 8-byte aligned");
+  *out = dsa::RopeArgs{r->turns, r->d_rot, r->layout == DSA_ROPE_HALF, r->magnitude};
+  return DSA_OK;
+}
+
+// Whether rows of n values at t * st + h * sh are pairwise disjoint.
+bool rows_disjoint(int64_t T, int64_t st, int64_t H, int64_t sh, int64_t n) {
+  if (T <= 1 && H <= 1) return true;
+  if (H <= 1) return st >= n;
+  if (T <= 1) return sh >= n;
+  return (sh >= n && st >= (H - 1) * sh + n) || (st >= n && sh >= (T - 1) * st + n);
+}
+
+}  // namespace
+
+dsa_status_t dsa_rope_turns(int32_t d_rot, double theta, dsa_rope_scaling_t scaling, double factor,
+                            double original_ctx, double beta_fast, double beta_slow, uint64_t* turns,
+                            float* magnitude) {
+  try {
+    if (d_rot < 2 || d_rot > 512 || d_rot % 2 != 0)
+      return fail(DSA_ERR_UNSUPPORTED, "d_rot must be even and in [2, 512]");
+    if (!turns || !magnitude) return fail(DSA_ERR_INVALID_ARG, "turns and magnitude must be non-NULL");
+    if (!(theta > 1.0) || !(theta < 1e30)) return fail(DSA_ERR_INVALID_ARG, "theta must be in (1, 1e30)");
+    if (scaling != DSA_ROPE_PLAIN && scaling != DSA_ROPE_LINEAR && scaling != DSA_ROPE_NTK && scaling != DSA_ROPE_YARN)
+      return fail(DSA_ERR_INVALID_ARG, "unknown rope scaling");
+    if (scaling != DSA_ROPE_PLAIN && (!(factor >= 1.0) || !(factor < 1e9)))
+      return fail(DSA_ERR_INVALID_ARG, "the scaling factor must be in [1, 1e9)");
+    if (scaling == DSA_ROPE_NTK && d_rot < 4) return fail(DSA_ERR_UNSUPPORTED, "NTK scaling needs d_rot >= 4");
+    if (scaling == DSA_ROPE_YARN &&
+        (!(original_ctx >= 1.0) || !(original_ctx < 1e18) || !(beta_slow > 0.0) || !(beta_fast >= beta_slow) || !(beta_fast < 1e18)))
+      return fail(DSA_ERR_INVALID_ARG, "YaRN scaling needs original_ctx >= 1 and beta_fast >= beta_slow > 0");
+    dsa::rope_turns(d_rot, theta, scaling, factor, original_ctx, beta_fast, beta_slow, turns, magnitude);
+    return DSA_OK;
+  } catch (...) {
+    return fail(DSA_ERR_CUDA, "unexpected host exception");
+  }
+}
+
+dsa_status_t dsa_rope(const dsa_rope_desc_t* rope, int32_t T, int32_t H, const int32_t* pos, dsa_dtype_t dtype,
+                      const void* x, int64_t x_stride_t, int64_t x_stride_h, void* out, int64_t out_stride_t,
+                      int64_t out_stride_h, int32_t inverse, dsa_stream_t stream) {
+  try {
+    dsa::RopeArgs r;
+    if (T < 0 || H < 0 || H > 65535) return fail(DSA_ERR_INVALID_ARG, "need T >= 0 and 0 <= H <= 65535");
+    const bool used = T > 0 && H > 0;
+    dsa_status_t st = check_rope(rope, used, &r);
+    if (st != DSA_OK) return st;
+    if (dtype != DSA_F32 && dtype != DSA_BF16) return fail(DSA_ERR_UNSUPPORTED, "rope dtype must be DSA_F32 or DSA_BF16");
+    if (used && (!pos || !x || !out)) return fail(DSA_ERR_INVALID_ARG, "pos, x and out must be non-NULL");
+    const uintptr_t es = dtype == DSA_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(x) % es || reinterpret_cast<uintptr_t>(out) % es ||
+        reinterpret_cast<uintptr_t>(pos) % 4)
+      return fail(DSA_ERR_INVALID_ARG, "pos, x and out must be aligned to their elements");
+    if (x_stride_t < 0 || x_stride_h < 0 || out_stride_t < 0 || out_stride_h < 0)
+      return fail(DSA_ERR_INVALID_ARG, "strides must be >= 0");
+    if (used && !rows_disjoint(T, out_stride_t, H, out_stride_h, r.d_rot))
+      return fail(DSA_ERR_INVALID_ARG, "rows of out overlap");
+    if (used && x == out && ((T > 1 && x_stride_t != out_stride_t) || (H > 1 && x_stride_h != out_stride_h)))
+      return fail(DSA_ERR_INVALID_ARG, "in place, x and out must have the same strides");
+    dsa::LaunchEnv env;
+    if ((st = make_env(stream, &env)) != DSA_OK) return st;
+    std::string plan;
+    const cudaError_t e = dsa::launch_rope(r, T, H, pos, dtype == DSA_BF16, x, x_stride_t, x_stride_h, out, out_stride_t,
+                                           out_stride_h, inverse != 0, env, &plan);
+    if (e != cudaSuccess) return cuda_fail(e, "rope launch");
+    g_last_plan = plan;
+    return DSA_OK;
+  } catch (...) {
+    return fail(DSA_ERR_CUDA, "unexpected host exception");
+  }
+}
+
+dsa_status_t dsa_latent_cache_append_rope(const dsa_seq_desc_t* seq, const dsa_mla_desc_t* mla,
+                                          const dsa_rope_desc_t* rope, const void* latent, int64_t latent_stride,
+                                          const void* k_rope, int64_t rope_stride, void* kv_cache,
+                                          dsa_stream_t stream) {
+  try {
+    dsa::SeqArgs s;
+    dsa::MlaArgs a;
+    dsa::RopeArgs r;
+    dsa_status_t st = check_seq(seq, &s);
+    if (st != DSA_OK) return st;
+    if ((st = check_mla_shape(mla, 1, &a)) != DSA_OK) return st;
+    if ((st = check_copied_rows(a, true)) != DSA_OK) return st;
+    if ((st = check_rope(rope, s.T > 0, &r)) != DSA_OK) return st;
+    if (r.d_rot != a.d_rope) return fail(DSA_ERR_INVALID_ARG, "the rotation's d_rot must be the cache's d_rope");
+    if (s.T > 0 && (!latent || !k_rope || !kv_cache))
+      return fail(DSA_ERR_INVALID_ARG, "latent, k_rope and kv_cache must be non-NULL");
+    if (!aligned16(latent) || !aligned16(k_rope) || !aligned16(kv_cache))
+      return fail(DSA_ERR_INVALID_ARG, "latent, k_rope and kv_cache must be 16-byte aligned");
+    const int64_t es = a.kind == dsa::MlaKind::kF32 ? 4 : 2;
+    if (latent_stride < 0 || rope_stride < 0 || latent_stride * es % 16 != 0 || rope_stride * es % 16 != 0)
+      return fail(DSA_ERR_INVALID_ARG, "strides of latent and k_rope must be >= 0 and multiples of 16 bytes");
+    dsa::LaunchEnv env;
+    if ((st = make_env(stream, &env)) != DSA_OK) return st;
+    std::string plan;
+    const cudaError_t e = dsa::launch_latent_write(s, a, r, latent, latent_stride * es, k_rope, rope_stride * es,
+                                                   kv_cache, env, &plan);
+    if (e != cudaSuccess) return cuda_fail(e, "latent append launch");
+    g_last_plan = plan;
+    return DSA_OK;
+  } catch (...) {
+    return fail(DSA_ERR_CUDA, "unexpected host exception");
+  }
+}
+
+dsa_status_t dsa_index_cache_append_rope(const dsa_seq_desc_t* seq, const dsa_rope_desc_t* rope, int32_t D_I,
+                                         int32_t rot_offset, dsa_dtype_t src_dtype, dsa_dtype_t key_dtype,
+                                         const void* k_new, int64_t k_stride, uint8_t* k_cache, void* k_scale,
+                                         dsa_stream_t stream) {
+  try {
+    dsa::SeqArgs s;
+    dsa::RopeArgs r;
+    dsa_status_t st = check_seq(seq, &s);
+    if (st != DSA_OK) return st;
+    if (key_dtype != DSA_E4M3 && key_dtype != DSA_MXFP8_E4M3)
+      return fail(DSA_ERR_UNSUPPORTED, "index keys are cached as DSA_E4M3 or DSA_MXFP8_E4M3");
+    const bool mx = key_dtype == DSA_MXFP8_E4M3;
+    if (mx ? (D_I < 32 || D_I > 1024 || D_I % 32 != 0) : (D_I < 4 || D_I > 1024 || D_I % 4 != 0))
+      return fail(DSA_ERR_UNSUPPORTED, mx ? "MXFP8 index-key append needs D_I in [32, 1024], a multiple of 32"
+                                          : "index-key append needs D_I in [4, 1024], a multiple of 4");
+    if (src_dtype != DSA_F32 && src_dtype != DSA_BF16)
+      return fail(DSA_ERR_UNSUPPORTED, "new index keys must be DSA_F32 or DSA_BF16");
+    if ((st = check_rope(rope, s.T > 0, &r)) != DSA_OK) return st;
+    if (rot_offset < 0 || rot_offset > D_I - r.d_rot)
+      return fail(DSA_ERR_INVALID_ARG, "the rotated dims must lie within the key");
+    if (s.T > 0 && (!k_new || !k_cache || !k_scale))
+      return fail(DSA_ERR_INVALID_ARG, "k_new, k_cache and k_scale must be non-NULL");
+    if (!aligned16(k_new) || !aligned16(k_cache) || !aligned16(k_scale))
+      return fail(DSA_ERR_INVALID_ARG, "k_new, k_cache and k_scale must be 16-byte aligned");
+    const int64_t es = src_dtype == DSA_F32 ? 4 : 2;
+    if (k_stride < 0 || k_stride % 4 != 0)
+      return fail(DSA_ERR_INVALID_ARG, "the stride of k_new must be >= 0 and a multiple of 4 values");
+    dsa::LaunchEnv env;
+    if ((st = make_env(stream, &env)) != DSA_OK) return st;
+    std::string plan;
+    const cudaError_t e = dsa::launch_index_write(s, r, D_I, rot_offset, src_dtype == DSA_BF16, mx, k_new, k_stride * es,
+                                                  k_cache, k_scale, env, &plan);
+    if (e != cudaSuccess) return cuda_fail(e, "index-key append launch");
+    g_last_plan = plan;
+    return DSA_OK;
+  } catch (...) {
+    return fail(DSA_ERR_CUDA, "unexpected host exception");
+  }
+}
+
+dsa_status_t dsa_latent_cache_read(const dsa_seq_desc_t* seq, const dsa_mla_desc_t* mla, const void* kv_cache,
+                                   dsa_dtype_t out_dtype, void* out, int64_t out_stride, dsa_stream_t stream) {
+  try {
+    dsa::SeqArgs s;
+    dsa::MlaArgs a;
+    dsa_status_t st = check_seq(seq, &s);
+    if (st != DSA_OK) return st;
+    if ((st = check_mla_shape(mla, 1, &a)) != DSA_OK) return st;
+    if ((st = check_copied_rows(a, false)) != DSA_OK) return st;
+    if (out_dtype != DSA_F32 && out_dtype != DSA_BF16)
+      return fail(DSA_ERR_UNSUPPORTED, "rows are read as DSA_F32 or DSA_BF16");
+    if (s.T > 0 && (!kv_cache || !out)) return fail(DSA_ERR_INVALID_ARG, "kv_cache and out must be non-NULL");
+    if (!aligned16(kv_cache) || !aligned16(out))
+      return fail(DSA_ERR_INVALID_ARG, "kv_cache and out must be 16-byte aligned");
+    const int64_t es = out_dtype == DSA_F32 ? 4 : 2;
+    if (s.T > 1 && (out_stride < a.d_latent + a.d_rope || out_stride * es % 16 != 0))
+      return fail(DSA_ERR_INVALID_ARG, "the stride of out must hold a row and be a multiple of 16 bytes");
+    dsa::LaunchEnv env;
+    if ((st = make_env(stream, &env)) != DSA_OK) return st;
+    std::string plan;
+    const cudaError_t e = dsa::launch_latent_read(s, a, kv_cache, out_dtype == DSA_F32, out, out_stride * es, env, &plan);
+    if (e != cudaSuccess) return cuda_fail(e, "latent read launch");
     g_last_plan = plan;
     return DSA_OK;
   } catch (...) {
@@ -616,7 +828,7 @@ dsa_status_t dsa_check_status(dsa_stream_t stream) {
     if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
     const uint32_t f = dsa_status_read_clear_indexer() | dsa_status_read_clear_topk() |
                        dsa_status_read_clear_attn() | dsa_status_read_clear_cache() |
-                       dsa_status_read_clear_prolog();
+                       dsa_status_read_clear_prolog() | dsa_status_read_clear_rows();
     if (f == 0) return DSA_OK;
     if (f == 0xFFFFFFFFu) return fail(DSA_ERR_CUDA, "could not read the device status word");
     std::string msg = "device flags:";

@@ -30,6 +30,7 @@
 
 #include "dsa_device.cuh"
 #include "dsa_internal.h"
+#include "latent_e2m1.cuh"
 
 DSA_DEFINE_STATUS_WORD(attn)
 
@@ -48,6 +49,9 @@ __device__ __forceinline__ float load_elem(MlaKind kind, const uint8_t* row, int
       return reinterpret_cast<const float*>(row)[d];
     case MlaKind::kBF16:
       return bf16_bits_to_float(reinterpret_cast<const uint16_t*>(row)[d]);
+    case MlaKind::kE2M1:
+      return d < 512 ? e2m1_latent(row, d)
+                     : bf16_bits_to_float(reinterpret_cast<const uint16_t*>(row + kE2m1Rope)[d - 512]);
     default: {  // 656-byte FP8 row
       // per-token scale at byte 512, or (per-128-tile rows) scale d / 128 at 512 + 4 (d / 128)
       const int si = kind == MlaKind::kFP8Tile ? d / 128 : 0;
@@ -1046,7 +1050,7 @@ cudaError_t launch_combine(const uint16_t* ws_o, const float* ws_lse, int n_spli
 
 bool tc_supported(const SeqArgs& seq, const MlaArgs& a) {
   if (a.H != kH || a.d_latent != kDv || a.d_rope != kDqk - kDv) return false;
-  if (a.kind == MlaKind::kF32) return false;
+  if (a.kind == MlaKind::kF32 || a.kind == MlaKind::kE2M1) return false;
   if (a.kind == MlaKind::kBF16 && a.row_bytes % 16 != 0) return false;
   if ((a.kind == MlaKind::kFP8Row || a.kind == MlaKind::kFP8Tile) && a.row_bytes % 16 != 0) return false;
   if (reinterpret_cast<uintptr_t>(a.kv) % 16 || reinterpret_cast<uintptr_t>(a.q) % 16 ||

@@ -36,7 +36,8 @@ struct IndexerArgs {
   int64_t ld;
 };
 
-enum class MlaKind { kF32 = 0, kBF16 = 1, kFP8Row = 2, kFP8Tile = 3 };   // kFP8Tile: scale per 128 latent dims
+// kFP8Tile: scale per 128 latent dims; kE2M1: 4-bit codes, scale per 16 dims and per row
+enum class MlaKind { kF32 = 0, kBF16 = 1, kFP8Row = 2, kFP8Tile = 3, kE2M1 = 4 };
 
 struct MlaArgs {
   int32_t H, d_latent, d_rope;
@@ -142,6 +143,25 @@ cudaError_t launch_index_append_mx(const SeqArgs& seq, int32_t D, bool bf16_in, 
 cudaError_t launch_latent_append(const SeqArgs& seq, const MlaArgs& a, const void* kv_new, void* kv_cache,
                                  const LaunchEnv& env, std::string* plan);
 
+// Rotary positions (rope.cuh holds RopeArgs): strided heads, and the host side's frequencies.
+struct RopeArgs;
+cudaError_t launch_rope(const RopeArgs& rope, int32_t T, int32_t H, const int32_t* pos, bool bf16, const void* x,
+                        int64_t x_st, int64_t x_sh, void* out, int64_t o_st, int64_t o_sh, bool inverse,
+                        const LaunchEnv& env, std::string* plan);
+void rope_turns(int32_t d_rot, double theta, int scaling, double factor, double original_ctx, double beta_fast,
+                double beta_slow, uint64_t* turns, float* magnitude);
+
+// Cache writers that rotate (rope.turns null: the rope part is copied) and the
+// cache reader.  Strides in bytes.
+cudaError_t launch_latent_write(const SeqArgs& seq, const MlaArgs& a, const RopeArgs& rope, const void* latent,
+                                int64_t latent_stride, const void* k_rope, int64_t rope_stride, void* kv_cache,
+                                const LaunchEnv& env, std::string* plan);
+cudaError_t launch_index_write(const SeqArgs& seq, const RopeArgs& rope, int32_t D, int32_t off, bool bf16_in, bool mx,
+                               const void* k_new, int64_t stride, uint8_t* k_cache, void* k_scale,
+                               const LaunchEnv& env, std::string* plan);
+cudaError_t launch_latent_read(const SeqArgs& seq, const MlaArgs& a, const void* kv_cache, bool f32_out, void* out,
+                               int64_t out_stride, const LaunchEnv& env, std::string* plan);
+
 // Sets the text dsa_last_error() returns on the calling thread.
 void set_last_error(const std::string& msg);
 
@@ -179,3 +199,4 @@ uint32_t dsa_status_read_clear_topk();
 uint32_t dsa_status_read_clear_attn();
 uint32_t dsa_status_read_clear_cache();
 uint32_t dsa_status_read_clear_prolog();
+uint32_t dsa_status_read_clear_rows();

@@ -67,7 +67,8 @@ class Workload:
     k_i: np.ndarray
     k_i_scale: np.ndarray        # float32 [cache_rows]
     # MLA latent attention
-    mla_dtype: str               # "bf16" | "e4m3" (per-token scale) | "e4m3_t128" (scale per 128 latent dims) | "f32"
+    mla_dtype: str               # "bf16" | "e4m3" (per-token scale) | "e4m3_t128" (scale per 128 latent dims) |
+    #                              "e2m1" (4-bit codes, scale per 16 latent dims and per row) | "f32"
     H: int
     d_latent: int
     d_rope: int
@@ -185,6 +186,37 @@ def _spread_blocks(g: torch.Generator, x: torch.Tensor, spread: int, block: int 
     x.view(*shp[:-1], shp[-1] // block, block).mul_(torch.pow(2.0, r.to(torch.float32)))
 
 
+E2M1_ROW_BYTES = 432         # 256 code bytes, 32 E4M3 scales, fp32 row scale, 12 reserved, 128 rope
+
+
+def _quant_rows_e2m1(x: torch.Tensor) -> np.ndarray:
+    """Rows [n, 576] -> 4-bit latent rows (uint8 [n, 432]): row scale 2**e with
+    e = floor(log2 amax) - 10, block scale = the E4M3 value nearest to the block's
+    amax * 2**-e / 6, code = the E2M1 value nearest to x * 2**-e / block scale
+    (ties to even), of bf16 latent values."""
+    n = x.shape[0]
+    lat = x[:, :512].to(torch.bfloat16).float()
+    amax = lat.abs().amax(dim=1, keepdim=True)
+    e = torch.where(amax > 0, torch.frexp(amax)[1] - 11, torch.zeros_like(amax, dtype=torch.int32))
+    b = torch.ldexp(lat, -e).view(n, 32, 16)
+    s8 = (b.abs().amax(dim=2) / 6.0).to(torch.float8_e4m3fn)
+    s = s8.float()[:, :, None]
+    q = torch.where(s > 0, b / torch.where(s > 0, s, torch.ones_like(s)), torch.zeros_like(b))
+    # magnitude codes by the midpoints between the values; a tie goes to the even code
+    a = q.abs()
+    code = torch.zeros_like(a, dtype=torch.uint8)
+    for mid, up in ((0.25, False), (0.75, True), (1.25, False), (1.75, True), (2.5, False), (3.5, True), (5.0, False)):
+        code += ((a >= mid) if up else (a > mid)).to(torch.uint8)
+    code += torch.signbit(q).to(torch.uint8) * 8
+    code = code.view(n, 256, 2)
+    kv = np.zeros((n, E2M1_ROW_BYTES), dtype=np.uint8)
+    kv[:, :256] = (code[:, :, 0] + 16 * code[:, :, 1]).numpy()
+    kv[:, 256:288] = s8.view(torch.uint8).numpy()
+    kv[:, 288:292] = torch.ldexp(torch.ones_like(amax), e).numpy().astype("<f4").view(np.uint8).reshape(n, 4)
+    kv[:, 304:] = _bf16_bits(x[:, 512:]).view(np.uint8).reshape(n, -1)
+    return kv
+
+
 def _bf16_bits(x: torch.Tensor) -> np.ndarray:
     return x.to(torch.bfloat16).view(torch.int16).numpy().view(np.uint16)
 
@@ -300,6 +332,12 @@ def make(name_or_spec, seed: int = 0, **over) -> Workload:
         kv[:, FP8_SCALE_OFFSET:FP8_SCALE_OFFSET + 16] = scales.view(np.uint8).reshape(-1, 16)
         kv[:, FP8_ROPE_OFFSET:] = _bf16_bits(kv_f[:, sp.d_latent:]).view(np.uint8).reshape(cache_rows, -1)
         row_bytes = FP8_ROW_BYTES
+    elif sp.mla_dtype == "e2m1":
+        # 432-byte rows: 512 E2M1 codes, 32 E4M3 scales (16 dims each), a
+        # power-of-two fp32 row scale, 64 bf16 rope values
+        assert sp.d_latent == 512 and sp.d_rope == 64
+        kv = _quant_rows_e2m1(kv_f)
+        row_bytes = E2M1_ROW_BYTES
     elif sp.mla_dtype == "f32":
         kv = kv_f.numpy()
         row_bytes = dk * 4
@@ -357,6 +395,9 @@ def device_tensors(wl: Workload, device, copies: int = 1) -> dict:
         elif wl.mla_dtype == "e4m3_t128":
             q, kv = t(wl.q.view(np.int16), torch.bfloat16), t(wl.kv)
             dt = 4  # FP8 rows with a power-of-two scale per 128 latent dims
+        elif wl.mla_dtype == "e2m1":
+            q, kv = t(wl.q.view(np.int16), torch.bfloat16), t(wl.kv)
+            dt = 5  # 4-bit rows
         else:
             q, kv = t(wl.q), t(wl.kv)
             dt = None

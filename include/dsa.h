@@ -31,7 +31,7 @@
  *    the offending element is skipped and a sticky device status word is set;
  *    dsa_check_status() reads and clears it.
  *  - Calls are thread-safe; dsa_last_error()/dsa_last_plan() are per thread.
- *  - Base pointers must be 16-byte aligned.  Row-major, densely packed layouts
+ *  - Base pointers must be 16-byte aligned (dsa_rope: aligned to their elements).  Row-major, densely packed layouts
  *    unless a stride is given.
  */
 #ifndef DSA_H_
@@ -64,8 +64,12 @@ typedef enum dsa_dtype {
   DSA_MXFP8_E4M3 = 3,        /* OCP MXFP8: E4M3 codes, one E8M0 scale byte         */
                              /* 2**(e - 127) per 32 consecutive elements (indexer  */
                              /* only)                                              */
-  DSA_E4M3_T128 = 4          /* MLA cache only: 656-byte FP8 rows with one fp32    */
+  DSA_E4M3_T128 = 4,         /* MLA cache only: 656-byte FP8 rows with one fp32    */
                              /* scale per 128 latent dims (layout below)           */
+  DSA_E2M1 = 5               /* MLA cache only: 432-byte rows of 4-bit E2M1 codes  */
+                             /* (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives)   */
+                             /* with one E4M3 scale per 16 latent dims and one fp32*/
+                             /* scale per row (layout below)                       */
 } dsa_dtype_t;
 
 typedef void* dsa_stream_t;  /* cudaStream_t */
@@ -136,6 +140,17 @@ typedef struct dsa_mla_desc {
                              /*   widens code * scale to bf16: exact when every    */
                              /*   scale is a power of two (as the cache writer     */
                              /*   produces them), rounded to bf16 otherwise.       */
+                             /*  DSA_E2M1: 432-byte row (d_latent 512, d_rope 64): */
+                             /*   [0,256) codes, latent dim 2 i in the low nibble  */
+                             /*   of byte i and dim 2 i + 1 in the high one;       */
+                             /*   [256,288) 32 E4M3 scales, scale b for latent     */
+                             /*   dims [16 b, 16 b + 16); [288,292) the fp32 row   */
+                             /*   scale; [292,304) reserved; [304,432) 64 bf16     */
+                             /*   rope values.  Value = code * scale * row scale.  */
+                             /*   The tensor-core path widens values to bf16:      */
+                             /*   exact when the row scale is a power of two (as   */
+                             /*   the cache writers store it), rounded otherwise.  */
+                             /*   row_bytes a multiple of 16.                      */
                              /*  DSA_F32 : row = d_latent+d_rope fp32 values       */
   const void* q;             /* device [T, H, d_latent+d_rope]: bf16, or fp32 when */
                              /* dtype == DSA_F32                                   */
@@ -256,9 +271,94 @@ dsa_status_t dsa_index_cache_append_mx(const dsa_seq_desc_t* seq, int32_t D_I, d
  *      part quantised with the exponent rule of dsa_index_cache_append_mx on
  *      128-value blocks, its scale 2**x_i stored as fp32 at [512 + 4 i, 516 + 4 i)
  *      (a power of two, so the attention kernel widens code * scale to bf16
- *      exactly), the rope copied to [528,656). */
+ *      exactly), the rope copied to [528,656);
+ *    DSA_E2M1 (432-byte rows, 512 + 64): row scale 2**e with
+ *      e = floor(log2 max_i |latent_i|) - 10 (clamped to [-126, 117]; 1 for an
+ *      all-zero latent part), block scale s_b = the E4M3 value nearest to
+ *      max_b |latent| * 2**-e / 6 (fp32 quotient), code = the E2M1 value nearest
+ *      to latent * 2**-e / s_b (fp32 quotient), ties to the even code, magnitudes
+ *      beyond 6 saturated; zero codes where s_b is 0; zero bytes at [292,304); the
+ *      rope copied to [304,432).  Latent values must be finite (an infinity is
+ *      stored as the largest magnitude of its row, a NaN as one of them). */
 dsa_status_t dsa_latent_cache_append(const dsa_seq_desc_t* seq, const dsa_mla_desc_t* mla, const void* kv_new,
                                      void* kv_cache, dsa_stream_t stream);
+
+/* Rotary positions.  The rope part of the cached rows and of the queries (64 dims
+ * of the MLA rows and heads, some dims of the indexer's) carries the position by
+ * rotating pairs of values: pair i at position p becomes
+ *   (a cos(p f_i) - b sin(p f_i), a sin(p f_i) + b cos(p f_i)) * magnitude.
+ * Pair i is (2 i, 2 i + 1) (INTERLEAVED) or (i, i + d_rot / 2) (HALF).  The
+ * frequencies are device data: turns[i] = frac(f_i / 2 pi) * 2**64, from
+ * dsa_rope_turns.  A position's angle is formed from them modulo one turn in
+ * 64-bit integers, so far positions lose nothing; cosines, sines and products are
+ * fp32, each output is rounded once. */
+typedef enum dsa_rope_layout { DSA_ROPE_INTERLEAVED = 0, DSA_ROPE_HALF = 1 } dsa_rope_layout_t;
+typedef enum dsa_rope_scaling {
+  DSA_ROPE_PLAIN = 0,        /* f_i = theta ** (-2 i / d_rot)                      */
+  DSA_ROPE_LINEAR = 1,       /* f_i / factor                                       */
+  DSA_ROPE_NTK = 2,          /* theta * factor ** (d_rot / (d_rot - 2)) for theta   */
+  DSA_ROPE_YARN = 3          /* f_i (1 - r_i) + f_i / factor * r_i: r ramps from 0  */
+                             /* to 1 over the pairs between the one that turns      */
+                             /* beta_fast times in original_ctx positions (rounded  */
+                             /* down, at least 0) and the one that turns beta_slow  */
+                             /* times (rounded up, at most d_rot - 1);              */
+                             /* magnitude 0.1 ln(factor) + 1                        */
+} dsa_rope_scaling_t;
+typedef struct dsa_rope_desc {
+  int32_t d_rot;             /* rotated dims (even, 2 .. 512)                      */
+  dsa_rope_layout_t layout;
+  const uint64_t* turns;     /* device [d_rot / 2]                                 */
+  float magnitude;           /* factor on cosine and sine                          */
+} dsa_rope_desc_t;
+/* Fills HOST memory turns[d_rot / 2] and *magnitude; the caller copies the turns
+ * to the device and keeps them.  theta > 1; factor >= 1 (not used by PLAIN);
+ * original_ctx, beta_fast and beta_slow are used by YARN (32 and 1 are usual betas).
+ * No CUDA call is made. */
+dsa_status_t dsa_rope_turns(int32_t d_rot, double theta, dsa_rope_scaling_t scaling, double factor,
+                            double original_ctx, double beta_fast, double beta_slow, uint64_t* turns,
+                            float* magnitude);
+/* out[t, h, :] = x[t, h, :] (d_rot values each) rotated by position pos[t] (device
+ * int32 [T], any value).  dtype: DSA_F32 or DSA_BF16, of x and out.  Strides in
+ * values; the values of a row are contiguous.  Part of a head is rotated by
+ * pointing x and out into it.  x may have equal rows (stride 0); the rows of out
+ * must be disjoint; out is x with the same strides (in place) or shares no value
+ * with it.  inverse != 0 applies the transposed matrix: the gradient of the
+ * rotation, and for magnitude 1 its inverse.  Rows and strides that are multiples
+ * of 16 bytes move in 16-byte vectors. */
+dsa_status_t dsa_rope(const dsa_rope_desc_t* rope, int32_t T, int32_t H, const int32_t* pos, dsa_dtype_t dtype,
+                      const void* x, int64_t x_stride_t, int64_t x_stride_h, void* out, int64_t out_stride_t,
+                      int64_t out_stride_h, int32_t inverse, dsa_stream_t stream);
+
+/* Cache writers that rotate on the way: as dsa_latent_cache_append and
+ * dsa_index_cache_append[_mx], with the rope part (index keys: dims
+ * [rot_offset, rot_offset + d_rot)) rotated by the token's position q_pos[t]
+ * in fp32 before it is rounded or quantised.
+ *
+ * Latent rows: latent device [T, d_latent] and k_rope device [T, d_rope], bf16
+ *   (fp32 when mla->dtype == DSA_F32), with strides between tokens in values
+ *   (multiples of 16 bytes; 0 writes one row for every token); rope->d_rot ==
+ *   mla->d_rope.  Every cache format. */
+dsa_status_t dsa_latent_cache_append_rope(const dsa_seq_desc_t* seq, const dsa_mla_desc_t* mla,
+                                          const dsa_rope_desc_t* rope, const void* latent, int64_t latent_stride,
+                                          const void* k_rope, int64_t rope_stride, void* kv_cache,
+                                          dsa_stream_t stream);
+/* Index keys: k_new device [T, D_I] fp32 or bf16 (src_dtype) with a stride between
+ *   tokens in values (a multiple of 4); key_dtype DSA_E4M3 (k_scale fp32
+ *   [cache_rows]) or DSA_MXFP8_E4M3 (k_scale uint8 [cache_rows, D_I / 32]). */
+dsa_status_t dsa_index_cache_append_rope(const dsa_seq_desc_t* seq, const dsa_rope_desc_t* rope, int32_t D_I,
+                                         int32_t rot_offset, dsa_dtype_t src_dtype, dsa_dtype_t key_dtype,
+                                         const void* k_new, int64_t k_stride, uint8_t* k_cache, void* k_scale,
+                                         dsa_stream_t stream);
+
+/* Cache reader: out[t, :] = the d_latent + d_rope values that the latent row of
+ * position q_pos[t] of sequence q_seq[t] stands for, as bf16 (rounded to nearest
+ * even) or fp32, with out_stride values between rows (multiples of 16 bytes).  Any
+ * cache format; the rope part comes as it is held (rotated).  A position or page
+ * out of range is flagged (dsa_check_status) and its row of out is left as it was.
+ * mla gives the dims, the format and row_bytes.  For expanding a cached prefix
+ * again, moving rows between formats, and looking at what a cache holds. */
+dsa_status_t dsa_latent_cache_read(const dsa_seq_desc_t* seq, const dsa_mla_desc_t* mla, const void* kv_cache,
+                                   dsa_dtype_t out_dtype, void* out, int64_t out_stride, dsa_stream_t stream);
 
 /* Testing aid for the failure-detection path; the pages have no counterpart.
  * Every pipeline wait in the kernels is bounded: a wait that gives up sets a

@@ -158,6 +158,87 @@ def quantize_e4m3_row(x) -> tuple:
     return e4m3_encode((x / scale).astype(np.float32)), scale
 
 
+E2M1_MAGNITUDES = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+E2M1_ROW_BYTES = 432
+E2M1_ROPE_OFFSET = 304
+
+
+def decode_e2m1(codes) -> np.ndarray:
+    """float64 value of 4-bit E2M1 codes (OCP FP4): bit 3 the sign, bits 2-1 the
+    exponent (bias 1), bit 0 the mantissa; codes 0..7 hold 0, 0.5, 1, 1.5, 2, 3, 4, 6."""
+    codes = np.asarray(codes, dtype=np.int64)
+    v = E2M1_MAGNITUDES[codes & 7]
+    return np.where(codes & 8, -v, v)
+
+
+def e2m1_encode(x) -> np.ndarray:
+    """E2M1 code nearest to each value, ties to the code with an even mantissa,
+    magnitudes beyond 6 saturated, the sign bit kept."""
+    x = np.asarray(x, dtype=np.float64)
+    d = np.abs(np.abs(x)[..., None] - E2M1_MAGNITUDES)
+    best = d.min(axis=-1, keepdims=True)
+    # among the (at most two) nearest codes the even one; the lone nearest otherwise
+    order = np.where(d == best, np.arange(8) % 2, 2)
+    return (order.argmin(axis=-1) | (np.signbit(x).astype(np.int64) << 3)).astype(np.uint8)
+
+
+def quantize_e2m1_row(x) -> tuple:
+    """One token's latent vector [512] -> (256 code bytes, 32 E4M3 scale codes,
+    row scale): row scale 2**e, e = floor(log2 amax) - 10 within [-126, 117] (1 for
+    an all-zero row); block scale = e4m3(amax of 16 values * 2**-e / 6), code =
+    e2m1(x * 2**-e / block scale), both quotients formed in float32; zero codes
+    where the block scale is 0.  Even dims in the low nibbles."""
+    x = np.asarray(x, dtype=np.float32)
+    amax = float(np.max(np.abs(x)))
+    e = int(np.clip(np.frexp(amax)[1] - 1 - 10, -126, 117)) if amax > 0 else 0
+    xs = np.ldexp(x.astype(np.float64), -e).astype(np.float32).reshape(32, 16)
+    sc = e4m3_encode((np.abs(xs).max(axis=1) / np.float32(6.0)).astype(np.float32))
+    s = decode_e4m3(sc).astype(np.float32)[:, None]
+    q = np.divide(xs, s, out=np.zeros_like(xs), where=s > 0)
+    codes = np.where(s > 0, e2m1_encode(q), 0).astype(np.uint8).reshape(256, 2)
+    return codes[:, 0] | (codes[:, 1] << 4), sc, np.float32(np.ldexp(1.0, e))
+
+
+def e2m1_row(latent, rope_bits) -> np.ndarray:
+    """The 432 bytes of a 4-bit latent row: codes, block scales, row scale, zeros, rope."""
+    codes, sc, rs = quantize_e2m1_row(latent)
+    row = np.zeros(E2M1_ROW_BYTES, dtype=np.uint8)
+    row[:256], row[256:288] = codes, sc
+    row[288:292] = np.frombuffer(np.float32(rs).astype("<f4").tobytes(), dtype=np.uint8)
+    row[E2M1_ROPE_OFFSET:] = np.frombuffer(np.asarray(rope_bits, dtype="<u2").tobytes(), dtype=np.uint8)
+    return row
+
+
+def rope_frequencies(d_rot, theta=10000.0, scaling="none", factor=1.0, original_ctx=0.0, beta_fast=32.0,
+                     beta_slow=1.0):
+    """(angular frequency of each of the d_rot / 2 pairs, factor on cosine and sine), float64."""
+    i = np.arange(d_rot // 2, dtype=np.float64)
+    if scaling == "ntk":
+        theta = theta * factor ** (d_rot / (d_rot - 2.0))
+    f = theta ** (-2.0 * i / d_rot)
+    if scaling == "linear":
+        f = f / factor
+    if scaling != "yarn":
+        return f, 1.0
+    at = [d_rot * math.log(original_ctx / (b * 2.0 * math.pi)) / (2.0 * math.log(theta)) for b in (beta_fast, beta_slow)]
+    lo, hi = max(math.floor(at[0]), 0), min(math.ceil(at[1]), d_rot - 1)
+    r = np.clip((i - lo) / max(hi - lo, 0.001), 0.0, 1.0)
+    return f * (1.0 - r) + f / factor * r, 0.1 * math.log(factor) + 1.0
+
+
+def rope_rotate(x, angle, layout="interleaved", magnitude=1.0, inverse=False) -> np.ndarray:
+    """x [T, ..., d_rot] rotated pair by pair by angle [T, d_rot / 2] (float64)."""
+    x = np.asarray(x, dtype=np.float64)
+    angle = np.asarray(angle, dtype=np.float64).reshape(angle.shape[0], *([1] * (x.ndim - 2)), angle.shape[1])
+    c, s = magnitude * np.cos(angle), magnitude * np.sin(angle) * (-1.0 if inverse else 1.0)
+    out = np.empty_like(x)
+    n = x.shape[-1] // 2
+    first, second = (np.s_[..., 0::2], np.s_[..., 1::2]) if layout == "interleaved" else (np.s_[..., :n], np.s_[..., n:])
+    out[first] = x[first] * c - x[second] * s
+    out[second] = x[first] * s + x[second] * c
+    return out
+
+
 def physical_rows(block_table_row: np.ndarray, page_size: int, pos: np.ndarray) -> np.ndarray:
     """Logical position -> cache row through the page table:
     row = block_table[s // page_size] * page_size + s % page_size."""
@@ -196,6 +277,12 @@ def latent_rows(wl, rows: np.ndarray) -> np.ndarray:
     if wl.mla_dtype == "f32":
         return wl.kv[rows].astype(np.float64)
     raw = wl.kv[rows]
+    if wl.mla_dtype == "e2m1":
+        # 432-byte row: codes, 32 E4M3 block scales, fp32 row scale, bf16 rope at 304
+        codes = np.stack([raw[:, :256] & 15, raw[:, :256] >> 4], axis=2).reshape(-1, 512)
+        scale = decode_e4m3(raw[:, 256:288]) * raw[:, 288:292].copy().view("<f4").astype(np.float64)
+        rope = decode_bf16(raw[:, 304:432].copy().view("<u2"))
+        return np.concatenate([decode_e2m1(codes) * np.repeat(scale, 16, axis=1), rope], axis=1)
     if wl.mla_dtype == "e4m3_t128":
         # 656-byte FP8 row with four fp32 scales at [512,528), one per 128 latent dims
         scales = raw[:, 512:528].copy().view("<f4").astype(np.float64)   # [n, 4]
