@@ -310,7 +310,9 @@ __device__ __forceinline__ void t48_issue_s(uint32_t tmem, uint32_t scol, uint64
 
 // kTile: FP8 rows with one power-of-two scale per 128 latent dims, widened to
 // bf16 as code * scale by the producers (exact); the rest runs the bf16 plan.
-template <bool kFp8, bool kTile = false>
+// kE4 (with kTile): 4-bit rows, widened the same way as code * block scale * row
+// scale (exact for a power-of-two row scale).
+template <bool kFp8, bool kTile = false, bool kE4 = false>
 __global__ void __launch_bounds__(kT48Threads, 1) attn_tc48_kernel(TcAttnParams p) {
   using C = T48<kFp8>;
   constexpr int S = C::kStages;
@@ -478,14 +480,32 @@ __global__ void __launch_bounds__(kT48Threads, 1) attn_tc48_kernel(TcAttnParams 
       float my_scale = 0.f;
       if constexpr (kFp8 || kTile) {
 #pragma unroll
-        for (int rr = 0; rr < kRows; ++rr)
-          raw[rr] = rows[rr] >= 0 ? ld_global_nc_v4(kv + static_cast<int64_t>(rows[rr]) * p.a.row_bytes + lane * 16)
-                                  : make_uint4(0u, 0u, 0u, 0u);
+        for (int rr = 0; rr < kRows; ++rr) {
+          raw[rr] = make_uint4(0u, 0u, 0u, 0u);
+          if (rows[rr] >= 0) {
+            const uint8_t* rp = kv + static_cast<int64_t>(rows[rr]) * p.a.row_bytes;
+            if constexpr (kE4) {
+              const uint2 u = __ldg(reinterpret_cast<const uint2*>(rp) + lane);
+              raw[rr].x = u.x;
+              raw[rr].y = u.y;
+            } else {
+              raw[rr] = ld_global_nc_v4(rp + lane * 16);
+            }
+          }
+        }
       }
       if constexpr (kFp8) {
         if (my_row >= 0) my_scale = __ldg(reinterpret_cast<const float*>(kv + my_row * p.a.row_bytes + kDv));
       }
-      if constexpr (kTile) {
+      if constexpr (kE4) {
+#pragma unroll
+        for (int rr = 0; rr < kRows; ++rr) {
+          const uint8_t* rp = kv + static_cast<int64_t>(rows[rr]) * p.a.row_bytes;
+          tsc[rr] = rows[rr] >= 0 ? e4m3_to_float(__ldg(rp + kE2m1Scales + lane)) *
+                                        __ldg(reinterpret_cast<const float*>(rp + kE2m1RowScale))
+                                  : 0.f;
+        }
+      } else if constexpr (kTile) {
 #pragma unroll
         for (int rr = 0; rr < kRows; ++rr)
           tsc[rr] = rows[rr] >= 0 ? __ldg(reinterpret_cast<const float*>(kv + static_cast<int64_t>(rows[rr]) *
@@ -548,7 +568,7 @@ __global__ void __launch_bounds__(kT48Threads, 1) attn_tc48_kernel(TcAttnParams 
           if (lane < 8) {
             const uint32_t dst = drow + 8 * kBR48 * 128 + static_cast<uint32_t>(((lane & 7) ^ (r & 7)) << 4);
             if (prow >= 0)
-              cp_async16(dst, kv + prow * p.a.row_bytes + 528 + lane * 16);
+              cp_async16(dst, kv + prow * p.a.row_bytes + (kE4 ? kE2m1Rope : 528) + lane * 16);
             else
               st_shared_v4(dst, 0u, 0u, 0u, 0u);
           }
@@ -557,8 +577,15 @@ __global__ void __launch_bounds__(kT48Threads, 1) attn_tc48_kernel(TcAttnParams 
           uint32_t o[8];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float2 lo = e4m3x2_to_float2(static_cast<uint16_t>(w[k] & 0xFFFFu));
-            const float2 hi = e4m3x2_to_float2(static_cast<uint16_t>(w[k] >> 16));
+            float2 lo, hi;
+            if constexpr (kE4) {   // four codes: half of word k / 2
+              const uint32_t c4 = w[k >> 1] >> (16 * (k & 1));
+              lo = e2m1x2_to_float2(c4 & 0xFFu);
+              hi = e2m1x2_to_float2((c4 >> 8) & 0xFFu);
+            } else {
+              lo = e4m3x2_to_float2(static_cast<uint16_t>(w[k] & 0xFFFFu));
+              hi = e4m3x2_to_float2(static_cast<uint16_t>(w[k] >> 16));
+            }
             o[2 * k] = pack_bf16x2(lo.x * sc, lo.y * sc);
             o[2 * k + 1] = pack_bf16x2(hi.x * sc, hi.y * sc);
           }
@@ -1050,7 +1077,7 @@ cudaError_t launch_combine(const uint16_t* ws_o, const float* ws_lse, int n_spli
 
 bool tc_supported(const SeqArgs& seq, const MlaArgs& a) {
   if (a.H != kH || a.d_latent != kDv || a.d_rope != kDqk - kDv) return false;
-  if (a.kind == MlaKind::kF32 || a.kind == MlaKind::kE2M1) return false;
+  if (a.kind == MlaKind::kF32) return false;
   if (a.kind == MlaKind::kBF16 && a.row_bytes % 16 != 0) return false;
   if ((a.kind == MlaKind::kFP8Row || a.kind == MlaKind::kFP8Tile) && a.row_bytes % 16 != 0) return false;
   if (reinterpret_cast<uintptr_t>(a.kv) % 16 || reinterpret_cast<uintptr_t>(a.q) % 16 ||
@@ -1094,7 +1121,7 @@ cudaError_t launch_attn(const SeqArgs& seq, const MlaArgs& a, void* workspace, s
   }
   if (tc_supported(seq, a)) {
     const bool fp8 = a.kind == MlaKind::kFP8Row;
-    const bool tile = a.kind == MlaKind::kFP8Tile;
+    const bool tile = a.kind == MlaKind::kFP8Tile, e4 = a.kind == MlaKind::kE2M1;
     const int tile_rows = kBR48;
     int split = choose_split(seq, a, env.num_sms);
     if (split > 1 && (workspace == nullptr || ws_bytes < attn_workspace_bytes(seq, a, env.num_sms)))
@@ -1108,8 +1135,10 @@ cudaError_t launch_attn(const SeqArgs& seq, const MlaArgs& a, void* workspace, s
       p.ws_o = static_cast<uint16_t*>(workspace);
       p.ws_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + ((o + 255) / 256) * 256);
     }
-    void (*kern)(TcAttnParams) = fp8 ? attn_tc48_kernel<true> : (tile ? attn_tc48_kernel<false, true>
-                                                                          : attn_tc48_kernel<false>);
+    void (*kern)(TcAttnParams) = fp8    ? attn_tc48_kernel<true>
+                                 : tile ? attn_tc48_kernel<false, true>
+                                 : e4   ? attn_tc48_kernel<false, true, true>
+                                        : attn_tc48_kernel<false>;
     const cudaError_t attr_err = ensure_smem_limit(reinterpret_cast<const void*>(kern), kT48SmemBytes, env.device);
     if (attr_err != cudaSuccess) return attr_err;
     const int grid = seq.T * split * 2;
@@ -1118,7 +1147,7 @@ cudaError_t launch_attn(const SeqArgs& seq, const MlaArgs& a, void* workspace, s
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     char buf[128];
-    snprintf(buf, sizeof(buf), "attn_tc<%s>[split=%d,grid=%d]", fp8 ? "fp8x48" : (tile ? "fp8t128x48" : "bf16x48"),
+    snprintf(buf, sizeof(buf), "attn_tc<%s>[split=%d,grid=%d]", fp8 ? "fp8x48" : (tile ? "fp8t128x48" : (e4 ? "e2m1x48" : "bf16x48")),
              split, grid);
     *plan += buf;
     if (split > 1) {
