@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdsa.so")
 SOURCES = ("api.cu", "indexer.cu", "topk.cu", "attn.cu", "static_ws.cu", "cache_append.cu", "prolog.cu",
-           "rope.cu", "cache_rows.cu")
+           "rope.cu", "cache_rows.cu", "attn_e2m1.cu")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 

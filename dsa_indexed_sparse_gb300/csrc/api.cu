@@ -457,6 +457,7 @@ dsa_status_t dsa_decode_step(const dsa_seq_desc_t* seq, const dsa_indexer_desc_t
       if (e != cudaSuccess) return cuda_fail(e, "topk launch");
     }
     plan += " -> ";
+    env.chained = true;
     e = dsa::launch_attn(s, a, ws + off_attn, workspace_bytes - off_attn, env, &plan, &unsupported, &why);
     if (unsupported) return fail(DSA_ERR_UNSUPPORTED, why);
     if (e != cudaSuccess) return cuda_fail(e, "attention launch");
@@ -828,7 +829,8 @@ dsa_status_t dsa_check_status(dsa_stream_t stream) {
     if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
     const uint32_t f = dsa_status_read_clear_indexer() | dsa_status_read_clear_topk() |
                        dsa_status_read_clear_attn() | dsa_status_read_clear_cache() |
-                       dsa_status_read_clear_prolog() | dsa_status_read_clear_rows();
+                       dsa_status_read_clear_prolog() | dsa_status_read_clear_rows() |
+                       dsa_status_read_clear_attn_e2m1();
     if (f == 0) return DSA_OK;
     if (f == 0xFFFFFFFFu) return fail(DSA_ERR_CUDA, "could not read the device status word");
     std::string msg = "device flags:";

@@ -30,7 +30,6 @@
 
 #include "dsa_device.cuh"
 #include "dsa_internal.h"
-#include "latent_e2m1.cuh"
 
 DSA_DEFINE_STATUS_WORD(attn)
 
@@ -49,9 +48,6 @@ __device__ __forceinline__ float load_elem(MlaKind kind, const uint8_t* row, int
       return reinterpret_cast<const float*>(row)[d];
     case MlaKind::kBF16:
       return bf16_bits_to_float(reinterpret_cast<const uint16_t*>(row)[d]);
-    case MlaKind::kE2M1:
-      return d < 512 ? e2m1_latent(row, d)
-                     : bf16_bits_to_float(reinterpret_cast<const uint16_t*>(row + kE2m1Rope)[d - 512]);
     default: {  // 656-byte FP8 row
       // per-token scale at byte 512, or (per-128-tile rows) scale d / 128 at 512 + 4 (d / 128)
       const int si = kind == MlaKind::kFP8Tile ? d / 128 : 0;
@@ -310,9 +306,7 @@ __device__ __forceinline__ void t48_issue_s(uint32_t tmem, uint32_t scol, uint64
 
 // kTile: FP8 rows with one power-of-two scale per 128 latent dims, widened to
 // bf16 as code * scale by the producers (exact); the rest runs the bf16 plan.
-// kE4 (with kTile): 4-bit rows, widened the same way as code * block scale * row
-// scale (exact for a power-of-two row scale).
-template <bool kFp8, bool kTile = false, bool kE4 = false>
+template <bool kFp8, bool kTile = false>
 __global__ void __launch_bounds__(kT48Threads, 1) attn_tc48_kernel(TcAttnParams p) {
   using C = T48<kFp8>;
   constexpr int S = C::kStages;
@@ -480,32 +474,14 @@ __global__ void __launch_bounds__(kT48Threads, 1) attn_tc48_kernel(TcAttnParams 
       float my_scale = 0.f;
       if constexpr (kFp8 || kTile) {
 #pragma unroll
-        for (int rr = 0; rr < kRows; ++rr) {
-          raw[rr] = make_uint4(0u, 0u, 0u, 0u);
-          if (rows[rr] >= 0) {
-            const uint8_t* rp = kv + static_cast<int64_t>(rows[rr]) * p.a.row_bytes;
-            if constexpr (kE4) {
-              const uint2 u = __ldg(reinterpret_cast<const uint2*>(rp) + lane);
-              raw[rr].x = u.x;
-              raw[rr].y = u.y;
-            } else {
-              raw[rr] = ld_global_nc_v4(rp + lane * 16);
-            }
-          }
-        }
+        for (int rr = 0; rr < kRows; ++rr)
+          raw[rr] = rows[rr] >= 0 ? ld_global_nc_v4(kv + static_cast<int64_t>(rows[rr]) * p.a.row_bytes + lane * 16)
+                                  : make_uint4(0u, 0u, 0u, 0u);
       }
       if constexpr (kFp8) {
         if (my_row >= 0) my_scale = __ldg(reinterpret_cast<const float*>(kv + my_row * p.a.row_bytes + kDv));
       }
-      if constexpr (kE4) {
-#pragma unroll
-        for (int rr = 0; rr < kRows; ++rr) {
-          const uint8_t* rp = kv + static_cast<int64_t>(rows[rr]) * p.a.row_bytes;
-          tsc[rr] = rows[rr] >= 0 ? e4m3_to_float(__ldg(rp + kE2m1Scales + lane)) *
-                                        __ldg(reinterpret_cast<const float*>(rp + kE2m1RowScale))
-                                  : 0.f;
-        }
-      } else if constexpr (kTile) {
+      if constexpr (kTile) {
 #pragma unroll
         for (int rr = 0; rr < kRows; ++rr)
           tsc[rr] = rows[rr] >= 0 ? __ldg(reinterpret_cast<const float*>(kv + static_cast<int64_t>(rows[rr]) *
@@ -568,7 +544,7 @@ __global__ void __launch_bounds__(kT48Threads, 1) attn_tc48_kernel(TcAttnParams 
           if (lane < 8) {
             const uint32_t dst = drow + 8 * kBR48 * 128 + static_cast<uint32_t>(((lane & 7) ^ (r & 7)) << 4);
             if (prow >= 0)
-              cp_async16(dst, kv + prow * p.a.row_bytes + (kE4 ? kE2m1Rope : 528) + lane * 16);
+              cp_async16(dst, kv + prow * p.a.row_bytes + 528 + lane * 16);
             else
               st_shared_v4(dst, 0u, 0u, 0u, 0u);
           }
@@ -577,15 +553,8 @@ __global__ void __launch_bounds__(kT48Threads, 1) attn_tc48_kernel(TcAttnParams 
           uint32_t o[8];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            float2 lo, hi;
-            if constexpr (kE4) {   // four codes: half of word k / 2
-              const uint32_t c4 = w[k >> 1] >> (16 * (k & 1));
-              lo = e2m1x2_to_float2(c4 & 0xFFu);
-              hi = e2m1x2_to_float2((c4 >> 8) & 0xFFu);
-            } else {
-              lo = e4m3x2_to_float2(static_cast<uint16_t>(w[k] & 0xFFFFu));
-              hi = e4m3x2_to_float2(static_cast<uint16_t>(w[k] >> 16));
-            }
+            const float2 lo = e4m3x2_to_float2(static_cast<uint16_t>(w[k] & 0xFFFFu));
+            const float2 hi = e4m3x2_to_float2(static_cast<uint16_t>(w[k] >> 16));
             o[2 * k] = pack_bf16x2(lo.x * sc, lo.y * sc);
             o[2 * k + 1] = pack_bf16x2(hi.x * sc, hi.y * sc);
           }
@@ -958,13 +927,14 @@ __global__ void __launch_bounds__(kT48Threads, 1) attn_tc48_kernel(TcAttnParams 
 // contiguous bytes.  A head's warps meet in shared memory with their running
 // (max, sum, weighted row), and its threads write the output four dims at a time.
 constexpr int kCombineBatch = 8;   // slices per warp per round trip
-template <int SW, int HPC>
+// HEADS is the head count (0: the argument n_heads, for the 4-bit rows' kernel).
+template <int SW, int HPC, int HEADS>
 __global__ void __launch_bounds__(32 * SW * HPC)
-    attn_combine_kernel(const uint16_t* ws_o, const float* ws_lse, int n_split, int T,
+    attn_combine_kernel(const uint16_t* ws_o, const float* ws_lse, int n_split, int T, int n_heads,
                         __nv_bfloat16* out, float* lse_out) {
   grid_dep_launch();   // the next kernel waits for this grid before it uses out
   grid_dep_wait();
-  constexpr int H = kH;
+  const int H = HEADS ? HEADS : n_heads;
   __shared__ float s_acc[SW * HPC][16][32];   // [warp][value slot][lane]
   __shared__ float s_m[SW * HPC], s_l[SW * HPC];
   const int t = blockIdx.x;
@@ -1066,8 +1036,8 @@ cudaError_t launch_combine(const uint16_t* ws_o, const float* ws_lse, int n_spli
   const int64_t pairs = static_cast<int64_t>(T) * kH;
   const int need = (n_split + kCombineBatch - 1) / kCombineBatch;
 #define DSA_COMBINE(SW_, HPC_)                                                                           \
-  launch_kernel(attn_combine_kernel<SW_, HPC_>, dim3(T, kH / (HPC_)), dim3(32 * (SW_) * (HPC_)), 0,      \
-                env.stream, true, 1, ws_o, ws_lse, n_split, T, out, lse_out)
+  launch_kernel(attn_combine_kernel<SW_, HPC_, kH>, dim3(T, kH / (HPC_)), dim3(32 * (SW_) * (HPC_)), 0,  \
+                env.stream, true, 1, ws_o, ws_lse, n_split, T, kH, out, lse_out)
   if (pairs <= env.num_sms) return DSA_COMBINE(4, 1);
   if (need > 2) return DSA_COMBINE(4, 2);
   if (need > 1) return DSA_COMBINE(2, 2);
@@ -1077,7 +1047,7 @@ cudaError_t launch_combine(const uint16_t* ws_o, const float* ws_lse, int n_spli
 
 bool tc_supported(const SeqArgs& seq, const MlaArgs& a) {
   if (a.H != kH || a.d_latent != kDv || a.d_rope != kDqk - kDv) return false;
-  if (a.kind == MlaKind::kF32) return false;
+  if (a.kind == MlaKind::kF32 || a.kind == MlaKind::kE2M1) return false;
   if (a.kind == MlaKind::kBF16 && a.row_bytes % 16 != 0) return false;
   if ((a.kind == MlaKind::kFP8Row || a.kind == MlaKind::kFP8Tile) && a.row_bytes % 16 != 0) return false;
   if (reinterpret_cast<uintptr_t>(a.kv) % 16 || reinterpret_cast<uintptr_t>(a.q) % 16 ||
@@ -1102,7 +1072,22 @@ int choose_split(const SeqArgs& seq, const MlaArgs& a, int num_sms) {
 
 }  // namespace
 
+cudaError_t launch_attn_combine(const uint16_t* ws_o, const float* ws_lse, int n_split, int T, int H, void* out,
+                                float* lse_out, const LaunchEnv& env) {
+  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);
+  if (H == kH) return launch_combine(ws_o, ws_lse, n_split, T, o, lse_out, env);
+  // other head counts: one head per CTA, enough warps that each takes one batch of slices
+  const int need = (n_split + kCombineBatch - 1) / kCombineBatch;
+#define DSA_COMBINE(SW_)                                                                                \
+  launch_kernel(attn_combine_kernel<SW_, 1, 0>, dim3(T, H), dim3(32 * (SW_)), 0, env.stream, true, 1, ws_o, ws_lse, \
+                n_split, T, H, o, lse_out)
+  if (need > 2) return DSA_COMBINE(4);
+  return need > 1 ? DSA_COMBINE(2) : DSA_COMBINE(1);
+#undef DSA_COMBINE
+}
+
 size_t attn_workspace_bytes(const SeqArgs& seq, const MlaArgs& a, int num_sms) {
+  if (a.kind == MlaKind::kE2M1) return attn_e2m1_workspace_bytes(seq, a, num_sms);
   if (!tc_supported(seq, a) || seq.T == 0) return 0;
   const int split = choose_split(seq, a, num_sms);
   if (split <= 1) return 0;
@@ -1119,9 +1104,10 @@ cudaError_t launch_attn(const SeqArgs& seq, const MlaArgs& a, void* workspace, s
     *plan += "attn[empty]";
     return cudaSuccess;
   }
+  if (a.kind == MlaKind::kE2M1) return launch_attn_e2m1(seq, a, workspace, ws_bytes, env, plan);
   if (tc_supported(seq, a)) {
     const bool fp8 = a.kind == MlaKind::kFP8Row;
-    const bool tile = a.kind == MlaKind::kFP8Tile, e4 = a.kind == MlaKind::kE2M1;
+    const bool tile = a.kind == MlaKind::kFP8Tile;
     const int tile_rows = kBR48;
     int split = choose_split(seq, a, env.num_sms);
     if (split > 1 && (workspace == nullptr || ws_bytes < attn_workspace_bytes(seq, a, env.num_sms)))
@@ -1135,10 +1121,8 @@ cudaError_t launch_attn(const SeqArgs& seq, const MlaArgs& a, void* workspace, s
       p.ws_o = static_cast<uint16_t*>(workspace);
       p.ws_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + ((o + 255) / 256) * 256);
     }
-    void (*kern)(TcAttnParams) = fp8    ? attn_tc48_kernel<true>
-                                 : tile ? attn_tc48_kernel<false, true>
-                                 : e4   ? attn_tc48_kernel<false, true, true>
-                                        : attn_tc48_kernel<false>;
+    void (*kern)(TcAttnParams) = fp8 ? attn_tc48_kernel<true> : (tile ? attn_tc48_kernel<false, true>
+                                                                          : attn_tc48_kernel<false>);
     const cudaError_t attr_err = ensure_smem_limit(reinterpret_cast<const void*>(kern), kT48SmemBytes, env.device);
     if (attr_err != cudaSuccess) return attr_err;
     const int grid = seq.T * split * 2;
@@ -1147,7 +1131,7 @@ cudaError_t launch_attn(const SeqArgs& seq, const MlaArgs& a, void* workspace, s
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     char buf[128];
-    snprintf(buf, sizeof(buf), "attn_tc<%s>[split=%d,grid=%d]", fp8 ? "fp8x48" : (tile ? "fp8t128x48" : (e4 ? "e2m1x48" : "bf16x48")),
+    snprintf(buf, sizeof(buf), "attn_tc<%s>[split=%d,grid=%d]", fp8 ? "fp8x48" : (tile ? "fp8t128x48" : "bf16x48"),
              split, grid);
     *plan += buf;
     if (split > 1) {

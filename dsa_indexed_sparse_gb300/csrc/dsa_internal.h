@@ -56,6 +56,7 @@ struct LaunchEnv {
   cudaStream_t stream;
   int num_sms;
   int device;
+  bool chained = false;   // decode step: the call's kernels before this one do not write the attention's query
 };
 
 // Each launcher validates kernel-specific limits, enqueues its kernels and
@@ -82,6 +83,14 @@ size_t attn_workspace_bytes(const SeqArgs& seq, const MlaArgs& a, int num_sms);
 cudaError_t launch_attn(const SeqArgs& seq, const MlaArgs& a, void* workspace, size_t ws_bytes,
                         const LaunchEnv& env, std::string* plan, bool* unsupported,
                         std::string* why);
+
+// Attention over 4-bit rows (attn_e2m1.cu), any head count; and the merge of row
+// slices' partial results, bf16 [n_split, T, H, 512] and their LSE.
+size_t attn_e2m1_workspace_bytes(const SeqArgs& seq, const MlaArgs& a, int num_sms);
+cudaError_t launch_attn_e2m1(const SeqArgs& seq, const MlaArgs& a, void* workspace, size_t ws_bytes,
+                             const LaunchEnv& env, std::string* plan);
+cudaError_t launch_attn_combine(const uint16_t* ws_o, const float* ws_lse, int n_split, int T, int H, void* out,
+                                float* lse_out, const LaunchEnv& env);
 
 // Launches a kernel, when `pdl` with programmatic stream serialization (it
 // may launch while the previous kernel on the stream is finishing; every
@@ -200,3 +209,4 @@ uint32_t dsa_status_read_clear_attn();
 uint32_t dsa_status_read_clear_cache();
 uint32_t dsa_status_read_clear_prolog();
 uint32_t dsa_status_read_clear_rows();
+uint32_t dsa_status_read_clear_attn_e2m1();

@@ -29,11 +29,16 @@ __device__ __forceinline__ float2 e2m1x2_to_float2(uint32_t byte) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// Value of latent dim d (< 512) of a row.
-__device__ __forceinline__ float e2m1_latent(const uint8_t* row, int d) {
-  const float2 v = e2m1x2_to_float2(row[d >> 1]);
-  return ((d & 1) ? v.y : v.x) * (e4m3_to_float(row[kE2m1Scales + (d >> 4)]) *
-                                  *reinterpret_cast<const float*>(row + kE2m1RowScale));
+// Eight codes (a 32-bit word, low nibble first) -> four pairs of halves, exact.
+__device__ __forceinline__ void e2m1x8_to_half2x4(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
 }
 
 // Exponent of the row scale of a row whose largest latent magnitude is amax:
