@@ -47,11 +47,13 @@
 //   N-wide accumulator of a pair MMA takes N/2 columns: lanes 0-63 are the CTA's heads
 //   for the first half of N, lanes 64-127 the same heads for the second.
 //
-// Warps: 0-7 own rows (8 each: codes, scales and rope in registers one tile ahead,
-// widened into the stage once P V of two tiles ago has freed it); 8-9 the other CTA's
-// rows (32 each, written once Q K^T is complete, beside the softmax); 10 Q K^T and 11
-// P V (rank 0 issues for both); 12-15 softmax: a thread owns one head and 64 of the
-// tile's rows, the two threads of a head agree on m and g through shared memory.
+// Warps: 0-7 producers, eight own and eight of the other CTA's rows each.  Their codes,
+// scales and rope are loaded into registers a tile ahead.  Turn by turn: the other
+// CTA's rows of tile j once Q K^T_j is complete (beside the softmax), the own rows of
+// tile j + 1 once P V_{j-1} has freed its stage (beside Q K^T_j + 1 of the other
+// stage).  8 Q K^T and 9 P V (rank 0 issues for both CTAs).  10-17 softmax: a thread
+// owns one head and 32 of the tile's rows, the four threads of a head agree on m and g
+// through shared memory.
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
@@ -76,24 +78,23 @@ constexpr int kDqk = 576, kDv = 512;
 constexpr int kAtom = 64 * 128;       // bytes of a [64 rows x 64 dims] atom
 constexpr int kStageBytes = 9 * kAtom;
 constexpr int kRopeAtom = 8 * kAtom;  // offset of the rope atom (P of rows 0-63 later) in a stage
-constexpr int kWarpsOwn = 8, kWarpsPeer = 2;
-constexpr int kPeerRows = kOwn / kWarpsPeer;             // rows per peer warp
-constexpr int kWarpQk = 10, kWarpPv = 11, kWarpSoft = 12;
-constexpr int kThreads = 512;
+constexpr int kProducers = 8;
+constexpr int kWarpQk = 8, kWarpPv = 9, kWarpSoft = 10;
+constexpr int kThreads = 576;
 
 constexpr int kOffQ = 0;
 constexpr int kOffStage = 9 * kAtom;
 constexpr int kOffP1 = kOffStage + 2 * kStageBytes;
 constexpr int kOffScale = kOffP1 + kAtom;                // float [2 stages][128] row scales
 constexpr int kOffMask = kOffScale + 2 * kTile * 4;      // uint64 [2 stages][2 halves of the tile]
-constexpr int kOffRmax = kOffMask + 64;                  // float [2 stages][16] largest row scale of a warp's rows
-constexpr int kOffMax = kOffRmax + 2 * 16 * 4;           // float [2][2 halves][64 heads]
-constexpr int kOffQexp = kOffMax + 2 * 2 * kHeads * 4;   // float [64] the heads' 2^a
-constexpr int kOffOk = kOffQexp + kHeads * 4;            // int [2][4 softmax warps]
-constexpr int kOffBar = kOffOk + 32;
+constexpr int kOffRmax = kOffMask + 64;                  // float [2 stages][8] largest row scale of a warp's rows
+constexpr int kOffQexp = kOffRmax + 64;                  // float [64] the heads' 2^a
+constexpr int kOffOk = kOffQexp + kHeads * 4;            // int [2][8 softmax warps]
+constexpr int kOffBar = kOffOk + 64;
 constexpr int kNumBars = 16;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;
-constexpr int kUsed = kOffMisc + 16;
+constexpr int kOffMax = kOffMisc + 16;                   // float [4 row quarters][64 heads]
+constexpr int kUsed = kOffMax + 4 * kHeads * 4;
 constexpr int kSmemBytes = 232448;
 constexpr int kSlack = kSmemBytes - kUsed;               // for re-aligning the base to 1024 bytes
 static_assert(kSlack >= 128, "shared memory budget");
@@ -157,6 +158,10 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
           smem_u32(bar)),
       "h"(static_cast<uint16_t>(3))
       : "memory");
+}
+
+__device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t nthreads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
 // Sixteen codes (8 bytes) times their E4M3 block scale -> sixteen halves, exact.
@@ -224,13 +229,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&full[i], 2 * kWarpsOwn);
-      mbar_init(&vfull[i], 2 * kWarpsPeer);
-      mbar_init(&pfull[i], 8);
-      mbar_init(&sfree[i], 8);
+      mbar_init(&full[i], 2 * kProducers);
+      mbar_init(&vfull[i], 2 * kProducers);
+      mbar_init(&pfull[i], 16);
+      mbar_init(&sfree[i], 16);
       mbar_init(&sfull[i], 1);
       mbar_init(&empty[i], 1);
-      mbar_init(&mfull[i], kWarpsOwn + kWarpsPeer);
+      mbar_init(&mfull[i], kProducers);
     }
     mbar_init(drain, 2);
     *abort_flag = 0;
@@ -275,9 +280,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
     return page * page_size + pos % page_size;   // < cache_rows < 2^31
   };
 
-  // The query: each warp four heads, eight lanes a head, lane c of them chunk c of
+  // The query: warps 0-15 four heads each, eight lanes a head, lane c of them chunk c of
   // every atom.  The latent part becomes f16 with its own power of two per head.
-  {
+  if (warp < kHeads / 4) {
     const int hl = warp * 4 + (lane >> 3), c = lane & 7;
     const bool have = h0 + hl < H;
     const uint4* qg = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.a.q) +
@@ -324,162 +329,150 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
     arrive_pair(leader_addr(&sfree[1]));
   }
 
-  if (warp < kWarpsOwn) {
-    // ------------------------------------------------ own rows: tile rows rank * 64 + [8 w, 8 w + 8)
+  if (warp < kProducers) {
+    // ------------------------------------------------ producers
     if (p.early_query) grid_dep_wait();   // the selected indices come from the kernel before
-    const int row0 = static_cast<int>(rank) * kOwn + warp * 8;
+    // lanes 0-7 look after own rows [8 w, 8 w + 8) of the tile, lanes 8-15 after the other CTA's
+    const int tile_row = (static_cast<int>(rank ^ static_cast<uint32_t>(lane >> 3)) & 1) * kOwn + warp * 8 + (lane & 7);
+    const int sub = lane >> 4, blk = lane & 15;
+    const uint32_t region = rank == 0 ? 4 * kAtom : 0;   // of the other CTA's rows: Y in rank 0, X in rank 1
     auto load_pos = [&](int j) -> int {
-      const int gi = r0 + j * kTile + row0 + lane;
-      return (lane < 8 && j < ntiles && gi < r1) ? __ldg(idx + gi) : -1;
+      const int gi = r0 + j * kTile + tile_row;
+      return (lane < 16 && j < ntiles && gi < r1) ? __ldg(idx + gi) : -1;
     };
-    // A tile's eight rows in registers: codes of block `lane` of each row; scale bytes
-    // as words, word lane & 7 of rows lane / 8 and lane / 8 + 4; row scales in lanes
-    // 0-7; rope chunk lane & 7 of the same two rows.
-    struct Raw {
-      uint2 code[8];
-      uint32_t sc[2];
-      float rs;
-      uint4 rope[2];
-      uint32_t bits;
-    };
-    auto fetch = [&](int my_row, Raw& r) {
-      r.bits = __ballot_sync(0xffffffffu, my_row >= 0) & 0xFFu;
-      r.rs = my_row >= 0 ? __ldg(reinterpret_cast<const float*>(kv + my_row * row_bytes + kE2m1RowScale)) : 0.f;
+    // Own rows: codes of block `lane`; scale bytes as words, word lane & 7 of rows lane / 8
+    // and lane / 8 + 4; rope chunk lane & 7 of the same rows.  Other rows: codes of block blk
+    // (of this CTA's value dims) of rows 2 k + sub; scale word lane & 3 of row lane / 4.  A
+    // row that selects nothing reads row 0, with scales and rope values of zero.
+    uint2 code[8], pcode[4];
+    uint32_t sc[2], psc = 0u;
+    uint4 rope[2];
+    float rs = 0.f;
+    uint32_t valid = 0u;   // of tile `my_row`: bits 0-7 own, 8-15 other
+    auto fetch_own = [&](int my_row) {
+      valid = __ballot_sync(0xffffffffu, my_row >= 0);
+      const int safe = max(my_row, 0);
+      int row[8], row2[2];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int64_t row = __shfl_sync(0xffffffffu, my_row, i);
-        r.code[i] = make_uint2(0u, 0u);
-        if (row >= 0) r.code[i] = __ldg(reinterpret_cast<const uint2*>(kv + row * row_bytes) + lane);
-      }
+      for (int i = 0; i < 8; ++i) row[i] = __shfl_sync(0xffffffffu, safe, i);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) row2[k] = __shfl_sync(0xffffffffu, safe, (lane >> 3) + 4 * k);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) code[i] = __ldg(reinterpret_cast<const uint2*>(kv + row[i] * row_bytes) + lane);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int64_t row = __shfl_sync(0xffffffffu, my_row, (lane >> 3) + 4 * k);
-        r.sc[k] = 0u;
-        r.rope[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (row >= 0) {
-          const uint8_t* rp = kv + row * row_bytes;
-          r.sc[k] = __ldg(reinterpret_cast<const uint32_t*>(rp + kE2m1Scales) + (lane & 7));
-          r.rope[k] = __ldg(reinterpret_cast<const uint4*>(rp + kE2m1Rope) + (lane & 7));
-        }
+        const uint8_t* rp = kv + row2[k] * row_bytes;
+        sc[k] = __ldg(reinterpret_cast<const uint32_t*>(rp + kE2m1Scales) + (lane & 7));
+        rope[k] = __ldg(reinterpret_cast<const uint4*>(rp + kE2m1Rope) + (lane & 7));
       }
+      rs = __ldg(reinterpret_cast<const float*>(kv + safe * row_bytes + kE2m1RowScale));
     };
-    Raw cur;
-    int pos = load_pos(0), pos1 = load_pos(1), pos2 = load_pos(2);
-    fetch(row_of(pos, load_page(pos)), cur);
-    int page1 = load_page(pos1);
-    const uint32_t full_leader0 = leader_addr(&full[0]), full_leader1 = leader_addr(&full[1]);
-    for (int j = 0; j < ntiles; ++j) {
-      const int st = j & 1;
-      if (j >= 2) {
-        const bool ok = wait_bar(&empty[st], ((j >> 1) - 1) & 1, abort_flag, wlim);
-        if (!__all_sync(0xffffffffu, ok)) break;
-      }
-      const uint32_t stage = smem_u32(sm + kOffStage + st * kStageBytes);
-      if (lane == 0) (sm + kOffMask + st * 16 + rank * 8)[warp] = static_cast<uint8_t>(cur.bits);
-      if (lane < 8) reinterpret_cast<float*>(sm + kOffScale)[st * kTile + row0 + lane] = cur.rs;
-      float rmax = cur.rs;   // 0 beyond lane 7
+    uint32_t pvalid = 0u;
+    auto fetch_other = [&](int my_row) {
+      pvalid = __ballot_sync(0xffffffffu, my_row >= 0) >> 8;
+      const int safe = max(my_row, 0);
+      int row[4];
 #pragma unroll
-      for (int o = 1; o < 8; o <<= 1) rmax = fmaxf(rmax, __shfl_xor_sync(0xffffffffu, rmax, o));
-      if (lane == 0) reinterpret_cast<float*>(sm + kOffRmax)[st * 16 + warp] = rmax;
+      for (int k = 0; k < 4; ++k) row[k] = __shfl_sync(0xffffffffu, safe, 8 + 2 * k + sub);
+      const int row1 = __shfl_sync(0xffffffffu, safe, 8 + (lane >> 2));
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        pcode[k] = __ldg(reinterpret_cast<const uint2*>(kv + row[k] * row_bytes) + rank * 16 + blk);
+      psc = __ldg(reinterpret_cast<const uint32_t*>(kv + row1 * row_bytes + kE2m1Scales) + rank * 4 + (lane & 3));
+    };
+    // Own rows into the stage, and the row scales and masks of all sixteen rows beside it.
+    auto write_own = [&](int j) {
+      const int st = j & 1;
+      const uint32_t stage = smem_u32(sm + kOffStage + st * kStageBytes);
+      uint32_t w[8];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) sc[k] = ((valid >> ((lane >> 3) + 4 * k)) & 1u) ? sc[k] : 0u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = __shfl_sync(0xffffffffu, sc[i >> 2], (i & 3) * 8 + (lane >> 2));
+      const float my_rs = ((valid >> lane) & 1u) ? rs : 0.f;
+      if (lane < 16) reinterpret_cast<float*>(sm + kOffScale)[st * kTile + tile_row] = my_rs;
+      float rmax = lane < 16 ? my_rs : 0.f;
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) rmax = fmaxf(rmax, __shfl_xor_sync(0xffffffffu, rmax, o));
+      if (lane == 0) {
+        reinterpret_cast<float*>(sm + kOffRmax)[st * 8 + warp] = rmax;
+        (sm + kOffMask + st * 16 + rank * 8)[warp] = static_cast<uint8_t>(valid);
+        (sm + kOffMask + st * 16 + (rank ^ 1u) * 8)[warp] = static_cast<uint8_t>(valid >> 8);
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const uint32_t scw = __shfl_sync(0xffffffffu, cur.sc[i >> 2], (i & 3) * 8 + (lane >> 2));
         uint32_t o[8];
-        widen_codes(cur.code[i], scw >> (8 * (lane & 3)), o);
+        widen_codes(code[i], w[i] >> (8 * (lane & 3)), o);
         store_block(stage, warp * 8 + i, lane, o);
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int r = warp * 8 + (lane >> 3) + 4 * k;
-        st_shared_v4(stage + static_cast<uint32_t>(kRopeAtom + r * 128 + (((lane & 7) ^ (r & 7)) << 4)), cur.rope[k].x,
-                     cur.rope[k].y, cur.rope[k].z, cur.rope[k].w);
+        const uint32_t keep = ((valid >> ((lane >> 3) + 4 * k)) & 1u) ? 0xFFFFFFFFu : 0u;
+        st_shared_v4(stage + static_cast<uint32_t>(kRopeAtom + r * 128 + (((lane & 7) ^ (r & 7)) << 4)), rope[k].x & keep,
+                     rope[k].y & keep, rope[k].z & keep, rope[k].w & keep);
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&mfull[st]);
-        if (!(p.dbg_withhold && warp == 0 && j == 0)) arrive_pair(st ? full_leader1 : full_leader0);
+        if (!(p.dbg_withhold && warp == 0 && j == 0)) arrive_pair(leader_addr(&full[st]));
       }
-      // the registers take the next tile's rows at once, a tile's time before their use
-      if (j + 1 < ntiles) fetch(row_of(pos1, page1), cur);
-      pos1 = pos2;
-      page1 = load_page(pos1);
-      pos2 = load_pos(j + 3);
-    }
-  } else if (warp < kWarpsOwn + kWarpsPeer) {
-    // ------------------------------------------------ the other CTA's rows, this CTA's value dims
-    if (p.early_query) grid_dep_wait();
-    const int w = warp - kWarpsOwn;
-    const int row0 = static_cast<int>(rank ^ 1u) * kOwn + w * kPeerRows;
-    const int blk = lane & 15, sub = lane >> 4;
-    const uint32_t region = rank == 0 ? 4 * kAtom : 0;   // Y in rank 0, X in rank 1
-    auto load_pos = [&](int j) -> int {
-      const int gi = r0 + j * kTile + row0 + lane;
-      return (j < ntiles && gi < r1) ? __ldg(idx + gi) : -1;
     };
-    // 32 rows: codes of block blk of rows 2 i + sub; scale bytes of this CTA's value dims
-    // as words, word lane & 3 of rows lane / 4 + 8 k; row scales one per lane
-    struct Raw {
-      uint2 code[16];
-      uint32_t sc[4];
-      float rs;
-      uint32_t bits;
-    };
-    auto fetch = [&](int my_row, Raw& r) {
-      r.bits = __ballot_sync(0xffffffffu, my_row >= 0);
-      r.rs = my_row >= 0 ? __ldg(reinterpret_cast<const float*>(kv + my_row * row_bytes + kE2m1RowScale)) : 0.f;
+    auto write_other = [&](int j) {
+      const int st = j & 1;
+      const uint32_t dst = smem_u32(sm + kOffStage + st * kStageBytes) + region;
+      psc = ((pvalid >> (lane >> 2)) & 1u) ? psc : 0u;
+      uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int64_t row = __shfl_sync(0xffffffffu, my_row, 2 * i + sub);
-        r.code[i] = make_uint2(0u, 0u);
-        if (row >= 0) r.code[i] = __ldg(reinterpret_cast<const uint2*>(kv + row * row_bytes) + rank * 16 + blk);
-      }
+      for (int k = 0; k < 4; ++k) w[k] = __shfl_sync(0xffffffffu, psc, (2 * k + sub) * 4 + (blk >> 2));
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int64_t row = __shfl_sync(0xffffffffu, my_row, (lane >> 2) + 8 * k);
-        r.sc[k] = row >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(kv + row * row_bytes + kE2m1Scales) + rank * 4 + (lane & 3))
-                           : 0u;
-      }
-    };
-    Raw cur;
-    int pos = load_pos(0), pos1 = load_pos(1), pos2 = load_pos(2);
-    fetch(row_of(pos, load_page(pos)), cur);
-    int page1 = load_page(pos1);
-    const uint32_t vfull_leader0 = leader_addr(&vfull[0]), vfull_leader1 = leader_addr(&vfull[1]);
-    for (int j = 0; j < ntiles; ++j) {
-      const int st = j & 1;
-      if (j >= 2) {   // the softmax has read this stage's earlier mask and scales
-        const bool ok = wait_bar(&empty[st], ((j >> 1) - 1) & 1, abort_flag, wlim);
-        if (!__all_sync(0xffffffffu, ok)) break;
-      }
-      reinterpret_cast<float*>(sm + kOffScale)[st * kTile + row0 + lane] = cur.rs;
-      float rmax = cur.rs;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) rmax = fmaxf(rmax, __shfl_xor_sync(0xffffffffu, rmax, o));
-      if (lane == 0) reinterpret_cast<float*>(sm + kOffRmax)[st * 16 + warp] = rmax;
-      if (lane == 0) reinterpret_cast<uint32_t*>(sm + kOffMask + st * 16 + (rank ^ 1u) * 8)[w] = cur.bits;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&mfull[st]);
-      // Q K^T has read the rows that these replace
-      const bool ok = wait_bar(&sfull[st], (j >> 1) & 1, abort_flag, wlim);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      const uint32_t dst = smem_u32(sm + kOffStage + st * kStageBytes) + region;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int r = 2 * i + sub;
-        const uint32_t scw = __shfl_sync(0xffffffffu, cur.sc[i >> 2], (r & 7) * 4 + (blk >> 2));
         uint32_t o[8];
-        widen_codes(cur.code[i], scw >> (8 * (blk & 3)), o);
-        store_block(dst, w * kPeerRows + r, blk, o);
+        widen_codes(pcode[k], w[k] >> (8 * (blk & 3)), o);
+        store_block(dst, warp * 8 + 2 * k + sub, blk, o);
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) arrive_pair(st ? vfull_leader1 : vfull_leader0);
-      // the registers take the next tile's rows at once, a tile's time before their use
-      if (j + 1 < ntiles) fetch(row_of(pos1, page1), cur);
-      pos1 = pos2;
-      page1 = load_page(pos1);
-      pos2 = load_pos(j + 3);
+      if (lane == 0) arrive_pair(leader_addr(&vfull[st]));
+    };
+    // Steps -1, 0, 1, ...: at step j the other CTA's rows of tile j, then the own rows of
+    // tile j + 1; own registers hold tile j + 1 and take tile j + 2, the other rows' hold
+    // tile j and take tile j + 1.  row1 / row2: rows of tiles j + 1 and j + 2.
+    int row1 = -1, row2;
+    int pos3, page3;
+    {
+      const int pos0 = load_pos(0), pos1 = load_pos(1);
+      pos3 = load_pos(2);
+      const int page0 = load_page(pos0), page1 = load_page(pos1);
+      page3 = load_page(pos3);
+      row1 = row_of(pos0, page0);
+      row2 = row_of(pos1, page1);
+    }
+    fetch_own(row1);
+    int pos4 = load_pos(3);
+#pragma unroll 1
+    for (int j = -1; j < ntiles; ++j) {
+      if (j >= 0) {
+        // Q K^T has read the rows that these replace
+        const bool ok = wait_bar(&sfull[j & 1], (j >> 1) & 1, abort_flag, wlim);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        write_other(j);
+      }
+      if (j + 1 < ntiles) {
+        fetch_other(row1);
+        if (j >= 1) {
+          const bool ok = wait_bar(&empty[(j + 1) & 1], ((j - 1) >> 1) & 1, abort_flag, wlim);
+          if (!__all_sync(0xffffffffu, ok)) break;
+        }
+        write_own(j + 1);
+        fetch_own(row2);
+      }
+      row1 = row2;
+      row2 = row_of(pos3, page3);
+      pos3 = pos4;
+      page3 = load_page(pos3);
+      pos4 = load_pos(j + 5);
     }
   } else if (warp == kWarpQk) {
     if (rank == 0) {
@@ -539,14 +532,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
     // ------------------------------------------------ softmax and epilogue
     const int quarter = warp & 3;
     const int hl = (quarter & 1) * 32 + lane;   // head within the CTA
-    const int half = quarter >> 1;              // tile rows [64 half, 64 half + 64)
+    const int half = quarter >> 1;              // tile rows [64 half, 64 half + 64), of which
+    const int part32 = (warp - kWarpSoft) >> 2; // this thread's [32 part32, 32 part32 + 32)
+    const int rq = half * 2 + part32;           // row quarter of the tile
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     // a scale of 0 becomes a tiny one, so that it leaves a masked logit at -inf
     const float sl2 = fmaxf(fabsf(p.a.softmax_scale) * kLog2e, 1e-30f);
-    const uint32_t pair_bar = 2 + (quarter & 1);
+    const uint32_t head_bar = 2 + (quarter & 1), read_bar = 4 + (quarter & 1);   // the 128 threads of 32 heads
     float* xmax = reinterpret_cast<float*>(sm + kOffMax);
     volatile int* oks = reinterpret_cast<volatile int*>(sm + kOffOk);
-    const volatile uint64_t* masks = reinterpret_cast<const volatile uint64_t*>(sm + kOffMask);
+    const volatile uint32_t* masks = reinterpret_cast<const volatile uint32_t*>(sm + kOffMask);
     const uint32_t sfree_leader0 = leader_addr(&sfree[0]), sfree_leader1 = leader_addr(&sfree[1]);
     const uint32_t pfull_leader0 = leader_addr(&pfull[0]), pfull_leader1 = leader_addr(&pfull[1]);
     const float qexp = reinterpret_cast<const float*>(sm + kOffQexp)[hl];
@@ -558,59 +553,55 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
            wait_bar(&sfull[st], (j >> 1) & 1, abort_flag, wlim);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
-      const uint32_t scales = smem_u32(sm + kOffScale) + static_cast<uint32_t>((st * kTile + half * kOwn) * 4);
-      float x[64];
+      const uint32_t scales = smem_u32(sm + kOffScale) + static_cast<uint32_t>((st * kTile + rq * 32) * 4);
+      float x[32];
       float mx = -INFINITY, rmax = 0.f;
       if (ok) {
-        const uint64_t vmask = masks[st * 2 + half];
-        const float* rmaxs = reinterpret_cast<const float*>(sm + kOffRmax) + st * 16;
+        uint32_t s0[32], s1[32];
+        tmem_ld32(tmem + lane_off + st * 64 + part32 * 32, s0);
+        tmem_ld32(tmem + lane_off + kColRope + st * 64 + part32 * 32, s1);
+        const uint32_t vmask = masks[st * 4 + rq];
+        const float* rmaxs = reinterpret_cast<const float*>(sm + kOffRmax) + st * 8;
 #pragma unroll
-        for (int i = 0; i < kWarpsOwn + kWarpsPeer; ++i) rmax = fmaxf(rmax, rmaxs[i]);
-        float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        for (int i = 0; i < kProducers; ++i) rmax = fmaxf(rmax, rmaxs[i]);
+        tmem_ld_wait();
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t s0[32];
-          tmem_ld32(tmem + lane_off + st * 64 + c * 32, s0);
-          tmem_ld_wait();
+        for (int i = 0; i < 32; i += 4) {
+          const uint4 rs = ld_shared_v4(scales + static_cast<uint32_t>(i * 4));
+          float t0, t1, t2, t3;
+          mul2(t0, t1, __uint_as_float(s0[i]), __uint_as_float(s0[i + 1]), qexp, qexp);
+          mul2(t2, t3, __uint_as_float(s0[i + 2]), __uint_as_float(s0[i + 3]), qexp, qexp);
 #pragma unroll
-          for (int c16 = 0; c16 < 2; ++c16) {
-            uint32_t s1[16];
-            tmem_ld16(tmem + lane_off + kColRope + st * 64 + c * 32 + c16 * 16, s1);
-            tmem_ld_wait();
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int k = c16 * 16 + 4 * q, i = c * 32 + k;
-              const uint4 rs = ld_shared_v4(scales + static_cast<uint32_t>(i * 4));
-              float t0, t1, t2, t3;
-              mul2(t0, t1, __uint_as_float(s0[k]), __uint_as_float(s0[k + 1]), qexp, qexp);
-              mul2(t2, t3, __uint_as_float(s0[k + 2]), __uint_as_float(s0[k + 3]), qexp, qexp);
-#pragma unroll
-              for (int k4 = 0; k4 < 4; ++k4) x[i + k4] = __uint_as_float(s1[4 * q + k4]);
-              fma2(x[i], x[i + 1], t0, t1, __uint_as_float(rs.x), __uint_as_float(rs.y));
-              fma2(x[i + 2], x[i + 3], t2, t3, __uint_as_float(rs.z), __uint_as_float(rs.w));
-            }
-          }
+          for (int k = 0; k < 4; ++k) x[i + k] = __uint_as_float(s1[i + k]);
+          fma2(x[i], x[i + 1], t0, t1, __uint_as_float(rs.x), __uint_as_float(rs.y));
+          fma2(x[i + 2], x[i + 3], t2, t3, __uint_as_float(rs.z), __uint_as_float(rs.w));
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_pair(st ? sfree_leader1 : sfree_leader0);
-        if (vmask != ~0ull) {
+        if (vmask != ~0u) {
 #pragma unroll
-          for (int i = 0; i < 64; ++i) x[i] = ((vmask >> i) & 1u) ? x[i] : -INFINITY;
+          for (int i = 0; i < 32; ++i) x[i] = ((vmask >> i) & 1u) ? x[i] : -INFINITY;
         }
+        float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 64; i += 2) mq[(i >> 1) & 3] = fmax3(mq[(i >> 1) & 3], x[i], x[i + 1]);
+        for (int i = 0; i < 32; i += 2) mq[(i >> 1) & 3] = fmax3(mq[(i >> 1) & 3], x[i], x[i + 1]);
         mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * sl2;
       }
-      // the two threads of a head take the larger maximum, and their warps leave together
-      // when either has given up (two buffers: the partner has read this one's last
-      // entry before it arrived at the barrier in between)
-      float* xm = xmax + st * 2 * kHeads;
-      xm[half * kHeads + hl] = mx;
-      if (lane == 0) oks[st * 4 + quarter] = ok ? 1 : 0;
-      named_bar_sync(pair_bar, 64);
-      mx = fmaxf(mx, xm[(half ^ 1) * kHeads + hl]);
-      ok = oks[st * 4 + quarter] != 0 && oks[st * 4 + (quarter ^ 2)] != 0;
+      // The four threads of a head take the largest maximum, and their warps leave together
+      // when one has given up.  There is room for one buffer: the last tile's entries have
+      // been read once all four warps have arrived on read_bar.
+      if (j >= 1) named_bar_sync(read_bar, 256);
+      xmax[rq * kHeads + hl] = mx;
+      if (lane == 0) oks[st * 8 + warp - kWarpSoft] = ok ? 1 : 0;
+      named_bar_sync(head_bar, 128);
+#pragma unroll
+      for (int k = 1; k < 4; ++k) mx = fmaxf(mx, xmax[(rq ^ k) * kHeads + hl]);
+      // the four warps: quarters with this one's low bit, both row halves of each
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (((k + kWarpSoft) & 1) == (quarter & 1)) ok = ok && oks[st * 8 + k] != 0;
+      named_bar_arrive(read_bar, 256);
       if (!ok) break;
       const float gx = mx + __log2f(rmax);
       const bool need_m = mx > m + kRescaleM, need_g = gx > g + kRescaleG;
@@ -620,13 +611,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
         tc_fence_after();
         const float f = need_g ? exp2f(g - gx) : 1.f;
 #pragma unroll 1
-        for (int cc = 0; cc < 16; ++cc) {
+        for (int cc = 0; cc < 8; ++cc) {   // this thread's half of the columns
           uint32_t o[16];
-          tmem_ld16(tmem + lane_off + kColO + cc * 16, o);
+          tmem_ld16(tmem + lane_off + kColO + part32 * 128 + cc * 16, o);
           tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-          tmem_st16(tmem + lane_off + kColO + cc * 16, o);
+          tmem_st16(tmem + lane_off + kColO + part32 * 128 + cc * 16, o);
         }
         tmem_st_wait();
       }
@@ -644,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
                             static_cast<uint32_t>(hl * 128);
       float se[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
+      for (int c = 0; c < 4; ++c) {
         uint32_t pk[4];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -664,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
             pk[2 * q + (k >> 1)] = *reinterpret_cast<const uint32_t*>(&h);
           }
         }
-        st_shared_v4(prow + static_cast<uint32_t>((c ^ (hl & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
+        st_shared_v4(prow + static_cast<uint32_t>(((part32 * 4 + c) ^ (hl & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
       }
       l += (se[0] + se[1]) + (se[2] + se[3]);
       fence_proxy_async_smem();
@@ -675,11 +666,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
     const int last = ntiles - 1;
     if (ok) ok = wait_bar(&empty[last & 1], (last >> 1) & 1, abort_flag, wlim);
     ok = __all_sync(0xffffffffu, ok);
-    // the sums of a head's two threads
-    named_bar_sync(pair_bar, 64);
-    xmax[half * kHeads + hl] = l;
-    named_bar_sync(pair_bar, 64);
-    l += xmax[(half ^ 1) * kHeads + hl];
+    // the sums of a head's four threads
+    named_bar_sync(head_bar, 128);
+    xmax[rq * kHeads + hl] = l;
+    named_bar_sync(head_bar, 128);
+#pragma unroll
+    for (int k = 1; k < 4; ++k) l += xmax[(rq ^ k) * kHeads + hl];
     if (ok) {
       tc_fence_after();
       // O holds sum p rs 2^(m - g) v over l = sum p
@@ -689,14 +681,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
       const bool part = p.n_split > 1;
       const int64_t head0 = (static_cast<int64_t>(part ? split : 0) * p.seq.T + t) * H + h0 + (quarter & 1) * 32;
       uint8_t* out = reinterpret_cast<uint8_t*>(part ? p.ws_o : static_cast<uint16_t*>(p.a.out)) +
-                     (head0 * kDv + half * 256) * 2;
-      const uint32_t stg = smem_u32(sm + kOffStage) + quarter * 4096;   // all MMAs are complete
+                     (head0 * kDv + half * 256 + part32 * 128) * 2;
+      const uint32_t stg = smem_u32(sm + kOffStage) + (warp - kWarpSoft) * 4096;   // all MMAs are complete
       if (heads > 0) {
 #pragma unroll 1
-        for (int cc = 0; cc < 4; ++cc) {
+        for (int cc = 0; cc < 2; ++cc) {
           uint32_t o0[32], o1[32];
-          tmem_ld32(tmem + lane_off + kColO + cc * 64, o0);
-          tmem_ld32(tmem + lane_off + kColO + cc * 64 + 32, o1);
+          tmem_ld32(tmem + lane_off + kColO + part32 * 128 + cc * 64, o0);
+          tmem_ld32(tmem + lane_off + kColO + part32 * 128 + cc * 64 + 32, o1);
           tmem_ld_wait();
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -720,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
           }
           __syncwarp();
         }
-        if (half == 0 && lane < heads) {
+        if (rq == 0 && lane < heads) {
           if (part)
             p.ws_lse[head0 + lane] = lse;
           else if (p.a.lse)
