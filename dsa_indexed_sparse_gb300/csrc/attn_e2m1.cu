@@ -34,26 +34,32 @@
 // f16 rounds P by 2^-12 of itself, an eighth of bf16's, so the sum that normalises
 // the output is that of the unrounded weights, the one the log-sum-exp takes too.
 //
-// A stage (72 KB, two of them) holds a tile: nine [64 rows x 64 dims] atoms, 128-byte
-// swizzle, the same bytes read K-major by Q K^T (rows = N) and MN-major by P V (rows =
-// K).  For Q K^T the CTA's own rows: X = dims [0, 256), Y = dims [256, 512), R = rope.
-// For P V both CTAs need rows 0-63 at one offset and rows 64-127 at another, each with
-// its own value dims: rank 0 (rows 0-63, dims [0, 256)) has them in X already and
-// overwrites Y, dead once Q K^T is complete, with rows 64-127; rank 1 (rows 64-127,
-// dims [256, 512)) has them in Y and overwrites X with rows 0-63.  P of tile rows 0-63
-// goes into R (dead as well), P of rows 64-127 into a buffer of its own.
-//   shared memory: Q 72 KB | stage 0 | stage 1 | P, rows 64-127 8 KB | row scales, masks, barriers
+// Keys and values have buffers of their own, one each, freed by what reads them: K the
+// CTA's own 64 rows as nine [64 rows x 64 dims] atoms, K-major, refilled after Q K^T; V
+// the CTA's 256 value dims of all 128 rows as four [128 rows x 64 dims] atoms,
+// MN-major, refilled after P V, as is P.  (With tiles of K and V in one, two stages,
+// the next tile's rows waited for a P V although Q K^T had long read the stage.)  All
+// atoms in 128-byte swizzle.
+//   shared memory: Q 72 KB | K 72 KB | V 64 KB | P 16 KB | rows, row scales, barriers
 //   TMEM: latent logits [0,64) [64,128), rope logits [128,192) [192,256), O [256,512).  An
 //   N-wide accumulator of a pair MMA takes N/2 columns: lanes 0-63 are the CTA's heads
 //   for the first half of N, lanes 64-127 the same heads for the second.
 //
-// Warps: 0-7 producers, eight own and eight of the other CTA's rows each.  Their codes,
-// scales and rope are loaded into registers a tile ahead.  Turn by turn: the other
-// CTA's rows of tile j once Q K^T_j is complete (beside the softmax), the own rows of
-// tile j + 1 once P V_{j-1} has freed its stage (beside Q K^T_j + 1 of the other
-// stage).  8 Q K^T and 9 P V (rank 0 issues for both CTAs).  10-17 softmax: a thread
-// owns one head and 32 of the tile's rows, the four threads of a head agree on m and g
-// through shared memory.
+// Warps.  0-15 producers, K of tile j + 1 (four own rows a warp) and V of tile j (eight
+// rows a warp) in turn; codes, scales and rope are loaded into registers a tile ahead,
+// right after the registers' last use, a row's whole 256 or 128 bytes by neighbouring lanes
+// (32-byte pieces of eight rows took three times as long).  16 Q K^T and 17 P V (rank 0
+// issues for both CTAs).  18 finds the tiles' cache rows, row scales and masks, three
+// tiles ahead.  20-27 softmax, a thread one head and 32 of the tile's rows; the four
+// threads of a head agree on m and g through shared memory.  Registers are dealt out by
+// setmaxnreg, so that no role spills: with 221 KB of shared memory taken almost nothing is left of the
+// L1, and a spilled word comes back from the L2.  The code is kept small (rolled loops,
+// short waits): with 98 KB of it every role ran from a cold instruction cache.
+//
+// Measured (2048 selected rows, 128 heads): 1314 us for 2048 queries, 889 TFLOP/s of the
+// 1926 measured; 57.3 us for 64 (one cluster a query: 128 of 152 SMs).
+// Splitting the 16 warps into 8 for K and 8 for V: 1376 and 61.7; eight warps with both: 1578
+// and 62.9; the 48-row kernel of attn.cu's kind, which widens every row in both CTAs: 2171 and 100.
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
@@ -76,25 +82,28 @@ constexpr int kTile = 128;            // selected rows per tile
 constexpr int kOwn = 64;              // of which this CTA's own
 constexpr int kDqk = 576, kDv = 512;
 constexpr int kAtom = 64 * 128;       // bytes of a [64 rows x 64 dims] atom
-constexpr int kStageBytes = 9 * kAtom;
-constexpr int kRopeAtom = 8 * kAtom;  // offset of the rope atom (P of rows 0-63 later) in a stage
-constexpr int kProducers = 8;
-constexpr int kWarpQk = 8, kWarpPv = 9, kWarpSoft = 10;
-constexpr int kThreads = 576;
+constexpr int kVAtom = kTile * 128;   // bytes of a [128 rows x 64 dims] atom
+constexpr int kProducers = 16;
+constexpr int kWarpQk = 16, kWarpPv = 17, kWarpRows = 18, kWarpSoft = 20;
+constexpr int kThreads = 896;
+// registers a thread: 72 at launch (7 groups of 4 warps, 504 in all), then
+constexpr int kRegsProducer = 64, kRegsMma = 56, kRegsSoft = 96;
+static_assert(4 * kRegsProducer + kRegsMma + 2 * kRegsSoft <= 7 * 72, "register split");
 
 constexpr int kOffQ = 0;
-constexpr int kOffStage = 9 * kAtom;
-constexpr int kOffP1 = kOffStage + 2 * kStageBytes;
-constexpr int kOffScale = kOffP1 + kAtom;                // float [2 stages][128] row scales
-constexpr int kOffMask = kOffScale + 2 * kTile * 4;      // uint64 [2 stages][2 halves of the tile]
-constexpr int kOffRmax = kOffMask + 64;                  // float [2 stages][8] largest row scale of a warp's rows
-constexpr int kOffQexp = kOffRmax + 64;                  // float [64] the heads' 2^a
-constexpr int kOffOk = kOffQexp + kHeads * 4;            // int [2][8 softmax warps]
+constexpr int kOffK = kOffQ + 9 * kAtom;
+constexpr int kOffV = kOffK + 9 * kAtom;
+constexpr int kOffP = kOffV + 4 * kVAtom;
+constexpr int kOffScale = kOffP + 2 * kAtom;             // float [2][128] row scales
+constexpr int kOffRows = kOffScale + 2 * kTile * 4;      // int [2][128] cache rows, -1 for none
+constexpr int kOffMax = kOffRows + 2 * kTile * 4;        // bf16 [4 row quarters][64 heads]; float [64] 2^a at first
+constexpr int kOffMask = kOffMax + 4 * kHeads * 2;       // uint32 [2][4] valid rows
+constexpr int kOffRmax = kOffMask + 32;                  // float [2] largest row scale of a tile
+constexpr int kOffOk = kOffRmax + 16;                    // int [2][8 softmax warps]
 constexpr int kOffBar = kOffOk + 64;
-constexpr int kNumBars = 16;
+constexpr int kNumBars = 18;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;
-constexpr int kOffMax = kOffMisc + 16;                   // float [4 row quarters][64 heads]
-constexpr int kUsed = kOffMax + 4 * kHeads * 4;
+constexpr int kUsed = kOffMisc + 16;
 constexpr int kSmemBytes = 232448;
 constexpr int kSlack = kSmemBytes - kUsed;               // for re-aligning the base to 1024 bytes
 static_assert(kSlack >= 128, "shared memory budget");
@@ -115,6 +124,8 @@ struct PairParams {
   float* ws_lse;            // [n_split, T, H]
   uint64_t wait_limit_ns;
   uint32_t dbg_withhold;
+  uint32_t page_mul;        // pos / page_size = (pos * page_mul) >> page_shift for 0 <= pos < 2^31
+  uint32_t page_shift;
   uint32_t early_query;     // the query was complete before the kernel before this one let it launch
 };
 
@@ -140,8 +151,22 @@ __device__ __forceinline__ uint32_t leader_addr(const uint64_t* bar) {
 __device__ __forceinline__ void arrive_pair(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns) {
-  return mbar_wait(bar, parity, &g_status_attn_e2m1, abort_flag, limit_ns);
+// Whether a wait must end: another thread of the CTA gave up, or the CTA has been running
+// for longer than the limit (which this sets the flags for).
+__device__ __noinline__ bool give_up(volatile int* abort_flag, uint64_t deadline) {
+  if (*abort_flag) return true;
+  if (globaltimer_ns() < deadline) return false;
+  atomicOr(&g_status_attn_e2m1, kDevTimeout);
+  *abort_flag = 1;
+  return true;
+}
+// Bounded wait for a phase of `bar`.  Short on purpose: fourteen copies of it, and the
+// kernel's code has to stay in the instruction cache.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t deadline) {
+  const uint32_t addr = smem_u32(bar);
+  for (uint32_t it = 1; !mbar_try_wait(addr, parity); ++it)
+    if ((it & 63u) == 0u && give_up(abort_flag, deadline)) return false;
+  return true;
 }
 __device__ __forceinline__ void umma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                           uint32_t accumulate) {
@@ -150,6 +175,14 @@ __device__ __forceinline__ void umma_pair(uint32_t d_tmem, uint64_t a_desc, uint
       "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+template <int kRegs>
+__device__ __forceinline__ void shrink_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void grow_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 // One arrival on `bar` of both CTAs when every MMA issued so far by this thread is complete.
 __device__ __forceinline__ void commit_pair(uint64_t* bar) {
@@ -181,18 +214,6 @@ __device__ __forceinline__ void widen_codes(uint2 u, uint32_t scale_code, uint32
   }
 }
 
-// Writes block `blk` (16 dims) of row r into the atoms at `region`: chunks 2 blk and
-// 2 blk + 1 of 16 bytes, at their swizzled places.  Lanes of odd atoms write their
-// second chunk first: eight lanes then cover all banks.
-__device__ __forceinline__ void store_block(uint32_t region, int r, int blk, const uint32_t (&o)[8]) {
-  const uint32_t base = region + static_cast<uint32_t>((blk >> 2) * kAtom + r * 128);
-  const int c = (blk & 3) * 2, flip = (blk >> 2) & 1;
-  const uint32_t a0 = base + static_cast<uint32_t>(((c + flip) ^ (r & 7)) << 4);
-  const uint32_t a1 = base + static_cast<uint32_t>(((c + 1 - flip) ^ (r & 7)) << 4);
-  st_shared_v4(a0, flip ? o[4] : o[0], flip ? o[5] : o[1], flip ? o[6] : o[2], flip ? o[7] : o[3]);
-  st_shared_v4(a1, flip ? o[0] : o[4], flip ? o[1] : o[5], flip ? o[2] : o[6], flip ? o[3] : o[7]);
-}
-
 __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
   grid_dep_launch();   // the kernel after waits for this grid before it reads what this grid writes
   extern __shared__ __align__(1024) uint8_t sm_raw[];
@@ -204,17 +225,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
     return;
   }
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kOffBar);
-  uint64_t* full = bars;          // [2] leader: own rows of both CTAs in the stage
-  uint64_t* vfull = bars + 2;     // [2] leader: the other CTA's rows in the stage, both CTAs
-  uint64_t* pfull = bars + 4;     // [2] leader: P written, both CTAs
+  uint64_t* kfull = bars;         // leader: K rows of both CTAs written
+  uint64_t* vfull = bars + 1;     // leader: V rows of both CTAs written
+  uint64_t* pfull = bars + 2;     // leader: P written, both CTAs
+  uint64_t* pvdone = bars + 3;    // P V complete: V and P free
+  uint64_t* drain = bars + 4;     // every MMA complete (teardown)
   uint64_t* sfree = bars + 6;     // [2] leader: logits read, both CTAs
-  uint64_t* sfull = bars + 8;     // [2] Q K^T complete
-  uint64_t* empty = bars + 10;    // [2] P V complete
-  uint64_t* mfull = bars + 12;    // [2] row masks of the stage written
-  uint64_t* drain = bars + 14;    // every MMA complete (teardown)
+  uint64_t* sfull = bars + 8;     // [2] Q K^T complete: logits there, K free
+  uint64_t* mfull = bars + 10;    // [2] row scales and mask of a tile written
+  uint64_t* mfree = bars + 12;    // [2] and read
+  uint64_t* rfull = bars + 14;    // [2] cache rows of a tile written
+  uint64_t* rfree = bars + 16;    // [2] and read
   uint32_t* misc = reinterpret_cast<uint32_t*>(sm + kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
-  const uint64_t wlim = p.wait_limit_ns;
+  const uint64_t wlim = globaltimer_ns() + p.wait_limit_ns;   // no wait of this CTA goes on beyond
 
   int item = blockIdx.x >> 1;
   const int split = item % p.n_split;
@@ -229,14 +253,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&full[i], 2 * kProducers);
-      mbar_init(&vfull[i], 2 * kProducers);
-      mbar_init(&pfull[i], 16);
       mbar_init(&sfree[i], 16);
       mbar_init(&sfull[i], 1);
-      mbar_init(&empty[i], 1);
-      mbar_init(&mfull[i], kProducers);
+      mbar_init(&mfull[i], 1);
+      mbar_init(&mfree[i], 8);
+      mbar_init(&rfull[i], 1);
+      mbar_init(&rfree[i], kProducers);
     }
+    mbar_init(kfull, 2 * kProducers);
+    mbar_init(vfull, 2 * kProducers);
+    mbar_init(pfull, 16);
+    mbar_init(pvdone, 1);
     mbar_init(drain, 2);
     *abort_flag = 0;
     fence_mbar_init();
@@ -264,20 +291,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
   const int64_t row_bytes = p.a.row_bytes;
   const int32_t* bt = p.seq.block_table + static_cast<int64_t>(b) * p.seq.bt_stride;
   const int32_t* idx = p.a.idx + static_cast<int64_t>(t) * K;
-  // A selected entry's way to its row, a tile's worth of time between the steps: the
-  // position (load_pos), its page id (load_page), the cache row or -1 (row_of).
-  const int page_size = p.seq.page_size;
-  auto load_page = [&](int pos) -> int {
-    if (pos > qp) atomicOr(&g_status_attn_e2m1, kDevBadIndex);
-    return (pos >= 0 && pos <= qp) ? __ldg(bt + pos / page_size) : -1;
-  };
-  auto row_of = [&](int pos, int page) -> int {
-    if (pos < 0 || pos > qp) return -1;
-    if (page < 0 || page >= p.seq.n_pages) {
-      atomicOr(&g_status_attn_e2m1, kDevBadIndex);
-      return -1;
-    }
-    return page * page_size + pos % page_size;   // < cache_rows < 2^31
+  auto page_of = [&](int pos) -> int {   // pos / page_size
+    return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(pos)) * p.page_mul) >> p.page_shift);
   };
 
   // The query: warps 0-15 four heads each, eight lanes a head, lane c of them chunk c of
@@ -305,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
     const bool negate = p.a.softmax_scale < 0.f;
     const float f = ldexpf(negate ? -1.f : 1.f, -e);
     const uint32_t flip = negate ? 0x80008000u : 0u;
-    if (c == 0) reinterpret_cast<float*>(sm + kOffQexp)[hl] = ldexpf(1.f, e);
+    if (c == 0) reinterpret_cast<float*>(sm + kOffMax)[hl] = ldexpf(1.f, e);
     const uint32_t dst = smem_u32(sm + kOffQ) + static_cast<uint32_t>(hl * 128 + ((c ^ (hl & 7)) << 4));
 #pragma unroll
     for (int a = 0; a < 8; ++a) {
@@ -322,214 +337,234 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
     fence_proxy_async_smem();
   }
   __syncthreads();
-  // both CTAs' queries must be there before the leader multiplies: the softmax warps'
-  // first arrivals on sfree say so
-  if (warp >= kWarpSoft && lane == 0) {
-    arrive_pair(leader_addr(&sfree[0]));
-    arrive_pair(leader_addr(&sfree[1]));
-  }
-
   if (warp < kProducers) {
     // ------------------------------------------------ producers
-    if (p.early_query) grid_dep_wait();   // the selected indices come from the kernel before
-    // lanes 0-7 look after own rows [8 w, 8 w + 8) of the tile, lanes 8-15 after the other CTA's
-    const int tile_row = (static_cast<int>(rank ^ static_cast<uint32_t>(lane >> 3)) & 1) * kOwn + warp * 8 + (lane & 7);
-    const int sub = lane >> 4, blk = lane & 15;
-    const uint32_t region = rank == 0 ? 4 * kAtom : 0;   // of the other CTA's rows: Y in rank 0, X in rank 1
-    auto load_pos = [&](int j) -> int {
-      const int gi = r0 + j * kTile + tile_row;
-      return (lane < 16 && j < ntiles && gi < r1) ? __ldg(idx + gi) : -1;
+    const int32_t* rows_sm = reinterpret_cast<const int32_t*>(sm + kOffRows);
+    shrink_registers<kRegsProducer>();
+    const int sub = lane >> 4, blk = lane & 15, l8 = lane >> 3, b8 = lane & 7;
+    // K in registers: codes of block `lane` of the warp's four own rows; scale word and rope
+    // chunk b8 of row l8.  V: codes of block blk of this CTA's value dims of rows 2 k + sub of
+    // eight; scale word lane & 3 of row lane / 4.  A row that selects nothing reads row 0: its
+    // logits are masked, and its values get scales of zero (row 0's own could be anything, NaN
+    // among it).
+    uint2 kcode[4], vcode[4];
+    uint32_t ksc, vsc;
+    uint4 rope;
+    bool vhave;
+    auto fetch_k = [&](int j) {
+      const int32_t* r = rows_sm + (j & 1) * kTile + rank * kOwn + warp * 4;
+      const int4 r4 = *reinterpret_cast<const int4*>(r);
+      const uint8_t* base = kv + lane * 8;
+      const int row[4] = {r4.x, r4.y, r4.z, r4.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) kcode[i] = __ldg(reinterpret_cast<const uint2*>(base + max(row[i], 0) * row_bytes));
+      const uint8_t* rp = kv + max(r[l8], 0) * row_bytes;
+      ksc = __ldg(reinterpret_cast<const uint32_t*>(rp + kE2m1Scales) + b8);
+      rope = __ldg(reinterpret_cast<const uint4*>(rp + kE2m1Rope) + b8);
     };
-    // Own rows: codes of block `lane`; scale bytes as words, word lane & 7 of rows lane / 8
-    // and lane / 8 + 4; rope chunk lane & 7 of the same rows.  Other rows: codes of block blk
-    // (of this CTA's value dims) of rows 2 k + sub; scale word lane & 3 of row lane / 4.  A
-    // row that selects nothing reads row 0, with scales and rope values of zero.
-    uint2 code[8], pcode[4];
-    uint32_t sc[2], psc = 0u;
-    uint4 rope[2];
-    float rs = 0.f;
-    uint32_t valid = 0u;   // of tile `my_row`: bits 0-7 own, 8-15 other
-    auto fetch_own = [&](int my_row) {
-      valid = __ballot_sync(0xffffffffu, my_row >= 0);
-      const int safe = max(my_row, 0);
-      int row[8], row2[2];
+    auto fetch_v = [&](int j) {
+      const int32_t* r = rows_sm + (j & 1) * kTile + warp * 8;
+      const uint8_t* base = kv + rank * 128 + blk * 8;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) row[i] = __shfl_sync(0xffffffffu, safe, i);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) row2[k] = __shfl_sync(0xffffffffu, safe, (lane >> 3) + 4 * k);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) code[i] = __ldg(reinterpret_cast<const uint2*>(kv + row[i] * row_bytes) + lane);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint8_t* rp = kv + row2[k] * row_bytes;
-        sc[k] = __ldg(reinterpret_cast<const uint32_t*>(rp + kE2m1Scales) + (lane & 7));
-        rope[k] = __ldg(reinterpret_cast<const uint4*>(rp + kE2m1Rope) + (lane & 7));
-      }
-      rs = __ldg(reinterpret_cast<const float*>(kv + safe * row_bytes + kE2m1RowScale));
-    };
-    uint32_t pvalid = 0u;
-    auto fetch_other = [&](int my_row) {
-      pvalid = __ballot_sync(0xffffffffu, my_row >= 0) >> 8;
-      const int safe = max(my_row, 0);
-      int row[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) row[k] = __shfl_sync(0xffffffffu, safe, 8 + 2 * k + sub);
-      const int row1 = __shfl_sync(0xffffffffu, safe, 8 + (lane >> 2));
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        pcode[k] = __ldg(reinterpret_cast<const uint2*>(kv + row[k] * row_bytes) + rank * 16 + blk);
-      psc = __ldg(reinterpret_cast<const uint32_t*>(kv + row1 * row_bytes + kE2m1Scales) + rank * 4 + (lane & 3));
-    };
-    // Own rows into the stage, and the row scales and masks of all sixteen rows beside it.
-    auto write_own = [&](int j) {
-      const int st = j & 1;
-      const uint32_t stage = smem_u32(sm + kOffStage + st * kStageBytes);
-      uint32_t w[8];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) sc[k] = ((valid >> ((lane >> 3) + 4 * k)) & 1u) ? sc[k] : 0u;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = __shfl_sync(0xffffffffu, sc[i >> 2], (i & 3) * 8 + (lane >> 2));
-      const float my_rs = ((valid >> lane) & 1u) ? rs : 0.f;
-      if (lane < 16) reinterpret_cast<float*>(sm + kOffScale)[st * kTile + tile_row] = my_rs;
-      float rmax = lane < 16 ? my_rs : 0.f;
-#pragma unroll
-      for (int o = 1; o < 16; o <<= 1) rmax = fmaxf(rmax, __shfl_xor_sync(0xffffffffu, rmax, o));
-      if (lane == 0) {
-        reinterpret_cast<float*>(sm + kOffRmax)[st * 8 + warp] = rmax;
-        (sm + kOffMask + st * 16 + rank * 8)[warp] = static_cast<uint8_t>(valid);
-        (sm + kOffMask + st * 16 + (rank ^ 1u) * 8)[warp] = static_cast<uint8_t>(valid >> 8);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint32_t o[8];
-        widen_codes(code[i], w[i] >> (8 * (lane & 3)), o);
-        store_block(stage, warp * 8 + i, lane, o);
-      }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int r = warp * 8 + (lane >> 3) + 4 * k;
-        const uint32_t keep = ((valid >> ((lane >> 3) + 4 * k)) & 1u) ? 0xFFFFFFFFu : 0u;
-        st_shared_v4(stage + static_cast<uint32_t>(kRopeAtom + r * 128 + (((lane & 7) ^ (r & 7)) << 4)), rope[k].x & keep,
-                     rope[k].y & keep, rope[k].z & keep, rope[k].w & keep);
-      }
-      fence_proxy_async_smem();
+      for (int k = 0; k < 4; ++k) vcode[k] = __ldg(reinterpret_cast<const uint2*>(base + max(r[2 * k + sub], 0) * row_bytes));
+      const int row = r[lane >> 2];
+      vhave = row >= 0;
+      vsc = __ldg(reinterpret_cast<const uint32_t*>(kv + max(row, 0) * row_bytes + kE2m1Scales + rank * 16 + (lane & 3) * 4));
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&mfull[st]);
-        if (!(p.dbg_withhold && warp == 0 && j == 0)) arrive_pair(leader_addr(&full[st]));
-      }
+      if (lane == 0) mbar_arrive(&rfree[j & 1]);   // both have been read
     };
-    auto write_other = [&](int j) {
-      const int st = j & 1;
-      const uint32_t dst = smem_u32(sm + kOffStage + st * kStageBytes) + region;
-      psc = ((pvalid >> (lane >> 2)) & 1u) ? psc : 0u;
-      uint32_t w[4];
+    // Block b of a row goes to chunks 2 (b & 3), 2 (b & 3) + 1 of its atom, swizzled by the row.
+    // Lanes of odd atoms take their second half first: eight lanes then cover all banks.
+    const bool flip = (lane >> 2) & 1;
+    auto put = [&](uint32_t at, uint2 c, uint32_t scale_word, int byte) {
+      uint32_t o[8];
+      widen_codes(flip ? make_uint2(c.y, c.x) : c, scale_word >> (8 * byte), o);
+      st_shared_v4(at, o[0], o[1], o[2], o[3]);
+      st_shared_v4(at ^ 16u, o[4], o[5], o[6], o[7]);
+    };
+    const uint32_t chunk = static_cast<uint32_t>((2 * (lane & 3) + (flip ? 1 : 0)) << 4);
+    const uint32_t khalf = static_cast<uint32_t>((warp & 1) << 6);   // rows 4 w: the swizzle of rows 4-7 of eight
+    const uint32_t kdst = smem_u32(sm + kOffK) + static_cast<uint32_t>((lane >> 2) * kAtom + warp * 512) + (chunk ^ khalf);
+    const uint32_t vdst = smem_u32(sm + kOffV) + static_cast<uint32_t>((blk >> 2) * kVAtom + warp * 1024 + sub * 128) + (chunk ^ static_cast<uint32_t>(sub << 4));
+    const uint32_t rdst = smem_u32(sm + kOffK) + static_cast<uint32_t>(8 * kAtom + warp * 512 + l8 * 128) + (static_cast<uint32_t>((b8 ^ l8) << 4) ^ khalf);
+    bool ok = wait_bar(&rfull[0], 0, abort_flag, wlim);
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok) {
+      fetch_k(0);
+      fetch_v(0);
+    }
+    // turn j: K of tile j + 1 and V of tile j (turn -1: K of tile 0)
+#pragma unroll 1
+    for (int j = -1; j < ntiles && ok; ++j) {
+      if (j + 1 < ntiles) {
+        if (j >= 0) ok = __all_sync(0xffffffffu, wait_bar(&sfull[j & 1], (j >> 1) & 1, abort_flag, wlim));
+        if (!ok) break;
+        uint32_t w[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) w[k] = __shfl_sync(0xffffffffu, psc, (2 * k + sub) * 4 + (blk >> 2));
+        for (int i = 0; i < 4; ++i) w[i] = __shfl_sync(0xffffffffu, ksc, i * 8 + (lane >> 2));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) put((kdst ^ (i << 4)) + i * 128, kcode[i], w[i], lane & 3);
+        st_shared_v4(rdst, rope.x, rope.y, rope.z, rope.w);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && !(p.dbg_withhold && warp == 0 && j < 0)) arrive_pair(leader_addr(kfull));
+      }
+      if (j + 2 < ntiles) {
+        ok = __all_sync(0xffffffffu, wait_bar(&rfull[j & 1], ((j + 2) >> 1) & 1, abort_flag, wlim));
+        if (!ok) break;
+        fetch_k(j + 2);
+      }
+      if (j >= 1) ok = __all_sync(0xffffffffu, wait_bar(pvdone, (j - 1) & 1, abort_flag, wlim));
+      if (!ok) break;
+      if (j >= 0) {
+        uint32_t w[4];
+        vsc = vhave ? vsc : 0u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = __shfl_sync(0xffffffffu, vsc, (2 * k + sub) * 4 + (blk >> 2));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) put((vdst ^ (2 * k << 4)) + k * 256, vcode[k], w[k], lane & 3);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive_pair(leader_addr(vfull));
+      }
+      if (j >= 0 && j + 1 < ntiles) fetch_v(j + 1);
+    }
+  } else if (warp < kWarpSoft) {
+    shrink_registers<kRegsMma>();
+    if (warp == kWarpRows) {
+    // ------------------------------------------------ the tiles' rows, row scales and masks
+    if (p.early_query) grid_dep_wait();   // the selected indices come from the kernel before
+    // Tile row 32 k + lane, k = 0..3.  A selected entry's way to its row, a tile's time between
+    // the steps: the position, its page id, the cache row, the row's scale.
+    int pos[4], pos1[4], page[4], row[4], row1[4];
+    float rs[4], rs1[4];
+    auto load_pos = [&](int j) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        uint32_t o[8];
-        widen_codes(pcode[k], w[k] >> (8 * (blk & 3)), o);
-        store_block(dst, warp * 8 + 2 * k + sub, blk, o);
+        const int gi = r0 + j * kTile + k * 32 + lane;
+        pos1[k] = j < ntiles && gi < r1 ? __ldg(idx + gi) : -1;
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) arrive_pair(leader_addr(&vfull[st]));
     };
-    // Steps -1, 0, 1, ...: at step j the other CTA's rows of tile j, then the own rows of
-    // tile j + 1; own registers hold tile j + 1 and take tile j + 2, the other rows' hold
-    // tile j and take tile j + 1.  row1 / row2: rows of tiles j + 1 and j + 2.
-    int row1 = -1, row2;
-    int pos3, page3;
-    {
-      const int pos0 = load_pos(0), pos1 = load_pos(1);
-      pos3 = load_pos(2);
-      const int page0 = load_page(pos0), page1 = load_page(pos1);
-      page3 = load_page(pos3);
-      row1 = row_of(pos0, page0);
-      row2 = row_of(pos1, page1);
-    }
-    fetch_own(row1);
-    int pos4 = load_pos(3);
-#pragma unroll 1
-    for (int j = -1; j < ntiles; ++j) {
-      if (j >= 0) {
-        // Q K^T has read the rows that these replace
-        const bool ok = wait_bar(&sfull[j & 1], (j >> 1) & 1, abort_flag, wlim);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        write_other(j);
-      }
-      if (j + 1 < ntiles) {
-        fetch_other(row1);
-        if (j >= 1) {
-          const bool ok = wait_bar(&empty[(j + 1) & 1], ((j - 1) >> 1) & 1, abort_flag, wlim);
-          if (!__all_sync(0xffffffffu, ok)) break;
+    auto load_page = [&]() {   // of pos <- pos1
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        pos[k] = pos1[k];
+        if (pos[k] > qp) {
+          atomicOr(&g_status_attn_e2m1, kDevBadIndex);
+          pos[k] = -1;
         }
-        write_own(j + 1);
-        fetch_own(row2);
+        page[k] = pos[k] >= 0 ? __ldg(bt + page_of(pos[k])) : -1;
       }
-      row1 = row2;
-      row2 = row_of(pos3, page3);
-      pos3 = pos4;
-      page3 = load_page(pos3);
-      pos4 = load_pos(j + 5);
+    };
+    auto load_scale = [&]() {   // row1, rs1 of pos, page
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool good = page[k] >= 0 && page[k] < p.seq.n_pages;
+        if (pos[k] >= 0 && !good) atomicOr(&g_status_attn_e2m1, kDevBadIndex);
+        row1[k] = good ? (page[k] - page_of(pos[k])) * p.seq.page_size + pos[k] : -1;   // < cache_rows < 2^31
+        const uint8_t* rp = kv + max(row1[k], 0) * row_bytes;
+        rs1[k] = __ldg(reinterpret_cast<const float*>(rp + kE2m1RowScale));
+      }
+    };
+    // steps -3, -2, -1 only load
+#pragma unroll 1
+    for (int j = -3; j < ntiles; ++j) {
+      if (j >= 0) {
+        const int st = j & 1;
+        bool ok = j < 2 || wait_bar(&rfree[st], ((j >> 1) - 1) & 1, abort_flag, wlim);
+        if (!__all_sync(0xffffffffu, ok)) break;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          row[k] = row1[k];
+          rs[k] = rs1[k];
+          reinterpret_cast<int32_t*>(sm + kOffRows)[st * kTile + k * 32 + lane] = row[k];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&rfull[st]);
+      }
+      if (j >= -1) load_scale();
+      if (j >= -2) load_page();
+      load_pos(j + 3);
+      if (j >= 0) {
+        const int st = j & 1;
+        bool ok = j < 2 || wait_bar(&mfree[st], ((j >> 1) - 1) & 1, abort_flag, wlim);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        float rmax = 0.f;
+        uint32_t mask[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float mine = row[k] >= 0 ? rs[k] : 0.f;
+          rmax = fmaxf(rmax, mine);
+          mask[k] = __ballot_sync(0xffffffffu, row[k] >= 0);
+          reinterpret_cast<float*>(sm + kOffScale)[st * kTile + k * 32 + lane] = mine;
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) rmax = fmaxf(rmax, __shfl_xor_sync(0xffffffffu, rmax, o));
+        if (lane == 0) {
+          *reinterpret_cast<uint4*>(sm + kOffMask + st * 16) = make_uint4(mask[0], mask[1], mask[2], mask[3]);
+          reinterpret_cast<float*>(sm + kOffRmax)[st] = rmax;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&mfull[st]);
+      }
     }
-  } else if (warp == kWarpQk) {
+    } else if (warp == kWarpQk) {
     if (rank == 0) {
       const uint64_t dq = make_sdesc(smem_u32(sm + kOffQ), 16, 1024, kLayoutSw128);
-      const uint64_t dk0 = make_sdesc(smem_u32(sm + kOffStage), 16, 1024, kLayoutSw128);
+      const uint64_t dk = make_sdesc(smem_u32(sm + kOffK), 16, 1024, kLayoutSw128);
       for (int j = 0; j < ntiles; ++j) {
-        const int st = j & 1;
-        // the logit buffer is free (the first phase: the queries are staged) and the tile has landed
-        if (!__all_sync(0xffffffffu, wait_bar(&sfree[st], (j >> 1) & 1, abort_flag, wlim))) break;
-        if (!__all_sync(0xffffffffu, wait_bar(&full[st], (j >> 1) & 1, abort_flag, wlim))) break;
+        const int sb = j & 1;
+        // the logit buffer is free (the first phase: the queries are staged) and the keys are there
+        if (!__all_sync(0xffffffffu, wait_bar(&sfree[sb], (j >> 1) & 1, abort_flag, wlim))) break;
+        if (!__all_sync(0xffffffffu, wait_bar(kfull, j & 1, abort_flag, wlim))) break;
         tc_fence_after();
         fence_proxy_async_smem();
         if (elect_one()) {
-          const uint64_t dk = dk0 + static_cast<uint64_t>((st * kStageBytes) >> 4);
+          const uint32_t d = tmem + sb * 64;
+#pragma unroll 1
+          for (int a = 0; a < 8; ++a) {   // 64 dims a turn
+            const uint64_t off = static_cast<uint64_t>((a * kAtom) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < kDqk / 16; ++kk) {
-            const uint64_t off = static_cast<uint64_t>(((kk >> 2) * kAtom + (kk & 3) * 32) >> 4);
-            if (kk < kDv / 16)
-              umma_pair(tmem + st * 64, dq + off, dk + off, kIdescLatent, kk > 0 ? 1u : 0u);
-            else
-              umma_pair(tmem + kColRope + st * 64, dq + off, dk + off, kIdescRope, kk > kDv / 16 ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk)
+              umma_pair(d, dq + off + 2 * kk, dk + off + 2 * kk, kIdescLatent, static_cast<uint32_t>(a | kk));
           }
-          commit_pair(&sfull[st]);
+          constexpr uint64_t off = (8 * kAtom) >> 4;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_pair(d + kColRope, dq + off + 2 * kk, dk + off + 2 * kk, kIdescRope, static_cast<uint32_t>(kk));
+          commit_pair(&sfull[sb]);
         }
         __syncwarp();
       }
     }
-  } else if (warp == kWarpPv) {
+    } else if (warp == kWarpPv) {
     if (rank == 0) {
-      const uint64_t dv0 = make_sdesc(smem_u32(sm + kOffStage), kAtom, 1024, kLayoutSw128);
-      const uint64_t dp0 = make_sdesc(smem_u32(sm + kOffStage + kRopeAtom), 16, 1024, kLayoutSw128);
-      const uint64_t dp1 = make_sdesc(smem_u32(sm + kOffP1), 16, 1024, kLayoutSw128);
+      const uint64_t dv = make_sdesc(smem_u32(sm + kOffV), kVAtom, 1024, kLayoutSw128);
+      const uint64_t dp = make_sdesc(smem_u32(sm + kOffP), 16, 1024, kLayoutSw128);
       for (int j = 0; j < ntiles; ++j) {
-        const int st = j & 1;
-        if (!__all_sync(0xffffffffu, wait_bar(&vfull[st], (j >> 1) & 1, abort_flag, wlim))) break;
-        if (!__all_sync(0xffffffffu, wait_bar(&pfull[st], (j >> 1) & 1, abort_flag, wlim))) break;
+        if (!__all_sync(0xffffffffu, wait_bar(vfull, j & 1, abort_flag, wlim))) break;
+        if (!__all_sync(0xffffffffu, wait_bar(pfull, j & 1, abort_flag, wlim))) break;
         tc_fence_after();
         fence_proxy_async_smem();
         if (elect_one()) {
-          const uint64_t so = static_cast<uint64_t>((st * kStageBytes) >> 4);
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {   // value atoms 2 (q / 2), tile rows [64 (q & 1), 64 (q & 1) + 64)
+            const uint64_t da = dp + static_cast<uint64_t>(((q & 1) * kAtom) >> 4);
+            const uint64_t db = dv + static_cast<uint64_t>(((q >> 1) * 2 * kVAtom + (q & 1) * 4 * 2048) >> 4);
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-#pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk) {
-              const uint64_t da = (kk < 4 ? dp0 + so : dp1) + static_cast<uint64_t>(((kk & 3) * 32) >> 4);
-              // rows 16 kk ..: X holds tile rows 0-63, Y rows 64-127; value atoms 2 q, 2 q + 1
-              const uint64_t db = dv0 + so + static_cast<uint64_t>(((kk >> 2) * 4 * kAtom + q * 2 * kAtom + (kk & 3) * 2048) >> 4);
-              umma_pair(tmem + kColO + q * 128, da, db, kIdescPV, (j > 0 || kk > 0) ? 1u : 0u);
-            }
+            for (int kk = 0; kk < 4; ++kk)
+              umma_pair(tmem + kColO + (q >> 1) * 128, da + 2 * kk, db + 128 * kk, kIdescPV,
+                        static_cast<uint32_t>(j | (q & 1) | kk));
           }
-          commit_pair(&empty[st]);
+          commit_pair(pvdone);
         }
         __syncwarp();
       }
+    }
     }
   } else {
     // ------------------------------------------------ softmax and epilogue
+    grow_registers<kRegsSoft>();
     const int quarter = warp & 3;
     const int hl = (quarter & 1) * 32 + lane;   // head within the CTA
     const int half = quarter >> 1;              // tile rows [64 half, 64 half + 64), of which
@@ -539,50 +574,58 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
     // a scale of 0 becomes a tiny one, so that it leaves a masked logit at -inf
     const float sl2 = fmaxf(fabsf(p.a.softmax_scale) * kLog2e, 1e-30f);
     const uint32_t head_bar = 2 + (quarter & 1), read_bar = 4 + (quarter & 1);   // the 128 threads of 32 heads
-    float* xmax = reinterpret_cast<float*>(sm + kOffMax);
+    __nv_bfloat16* xmax = reinterpret_cast<__nv_bfloat16*>(sm + kOffMax);
     volatile int* oks = reinterpret_cast<volatile int*>(sm + kOffOk);
     const volatile uint32_t* masks = reinterpret_cast<const volatile uint32_t*>(sm + kOffMask);
-    const uint32_t sfree_leader0 = leader_addr(&sfree[0]), sfree_leader1 = leader_addr(&sfree[1]);
-    const uint32_t pfull_leader0 = leader_addr(&pfull[0]), pfull_leader1 = leader_addr(&pfull[1]);
-    const float qexp = reinterpret_cast<const float*>(sm + kOffQexp)[hl];
+    const float qexp = reinterpret_cast<const float*>(sm + kOffMax)[hl];
+    // The leader multiplies once both CTAs' queries are there and their 2^a have been read:
+    // these warps' first arrivals on sfree say so
+    __syncwarp();
+    if (lane == 0) {
+      arrive_pair(leader_addr(&sfree[0]));
+      arrive_pair(leader_addr(&sfree[1]));
+    }
+    const uint32_t prow = smem_u32(sm + kOffP) + static_cast<uint32_t>(half * kAtom + hl * 128);
     float m = -INFINITY, g = -INFINITY, l = 0.f;
     bool ok = true;
+#pragma unroll 1
     for (int j = 0; j < ntiles; ++j) {
       const int st = j & 1;
-      ok = wait_bar(&mfull[st], (j >> 1) & 1, abort_flag, wlim) &&
-           wait_bar(&sfull[st], (j >> 1) & 1, abort_flag, wlim);
+      ok = wait_bar(&mfull[st], (j >> 1) & 1, abort_flag, wlim) && wait_bar(&sfull[st], (j >> 1) & 1, abort_flag, wlim);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
       const uint32_t scales = smem_u32(sm + kOffScale) + static_cast<uint32_t>((st * kTile + rq * 32) * 4);
       float x[32];
       float mx = -INFINITY, rmax = 0.f;
       if (ok) {
-        uint32_t s0[32], s1[32];
+        // x = latent * 2^a * row scale + rope, -inf for rows that select nothing
+        uint32_t s0[32];
         tmem_ld32(tmem + lane_off + st * 64 + part32 * 32, s0);
-        tmem_ld32(tmem + lane_off + kColRope + st * 64 + part32 * 32, s1);
-        const uint32_t vmask = masks[st * 4 + rq];
-        const float* rmaxs = reinterpret_cast<const float*>(sm + kOffRmax) + st * 8;
+        {
+          uint32_t s1[32];
+          tmem_ld32(tmem + lane_off + kColRope + st * 64 + part32 * 32, s1);
+          tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < kProducers; ++i) rmax = fmaxf(rmax, rmaxs[i]);
-        tmem_ld_wait();
+          for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(s1[i]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_pair(leader_addr(&sfree[st]));   // the logit buffer has been read
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
           const uint4 rs = ld_shared_v4(scales + static_cast<uint32_t>(i * 4));
           float t0, t1, t2, t3;
           mul2(t0, t1, __uint_as_float(s0[i]), __uint_as_float(s0[i + 1]), qexp, qexp);
           mul2(t2, t3, __uint_as_float(s0[i + 2]), __uint_as_float(s0[i + 3]), qexp, qexp);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[i + k] = __uint_as_float(s1[i + k]);
           fma2(x[i], x[i + 1], t0, t1, __uint_as_float(rs.x), __uint_as_float(rs.y));
           fma2(x[i + 2], x[i + 3], t2, t3, __uint_as_float(rs.z), __uint_as_float(rs.w));
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_pair(st ? sfree_leader1 : sfree_leader0);
+        const uint32_t vmask = masks[st * 4 + rq];
         if (vmask != ~0u) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) x[i] = ((vmask >> i) & 1u) ? x[i] : -INFINITY;
         }
+        rmax = reinterpret_cast<const volatile float*>(sm + kOffRmax)[st];
         float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int i = 0; i < 32; i += 2) mq[(i >> 1) & 3] = fmax3(mq[(i >> 1) & 3], x[i], x[i + 1]);
@@ -592,32 +635,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
       // when one has given up.  There is room for one buffer: the last tile's entries have
       // been read once all four warps have arrived on read_bar.
       if (j >= 1) named_bar_sync(read_bar, 256);
-      xmax[rq * kHeads + hl] = mx;
+      const __nv_bfloat16 mxb = __float2bfloat16_ru(mx);   // a bound is enough, rounded up
+      xmax[rq * kHeads + hl] = mxb;
+      mx = __bfloat162float(mxb);
       if (lane == 0) oks[st * 8 + warp - kWarpSoft] = ok ? 1 : 0;
       named_bar_sync(head_bar, 128);
 #pragma unroll
-      for (int k = 1; k < 4; ++k) mx = fmaxf(mx, xmax[(rq ^ k) * kHeads + hl]);
-      // the four warps: quarters with this one's low bit, both row halves of each
+      for (int k = 1; k < 4; ++k) mx = fmaxf(mx, __bfloat162float(xmax[(rq ^ k) * kHeads + hl]));
+      // the four warps: those whose number is as odd as this one's
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (((k + kWarpSoft) & 1) == (quarter & 1)) ok = ok && oks[st * 8 + k] != 0;
+      for (int k = 0; k < 4; ++k) ok = ok && oks[st * 8 + 2 * k + (warp & 1)] != 0;
       named_bar_arrive(read_bar, 256);
       if (!ok) break;
       const float gx = mx + __log2f(rmax);
       const bool need_m = mx > m + kRescaleM, need_g = gx > g + kRescaleG;
+      // P has one buffer and O may have to be rescaled: P V of the tile before is complete
+      if (j >= 1) ok = wait_bar(pvdone, (j - 1) & 1, abort_flag, wlim);
       if (j >= 1 && __any_sync(0xffffffffu, need_g)) {
-        // O is rescaled: P V of the tile before must have written it
-        ok = wait_bar(&empty[st ^ 1], ((j - 1) >> 1) & 1, abort_flag, wlim);
         tc_fence_after();
         const float f = need_g ? exp2f(g - gx) : 1.f;
 #pragma unroll 1
         for (int cc = 0; cc < 8; ++cc) {   // this thread's half of the columns
           uint32_t o[16];
-          tmem_ld16(tmem + lane_off + kColO + part32 * 128 + cc * 16, o);
+          const uint32_t at = tmem + lane_off + kColO + part32 * 128 + cc * 16;
+          tmem_ld16(at, o);
           tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-          tmem_st16(tmem + lane_off + kColO + part32 * 128 + cc * 16, o);
+          tmem_st16(at, o);
         }
         tmem_st_wait();
       }
@@ -629,10 +674,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
       const float msub = (m == -INFINITY) ? 0.f : m;
       // 2^(m - g), kept finite and nonzero
       const float gain = (g == -INFINITY) ? 1.f : exp2f(fminf(fmaxf(msub - g, -126.f), 126.f));
-      // P of tile rows 64-127 has one buffer: P V of the tile before must have read it
-      if (half == 1 && j >= 1) ok = ok && wait_bar(&empty[st ^ 1], ((j - 1) >> 1) & 1, abort_flag, wlim);
-      const uint32_t prow = smem_u32(half == 0 ? sm + kOffStage + st * kStageBytes + kRopeAtom : sm + kOffP1) +
-                            static_cast<uint32_t>(hl * 128);
       float se[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -661,17 +702,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive_pair(st ? pfull_leader1 : pfull_leader0);
+      if (lane == 0) {
+        arrive_pair(leader_addr(pfull));
+        mbar_arrive(&mfree[st]);
+      }
     }
-    const int last = ntiles - 1;
-    if (ok) ok = wait_bar(&empty[last & 1], (last >> 1) & 1, abort_flag, wlim);
+    if (ok) ok = wait_bar(pvdone, (ntiles - 1) & 1, abort_flag, wlim);
     ok = __all_sync(0xffffffffu, ok);
-    // the sums of a head's four threads
+    // the sums of a head's four threads, through the row scales' space
+    float* sums = reinterpret_cast<float*>(sm + kOffScale);
     named_bar_sync(head_bar, 128);
-    xmax[rq * kHeads + hl] = l;
+    sums[rq * kHeads + hl] = l;
     named_bar_sync(head_bar, 128);
 #pragma unroll
-    for (int k = 1; k < 4; ++k) l += xmax[(rq ^ k) * kHeads + hl];
+    for (int k = 1; k < 4; ++k) l += sums[(rq ^ k) * kHeads + hl];
     if (ok) {
       tc_fence_after();
       // O holds sum p rs 2^(m - g) v over l = sum p
@@ -682,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
       const int64_t head0 = (static_cast<int64_t>(part ? split : 0) * p.seq.T + t) * H + h0 + (quarter & 1) * 32;
       uint8_t* out = reinterpret_cast<uint8_t*>(part ? p.ws_o : static_cast<uint16_t*>(p.a.out)) +
                      (head0 * kDv + half * 256 + part32 * 128) * 2;
-      const uint32_t stg = smem_u32(sm + kOffStage) + (warp - kWarpSoft) * 4096;   // all MMAs are complete
+      const uint32_t stg = smem_u32(sm + kOffK) + (warp - kWarpSoft) * 4096;   // all MMAs are complete
       if (heads > 0) {
 #pragma unroll 1
         for (int cc = 0; cc < 2; ++cc) {
@@ -765,7 +809,13 @@ cudaError_t launch_attn_e2m1(const SeqArgs& seq, const MlaArgs& a, void* workspa
   const int tiles = (a.K + kTile - 1) / kTile;
   const int rps = (tiles + split - 1) / split * kTile;
   split = (a.K + rps - 1) / rps;   // every slice non-empty
-  PairParams p{seq, a, split, rps, (a.H + 127) / 128, nullptr, nullptr, kWaitLimitNs, 0u, env.chained ? 1u : 0u};
+  PairParams p{seq, a, split, rps, (a.H + 127) / 128, nullptr, nullptr, kWaitLimitNs, 0u, 0u, 0u, env.chained ? 1u : 0u};
+  // division by the page size: with 2^(s - 1) < d <= 2^s and m = ceil(2^(31 + s) / d), the
+  // error m d - 2^(31 + s) < d <= 2^s keeps floor(n m / 2^(31 + s)) = floor(n / d) for n < 2^31
+  uint32_t shift = 0;
+  while ((1ll << shift) < seq.page_size) ++shift;
+  p.page_shift = 31 + shift;
+  p.page_mul = static_cast<uint32_t>(((1ull << (31 + shift)) + seq.page_size - 1) / seq.page_size);
   debug_wait_state(&p.wait_limit_ns, &p.dbg_withhold);
   if (split > 1) {
     const size_t o = static_cast<size_t>(split) * seq.T * a.H * kDv * sizeof(uint16_t);
