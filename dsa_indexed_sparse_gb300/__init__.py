@@ -139,17 +139,22 @@ def _ptr(t: Optional[torch.Tensor]):
     return t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it: 0.1 us against 2.9, of
+# the 3.4 that a small step's C call takes.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _stream(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return _raw_stream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _rows(t: torch.Tensor, name: str) -> int:
     """Data pointer of a tensor whose values are contiguous along its last dim, on the current GPU."""
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name} must be on the current CUDA device, not on {t.device}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"the last dim of {name} must be contiguous")
     return t.data_ptr()
 
