@@ -128,7 +128,8 @@ dsa_status_t check_mla_shape(const dsa_mla_desc_t* m, int32_t K, dsa::MlaArgs* a
     case DSA_E2M1:
       if (m->d_latent != 512 || m->d_rope != 64)
         return fail(DSA_ERR_UNSUPPORTED, "4-bit latent rows are defined for 512 + 64 dims only");
-      if (m->row_bytes % 16 != 0) return fail(DSA_ERR_INVALID_ARG, "row_bytes of 4-bit rows must be a multiple of 16");
+      if (m->row_bytes % 16 != 0 || m->row_bytes > 0x7FFFFFF0ll)
+        return fail(DSA_ERR_INVALID_ARG, "row_bytes of 4-bit rows must be a multiple of 16 below 2^31");
       kind = dsa::MlaKind::kE2M1;
       min_row = 432;
       break;

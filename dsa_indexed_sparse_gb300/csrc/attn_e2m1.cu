@@ -34,32 +34,36 @@
 // f16 rounds P by 2^-12 of itself, an eighth of bf16's, so the sum that normalises
 // the output is that of the unrounded weights, the one the log-sum-exp takes too.
 //
-// Keys and values have buffers of their own, one each, freed by what reads them: K the
-// CTA's own 64 rows as nine [64 rows x 64 dims] atoms, K-major, refilled after Q K^T; V
-// the CTA's 256 value dims of all 128 rows as four [128 rows x 64 dims] atoms,
-// MN-major, refilled after P V, as is P.  (With tiles of K and V in one, two stages,
-// the next tile's rows waited for a P V although Q K^T had long read the stage.)  All
-// atoms in 128-byte swizzle.
-//   shared memory: Q 72 KB | K 72 KB | V 64 KB | P 16 KB | rows, row scales, barriers
+// A stage (72 KB, two of them) holds a tile: nine [64 rows x 64 dims] atoms, 128-byte
+// swizzle, the same bytes read K-major by Q K^T (rows = N) and MN-major by P V (rows =
+// K).  For Q K^T the CTA's own rows: X = dims [0, 256), Y = dims [256, 512), R = rope.
+// For P V both CTAs need rows 0-63 at one offset and rows 64-127 at another, each with
+// its own value dims: rank 0 (rows 0-63, dims [0, 256)) has them in X already and
+// overwrites Y, dead once Q K^T is complete, with rows 64-127; rank 1 (rows 64-127,
+// dims [256, 512)) has them in Y and overwrites X with rows 0-63.  P of tile rows 0-63
+// goes into R (dead as well), P of rows 64-127 into a buffer of its own.  (Buffers of their
+// own for keys and values write and load a third more; the pipe to shared memory, which
+// the MMAs, the producers' stores and every load share, is what is nearest its limit.)
+//   shared memory: Q 72 KB | stage 0 | stage 1 | P, rows 64-127 8 KB | row scales, rows, masks, barriers
 //   TMEM: latent logits [0,64) [64,128), rope logits [128,192) [192,256), O [256,512).  An
 //   N-wide accumulator of a pair MMA takes N/2 columns: lanes 0-63 are the CTA's heads
 //   for the first half of N, lanes 64-127 the same heads for the second.
 //
-// Warps.  0-15 producers, K of tile j + 1 (four own rows a warp) and V of tile j (eight
-// rows a warp) in turn; codes, scales and rope are loaded into registers a tile ahead,
-// right after the registers' last use, a row's whole 256 or 128 bytes by neighbouring lanes
-// (32-byte pieces of eight rows took three times as long).  16 Q K^T and 17 P V (rank 0
-// issues for both CTAs).  18 finds the tiles' cache rows, row scales and masks, three
-// tiles ahead.  20-27 softmax, a thread one head and 32 of the tile's rows; the four
-// threads of a head agree on m and g through shared memory.  Registers are dealt out by
-// setmaxnreg, so that no role spills: with 221 KB of shared memory taken almost nothing is left of the
+// Warps.  0-15 producers, four own and four other rows of a tile each, whichever can go on
+// (in a fixed order the other rows wait for Q K^T of rows just written: 1496 us); codes, scales
+// and rope are loaded into registers a tile ahead, right after the registers' last use, a
+// row's whole 256 or 128 bytes by neighbouring lanes (32-byte pieces of eight rows took three
+// times as long).  16 Q K^T and 17 P V (rank 0 issues for both CTAs).  18 finds the
+// tiles' cache rows, row scales and masks, three tiles ahead.  20-27 stage the query, then softmax, a
+// thread one head and 32 of the tile's rows; the four threads of a head agree on m and g
+// through shared memory, when one of them has to let them grow.  Registers are dealt out by
+// setmaxnreg, so that no role spills: with 224 KB of shared memory taken almost nothing is left of the
 // L1, and a spilled word comes back from the L2.  The code is kept small (rolled loops,
 // short waits): with 98 KB of it every role ran from a cold instruction cache.
 //
-// Measured (2048 selected rows, 128 heads): 1314 us for 2048 queries, 889 TFLOP/s of the
-// 1926 measured; 57.3 us for 64 (one cluster a query: 128 of 152 SMs).
-// Splitting the 16 warps into 8 for K and 8 for V: 1376 and 61.7; eight warps with both: 1578
-// and 62.9; the 48-row kernel of attn.cu's kind, which widens every row in both CTAs: 2171 and 100.
+// Measured (2048 selected rows, 128 heads): 1287 us for 2048 queries, 908 TFLOP/s of the
+// 1926 measured; 54.9 us for 64 (one cluster a query: 128 of 152 SMs), 11.7 us for one.
+// The 48-row kernel of attn.cu's kind, which widens every row in both CTAs: 2171, 100 and 11.7.
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
@@ -82,7 +86,7 @@ constexpr int kTile = 128;            // selected rows per tile
 constexpr int kOwn = 64;              // of which this CTA's own
 constexpr int kDqk = 576, kDv = 512;
 constexpr int kAtom = 64 * 128;       // bytes of a [64 rows x 64 dims] atom
-constexpr int kVAtom = kTile * 128;   // bytes of a [128 rows x 64 dims] atom
+constexpr int kStage = 9 * kAtom;
 constexpr int kProducers = 16;
 constexpr int kWarpQk = 16, kWarpPv = 17, kWarpRows = 18, kWarpSoft = 20;
 constexpr int kThreads = 896;
@@ -91,15 +95,14 @@ constexpr int kRegsProducer = 64, kRegsMma = 56, kRegsSoft = 96;
 static_assert(4 * kRegsProducer + kRegsMma + 2 * kRegsSoft <= 7 * 72, "register split");
 
 constexpr int kOffQ = 0;
-constexpr int kOffK = kOffQ + 9 * kAtom;
-constexpr int kOffV = kOffK + 9 * kAtom;
-constexpr int kOffP = kOffV + 4 * kVAtom;
-constexpr int kOffScale = kOffP + 2 * kAtom;             // float [2][128] row scales
+constexpr int kOffStage = kOffQ + 9 * kAtom;             // [2]
+constexpr int kOffP1 = kOffStage + 2 * kStage;           // P of tile rows 64-127
+constexpr int kOffScale = kOffP1 + kAtom;                 // float [2][128] row scales
 constexpr int kOffRows = kOffScale + 2 * kTile * 4;      // int [2][128] cache rows, -1 for none
 constexpr int kOffMax = kOffRows + 2 * kTile * 4;        // bf16 [4 row quarters][64 heads]; float [64] 2^a at first
 constexpr int kOffMask = kOffMax + 4 * kHeads * 2;       // uint32 [2][4] valid rows
 constexpr int kOffRmax = kOffMask + 32;                  // float [2] largest row scale of a tile
-constexpr int kOffOk = kOffRmax + 16;                    // int [2][8 softmax warps]
+constexpr int kOffOk = kOffRmax + 16;                    // int [8 softmax warps]
 constexpr int kOffBar = kOffOk + 64;
 constexpr int kNumBars = 18;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;
@@ -160,6 +163,16 @@ __device__ __noinline__ bool give_up(volatile int* abort_flag, uint64_t deadline
   *abort_flag = 1;
   return true;
 }
+// Whether a phase of `bar` is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
 // Bounded wait for a phase of `bar`.  Short on purpose: fourteen copies of it, and the
 // kernel's code has to stay in the instruction cache.
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t deadline) {
@@ -193,8 +206,16 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
       : "memory");
 }
 
-__device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t nthreads) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+// A barrier of `nthreads` threads that tells each whether any of them gave true.
+__device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t nthreads, bool mine) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbarrier.cta.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"(nthreads), "r"(static_cast<uint32_t>(mine))
+      : "memory");
+  return any != 0;
 }
 
 // Sixteen codes (8 bytes) times their E4M3 block scale -> sixteen halves, exact.
@@ -225,13 +246,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
     return;
   }
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kOffBar);
-  uint64_t* kfull = bars;         // leader: K rows of both CTAs written
-  uint64_t* vfull = bars + 1;     // leader: V rows of both CTAs written
+  uint64_t* ownfull = bars;       // leader: both CTAs' own rows written
+  uint64_t* othfull = bars + 1;   // leader: the other CTA's rows written, in both
   uint64_t* pfull = bars + 2;     // leader: P written, both CTAs
-  uint64_t* pvdone = bars + 3;    // P V complete: V and P free
-  uint64_t* drain = bars + 4;     // every MMA complete (teardown)
+  uint64_t* drain = bars + 3;     // every MMA complete (teardown)
+  uint64_t* pvdone = bars + 4;    // [2] P V complete: the tile's stage and P free
   uint64_t* sfree = bars + 6;     // [2] leader: logits read, both CTAs
-  uint64_t* sfull = bars + 8;     // [2] Q K^T complete: logits there, K free
+  uint64_t* sfull = bars + 8;     // [2] Q K^T complete: logits there, half of the stage and its rope atom dead
   uint64_t* mfull = bars + 10;    // [2] row scales and mask of a tile written
   uint64_t* mfree = bars + 12;    // [2] and read
   uint64_t* rfull = bars + 14;    // [2] cache rows of a tile written
@@ -255,15 +276,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sfree[i], 16);
       mbar_init(&sfull[i], 1);
+      mbar_init(&pvdone[i], 1);
       mbar_init(&mfull[i], 1);
       mbar_init(&mfree[i], 8);
       mbar_init(&rfull[i], 1);
       mbar_init(&rfree[i], kProducers);
     }
-    mbar_init(kfull, 2 * kProducers);
-    mbar_init(vfull, 2 * kProducers);
+    mbar_init(ownfull, 2 * kProducers);
+    mbar_init(othfull, 2 * kProducers);
     mbar_init(pfull, 16);
-    mbar_init(pvdone, 1);
     mbar_init(drain, 2);
     *abort_flag = 0;
     fence_mbar_init();
@@ -288,90 +309,54 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
     b = 0;
   }
   const uint8_t* kv = static_cast<const uint8_t*>(p.a.kv);
-  const int64_t row_bytes = p.a.row_bytes;
+  const uint32_t row_bytes = static_cast<uint32_t>(p.a.row_bytes);   // < 2^31, the host sees to that
   const int32_t* bt = p.seq.block_table + static_cast<int64_t>(b) * p.seq.bt_stride;
   const int32_t* idx = p.a.idx + static_cast<int64_t>(t) * K;
   auto page_of = [&](int pos) -> int {   // pos / page_size
     return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(pos)) * p.page_mul) >> p.page_shift);
   };
 
-  // The query: warps 0-15 four heads each, eight lanes a head, lane c of them chunk c of
-  // every atom.  The latent part becomes f16 with its own power of two per head.
-  if (warp < kHeads / 4) {
-    const int hl = warp * 4 + (lane >> 3), c = lane & 7;
-    const bool have = h0 + hl < H;
-    const uint4* qg = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.a.q) +
-                                                     (static_cast<int64_t>(t) * H + h0 + hl) * kDqk) + c;
-    uint4 v[9];
-#pragma unroll
-    for (int a = 0; a < 9; ++a) v[a] = have ? __ldg(qg + 8 * a) : make_uint4(0u, 0u, 0u, 0u);
-    __nv_bfloat162 mx = __float2bfloat162_rn(0.f);
-#pragma unroll
-    for (int a = 0; a < 8; ++a) {
-      const uint32_t w[4] = {v[a].x, v[a].y, v[a].z, v[a].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) mx = __hmax2(mx, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
-    }
-    float amax = fmaxf(__low2float(mx), __high2float(mx));
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const int e = amax > 0.f ? max(-110, min(113, ilogbf(amax) - 14)) : 0;
-    // the maximum is taken over unscaled logits: a negative scale turns the query round
-    const bool negate = p.a.softmax_scale < 0.f;
-    const float f = ldexpf(negate ? -1.f : 1.f, -e);
-    const uint32_t flip = negate ? 0x80008000u : 0u;
-    if (c == 0) reinterpret_cast<float*>(sm + kOffMax)[hl] = ldexpf(1.f, e);
-    const uint32_t dst = smem_u32(sm + kOffQ) + static_cast<uint32_t>(hl * 128 + ((c ^ (hl & 7)) << 4));
-#pragma unroll
-    for (int a = 0; a < 8; ++a) {
-      const uint32_t w[4] = {v[a].x, v[a].y, v[a].z, v[a].w};
-      uint32_t o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __half2 q2 = __floats2half2_rn(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xFFFF0000u) * f);
-        o[i] = *reinterpret_cast<const uint32_t*>(&q2);
-      }
-      st_shared_v4(dst + static_cast<uint32_t>(a * kAtom), o[0], o[1], o[2], o[3]);
-    }
-    st_shared_v4(dst + static_cast<uint32_t>(8 * kAtom), v[8].x ^ flip, v[8].y ^ flip, v[8].z ^ flip, v[8].w ^ flip);
-    fence_proxy_async_smem();
-  }
-  __syncthreads();
   if (warp < kProducers) {
     // ------------------------------------------------ producers
     const int32_t* rows_sm = reinterpret_cast<const int32_t*>(sm + kOffRows);
     shrink_registers<kRegsProducer>();
     const int sub = lane >> 4, blk = lane & 15, l8 = lane >> 3, b8 = lane & 7;
-    // K in registers: codes of block `lane` of the warp's four own rows; scale word and rope
-    // chunk b8 of row l8.  V: codes of block blk of this CTA's value dims of rows 2 k + sub of
-    // eight; scale word lane & 3 of row lane / 4.  A row that selects nothing reads row 0: its
-    // logits are masked, and its values get scales of zero (row 0's own could be anything, NaN
-    // among it).
-    uint2 kcode[4], vcode[4];
+    // In registers.  Own: codes of block `lane` of the warp's four own rows; scale word and
+    // rope chunk b8 of row l8.  Other: codes of block blk of this CTA's value dims of rows
+    // 2 k + sub of four; scale word lane & 3 of row (lane / 4) & 3.  A row that selects nothing reads
+    // row 0 with scales of zero: its logits are masked, and its values must not be row 0's
+    // own, which could be anything, NaN among it.
+    uint2 kcode[4], vcode[2];
     uint32_t ksc, vsc;
+    bool khave, vhave;
     uint4 rope;
-    bool vhave;
-    auto fetch_k = [&](int j) {
+    int krow[5], vrow[3];   // the next tile's cache rows
+    auto at_row = [&](int row) { return kv + static_cast<uint64_t>(static_cast<uint32_t>(max(row, 0))) * row_bytes; };
+    auto rows_k = [&](int j) {
       const int32_t* r = rows_sm + (j & 1) * kTile + rank * kOwn + warp * 4;
       const int4 r4 = *reinterpret_cast<const int4*>(r);
-      const uint8_t* base = kv + lane * 8;
-      const int row[4] = {r4.x, r4.y, r4.z, r4.w};
+      krow[0] = r4.x, krow[1] = r4.y, krow[2] = r4.z, krow[3] = r4.w;
+      krow[4] = r[l8];
+    };
+    auto fetch_k = [&]() {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) kcode[i] = __ldg(reinterpret_cast<const uint2*>(base + max(row[i], 0) * row_bytes));
-      const uint8_t* rp = kv + max(r[l8], 0) * row_bytes;
+      for (int i = 0; i < 4; ++i) kcode[i] = __ldg(reinterpret_cast<const uint2*>(at_row(krow[i])) + lane);
+      const uint8_t* rp = at_row(krow[4]);
       ksc = __ldg(reinterpret_cast<const uint32_t*>(rp + kE2m1Scales) + b8);
       rope = __ldg(reinterpret_cast<const uint4*>(rp + kE2m1Rope) + b8);
+      khave = krow[4] >= 0;
     };
-    auto fetch_v = [&](int j) {
-      const int32_t* r = rows_sm + (j & 1) * kTile + warp * 8;
-      const uint8_t* base = kv + rank * 128 + blk * 8;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) vcode[k] = __ldg(reinterpret_cast<const uint2*>(base + max(r[2 * k + sub], 0) * row_bytes));
-      const int row = r[lane >> 2];
-      vhave = row >= 0;
-      vsc = __ldg(reinterpret_cast<const uint32_t*>(kv + max(row, 0) * row_bytes + kE2m1Scales + rank * 16 + (lane & 3) * 4));
+    auto rows_v = [&](int j) {
+      const int32_t* r = rows_sm + (j & 1) * kTile + (rank ^ 1u) * kOwn + warp * 4;
+      vrow[0] = r[sub], vrow[1] = r[2 + sub], vrow[2] = r[(lane >> 2) & 3];
       __syncwarp();
       if (lane == 0) mbar_arrive(&rfree[j & 1]);   // both have been read
+    };
+    auto fetch_v = [&]() {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) vcode[k] = __ldg(reinterpret_cast<const uint2*>(at_row(vrow[k])) + rank * 16 + blk);
+      vsc = __ldg(reinterpret_cast<const uint32_t*>(at_row(vrow[2]) + kE2m1Scales) + rank * 4 + (lane & 3));
+      vhave = vrow[2] >= 0;
     };
     // Block b of a row goes to chunks 2 (b & 3), 2 (b & 3) + 1 of its atom, swizzled by the row.
     // Lanes of odd atoms take their second half first: eight lanes then cover all banks.
@@ -382,52 +367,64 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
       st_shared_v4(at, o[0], o[1], o[2], o[3]);
       st_shared_v4(at ^ 16u, o[4], o[5], o[6], o[7]);
     };
-    const uint32_t chunk = static_cast<uint32_t>((2 * (lane & 3) + (flip ? 1 : 0)) << 4);
-    const uint32_t khalf = static_cast<uint32_t>((warp & 1) << 6);   // rows 4 w: the swizzle of rows 4-7 of eight
-    const uint32_t kdst = smem_u32(sm + kOffK) + static_cast<uint32_t>((lane >> 2) * kAtom + warp * 512) + (chunk ^ khalf);
-    const uint32_t vdst = smem_u32(sm + kOffV) + static_cast<uint32_t>((blk >> 2) * kVAtom + warp * 1024 + sub * 128) + (chunk ^ static_cast<uint32_t>(sub << 4));
-    const uint32_t rdst = smem_u32(sm + kOffK) + static_cast<uint32_t>(8 * kAtom + warp * 512 + l8 * 128) + (static_cast<uint32_t>((b8 ^ l8) << 4) ^ khalf);
-    bool ok = wait_bar(&rfull[0], 0, abort_flag, wlim);
-    ok = __all_sync(0xffffffffu, ok);
-    if (ok) {
-      fetch_k(0);
-      fetch_v(0);
-    }
-    // turn j: K of tile j + 1 and V of tile j (turn -1: K of tile 0)
+    // rows 4 w + i: the swizzle of rows 4-7 of eight
+    const uint32_t chunk = static_cast<uint32_t>(((2 * (lane & 3) + (flip ? 1 : 0)) << 4) ^ ((warp & 1) << 6));
+    const uint32_t stage0 = smem_u32(sm + kOffStage) + static_cast<uint32_t>(warp * 512);
+    const uint32_t kdst = stage0 + static_cast<uint32_t>((lane >> 2) * kAtom) + chunk;
+    const uint32_t vdst = stage0 + static_cast<uint32_t>(((rank ^ 1u) * 4 + (blk >> 2)) * kAtom + sub * 128) + (chunk ^ static_cast<uint32_t>(sub << 4));
+    const uint32_t rdst = stage0 + static_cast<uint32_t>(8 * kAtom + l8 * 128 + (((b8 ^ l8) << 4) ^ ((warp & 1) << 6)));
+    auto wait = [&](uint64_t* bar, int use) -> bool {
+      return __all_sync(0xffffffffu, wait_bar(bar, use & 1, abort_flag, wlim));
+    };
+    // Own rows of tile a once P V of a - 2 has freed the stage, the other CTA's rows of tile b
+    // over the half of the stage that is dead once Q K^T of b is complete, whichever can go on.
+    // The next tile's row numbers are read before the writes, its codes loaded right after.
+    if (wait(&rfull[0], 0)) {
+      rows_k(0);
+      rows_v(0);
+      fetch_k();
+      fetch_v();
+      int a = 0, b = 0;
+      uint32_t idle = 0;
 #pragma unroll 1
-    for (int j = -1; j < ntiles && ok; ++j) {
-      if (j + 1 < ntiles) {
-        if (j >= 0) ok = __all_sync(0xffffffffu, wait_bar(&sfull[j & 1], (j >> 1) & 1, abort_flag, wlim));
-        if (!ok) break;
-        uint32_t w[4];
+      while (b < ntiles) {
+        if (b < a && __all_sync(0xffffffffu, mbar_test(&sfull[b & 1], (b >> 1) & 1))) {
+          const uint32_t at = vdst + static_cast<uint32_t>((b & 1) * kStage);
+          if (b + 1 < ntiles) rows_v(b + 1);   // rfull of b + 1: seen for own rows of b
+          vsc = vhave ? vsc : 0u;
+          uint32_t w[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __shfl_sync(0xffffffffu, ksc, i * 8 + (lane >> 2));
+          for (int k = 0; k < 2; ++k) w[k] = __shfl_sync(0xffffffffu, vsc, (2 * k + sub) * 4 + (blk >> 2));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) put((kdst ^ (i << 4)) + i * 128, kcode[i], w[i], lane & 3);
-        st_shared_v4(rdst, rope.x, rope.y, rope.z, rope.w);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && !(p.dbg_withhold && warp == 0 && j < 0)) arrive_pair(leader_addr(kfull));
+          for (int k = 0; k < 2; ++k) put((at ^ (2 * k << 4)) + k * 256, vcode[k], w[k], lane & 3);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) arrive_pair(leader_addr(othfull));
+          if (b + 1 < ntiles) fetch_v();
+          ++b;
+        } else if (a < ntiles && (a < 2 || __all_sync(0xffffffffu, mbar_test(&pvdone[a & 1], ((a >> 1) - 1) & 1)))) {
+          const uint32_t st = static_cast<uint32_t>((a & 1) * kStage);
+          if (a + 1 < ntiles) {
+            if (!wait(&rfull[(a + 1) & 1], (a + 1) >> 1)) break;
+            rows_k(a + 1);
+          }
+          ksc = khave ? ksc : 0u;
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = __shfl_sync(0xffffffffu, ksc, i * 8 + (lane >> 2));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) put(((kdst + st) ^ (i << 4)) + i * 128, kcode[i], w[i], lane & 3);
+          st_shared_v4(rdst + st, rope.x, rope.y, rope.z, rope.w);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && !(p.dbg_withhold && warp == 0 && a == 0)) arrive_pair(leader_addr(ownfull));
+          if (a + 1 < ntiles) fetch_k();
+          ++a;
+        } else {
+          __nanosleep(32);
+          if ((++idle & 31u) == 0u && __any_sync(0xffffffffu, give_up(abort_flag, wlim))) break;
+        }
       }
-      if (j + 2 < ntiles) {
-        ok = __all_sync(0xffffffffu, wait_bar(&rfull[j & 1], ((j + 2) >> 1) & 1, abort_flag, wlim));
-        if (!ok) break;
-        fetch_k(j + 2);
-      }
-      if (j >= 1) ok = __all_sync(0xffffffffu, wait_bar(pvdone, (j - 1) & 1, abort_flag, wlim));
-      if (!ok) break;
-      if (j >= 0) {
-        uint32_t w[4];
-        vsc = vhave ? vsc : 0u;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = __shfl_sync(0xffffffffu, vsc, (2 * k + sub) * 4 + (blk >> 2));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) put((vdst ^ (2 * k << 4)) + k * 256, vcode[k], w[k], lane & 3);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) arrive_pair(leader_addr(vfull));
-      }
-      if (j >= 0 && j + 1 < ntiles) fetch_v(j + 1);
     }
   } else if (warp < kWarpSoft) {
     shrink_registers<kRegsMma>();
@@ -462,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
         const bool good = page[k] >= 0 && page[k] < p.seq.n_pages;
         if (pos[k] >= 0 && !good) atomicOr(&g_status_attn_e2m1, kDevBadIndex);
         row1[k] = good ? (page[k] - page_of(pos[k])) * p.seq.page_size + pos[k] : -1;   // < cache_rows < 2^31
-        const uint8_t* rp = kv + max(row1[k], 0) * row_bytes;
+        const uint8_t* rp = kv + static_cast<uint64_t>(static_cast<uint32_t>(max(row1[k], 0))) * row_bytes;
         rs1[k] = __ldg(reinterpret_cast<const float*>(rp + kE2m1RowScale));
       }
     };
@@ -511,16 +508,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
     } else if (warp == kWarpQk) {
     if (rank == 0) {
       const uint64_t dq = make_sdesc(smem_u32(sm + kOffQ), 16, 1024, kLayoutSw128);
-      const uint64_t dk = make_sdesc(smem_u32(sm + kOffK), 16, 1024, kLayoutSw128);
+      const uint64_t dk0 = make_sdesc(smem_u32(sm + kOffStage), 16, 1024, kLayoutSw128);
       for (int j = 0; j < ntiles; ++j) {
         const int sb = j & 1;
         // the logit buffer is free (the first phase: the queries are staged) and the keys are there
         if (!__all_sync(0xffffffffu, wait_bar(&sfree[sb], (j >> 1) & 1, abort_flag, wlim))) break;
-        if (!__all_sync(0xffffffffu, wait_bar(kfull, j & 1, abort_flag, wlim))) break;
+        if (!__all_sync(0xffffffffu, wait_bar(ownfull, j & 1, abort_flag, wlim))) break;
         tc_fence_after();
         fence_proxy_async_smem();
         if (elect_one()) {
           const uint32_t d = tmem + sb * 64;
+          const uint64_t dk = dk0 + static_cast<uint64_t>((sb * kStage) >> 4);
 #pragma unroll 1
           for (int a = 0; a < 8; ++a) {   // 64 dims a turn
             const uint64_t off = static_cast<uint64_t>((a * kAtom) >> 4);
@@ -539,24 +537,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
     }
     } else if (warp == kWarpPv) {
     if (rank == 0) {
-      const uint64_t dv = make_sdesc(smem_u32(sm + kOffV), kVAtom, 1024, kLayoutSw128);
-      const uint64_t dp = make_sdesc(smem_u32(sm + kOffP), 16, 1024, kLayoutSw128);
+      const uint64_t dv0 = make_sdesc(smem_u32(sm + kOffStage), kAtom, 1024, kLayoutSw128);
+      const uint64_t dp0 = make_sdesc(smem_u32(sm + kOffStage + 8 * kAtom), 16, 1024, kLayoutSw128);
+      const uint64_t dp1 = make_sdesc(smem_u32(sm + kOffP1), 16, 1024, kLayoutSw128);
       for (int j = 0; j < ntiles; ++j) {
-        if (!__all_sync(0xffffffffu, wait_bar(vfull, j & 1, abort_flag, wlim))) break;
+        if (!__all_sync(0xffffffffu, wait_bar(othfull, j & 1, abort_flag, wlim))) break;
         if (!__all_sync(0xffffffffu, wait_bar(pfull, j & 1, abort_flag, wlim))) break;
         tc_fence_after();
         fence_proxy_async_smem();
         if (elect_one()) {
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {   // value atoms 2 (q / 2), tile rows [64 (q & 1), 64 (q & 1) + 64)
-            const uint64_t da = dp + static_cast<uint64_t>(((q & 1) * kAtom) >> 4);
-            const uint64_t db = dv + static_cast<uint64_t>(((q >> 1) * 2 * kVAtom + (q & 1) * 4 * 2048) >> 4);
+            const uint64_t st = static_cast<uint64_t>(((j & 1) * kStage) >> 4);
+            const uint64_t da = (q & 1) ? dp1 : dp0 + st;
+            const uint64_t db = dv0 + st + static_cast<uint64_t>((((q & 1) * 4 + (q >> 1) * 2) * kAtom) >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               umma_pair(tmem + kColO + (q >> 1) * 128, da + 2 * kk, db + 128 * kk, kIdescPV,
                         static_cast<uint32_t>(j | (q & 1) | kk));
           }
-          commit_pair(pvdone);
+          commit_pair(&pvdone[j & 1]);
         }
         __syncwarp();
       }
@@ -565,6 +565,49 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
   } else {
     // ------------------------------------------------ softmax and epilogue
     grow_registers<kRegsSoft>();
+    // The query: eight heads a warp, four at a time, eight lanes a head, lane c of them chunk c
+    // of every atom.  The latent part becomes f16 with its own power of two per head.
+#pragma unroll 1
+    for (int h4 = 0; h4 < 2; ++h4) {
+    const int hl = (warp - kWarpSoft) * 8 + h4 * 4 + (lane >> 3), c = lane & 7;
+    const bool have = h0 + hl < H;
+    const uint4* qg = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.a.q) +
+                                                     (static_cast<int64_t>(t) * H + h0 + hl) * kDqk) + c;
+    uint4 v[9];
+#pragma unroll
+    for (int a = 0; a < 9; ++a) v[a] = have ? __ldg(qg + 8 * a) : make_uint4(0u, 0u, 0u, 0u);
+    __nv_bfloat162 mx = __float2bfloat162_rn(0.f);
+#pragma unroll
+    for (int a = 0; a < 8; ++a) {
+      const uint32_t w[4] = {v[a].x, v[a].y, v[a].z, v[a].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mx = __hmax2(mx, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
+    }
+    float amax = fmaxf(__low2float(mx), __high2float(mx));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const int e = amax > 0.f ? max(-110, min(113, ilogbf(amax) - 14)) : 0;
+    // the maximum is taken over unscaled logits: a negative scale turns the query round
+    const bool negate = p.a.softmax_scale < 0.f;
+    const float f = ldexpf(negate ? -1.f : 1.f, -e);
+    const uint32_t flip = negate ? 0x80008000u : 0u;
+    if (c == 0) reinterpret_cast<float*>(sm + kOffMax)[hl] = ldexpf(1.f, e);
+    const uint32_t dst = smem_u32(sm + kOffQ) + static_cast<uint32_t>(hl * 128 + ((c ^ (hl & 7)) << 4));
+#pragma unroll
+    for (int a = 0; a < 8; ++a) {
+      const uint32_t w[4] = {v[a].x, v[a].y, v[a].z, v[a].w};
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __half2 q2 = __floats2half2_rn(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xFFFF0000u) * f);
+        o[i] = *reinterpret_cast<const uint32_t*>(&q2);
+      }
+      st_shared_v4(dst + static_cast<uint32_t>(a * kAtom), o[0], o[1], o[2], o[3]);
+    }
+    st_shared_v4(dst + static_cast<uint32_t>(8 * kAtom), v[8].x ^ flip, v[8].y ^ flip, v[8].z ^ flip, v[8].w ^ flip);
+    }
+    fence_proxy_async_smem();
+    named_bar_sync(1, 256);
     const int quarter = warp & 3;
     const int hl = (quarter & 1) * 32 + lane;   // head within the CTA
     const int half = quarter >> 1;              // tile rows [64 half, 64 half + 64), of which
@@ -573,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     // a scale of 0 becomes a tiny one, so that it leaves a masked logit at -inf
     const float sl2 = fmaxf(fabsf(p.a.softmax_scale) * kLog2e, 1e-30f);
-    const uint32_t head_bar = 2 + (quarter & 1), read_bar = 4 + (quarter & 1);   // the 128 threads of 32 heads
+    const uint32_t head_bar = 2 + (quarter & 1);   // the 128 threads of 32 heads
     __nv_bfloat16* xmax = reinterpret_cast<__nv_bfloat16*>(sm + kOffMax);
     volatile int* oks = reinterpret_cast<volatile int*>(sm + kOffOk);
     const volatile uint32_t* masks = reinterpret_cast<const volatile uint32_t*>(sm + kOffMask);
@@ -585,7 +628,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
       arrive_pair(leader_addr(&sfree[0]));
       arrive_pair(leader_addr(&sfree[1]));
     }
-    const uint32_t prow = smem_u32(sm + kOffP) + static_cast<uint32_t>(half * kAtom + hl * 128);
+    const uint32_t prow0 = smem_u32(sm + (half ? kOffP1 : kOffStage + 8 * kAtom)) + static_cast<uint32_t>(hl * 128);
+    const uint32_t pstep = half ? 0u : static_cast<uint32_t>(kStage);   // P of tile rows 0-63 takes the stage's rope atom
     float m = -INFINITY, g = -INFINITY, l = 0.f;
     bool ok = true;
 #pragma unroll 1
@@ -631,49 +675,56 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
         for (int i = 0; i < 32; i += 2) mq[(i >> 1) & 3] = fmax3(mq[(i >> 1) & 3], x[i], x[i + 1]);
         mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * sl2;
       }
-      // The four threads of a head take the largest maximum, and their warps leave together
-      // when one has given up.  There is room for one buffer: the last tile's entries have
-      // been read once all four warps have arrived on read_bar.
-      if (j >= 1) named_bar_sync(read_bar, 256);
-      const __nv_bfloat16 mxb = __float2bfloat16_ru(mx);   // a bound is enough, rounded up
-      xmax[rq * kHeads + hl] = mxb;
-      mx = __bfloat162float(mxb);
-      if (lane == 0) oks[st * 8 + warp - kWarpSoft] = ok ? 1 : 0;
-      named_bar_sync(head_bar, 128);
-#pragma unroll
-      for (int k = 1; k < 4; ++k) mx = fmaxf(mx, __bfloat162float(xmax[(rq ^ k) * kHeads + hl]));
-      // the four warps: those whose number is as odd as this one's
-#pragma unroll
-      for (int k = 0; k < 4; ++k) ok = ok && oks[st * 8 + 2 * k + (warp & 1)] != 0;
-      named_bar_arrive(read_bar, 256);
-      if (!ok) break;
-      const float gx = mx + __log2f(rmax);
-      const bool need_m = mx > m + kRescaleM, need_g = gx > g + kRescaleG;
+      // The four threads of a head share m and g, and their warps leave together when one
+      // has given up.  One barrier tells the 128 threads of 32 heads whether any of them has
+      // to let m or g grow; only then (the first tile, and seldom after) do they exchange
+      // their maxima.
+      const float lrmax = __log2f(rmax);
+      const bool grow = named_bar_or(head_bar, 128, !ok || mx > m + kRescaleM || mx + lrmax > g + kRescaleG);
       // P has one buffer and O may have to be rescaled: P V of the tile before is complete
-      if (j >= 1) ok = wait_bar(pvdone, (j - 1) & 1, abort_flag, wlim);
-      if (j >= 1 && __any_sync(0xffffffffu, need_g)) {
-        tc_fence_after();
-        const float f = need_g ? exp2f(g - gx) : 1.f;
-#pragma unroll 1
-        for (int cc = 0; cc < 8; ++cc) {   // this thread's half of the columns
-          uint32_t o[16];
-          const uint32_t at = tmem + lane_off + kColO + part32 * 128 + cc * 16;
-          tmem_ld16(at, o);
-          tmem_ld_wait();
+      bool pv_ok = true;
+      if (j >= 1 && ok) pv_ok = wait_bar(&pvdone[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, wlim);
+      if (grow) {
+        const __nv_bfloat16 mxb = __float2bfloat16_ru(mx);   // a bound is enough, rounded up
+        xmax[rq * kHeads + hl] = mxb;
+        mx = __bfloat162float(mxb);
+        if (lane == 0) oks[warp - kWarpSoft] = ok ? 1 : 0;
+        named_bar_sync(head_bar, 128);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-          tmem_st16(at, o);
+        for (int k = 1; k < 4; ++k) mx = fmaxf(mx, __bfloat162float(xmax[(rq ^ k) * kHeads + hl]));
+        // the four warps: those whose number is as odd as this one's
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ok = ok && oks[2 * k + (warp & 1)] != 0;
+        named_bar_sync(head_bar, 128);
+        if (!ok) break;
+        const float gx = mx + lrmax;
+        const bool need_m = mx > m + kRescaleM, need_g = gx > g + kRescaleG;
+        if (j >= 1 && __any_sync(0xffffffffu, need_g)) {
+          tc_fence_after();
+          const float f = need_g ? exp2f(g - gx) : 1.f;
+#pragma unroll 1
+          for (int cc = 0; cc < 8; ++cc) {   // this thread's half of the columns
+            uint32_t o[16];
+            const uint32_t at = tmem + lane_off + kColO + part32 * 128 + cc * 16;
+            tmem_ld16(at, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st16(at, o);
+          }
+          tmem_st_wait();
         }
-        tmem_st_wait();
+        if (need_g) g = gx;
+        if (need_m) {
+          l *= exp2f(m - mx);
+          m = mx;
+        }
       }
-      if (need_g) g = gx;
-      if (need_m) {
-        l *= exp2f(m - mx);
-        m = mx;
-      }
+      ok = __all_sync(0xffffffffu, pv_ok);
       const float msub = (m == -INFINITY) ? 0.f : m;
       // 2^(m - g), kept finite and nonzero
       const float gain = (g == -INFINITY) ? 1.f : exp2f(fminf(fmaxf(msub - g, -126.f), 126.f));
+      const uint32_t prow = prow0 + (j & 1) * pstep;
       float se[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -707,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
         mbar_arrive(&mfree[st]);
       }
     }
-    if (ok) ok = wait_bar(pvdone, (ntiles - 1) & 1, abort_flag, wlim);
+    if (ok) ok = wait_bar(&pvdone[(ntiles - 1) & 1], ((ntiles - 1) >> 1) & 1, abort_flag, wlim);
     ok = __all_sync(0xffffffffu, ok);
     // the sums of a head's four threads, through the row scales' space
     float* sums = reinterpret_cast<float*>(sm + kOffScale);
@@ -726,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
       const int64_t head0 = (static_cast<int64_t>(part ? split : 0) * p.seq.T + t) * H + h0 + (quarter & 1) * 32;
       uint8_t* out = reinterpret_cast<uint8_t*>(part ? p.ws_o : static_cast<uint16_t*>(p.a.out)) +
                      (head0 * kDv + half * 256 + part32 * 128) * 2;
-      const uint32_t stg = smem_u32(sm + kOffK) + (warp - kWarpSoft) * 4096;   // all MMAs are complete
+      const uint32_t stg = smem_u32(sm + kOffStage) + (warp - kWarpSoft) * 4096;   // all MMAs are complete
       if (heads > 0) {
 #pragma unroll 1
         for (int cc = 0; cc < 2; ++cc) {
@@ -772,7 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
     if (elect_one()) commit_pair(drain);
     __syncwarp();
   }
-  if (warp == kWarpQk) mbar_drain(drain, 0, &g_status_attn_e2m1, wlim);
+  if (warp == kWarpQk) mbar_drain(drain, 0, &g_status_attn_e2m1, p.wait_limit_ns);
   tc_fence_before();
   __syncwarp();
   cluster_sync();
