@@ -49,22 +49,30 @@
 //   N-wide accumulator of a pair MMA takes N/2 columns: lanes 0-63 are the CTA's heads
 //   for the first half of N, lanes 64-127 the same heads for the second.
 //
+// Work.  An item is a row slice (few queries: joined by attn_combine) of 128 heads of a
+// query; the clusters that fit the GPU at once share the items out.  Tiles are counted through a
+// cluster's items, so the next item's rows, codes and first logits are on their way during
+// the last softmax and the output (with a cluster for each item 1290 us instead of 1177).
+//
 // Warps.  0-15 producers, four own and four other rows of a tile each, whichever can go on
 // (in a fixed order the other rows wait for Q K^T of rows just written: 1496 us); codes, scales
 // and rope are loaded into registers a tile ahead, right after the registers' last use, a
 // row's whole 256 or 128 bytes by neighbouring lanes (32-byte pieces of eight rows took three
-// times as long).  16 Q K^T and 17 P V (rank 0 issues for both CTAs).  18 finds the
-// tiles' cache rows, row scales and masks, three tiles ahead.  20-27 stage the query, then softmax, a
-// thread one head and 32 of the tile's rows; the four threads of a head agree on m and g
-// through shared memory, when one of them has to let them grow.  Registers are dealt out by
-// setmaxnreg, so that no role spills: with 224 KB of shared memory taken almost nothing is left of the
-// L1, and a spilled word comes back from the L2.  The code is kept small (rolled loops,
-// short waits): with 98 KB of it every role ran from a cold instruction cache.
+// times as long).  16 Q K^T and 17 P V (rank 0 issues for both CTAs).  18 and 19 find the
+// tiles' cache rows, row scales and masks, two tiles ahead.  20-27 stage the query, then
+// softmax, a thread one head and 32 of the tile's rows; the four threads of a head agree on m
+// and g through shared memory, when one of them has to let them grow.  Registers are dealt out
+// by setmaxnreg: 224 KB of shared memory leave almost nothing of the L1, and a spilled word
+// comes back from the L2 (24 bytes are, outside the loops' chains).  The code is kept small
+// (rolled loops, short waits): with 98 KB of it every role ran from a cold instruction cache.
 //
-// Measured (2048 selected rows, 128 heads): 1287 us for 2048 queries, 908 TFLOP/s of the
-// 1926 measured; 54.9 us for 64 (one cluster a query: 128 of 152 SMs), 11.7 us for one.
+// Measured (2048 selected rows, 128 heads): 1177 us for 2048 queries, 992 TFLOP/s of the
+// 1926 measured; 54.0 us for 64 (one cluster a query: 128 of 152 SMs), 12.4 us for one (a
+// tile each for 16 clusters: latencies).  A tile takes 4300 clocks where its MMAs need 2176: they,
+// the producers' stores and the loads pass 4100 wavefronts of 128 bytes through the one pipe.
 // The 48-row kernel of attn.cu's kind, which widens every row in both CTAs: 2171, 100 and 11.7.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 
@@ -91,7 +99,7 @@ constexpr int kProducers = 16;
 constexpr int kWarpQk = 16, kWarpPv = 17, kWarpRows = 18, kWarpSoft = 20;
 constexpr int kThreads = 896;
 // registers a thread: 72 at launch (7 groups of 4 warps, 504 in all), then
-constexpr int kRegsProducer = 64, kRegsMma = 56, kRegsSoft = 96;
+constexpr int kRegsProducer = 56, kRegsMma = 72, kRegsSoft = 104;
 static_assert(4 * kRegsProducer + kRegsMma + 2 * kRegsSoft <= 7 * 72, "register split");
 
 constexpr int kOffQ = 0;
@@ -99,12 +107,13 @@ constexpr int kOffStage = kOffQ + 9 * kAtom;             // [2]
 constexpr int kOffP1 = kOffStage + 2 * kStage;           // P of tile rows 64-127
 constexpr int kOffScale = kOffP1 + kAtom;                 // float [2][128] row scales
 constexpr int kOffRows = kOffScale + 2 * kTile * 4;      // int [2][128] cache rows, -1 for none
-constexpr int kOffMax = kOffRows + 2 * kTile * 4;        // bf16 [4 row quarters][64 heads]; float [64] 2^a at first
+constexpr int kOffMax = kOffRows + 2 * kTile * 4;        // for 32 heads each: bf16 [4 row quarters][32], float [2][32]
 constexpr int kOffMask = kOffMax + 4 * kHeads * 2;       // uint32 [2][4] valid rows
-constexpr int kOffRmax = kOffMask + 32;                  // float [2] largest row scale of a tile
+constexpr int kOffRmax = kOffMask + 32;                  // float [2][2] largest row scale of a tile's halves
 constexpr int kOffOk = kOffRmax + 16;                    // int [8 softmax warps]
-constexpr int kOffBar = kOffOk + 64;
-constexpr int kNumBars = 18;
+constexpr int kOffExp = kOffOk + 32;                     // int8 [64 heads] a
+constexpr int kOffBar = kOffExp + kHeads;
+constexpr int kNumBars = 24;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;
 constexpr int kUsed = kOffMisc + 16;
 constexpr int kSmemBytes = 232448;
@@ -117,18 +126,31 @@ constexpr uint32_t kIdescLatent = make_idesc(kFmtF16, kFmtF16, false, false, 128
 constexpr uint32_t kIdescRope = make_idesc(kFmtBF16, kFmtBF16, false, false, 128, 128);
 constexpr uint32_t kIdescPV = make_idesc(kFmtF16, kFmtF16, false, true, 128, 256);
 
+// floor(n / d) for 0 <= n < 2^31 as (2 n mul) >> (32 + s): with 2^(s - 1) < d <= 2^s and mul =
+// ceil(2^(31 + s) / d) < 2^32, the error mul d - 2^(31 + s) < d <= 2^s is too small to reach the next quotient.
+struct Divisor {
+  uint32_t mul, s;
+  explicit Divisor(int64_t d) : s(0) {
+    while ((1ll << s) < d) ++s;
+    mul = static_cast<uint32_t>(((1ull << (31 + s)) + d - 1) / d);
+  }
+  __device__ __forceinline__ int operator()(int n) const {
+    return static_cast<int>(__umulhi(static_cast<uint32_t>(n) << 1, mul) >> s);
+  }
+};
+
 struct PairParams {
   SeqArgs seq;
   MlaArgs a;
   int32_t n_split;          // row slices per query
   int32_t rows_per_split;   // a multiple of kTile
   int32_t head_blocks;      // blocks of 128 heads
+  int32_t items;            // T * head_blocks * n_split, shared out among the clusters
   uint16_t* ws_o;           // [n_split, T, H, 512] bf16 partials (n_split > 1), each normalised by its own sum
   float* ws_lse;            // [n_split, T, H]
   uint64_t wait_limit_ns;
   uint32_t dbg_withhold;
-  uint32_t page_mul;        // pos / page_size = (pos * page_mul) >> page_shift for 0 <= pos < 2^31
-  uint32_t page_shift;
+  Divisor page, split, heads;   // by the page size, n_split, head_blocks
   uint32_t early_query;     // the query was complete before the kernel before this one let it launch
 };
 
@@ -138,8 +160,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // The address of `bar` in the leader CTA (rank 0) of the cluster.
 __device__ __forceinline__ uint32_t leader_addr(const uint64_t* bar) {
@@ -154,13 +179,24 @@ __device__ __forceinline__ uint32_t leader_addr(const uint64_t* bar) {
 __device__ __forceinline__ void arrive_pair(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-// Whether a wait must end: another thread of the CTA gave up, or the CTA has been running
-// for longer than the limit (which this sets the flags for).
-__device__ __noinline__ bool give_up(volatile int* abort_flag, uint64_t deadline) {
-  if (*abort_flag) return true;
-  if (globaltimer_ns() < deadline) return false;
+// Whether a wait must end (1): another thread of the CTA gave up, or the wait has been going
+// on for longer than the limit (which this sets the flags for).  Else when it must.
+__device__ __noinline__ uint64_t wait_until(volatile int* abort_flag, uint64_t until, uint64_t limit_ns) {
+  if (*abort_flag) return 1;
+  const uint64_t now = globaltimer_ns();
+  if (until == 0) return now + limit_ns;
+  if (now < until) return until;
   atomicOr(&g_status_attn_e2m1, kDevTimeout);
   *abort_flag = 1;
+  return 1;
+}
+// Bounded wait for a phase of `bar`.  Short on purpose: fourteen copies of it, and the
+// kernel's code has to stay in the instruction cache.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns) {
+  const uint32_t addr = smem_u32(bar);
+  uint64_t until = 0;
+  for (uint32_t it = 1; !mbar_try_wait(addr, parity); ++it)
+    if ((it & 63u) == 0u && (until = wait_until(abort_flag, until, limit_ns)) == 1) return false;
   return true;
 }
 // Whether a phase of `bar` is complete, without waiting.
@@ -172,14 +208,6 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
       : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   return done != 0;
-}
-// Bounded wait for a phase of `bar`.  Short on purpose: fourteen copies of it, and the
-// kernel's code has to stay in the instruction cache.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t deadline) {
-  const uint32_t addr = smem_u32(bar);
-  for (uint32_t it = 1; !mbar_try_wait(addr, parity); ++it)
-    if ((it & 63u) == 0u && give_up(abort_flag, deadline)) return false;
-  return true;
 }
 __device__ __forceinline__ void umma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                           uint32_t accumulate) {
@@ -246,10 +274,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
     return;
   }
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kOffBar);
-  uint64_t* ownfull = bars;       // leader: both CTAs' own rows written
-  uint64_t* othfull = bars + 1;   // leader: the other CTA's rows written, in both
-  uint64_t* pfull = bars + 2;     // leader: P written, both CTAs
-  uint64_t* drain = bars + 3;     // every MMA complete (teardown)
+  // Barriers in pairs belong to a tile's stage or logit buffer: nothing comes to one for the
+  // tile after next before its waiter has passed it for this one.
+  uint64_t* ownfull = bars;       // [2] leader: both CTAs' own rows written
+  uint64_t* othfull = bars + 2;   // [2] leader: the other CTA's rows written, in both
   uint64_t* pvdone = bars + 4;    // [2] P V complete: the tile's stage and P free
   uint64_t* sfree = bars + 6;     // [2] leader: logits read, both CTAs
   uint64_t* sfull = bars + 8;     // [2] Q K^T complete: logits there, half of the stage and its rope atom dead
@@ -257,69 +285,77 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
   uint64_t* mfree = bars + 12;    // [2] and read
   uint64_t* rfull = bars + 14;    // [2] cache rows of a tile written
   uint64_t* rfree = bars + 16;    // [2] and read
+  uint64_t* qstaged = bars + 18;  // this CTA's query staged
+  uint64_t* qfull = bars + 19;    // leader: both CTAs' queries staged and their a read
+  uint64_t* pfull = bars + 20;    // leader: P written, both CTAs (one buffer: P V of the tile before is complete)
+  uint64_t* drain = bars + 21;    // every MMA complete (teardown)
+  uint64_t* edone = bars + 22;    // [2] an item's output has left the stage of its last tile
   uint32_t* misc = reinterpret_cast<uint32_t*>(sm + kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
-  const uint64_t wlim = globaltimer_ns() + p.wait_limit_ns;   // no wait of this CTA goes on beyond
-
-  int item = blockIdx.x >> 1;
-  const int split = item % p.n_split;
-  item /= p.n_split;
-  const int hb = item % p.head_blocks;
-  const int t = p.seq.T - 1 - item / p.head_blocks;   // last query first (longest causal history)
+  const uint64_t wlim = p.wait_limit_ns;
   const int K = p.a.K, H = p.a.H;
-  const int r0 = split * p.rows_per_split;
-  const int r1 = min(K, r0 + p.rows_per_split);
-  const int ntiles = (r1 - r0 + kTile - 1) / kTile;
-  const int h0 = hb * 128 + static_cast<int>(rank) * kHeads;   // this CTA's first head
 
-  if (threadIdx.x == 0) {
+  // Work items, one after the other, the clusters in turn: a row slice of 128 heads of a query,
+  // the last query first (longest causal history).  Tiles, buffers and phases are counted
+  // through all of a cluster's items, so that the next item's rows and codes are fetched, its
+  // keys written and multiplied while this one's last tile is in its softmax.
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  auto slice_of = [&](int item) -> int { return item - p.split(item) * p.n_split; };
+  auto tiles_of = [&](int item) -> int {
+    const int r0 = slice_of(item) * p.rows_per_split;
+    return (min(K, r0 + p.rows_per_split) - r0 + kTile - 1) / kTile;
+  };
+  auto tiles_in_all = [&]() -> int {
+    int n = 0;   // items: one for each cluster when there are slices
+    for (int item = first; item < p.items; item += step) n += tiles_of(item);
+    return n;
+  };
+  auto query_of = [&](int item) -> int { return p.seq.T - 1 - p.heads(p.split(item)); };
+  auto head_of = [&](int item) -> int {   // this CTA's first head
+    const int i = p.split(item);
+    return (i - p.heads(i) * p.head_blocks) * 128 + static_cast<int>(rank) * kHeads;
+  };
+
+  // Warps set out as soon as they can: only what reaches the other CTA, the barriers or TMEM
+  // comes after cluster_wait.
+  if (warp == kWarpRows && lane == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sfree[i], 16);
+      mbar_init(&ownfull[i], 2 * kProducers);
+      mbar_init(&othfull[i], 2 * kProducers);
       mbar_init(&sfull[i], 1);
+      mbar_init(&edone[i], 8);
       mbar_init(&pvdone[i], 1);
-      mbar_init(&mfull[i], 1);
+      mbar_init(&mfull[i], 2);
       mbar_init(&mfree[i], 8);
-      mbar_init(&rfull[i], 1);
+      mbar_init(&rfull[i], 2);
       mbar_init(&rfree[i], kProducers);
     }
-    mbar_init(ownfull, 2 * kProducers);
-    mbar_init(othfull, 2 * kProducers);
     mbar_init(pfull, 16);
     mbar_init(drain, 2);
+    mbar_init(qstaged, 8);
+    mbar_init(qfull, 16);
     *abort_flag = 0;
     fence_mbar_init();
   }
+  __syncwarp();
   if (warp == kWarpQk) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(misc)), "r"(512u)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
-  __syncthreads();
-  cluster_sync();   // the leader's barriers and both CTAs' TMEM exist before anyone arrives or multiplies
-  tc_fence_after();
-  const uint32_t tmem = misc[0];
-
+  cluster_arrive();
   if (!p.early_query) grid_dep_wait();
-  int qp = __ldg(p.seq.q_pos + t);
-  int b = __ldg(p.seq.q_seq + t);
-  if (qp < 0 || qp >= p.seq.max_ctx || b < 0 || b >= p.seq.B) {
-    if (threadIdx.x == 0) atomicOr(&g_status_attn_e2m1, kDevBadPos);
-    qp = -1;
-    b = 0;
-  }
+
   const uint8_t* kv = static_cast<const uint8_t*>(p.a.kv);
   const uint32_t row_bytes = static_cast<uint32_t>(p.a.row_bytes);   // < 2^31, the host sees to that
-  const int32_t* bt = p.seq.block_table + static_cast<int64_t>(b) * p.seq.bt_stride;
-  const int32_t* idx = p.a.idx + static_cast<int64_t>(t) * K;
-  auto page_of = [&](int pos) -> int {   // pos / page_size
-    return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(pos)) * p.page_mul) >> p.page_shift);
-  };
-
   if (warp < kProducers) {
     // ------------------------------------------------ producers
     const int32_t* rows_sm = reinterpret_cast<const int32_t*>(sm + kOffRows);
     shrink_registers<kRegsProducer>();
+    cluster_wait();
+    const int ntiles = tiles_in_all();
     const int sub = lane >> 4, blk = lane & 15, l8 = lane >> 3, b8 = lane & 7;
     // In registers.  Own: codes of block `lane` of the warp's four own rows; scale word and
     // rope chunk b8 of row l8.  Other: codes of block blk of this CTA's value dims of rows
@@ -371,7 +407,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
     const uint32_t chunk = static_cast<uint32_t>(((2 * (lane & 3) + (flip ? 1 : 0)) << 4) ^ ((warp & 1) << 6));
     const uint32_t stage0 = smem_u32(sm + kOffStage) + static_cast<uint32_t>(warp * 512);
     const uint32_t kdst = stage0 + static_cast<uint32_t>((lane >> 2) * kAtom) + chunk;
-    const uint32_t vdst = stage0 + static_cast<uint32_t>(((rank ^ 1u) * 4 + (blk >> 2)) * kAtom + sub * 128) + (chunk ^ static_cast<uint32_t>(sub << 4));
+    const uint32_t vdst = stage0 + static_cast<uint32_t>(((rank ^ 1u) * 4 + (blk >> 2)) * kAtom + sub * 128) +
+                          (chunk ^ static_cast<uint32_t>(sub << 4));
     const uint32_t rdst = stage0 + static_cast<uint32_t>(8 * kAtom + l8 * 128 + (((b8 ^ l8) << 4) ^ ((warp & 1) << 6)));
     auto wait = [&](uint64_t* bar, int use) -> bool {
       return __all_sync(0xffffffffu, wait_bar(bar, use & 1, abort_flag, wlim));
@@ -384,8 +421,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
       rows_v(0);
       fetch_k();
       fetch_v();
-      int a = 0, b = 0;
+      // Own rows of tile a take the stage of a - 2: free once P V of that is complete or, when that
+      // was an item's last tile, once the item's output, which goes through the stage, has been
+      // written.  (A cluster has more than one item only without slices, all of one length.)
+      const int per_item = tiles_of(first);
+      int a = 0, b = 0, after_last = per_item + 1, item_n = 0;
+      auto own_free = [&](int a) -> bool {
+        if (a < 2) return true;
+        return a == after_last ? mbar_test(&edone[item_n & 1], (item_n >> 1) & 1)
+                               : mbar_test(&pvdone[a & 1], ((a >> 1) - 1) & 1);
+      };
       uint32_t idle = 0;
+      uint64_t until = 0;
 #pragma unroll 1
       while (b < ntiles) {
         if (b < a && __all_sync(0xffffffffu, mbar_test(&sfull[b & 1], (b >> 1) & 1))) {
@@ -399,10 +446,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
           for (int k = 0; k < 2; ++k) put((at ^ (2 * k << 4)) + k * 256, vcode[k], w[k], lane & 3);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) arrive_pair(leader_addr(othfull));
+          if (lane == 0) arrive_pair(leader_addr(&othfull[b & 1]));
           if (b + 1 < ntiles) fetch_v();
           ++b;
-        } else if (a < ntiles && (a < 2 || __all_sync(0xffffffffu, mbar_test(&pvdone[a & 1], ((a >> 1) - 1) & 1)))) {
+        } else if (a < ntiles && __all_sync(0xffffffffu, own_free(a))) {
           const uint32_t st = static_cast<uint32_t>((a & 1) * kStage);
           if (a + 1 < ntiles) {
             if (!wait(&rfull[(a + 1) & 1], (a + 1) >> 1)) break;
@@ -417,197 +464,209 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
           st_shared_v4(rdst + st, rope.x, rope.y, rope.z, rope.w);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0 && !(p.dbg_withhold && warp == 0 && a == 0)) arrive_pair(leader_addr(ownfull));
+          if (lane == 0 && !(p.dbg_withhold && warp == 0 && a == 0)) arrive_pair(leader_addr(&ownfull[a & 1]));
           if (a + 1 < ntiles) fetch_k();
+          if (a == after_last) {
+            after_last += per_item;
+            ++item_n;
+          }
           ++a;
         } else {
           __nanosleep(32);
-          if ((++idle & 31u) == 0u && __any_sync(0xffffffffu, give_up(abort_flag, wlim))) break;
+          if ((++idle & 31u) == 0u) {
+            until = wait_until(abort_flag, until, wlim);
+            if (__any_sync(0xffffffffu, until == 1)) break;
+          }
+          continue;
         }
+        until = 0;
       }
     }
   } else if (warp < kWarpSoft) {
     shrink_registers<kRegsMma>();
-    if (warp == kWarpRows) {
-    // ------------------------------------------------ the tiles' rows, row scales and masks
-    if (p.early_query) grid_dep_wait();   // the selected indices come from the kernel before
-    // Tile row 32 k + lane, k = 0..3.  A selected entry's way to its row, a tile's time between
-    // the steps: the position, its page id, the cache row, the row's scale.
-    int pos[4], pos1[4], page[4], row[4], row1[4];
-    float rs[4], rs1[4];
-    auto load_pos = [&](int j) {
+    if (warp >= kWarpRows) {
+      // ------------------------------------------------ the tiles' rows, row scales and masks
+      if (p.early_query) grid_dep_wait();   // the selected indices come from the kernel before
+      // Tile row 32 k + lane from wrow on, k = 0, 1.  A selected entry's way to its row, a tile's time between
+      // the steps: the position, its page id, the cache row, the row's scale.
+      int pos[2], pos1[2], page[2], row1[2];
+      float rs1[2];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int gi = r0 + j * kTile + k * 32 + lane;
-        pos1[k] = j < ntiles && gi < r1 ? __ldg(idx + gi) : -1;
-      }
-    };
-    auto load_page = [&]() {   // of pos <- pos1
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        pos[k] = pos1[k];
-        if (pos[k] > qp) {
-          atomicOr(&g_status_attn_e2m1, kDevBadIndex);
-          pos[k] = -1;
+      for (int k = 0; k < 2; ++k) pos[k] = pos1[k] = page[k] = row1[k] = -1;
+      // the tile that load_pos comes to next: its item and its number there; the query's position
+      // and sequence go with the tile from step to step
+      int item = first, gi0 = 0, gi1 = 0, qp1 = 0, b1 = 0;   // entries [gi0, gi1) of the item are left
+      const int32_t* idx = nullptr;
+      uint32_t bad = 0;
+      const int wrow = (warp - kWarpRows) * 64;
+      auto load_pos = [&]() {
+        if (gi0 >= gi1 && item < p.items) {
+          const int t = query_of(item);
+          gi0 = slice_of(item) * p.rows_per_split;
+          gi1 = min(K, gi0 + p.rows_per_split);
+          idx = p.a.idx + static_cast<int64_t>(t) * K;
+          qp1 = __ldg(p.seq.q_pos + t);
+          b1 = __ldg(p.seq.q_seq + t);
+          item += step;
         }
-        page[k] = pos[k] >= 0 ? __ldg(bt + page_of(pos[k])) : -1;
-      }
-    };
-    auto load_scale = [&]() {   // row1, rs1 of pos, page
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const bool good = page[k] >= 0 && page[k] < p.seq.n_pages;
-        if (pos[k] >= 0 && !good) atomicOr(&g_status_attn_e2m1, kDevBadIndex);
-        row1[k] = good ? (page[k] - page_of(pos[k])) * p.seq.page_size + pos[k] : -1;   // < cache_rows < 2^31
-        const uint8_t* rp = kv + static_cast<uint64_t>(static_cast<uint32_t>(max(row1[k], 0))) * row_bytes;
-        rs1[k] = __ldg(reinterpret_cast<const float*>(rp + kE2m1RowScale));
-      }
-    };
-    // steps -3, -2, -1 only load
+        for (int k = 0; k < 2; ++k) {
+          const int i = gi0 + wrow + k * 32 + lane;
+          pos1[k] = i < gi1 ? __ldg(idx + i) : -1;
+        }
+        gi0 += kTile;
+      };
+      auto load_page = [&]() {   // of pos <- pos1
+        int qp = qp1, b = b1;
+        if (qp < 0 || qp >= p.seq.max_ctx || b < 0 || b >= p.seq.B) {
+          bad |= kDevBadPos;
+          qp = -1;
+          b = 0;
+        }
+        const int32_t* bt = p.seq.block_table + static_cast<int64_t>(b) * p.seq.bt_stride;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          pos[k] = pos1[k];
+          if (pos[k] > qp) {
+            bad |= kDevBadIndex;
+            pos[k] = -1;
+          }
+          page[k] = pos[k] >= 0 ? __ldg(bt + p.page(pos[k])) : -1;
+        }
+      };
+      auto load_scale = [&]() {   // row1, rs1 of pos, page
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const bool good = page[k] >= 0 && page[k] < p.seq.n_pages;
+          if (pos[k] >= 0 && !good) bad |= kDevBadIndex;
+          row1[k] = good ? (page[k] - p.page(pos[k])) * p.seq.page_size + pos[k] : -1;   // < cache_rows < 2^31
+          const uint8_t* rp = kv + static_cast<uint64_t>(static_cast<uint32_t>(max(row1[k], 0))) * row_bytes;
+          rs1[k] = __ldg(reinterpret_cast<const float*>(rp + kE2m1RowScale));
+        }
+      };
+      // step j: scales and mask of tile j - 1 and rows of tile j given out, pages of j + 1 and
+      // positions of j + 2 loaded; step -1 only loads
+      load_pos();
+      const int todo = tiles_in_all();
 #pragma unroll 1
-    for (int j = -3; j < ntiles; ++j) {
-      if (j >= 0) {
+      for (int j = -1; j <= todo; ++j) {
+        asm volatile("" : "+r"(j));   // one copy of the loop's code
+        if (j == 0) cluster_wait();
         const int st = j & 1;
-        bool ok = j < 2 || wait_bar(&rfree[st], ((j >> 1) - 1) & 1, abort_flag, wlim);
-        if (!__all_sync(0xffffffffu, ok)) break;
+        if (j >= 1) {
+          if (j >= 3 &&
+              !__all_sync(0xffffffffu, wait_bar(&mfree[st ^ 1], (((j - 1) >> 1) - 1) & 1, abort_flag, wlim)))
+            break;
+          float rmax = 0.f;
+          uint32_t mask[2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          row[k] = row1[k];
-          rs[k] = rs1[k];
-          reinterpret_cast<int32_t*>(sm + kOffRows)[st * kTile + k * 32 + lane] = row[k];
+          for (int k = 0; k < 2; ++k) {
+            const float mine = row1[k] >= 0 ? rs1[k] : 0.f;
+            rmax = fmaxf(rmax, mine);
+            mask[k] = __ballot_sync(0xffffffffu, row1[k] >= 0);
+            reinterpret_cast<float*>(sm + kOffScale)[(st ^ 1) * kTile + wrow + k * 32 + lane] = mine;
+          }
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) rmax = fmaxf(rmax, __shfl_xor_sync(0xffffffffu, rmax, o));
+          if (lane == 0) {
+            *reinterpret_cast<uint2*>(sm + kOffMask + (st ^ 1) * 16 + wrow / 8) = make_uint2(mask[0], mask[1]);
+            reinterpret_cast<float*>(sm + kOffRmax)[(st ^ 1) * 2 + wrow / 64] = rmax;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&mfull[st ^ 1]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&rfull[st]);
+        if (j >= 0 && j < todo) {
+          if (j >= 2 && !__all_sync(0xffffffffu, wait_bar(&rfree[st], ((j >> 1) - 1) & 1, abort_flag, wlim))) break;
+          load_scale();
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            reinterpret_cast<int32_t*>(sm + kOffRows)[st * kTile + wrow + k * 32 + lane] = row1[k];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&rfull[st]);
+        }
+        load_page();
+        load_pos();
       }
-      if (j >= -1) load_scale();
-      if (j >= -2) load_page();
-      load_pos(j + 3);
-      if (j >= 0) {
-        const int st = j & 1;
-        bool ok = j < 2 || wait_bar(&mfree[st], ((j >> 1) - 1) & 1, abort_flag, wlim);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        float rmax = 0.f;
-        uint32_t mask[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float mine = row[k] >= 0 ? rs[k] : 0.f;
-          rmax = fmaxf(rmax, mine);
-          mask[k] = __ballot_sync(0xffffffffu, row[k] >= 0);
-          reinterpret_cast<float*>(sm + kOffScale)[st * kTile + k * 32 + lane] = mine;
-        }
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) rmax = fmaxf(rmax, __shfl_xor_sync(0xffffffffu, rmax, o));
-        if (lane == 0) {
-          *reinterpret_cast<uint4*>(sm + kOffMask + st * 16) = make_uint4(mask[0], mask[1], mask[2], mask[3]);
-          reinterpret_cast<float*>(sm + kOffRmax)[st] = rmax;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&mfull[st]);
-      }
-    }
+      if (bad) atomicOr(&g_status_attn_e2m1, bad);
     } else if (warp == kWarpQk) {
-    if (rank == 0) {
+      cluster_wait();
+      tc_fence_after();
+      const uint32_t tmem = misc[0];
       const uint64_t dq = make_sdesc(smem_u32(sm + kOffQ), 16, 1024, kLayoutSw128);
       const uint64_t dk0 = make_sdesc(smem_u32(sm + kOffStage), 16, 1024, kLayoutSw128);
-      for (int j = 0; j < ntiles; ++j) {
-        const int sb = j & 1;
-        // the logit buffer is free (the first phase: the queries are staged) and the keys are there
-        if (!__all_sync(0xffffffffu, wait_bar(&sfree[sb], (j >> 1) & 1, abort_flag, wlim))) break;
-        if (!__all_sync(0xffffffffu, wait_bar(ownfull, j & 1, abort_flag, wlim))) break;
-        tc_fence_after();
-        fence_proxy_async_smem();
-        if (elect_one()) {
-          const uint32_t d = tmem + sb * 64;
-          const uint64_t dk = dk0 + static_cast<uint64_t>((sb * kStage) >> 4);
+      int g = 0, n = 0;   // tiles, items
+      bool ok = rank == 0;
 #pragma unroll 1
-          for (int a = 0; a < 8; ++a) {   // 64 dims a turn
-            const uint64_t off = static_cast<uint64_t>((a * kAtom) >> 4);
+      for (int item = first; item < p.items && ok; item += step, ++n) {
+        ok = __all_sync(0xffffffffu, wait_bar(qfull, n & 1, abort_flag, wlim));
+        const int end = g + tiles_of(item);
+#pragma unroll 1
+        for (; g < end && ok; ++g) {
+          const int sb = g & 1;
+          // the logit buffer is free and the keys are there
+          if (g >= 2) ok = __all_sync(0xffffffffu, wait_bar(&sfree[sb], ((g >> 1) - 1) & 1, abort_flag, wlim));
+          if (ok) ok = __all_sync(0xffffffffu, wait_bar(&ownfull[sb], (g >> 1) & 1, abort_flag, wlim));
+          if (!ok) break;
+          tc_fence_after();
+          fence_proxy_async_smem();
+          if (elect_one()) {
+            const uint32_t d = tmem + sb * 64;
+            const uint64_t dk = dk0 + static_cast<uint64_t>((sb * kStage) >> 4);
+#pragma unroll 1
+            for (int a = 0; a < 8; ++a) {   // 64 dims a turn
+              const uint64_t off = static_cast<uint64_t>((a * kAtom) >> 4);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_pair(d, dq + off + 2 * kk, dk + off + 2 * kk, kIdescLatent, static_cast<uint32_t>(a | kk));
+            }
+            constexpr uint64_t off = (8 * kAtom) >> 4;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              umma_pair(d, dq + off + 2 * kk, dk + off + 2 * kk, kIdescLatent, static_cast<uint32_t>(a | kk));
+              umma_pair(d + kColRope, dq + off + 2 * kk, dk + off + 2 * kk, kIdescRope, static_cast<uint32_t>(kk));
+            commit_pair(&sfull[sb]);
           }
-          constexpr uint64_t off = (8 * kAtom) >> 4;
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_pair(d + kColRope, dq + off + 2 * kk, dk + off + 2 * kk, kIdescRope, static_cast<uint32_t>(kk));
-          commit_pair(&sfull[sb]);
+          __syncwarp();
         }
-        __syncwarp();
       }
-    }
     } else if (warp == kWarpPv) {
-    if (rank == 0) {
+      cluster_wait();
+      tc_fence_after();
+      const uint32_t tmem = misc[0];
       const uint64_t dv0 = make_sdesc(smem_u32(sm + kOffStage), kAtom, 1024, kLayoutSw128);
       const uint64_t dp0 = make_sdesc(smem_u32(sm + kOffStage + 8 * kAtom), 16, 1024, kLayoutSw128);
       const uint64_t dp1 = make_sdesc(smem_u32(sm + kOffP1), 16, 1024, kLayoutSw128);
-      for (int j = 0; j < ntiles; ++j) {
-        if (!__all_sync(0xffffffffu, wait_bar(othfull, j & 1, abort_flag, wlim))) break;
-        if (!__all_sync(0xffffffffu, wait_bar(pfull, j & 1, abort_flag, wlim))) break;
-        tc_fence_after();
-        fence_proxy_async_smem();
-        if (elect_one()) {
+      int g = 0;
+      bool ok = rank == 0;
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {   // value atoms 2 (q / 2), tile rows [64 (q & 1), 64 (q & 1) + 64)
-            const uint64_t st = static_cast<uint64_t>(((j & 1) * kStage) >> 4);
-            const uint64_t da = (q & 1) ? dp1 : dp0 + st;
-            const uint64_t db = dv0 + st + static_cast<uint64_t>((((q & 1) * 4 + (q >> 1) * 2) * kAtom) >> 4);
+      for (int item = first; item < p.items && ok; item += step) {
+        const int begin = g, end = g + tiles_of(item);
+#pragma unroll 1
+        for (; g < end && ok; ++g) {
+          ok = __all_sync(0xffffffffu, wait_bar(&othfull[g & 1], (g >> 1) & 1, abort_flag, wlim));
+          if (ok) ok = __all_sync(0xffffffffu, wait_bar(pfull, g & 1, abort_flag, wlim));
+          if (!ok) break;
+          tc_fence_after();
+          fence_proxy_async_smem();
+          if (elect_one()) {
+            const uint64_t st = static_cast<uint64_t>(((g & 1) * kStage) >> 4);
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {   // value atoms 2 (q / 2), tile rows [64 (q & 1), 64 (q & 1) + 64)
+              const uint64_t da = (q & 1) ? dp1 : dp0 + st;
+              const uint64_t db = dv0 + st + static_cast<uint64_t>((((q & 1) * 4 + (q >> 1) * 2) * kAtom) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_pair(tmem + kColO + (q >> 1) * 128, da + 2 * kk, db + 128 * kk, kIdescPV,
-                        static_cast<uint32_t>(j | (q & 1) | kk));
+              for (int kk = 0; kk < 4; ++kk)
+                umma_pair(tmem + kColO + (q >> 1) * 128, da + 2 * kk, db + 128 * kk, kIdescPV,
+                          static_cast<uint32_t>((g - begin) | (q & 1) | kk));
+            }
+            commit_pair(&pvdone[g & 1]);
           }
-          commit_pair(&pvdone[j & 1]);
+          __syncwarp();
         }
-        __syncwarp();
       }
-    }
     }
   } else {
     // ------------------------------------------------ softmax and epilogue
     grow_registers<kRegsSoft>();
-    // The query: eight heads a warp, four at a time, eight lanes a head, lane c of them chunk c
-    // of every atom.  The latent part becomes f16 with its own power of two per head.
-#pragma unroll 1
-    for (int h4 = 0; h4 < 2; ++h4) {
-    const int hl = (warp - kWarpSoft) * 8 + h4 * 4 + (lane >> 3), c = lane & 7;
-    const bool have = h0 + hl < H;
-    const uint4* qg = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.a.q) +
-                                                     (static_cast<int64_t>(t) * H + h0 + hl) * kDqk) + c;
-    uint4 v[9];
-#pragma unroll
-    for (int a = 0; a < 9; ++a) v[a] = have ? __ldg(qg + 8 * a) : make_uint4(0u, 0u, 0u, 0u);
-    __nv_bfloat162 mx = __float2bfloat162_rn(0.f);
-#pragma unroll
-    for (int a = 0; a < 8; ++a) {
-      const uint32_t w[4] = {v[a].x, v[a].y, v[a].z, v[a].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) mx = __hmax2(mx, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
-    }
-    float amax = fmaxf(__low2float(mx), __high2float(mx));
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const int e = amax > 0.f ? max(-110, min(113, ilogbf(amax) - 14)) : 0;
-    // the maximum is taken over unscaled logits: a negative scale turns the query round
-    const bool negate = p.a.softmax_scale < 0.f;
-    const float f = ldexpf(negate ? -1.f : 1.f, -e);
-    const uint32_t flip = negate ? 0x80008000u : 0u;
-    if (c == 0) reinterpret_cast<float*>(sm + kOffMax)[hl] = ldexpf(1.f, e);
-    const uint32_t dst = smem_u32(sm + kOffQ) + static_cast<uint32_t>(hl * 128 + ((c ^ (hl & 7)) << 4));
-#pragma unroll
-    for (int a = 0; a < 8; ++a) {
-      const uint32_t w[4] = {v[a].x, v[a].y, v[a].z, v[a].w};
-      uint32_t o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __half2 q2 = __floats2half2_rn(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xFFFF0000u) * f);
-        o[i] = *reinterpret_cast<const uint32_t*>(&q2);
-      }
-      st_shared_v4(dst + static_cast<uint32_t>(a * kAtom), o[0], o[1], o[2], o[3]);
-    }
-    st_shared_v4(dst + static_cast<uint32_t>(8 * kAtom), v[8].x ^ flip, v[8].y ^ flip, v[8].z ^ flip, v[8].w ^ flip);
-    }
-    fence_proxy_async_smem();
-    named_bar_sync(1, 256);
     const int quarter = warp & 3;
     const int hl = (quarter & 1) * 32 + lane;   // head within the CTA
     const int half = quarter >> 1;              // tile rows [64 half, 64 half + 64), of which
@@ -617,203 +676,312 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
     // a scale of 0 becomes a tiny one, so that it leaves a masked logit at -inf
     const float sl2 = fmaxf(fabsf(p.a.softmax_scale) * kLog2e, 1e-30f);
     const uint32_t head_bar = 2 + (quarter & 1);   // the 128 threads of 32 heads
-    __nv_bfloat16* xmax = reinterpret_cast<__nv_bfloat16*>(sm + kOffMax);
+    // the space in which the four threads of a head exchange maxima (xmax) and sums
+    uint8_t* exchange = sm + kOffMax + (quarter & 1) * 256;
+    __nv_bfloat16* xmax = reinterpret_cast<__nv_bfloat16*>(exchange) + lane;
     volatile int* oks = reinterpret_cast<volatile int*>(sm + kOffOk);
     const volatile uint32_t* masks = reinterpret_cast<const volatile uint32_t*>(sm + kOffMask);
-    const float qexp = reinterpret_cast<const float*>(sm + kOffMax)[hl];
-    // The leader multiplies once both CTAs' queries are there and their 2^a have been read:
-    // these warps' first arrivals on sfree say so
-    __syncwarp();
-    if (lane == 0) {
-      arrive_pair(leader_addr(&sfree[0]));
-      arrive_pair(leader_addr(&sfree[1]));
-    }
     const uint32_t prow0 = smem_u32(sm + (half ? kOffP1 : kOffStage + 8 * kAtom)) + static_cast<uint32_t>(hl * 128);
-    const uint32_t pstep = half ? 0u : static_cast<uint32_t>(kStage);   // P of tile rows 0-63 takes the stage's rope atom
-    float m = -INFINITY, g = -INFINITY, l = 0.f;
-    bool ok = true;
+    const uint32_t pstep = half ? 0u : static_cast<uint32_t>(kStage);   // rows 0-63: the stage's rope atom
+    // The query: eight heads a warp, copied as they are and, the latent part, turned in place
+    // into f16 with a power of two per head.  Loops, not straight code: this runs once an item, from
+    // a cold instruction cache.
+    const uint32_t qsm = smem_u32(sm + kOffQ);
+    auto stage_query = [&](int item) {
+      const int t = query_of(item), h0 = head_of(item), w8 = (warp - kWarpSoft) * 8;
+      const uint4* qg = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.a.q) +
+                                                       (static_cast<int64_t>(t) * H + h0 + w8) * kDqk);
 #pragma unroll 1
-    for (int j = 0; j < ntiles; ++j) {
-      const int st = j & 1;
-      ok = wait_bar(&mfull[st], (j >> 1) & 1, abort_flag, wlim) && wait_bar(&sfull[st], (j >> 1) & 1, abort_flag, wlim);
-      ok = __all_sync(0xffffffffu, ok);
-      tc_fence_after();
-      const uint32_t scales = smem_u32(sm + kOffScale) + static_cast<uint32_t>((st * kTile + rq * 32) * 4);
-      float x[32];
-      float mx = -INFINITY, rmax = 0.f;
-      if (ok) {
-        // x = latent * 2^a * row scale + rope, -inf for rows that select nothing
-        uint32_t s0[32];
-        tmem_ld32(tmem + lane_off + st * 64 + part32 * 32, s0);
-        {
-          uint32_t s1[32];
-          tmem_ld32(tmem + lane_off + kColRope + st * 64 + part32 * 32, s1);
-          tmem_ld_wait();
+      for (int h = 0; h < 8; ++h, qg += kDqk / 8) {
+        const uint32_t have = h0 + w8 + h < H ? 16u : 0u;   // else zeros
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(s1[i]);
+        for (int k = 0; k < 3; ++k) {
+          const int c = lane + 32 * k;   // chunk c & 7 of atom c / 8
+          const uint32_t dst = qsm + static_cast<uint32_t>((c >> 3) * kAtom + (w8 + h) * 128 + (((c ^ h) & 7) << 4));
+          if (k < 2 || lane < 8)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+                         "l"(have ? qg + c : static_cast<const uint4*>(p.a.q)), "r"(have)
+                         : "memory");
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_pair(leader_addr(&sfree[st]));   // the logit buffer has been read
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const uint4 rs = ld_shared_v4(scales + static_cast<uint32_t>(i * 4));
-          float t0, t1, t2, t3;
-          mul2(t0, t1, __uint_as_float(s0[i]), __uint_as_float(s0[i + 1]), qexp, qexp);
-          mul2(t2, t3, __uint_as_float(s0[i + 2]), __uint_as_float(s0[i + 3]), qexp, qexp);
-          fma2(x[i], x[i + 1], t0, t1, __uint_as_float(rs.x), __uint_as_float(rs.y));
-          fma2(x[i + 2], x[i + 3], t2, t3, __uint_as_float(rs.z), __uint_as_float(rs.w));
-        }
-        const uint32_t vmask = masks[st * 4 + rq];
-        if (vmask != ~0u) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = ((vmask >> i) & 1u) ? x[i] : -INFINITY;
-        }
-        rmax = reinterpret_cast<const volatile float*>(sm + kOffRmax)[st];
-        float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) mq[(i >> 1) & 3] = fmax3(mq[(i >> 1) & 3], x[i], x[i + 1]);
-        mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * sl2;
       }
-      // The four threads of a head share m and g, and their warps leave together when one
-      // has given up.  One barrier tells the 128 threads of 32 heads whether any of them has
-      // to let m or g grow; only then (the first tile, and seldom after) do they exchange
-      // their maxima.
-      const float lrmax = __log2f(rmax);
-      const bool grow = named_bar_or(head_bar, 128, !ok || mx > m + kRescaleM || mx + lrmax > g + kRescaleG);
-      // P has one buffer and O may have to be rescaled: P V of the tile before is complete
-      bool pv_ok = true;
-      if (j >= 1 && ok) pv_ok = wait_bar(&pvdone[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, wlim);
-      if (grow) {
-        const __nv_bfloat16 mxb = __float2bfloat16_ru(mx);   // a bound is enough, rounded up
-        xmax[rq * kHeads + hl] = mxb;
-        mx = __bfloat162float(mxb);
-        if (lane == 0) oks[warp - kWarpSoft] = ok ? 1 : 0;
-        named_bar_sync(head_bar, 128);
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+      // head lane & 7, atoms 2 (lane / 8) and the next
+      const int h = lane & 7;
+      const uint32_t at = qsm + static_cast<uint32_t>((lane >> 3) * 2 * kAtom + (w8 + h) * 128);
+      auto chunk_at = [&](int c) { return static_cast<uint32_t>((c >> 3) * kAtom + (((c ^ h) & 7) << 4)); };
+      __nv_bfloat162 mx = __float2bfloat162_rn(0.f);
+#pragma unroll 4
+      for (int c = 0; c < 16; ++c) {
+        const uint4 v = ld_shared_v4(at + chunk_at(c));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int k = 1; k < 4; ++k) mx = fmaxf(mx, __bfloat162float(xmax[(rq ^ k) * kHeads + hl]));
-        // the four warps: those whose number is as odd as this one's
-#pragma unroll
-        for (int k = 0; k < 4; ++k) ok = ok && oks[2 * k + (warp & 1)] != 0;
-        named_bar_sync(head_bar, 128);
-        if (!ok) break;
-        const float gx = mx + lrmax;
-        const bool need_m = mx > m + kRescaleM, need_g = gx > g + kRescaleG;
-        if (j >= 1 && __any_sync(0xffffffffu, need_g)) {
-          tc_fence_after();
-          const float f = need_g ? exp2f(g - gx) : 1.f;
+        for (int i = 0; i < 4; ++i) mx = __hmax2(mx, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
+      }
+      float amax = fmaxf(__low2float(mx), __high2float(mx));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 8));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 16));
+      // floor(log2 amax) - 14 from the exponent's bits; a subnormal maximum is small enough for the clamp
+      const int e = amax > 0.f ? max(-110, min(113, static_cast<int>(__float_as_uint(amax) >> 23) - 141)) : 0;
+      // the maximum is taken over unscaled logits: a negative scale turns the query round
+      const uint32_t flip = p.a.softmax_scale < 0.f ? 0x80008000u : 0u;
+      const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23 | (flip & 0x80000000u));   // +-2^-e
+      if (lane < 8) reinterpret_cast<int8_t*>(sm + kOffExp)[w8 + h] = static_cast<int8_t>(e);
 #pragma unroll 1
-          for (int cc = 0; cc < 8; ++cc) {   // this thread's half of the columns
-            uint32_t o[16];
-            const uint32_t at = tmem + lane_off + kColO + part32 * 128 + cc * 16;
-            tmem_ld16(at, o);
+      for (int c4 = 0; c4 < 16; c4 += 8) {   // eight loads, then eight stores
+        uint4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = ld_shared_v4(at + chunk_at(c4 + k));
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+          uint32_t o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const __half2 q2 =
+                __floats2half2_rn(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xFFFF0000u) * f);
+            o[i] = *reinterpret_cast<const uint32_t*>(&q2);
+          }
+          st_shared_v4(at + chunk_at(c4 + k), o[0], o[1], o[2], o[3]);
+        }
+      }
+      if (flip) {   // the rope part: chunks lane / 8 and that plus four of the eight
+#pragma unroll 1
+        for (int c = lane >> 3; c < 8; c += 4) {
+          const uint32_t a = qsm + static_cast<uint32_t>(8 * kAtom + (w8 + h) * 128 + ((c ^ h) << 4));
+          const uint4 v = ld_shared_v4(a);
+          st_shared_v4(a, v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+    };
+    // Tells the CTA's softmax warps that the query is staged, waits for all of them, fetches this
+    // thread's 2^a and lets the leader multiply.
+    auto query_exp = [&](int n, bool& ok) -> float {
+      if (lane == 0) mbar_arrive(qstaged);
+      ok = __all_sync(0xffffffffu, wait_bar(qstaged, n & 1, abort_flag, wlim)) && ok;
+      const int e = reinterpret_cast<const volatile int8_t*>(sm + kOffExp)[hl];
+      const float f = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+      __syncwarp();
+      if (lane == 0) arrive_pair(leader_addr(qfull));
+      return f;
+    };
+    // Turn by turn: the next item's query is staged (Q K^T of the last tile is complete), the
+    // last item's output written, the next item's tiles taken.
+    uint32_t tmem = 0;
+    bool ok = true;
+    float m = -INFINITY, g = -INFINITY, l = 0.f, qexp = 0.f;
+    int gt = 0, n = 0, done = 0;   // tiles, items staged and done
+#pragma unroll 1
+    for (int item = first;; item += step) {
+      const bool more = item < p.items;
+      if (more) {
+        stage_query(item);
+        if (item == first) {
+          cluster_wait();
+          tc_fence_after();
+          tmem = misc[0] + lane_off;
+        }
+        qexp = query_exp(n++, ok);
+      }
+      if (item != first) {
+        const int last = item - step;
+        ok = __all_sync(0xffffffffu, ok && wait_bar(&pvdone[(gt - 1) & 1], ((gt - 1) >> 1) & 1, abort_flag, wlim));
+        // the sums of a head's four threads
+        float* sums = reinterpret_cast<float*>(exchange) + lane;
+        if (rq >= 2) sums[(rq - 2) * 32] = l;
+        named_bar_sync(head_bar, 128);
+        if (rq < 2) sums[rq * 32] += l;
+        named_bar_sync(head_bar, 128);
+        l = sums[0] + sums[32];
+        if (ok) {
+          tc_fence_after();
+          // O holds sum p rs 2^(m - g) v over l = sum p
+          const float inv = l > 0.f ? exp2f(fminf(fmaxf(g - m, -126.f), 126.f)) / l : 0.f;
+          const float lse = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+          const int t = query_of(last), h0 = head_of(last);
+          const int heads = min(32, H - (h0 + (quarter & 1) * 32));   // of this warp's 32 that exist
+          const bool part = p.n_split > 1;
+          const int64_t head0 =
+              (static_cast<int64_t>(part ? slice_of(last) : 0) * p.seq.T + t) * H + h0 + (quarter & 1) * 32;
+          uint8_t* out = reinterpret_cast<uint8_t*>(part ? p.ws_o : static_cast<uint16_t*>(p.a.out)) +
+                         (head0 * kDv + half * 256 + part32 * 128) * 2;
+          // through the last tile's stage, which P V has left and the producers leave alone till edone:
+          // a thread holds one head's values, and neighbouring lanes should store a head's
+          const uint32_t stg = smem_u32(sm + kOffStage) + ((gt - 1) & 1) * kStage + (warp - kWarpSoft) * 4096;
+          if (heads > 0) {
+#pragma unroll 1
+            for (int cc = 0; cc < 2; ++cc) {
+#pragma unroll 1
+              for (int hf = 0; hf < 2; ++hf) {
+                uint32_t o[32];
+                tmem_ld32(tmem + kColO + part32 * 128 + cc * 64 + hf * 32, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  st_shared_v4(stg + lane * 128 + (((hf * 4 + k) ^ (lane & 7)) << 4),
+                               pack_bf16x2(__uint_as_float(o[8 * k]) * inv, __uint_as_float(o[8 * k + 1]) * inv),
+                               pack_bf16x2(__uint_as_float(o[8 * k + 2]) * inv, __uint_as_float(o[8 * k + 3]) * inv),
+                               pack_bf16x2(__uint_as_float(o[8 * k + 4]) * inv, __uint_as_float(o[8 * k + 5]) * inv),
+                               pack_bf16x2(__uint_as_float(o[8 * k + 6]) * inv, __uint_as_float(o[8 * k + 7]) * inv));
+              }
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int row = i * 4 + (lane >> 3), c4 = lane & 7;
+                const uint4 v = ld_shared_v4(stg + row * 128 + ((c4 ^ (row & 7)) << 4));
+                if (row < heads)
+                  *reinterpret_cast<uint4*>(out + static_cast<int64_t>(row) * kDv * 2 + cc * 128 + c4 * 16) = v;
+              }
+              __syncwarp();
+            }
+            if (rq == 0 && lane < heads) {
+              if (part)
+                p.ws_lse[head0 + lane] = lse;
+              else if (p.a.lse)
+                p.a.lse[head0 + lane] = lse;
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&edone[done++ & 1]);
+      }
+      if (!more) break;
+      const int end = gt + tiles_of(item);
+      m = g = -INFINITY;
+      l = 0.f;
+#pragma unroll 1
+      for (; gt < end; ++gt) {
+        const int j = gt, st = j & 1;
+        ok = ok && wait_bar(&mfull[st], (j >> 1) & 1, abort_flag, wlim) &&
+             wait_bar(&sfull[st], (j >> 1) & 1, abort_flag, wlim);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+        const uint32_t scales = smem_u32(sm + kOffScale) + static_cast<uint32_t>((st * kTile + rq * 32) * 4);
+        float x[32];
+        float mx = -INFINITY, rmax = 0.f;
+        if (ok) {
+          // x = latent * 2^a * row scale + rope, -inf for rows that select nothing
+          uint32_t s0[32];
+          tmem_ld32(tmem + st * 64 + part32 * 32, s0);
+          {
+            uint32_t s1[32];
+            tmem_ld32(tmem + kColRope + st * 64 + part32 * 32, s1);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tmem_st16(at, o);
+            for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(s1[i]);
           }
-          tmem_st_wait();
-        }
-        if (need_g) g = gx;
-        if (need_m) {
-          l *= exp2f(m - mx);
-          m = mx;
-        }
-      }
-      ok = __all_sync(0xffffffffu, pv_ok);
-      const float msub = (m == -INFINITY) ? 0.f : m;
-      // 2^(m - g), kept finite and nonzero
-      const float gain = (g == -INFINITY) ? 1.f : exp2f(fminf(fmaxf(msub - g, -126.f), 126.f));
-      const uint32_t prow = prow0 + (j & 1) * pstep;
-      float se[4] = {0.f, 0.f, 0.f, 0.f};
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_pair(leader_addr(&sfree[st]));   // the logit buffer has been read
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t pk[4];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int i = 8 * c + 4 * q;
-          const uint4 rs = ld_shared_v4(scales + static_cast<uint32_t>(i * 4));
-          const float r[4] = {__uint_as_float(rs.x), __uint_as_float(rs.y), __uint_as_float(rs.z), __uint_as_float(rs.w)};
-#pragma unroll
-          for (int k = 0; k < 4; k += 2) {
-            float d0 = -msub, d1 = -msub;
-            fma2(d0, d1, x[i + k], x[i + k + 1], sl2, sl2);
-            const float p0 = fast_exp2(d0), p1 = fast_exp2(d1);
-            add2(se[k], se[k + 1], se[k], se[k + 1], p0, p1);
-            float w0, w1;
-            mul2(w0, w1, p0, p1, gain, gain);
-            mul2(w0, w1, w0, w1, r[k], r[k + 1]);
-            const __half2 h = __floats2half2_rn(w0, w1);
-            pk[2 * q + (k >> 1)] = *reinterpret_cast<const uint32_t*>(&h);
+          for (int i = 0; i < 32; i += 4) {
+            const uint4 rs = ld_shared_v4(scales + static_cast<uint32_t>(i * 4));
+            float t0, t1, t2, t3;
+            mul2(t0, t1, __uint_as_float(s0[i]), __uint_as_float(s0[i + 1]), qexp, qexp);
+            mul2(t2, t3, __uint_as_float(s0[i + 2]), __uint_as_float(s0[i + 3]), qexp, qexp);
+            fma2(x[i], x[i + 1], t0, t1, __uint_as_float(rs.x), __uint_as_float(rs.y));
+            fma2(x[i + 2], x[i + 3], t2, t3, __uint_as_float(rs.z), __uint_as_float(rs.w));
           }
-        }
-        st_shared_v4(prow + static_cast<uint32_t>(((part32 * 4 + c) ^ (hl & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
-      }
-      l += (se[0] + se[1]) + (se[2] + se[3]);
-      fence_proxy_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        arrive_pair(leader_addr(pfull));
-        mbar_arrive(&mfree[st]);
-      }
-    }
-    if (ok) ok = wait_bar(&pvdone[(ntiles - 1) & 1], ((ntiles - 1) >> 1) & 1, abort_flag, wlim);
-    ok = __all_sync(0xffffffffu, ok);
-    // the sums of a head's four threads, through the row scales' space
-    float* sums = reinterpret_cast<float*>(sm + kOffScale);
-    named_bar_sync(head_bar, 128);
-    sums[rq * kHeads + hl] = l;
-    named_bar_sync(head_bar, 128);
+          const uint32_t vmask = masks[st * 4 + rq];
+          if (vmask != ~0u) {
 #pragma unroll
-    for (int k = 1; k < 4; ++k) l += sums[(rq ^ k) * kHeads + hl];
-    if (ok) {
-      tc_fence_after();
-      // O holds sum p rs 2^(m - g) v over l = sum p
-      const float inv = l > 0.f ? exp2f(fminf(fmaxf(g - m, -126.f), 126.f)) / l : 0.f;
-      const float lse = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
-      const int heads = min(32, H - (h0 + (quarter & 1) * 32));   // of this warp's 32 that exist
-      const bool part = p.n_split > 1;
-      const int64_t head0 = (static_cast<int64_t>(part ? split : 0) * p.seq.T + t) * H + h0 + (quarter & 1) * 32;
-      uint8_t* out = reinterpret_cast<uint8_t*>(part ? p.ws_o : static_cast<uint16_t*>(p.a.out)) +
-                     (head0 * kDv + half * 256 + part32 * 128) * 2;
-      const uint32_t stg = smem_u32(sm + kOffStage) + (warp - kWarpSoft) * 4096;   // all MMAs are complete
-      if (heads > 0) {
+            for (int i = 0; i < 32; ++i) x[i] = ((vmask >> i) & 1u) ? x[i] : -INFINITY;
+          }
+          rmax = fmaxf(reinterpret_cast<const volatile float*>(sm + kOffRmax)[2 * st],
+                       reinterpret_cast<const volatile float*>(sm + kOffRmax)[2 * st + 1]);
+          float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) mq[(i >> 1) & 3] = fmax3(mq[(i >> 1) & 3], x[i], x[i + 1]);
+          mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * sl2;
+        }
+        // The four threads of a head share m and g, and their warps leave together when one
+        // has given up.  One barrier tells the 128 threads of 32 heads whether any of them has
+        // to let m or g grow; only then (the first tile, and seldom after) do they exchange
+        // their maxima.
+        const float lrmax = __log2f(rmax);
+        const bool grow = named_bar_or(head_bar, 128, !ok || mx > m + kRescaleM || mx + lrmax > g + kRescaleG);
+        // P has one buffer and O may have to be rescaled: P V of the tile before is complete
+        bool pv_ok = true;
+        if (j >= 1 && ok) pv_ok = wait_bar(&pvdone[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, wlim);
+        if (grow) {
+          const __nv_bfloat16 mxb = __float2bfloat16_ru(mx);   // a bound is enough, rounded up
+          xmax[rq * 32] = mxb;
+          mx = __bfloat162float(mxb);
+          if (lane == 0) oks[warp - kWarpSoft] = ok ? 1 : 0;
+          named_bar_sync(head_bar, 128);
+#pragma unroll
+          for (int k = 1; k < 4; ++k) mx = fmaxf(mx, __bfloat162float(xmax[(rq ^ k) * 32]));
+          // the four warps: those whose number is as odd as this one's
+#pragma unroll
+          for (int k = 0; k < 4; ++k) ok = ok && oks[2 * k + (warp & 1)] != 0;
+          named_bar_sync(head_bar, 128);
+          if (!ok) break;
+          const float gx = mx + lrmax;
+          const bool need_m = mx > m + kRescaleM, need_g = gx > g + kRescaleG;
+          // (g of -inf: nothing in O yet)
+          if (__any_sync(0xffffffffu, need_g && g > -INFINITY)) {
+            tc_fence_after();
+            const float f = need_g && g > -INFINITY ? exp2f(g - gx) : 1.f;
 #pragma unroll 1
-        for (int cc = 0; cc < 2; ++cc) {
-          uint32_t o0[32], o1[32];
-          tmem_ld32(tmem + lane_off + kColO + part32 * 128 + cc * 64, o0);
-          tmem_ld32(tmem + lane_off + kColO + part32 * 128 + cc * 64 + 32, o1);
-          tmem_ld_wait();
+            for (int cc = 0; cc < 8; ++cc) {   // this thread's half of the columns
+              uint32_t o[16];
+              const uint32_t at = tmem + kColO + part32 * 128 + cc * 16;
+              tmem_ld16(at, o);
+              tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            st_shared_v4(stg + lane * 128 + ((k ^ (lane & 7)) << 4),
-                         pack_bf16x2(__uint_as_float(o0[8 * k]) * inv, __uint_as_float(o0[8 * k + 1]) * inv),
-                         pack_bf16x2(__uint_as_float(o0[8 * k + 2]) * inv, __uint_as_float(o0[8 * k + 3]) * inv),
-                         pack_bf16x2(__uint_as_float(o0[8 * k + 4]) * inv, __uint_as_float(o0[8 * k + 5]) * inv),
-                         pack_bf16x2(__uint_as_float(o0[8 * k + 6]) * inv, __uint_as_float(o0[8 * k + 7]) * inv));
-            st_shared_v4(stg + lane * 128 + (((k + 4) ^ (lane & 7)) << 4),
-                         pack_bf16x2(__uint_as_float(o1[8 * k]) * inv, __uint_as_float(o1[8 * k + 1]) * inv),
-                         pack_bf16x2(__uint_as_float(o1[8 * k + 2]) * inv, __uint_as_float(o1[8 * k + 3]) * inv),
-                         pack_bf16x2(__uint_as_float(o1[8 * k + 4]) * inv, __uint_as_float(o1[8 * k + 5]) * inv),
-                         pack_bf16x2(__uint_as_float(o1[8 * k + 6]) * inv, __uint_as_float(o1[8 * k + 7]) * inv));
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st16(at, o);
+            }
+            tmem_st_wait();
           }
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int row = i * 4 + (lane >> 3), c4 = lane & 7;
-            const uint4 v = ld_shared_v4(stg + row * 128 + ((c4 ^ (row & 7)) << 4));
-            if (row < heads) *reinterpret_cast<uint4*>(out + static_cast<int64_t>(row) * kDv * 2 + cc * 128 + c4 * 16) = v;
+          if (need_g) g = gx;
+          if (need_m) {
+            l *= exp2f(m - mx);
+            m = mx;
           }
-          __syncwarp();
         }
-        if (rq == 0 && lane < heads) {
-          if (part)
-            p.ws_lse[head0 + lane] = lse;
-          else if (p.a.lse)
-            p.a.lse[head0 + lane] = lse;
+        ok = __all_sync(0xffffffffu, pv_ok);
+        const float msub = (m == -INFINITY) ? 0.f : m;
+        // 2^(m - g), kept finite and nonzero
+        const float gain = (g == -INFINITY) ? 1.f : exp2f(fminf(fmaxf(msub - g, -126.f), 126.f));
+        const uint32_t prow = prow0 + (j & 1) * pstep;
+        float se[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[4];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int i = 8 * c + 4 * q;
+            const uint4 rs = ld_shared_v4(scales + static_cast<uint32_t>(i * 4));
+            const float r[4] = {__uint_as_float(rs.x), __uint_as_float(rs.y), __uint_as_float(rs.z),
+                                __uint_as_float(rs.w)};
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+              float d0 = -msub, d1 = -msub;
+              fma2(d0, d1, x[i + k], x[i + k + 1], sl2, sl2);
+              const float p0 = fast_exp2(d0), p1 = fast_exp2(d1);
+              add2(se[k], se[k + 1], se[k], se[k + 1], p0, p1);
+              float w0, w1;
+              mul2(w0, w1, p0, p1, gain, gain);
+              mul2(w0, w1, w0, w1, r[k], r[k + 1]);
+              const __half2 h = __floats2half2_rn(w0, w1);
+              pk[2 * q + (k >> 1)] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+          }
+          st_shared_v4(prow + static_cast<uint32_t>(((part32 * 4 + c) ^ (hl & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
+        }
+        l += (se[0] + se[1]) + (se[2] + se[3]);
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          arrive_pair(leader_addr(pfull));
+          mbar_arrive(&mfree[st]);
         }
       }
+      if (gt < end) break;
     }
   }
 
@@ -826,11 +994,41 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
   if (warp == kWarpQk) mbar_drain(drain, 0, &g_status_attn_e2m1, p.wait_limit_ns);
   tc_fence_before();
   __syncwarp();
-  cluster_sync();
+  cluster_arrive();
+  cluster_wait();
   if (warp == kWarpQk) {
     tc_fence_after();
+    const uint32_t tmem = misc[0];
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
   }
+}
+
+// Clusters that the current device holds at once (its SMs need not pair up everywhere), asked once.
+int resident_clusters(int num_sms) {
+  static std::atomic<int> cache[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return std::max(1, num_sms / 2);
+  int n = cache[dev].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  const void* kernel = reinterpret_cast<const void*>(attn_e2m1_kernel);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::max(2, num_sms & ~1)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (ensure_smem_limit(kernel, kSmemBytes, dev) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
+    static_cast<void>(cudaGetLastError());
+    return std::max(1, num_sms / 2);
+  }
+  cache[dev].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 // Row slices per query: one cluster for each while the GPU holds them all at once, a
@@ -838,7 +1036,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
 int choose_split(const SeqArgs& seq, const MlaArgs& a, int num_sms) {
   const int tiles = (a.K + kTile - 1) / kTile;
   const int64_t clusters = static_cast<int64_t>(seq.T) * ((a.H + 127) / 128);
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(tiles, (num_sms / 2) / std::max<int64_t>(1, clusters))));
+  return static_cast<int>(
+      std::max<int64_t>(1, std::min<int64_t>(tiles, resident_clusters(num_sms) / std::max<int64_t>(1, clusters))));
 }
 
 }  // namespace
@@ -860,13 +1059,12 @@ cudaError_t launch_attn_e2m1(const SeqArgs& seq, const MlaArgs& a, void* workspa
   const int tiles = (a.K + kTile - 1) / kTile;
   const int rps = (tiles + split - 1) / split * kTile;
   split = (a.K + rps - 1) / rps;   // every slice non-empty
-  PairParams p{seq, a, split, rps, (a.H + 127) / 128, nullptr, nullptr, kWaitLimitNs, 0u, 0u, 0u, env.chained ? 1u : 0u};
-  // division by the page size: with 2^(s - 1) < d <= 2^s and m = ceil(2^(31 + s) / d), the
-  // error m d - 2^(31 + s) < d <= 2^s keeps floor(n m / 2^(31 + s)) = floor(n / d) for n < 2^31
-  uint32_t shift = 0;
-  while ((1ll << shift) < seq.page_size) ++shift;
-  p.page_shift = 31 + shift;
-  p.page_mul = static_cast<uint32_t>(((1ull << (31 + shift)) + seq.page_size - 1) / seq.page_size);
+  const int head_blocks = (a.H + 127) / 128;
+  const int64_t items = static_cast<int64_t>(seq.T) * head_blocks * split;
+  if (items > 0x3FFFFFFFll) return cudaErrorInvalidConfiguration;
+  PairParams p{seq,     a,  split,        rps,  head_blocks, static_cast<int32_t>(items),
+               nullptr, nullptr, kWaitLimitNs, 0u, Divisor(seq.page_size), Divisor(split), Divisor(head_blocks),
+               env.chained ? 1u : 0u};
   debug_wait_state(&p.wait_limit_ns, &p.dbg_withhold);
   if (split > 1) {
     const size_t o = static_cast<size_t>(split) * seq.T * a.H * kDv * sizeof(uint16_t);
@@ -875,9 +1073,9 @@ cudaError_t launch_attn_e2m1(const SeqArgs& seq, const MlaArgs& a, void* workspa
   }
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(attn_e2m1_kernel), kSmemBytes, env.device);
   if (e != cudaSuccess) return e;
-  const int64_t grid = 2ll * seq.T * p.head_blocks * split;
-  if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-  e = launch_kernel(attn_e2m1_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmemBytes, env.stream, true, 2, p);
+  const int64_t grid = 2 * std::min<int64_t>(items, resident_clusters(env.num_sms));
+  e = launch_kernel(attn_e2m1_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmemBytes, env.stream, true,
+                    2, p);
   if (e != cudaSuccess) return e;
   char buf[96];
   snprintf(buf, sizeof(buf), "attn_tc<e2m1x128>[split=%d,grid=%lld]", split, static_cast<long long>(grid));
