@@ -142,6 +142,8 @@ def _ptr(t: Optional[torch.Tensor]):
 # The current stream's handle without a Stream object around it: 0.1 us against 2.9, of
 # the 3.4 that a small step's C call takes.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice      # for callers that have seen a CUDA tensor
+_FLOAT_CODES = {torch.float32: DSA_F32, torch.bfloat16: DSA_BF16}
 
 
 def _stream(stream) -> int:
@@ -152,7 +154,7 @@ def _stream(stream) -> int:
 
 def _rows(t: torch.Tensor, name: str) -> int:
     """Data pointer of a tensor whose values are contiguous along its last dim, on the current GPU."""
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if not t.is_cuda or t.get_device() != _current_device():
         raise ValueError(f"{name} must be on the current CUDA device, not on {t.device}")
     if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"the last dim of {name} must be contiguous")
@@ -280,7 +282,7 @@ class Rope(_CachedDesc):
         mag = ctypes.c_float()
         _check(_lib.dsa_rope_turns(d_rot, theta, ROPE_SCALINGS[scaling], factor, original_ctx, beta_fast, beta_slow,
                                    host, ctypes.byref(mag)))
-        turns = torch.tensor([ctypes.c_int64(v).value for v in host], dtype=torch.int64, device=device)
+        turns = torch.frombuffer(host, dtype=torch.int64).to(device, copy=True)
         return cls(d_rot, turns, mag.value if magnitude is None else float(magnitude), layout)
 
     def _build_desc(self) -> RopeDesc:
@@ -302,14 +304,17 @@ def rope(plan: Rope, pos: torch.Tensor, x: torch.Tensor, out: torch.Tensor, inve
     shape = x.shape
     if len(shape) not in (2, 3) or shape[-1] != d.d_rot or out.shape != shape:
         raise ValueError("x and out must be [T, H, d_rot] or [T, d_rot]")
-    if out.dtype != x.dtype or x.dtype not in (torch.bfloat16, torch.float32):
+    dtype = _FLOAT_CODES.get(x.dtype)
+    if dtype is None or out.dtype != x.dtype:
         raise ValueError("x and out must both be bfloat16 or float32")
     if pos.dtype != torch.int32 or pos.shape != shape[:1] or not pos.is_contiguous():
         raise ValueError("pos must be contiguous int32 [T]")
-    xs, os_ = x.stride(), out.stride()
-    H, xh, oh = (shape[1], xs[1], os_[1]) if len(shape) == 3 else (1, 0, 0)
-    _check(_lib.dsa_rope(ctypes.byref(d), shape[0], H, _rows(pos, "pos"), DSA_F32 if x.dtype == torch.float32 else DSA_BF16,
-                         _rows(x, "x"), xs[0], xh, _rows(out, "out"), os_[0], oh, 1 if inverse else 0, _stream(stream)))
+    if len(shape) == 3:
+        H, (xt, xh, _), (ot, oh, _) = shape[1], x.stride(), out.stride()
+    else:
+        H, xt, xh, ot, oh = 1, x.stride(0), 0, out.stride(0), 0
+    _check(_lib.dsa_rope(ctypes.byref(d), shape[0], H, _rows(pos, "pos"), dtype, _rows(x, "x"), xt, xh,
+                         _rows(out, "out"), ot, oh, 1 if inverse else 0, _stream(stream)))
     return out
 
 
@@ -440,10 +445,10 @@ def latent_cache_read(seq: Seq, mla: Mla, out: torch.Tensor, stream=None) -> tor
     s, m = seq.desc(), mla.desc()
     if out.shape != (s.T, m.d_latent + m.d_rope):
         raise ValueError("out must be [T, d_latent + d_rope]")
-    if out.dtype not in (torch.bfloat16, torch.float32):
+    dtype = _FLOAT_CODES.get(out.dtype)
+    if dtype is None:
         raise ValueError("out must be bfloat16 or float32")
-    _check(_lib.dsa_latent_cache_read(ctypes.byref(s), ctypes.byref(m), m.kv_cache,
-                                      DSA_F32 if out.dtype == torch.float32 else DSA_BF16, _rows(out, "out"),
+    _check(_lib.dsa_latent_cache_read(ctypes.byref(s), ctypes.byref(m), m.kv_cache, dtype, _rows(out, "out"),
                                       out.stride(0), _stream(stream)))
     return out
 
