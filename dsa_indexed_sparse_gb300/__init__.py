@@ -227,7 +227,8 @@ class Indexer(_CachedDesc):
 @dataclasses.dataclass
 class Mla(_CachedDesc):
     """Latent attention inputs; see dsa_mla_desc_t.  kv_cache is [cache_rows, row] of
-    bf16/fp32 values or uint8 656-byte FP8 rows (dtype given explicitly then)."""
+    bf16/fp32 values, or uint8 656-byte FP8 or 432-byte 4-bit rows (dtype given explicitly
+    then)."""
     q: torch.Tensor                    # [T, H, d_latent + d_rope]
     kv_cache: torch.Tensor
     d_latent: int
@@ -402,7 +403,7 @@ def index_cache_append(seq: Seq, k_new: torch.Tensor, k_cache: torch.Tensor, k_s
 
 def latent_cache_append(seq: Seq, mla: Mla, kv_new: torch.Tensor, stream=None) -> None:
     """Writes the new tokens' latent rows kv_new [T, d_latent + d_rope] into
-    mla.kv_cache (copied, or quantised into 656-byte FP8 rows)."""
+    mla.kv_cache (copied, or quantised into 656-byte FP8 or 432-byte 4-bit rows)."""
     s, m = seq.desc(), mla.desc()
     _check(_lib.dsa_latent_cache_append(ctypes.byref(s), ctypes.byref(m), _ptr(kv_new), _ptr(mla.kv_cache),
                                         _stream(stream)))

@@ -42,8 +42,8 @@
 // overwrites Y, dead once Q K^T is complete, with rows 64-127; rank 1 (rows 64-127,
 // dims [256, 512)) has them in Y and overwrites X with rows 0-63.  P of tile rows 0-63
 // goes into R (dead as well), P of rows 64-127 into a buffer of its own.  (Buffers of their
-// own for keys and values write and load a third more; the pipe to shared memory, which
-// the MMAs, the producers' stores and every load share, is what is nearest its limit.)
+// own for keys and values write and load a third more, and the load/store pipe is what is
+// nearest its limit.)
 //   shared memory: Q 72 KB | stage 0 | stage 1 | P, rows 64-127 8 KB | row scales, rows, masks, barriers
 //   TMEM: latent logits [0,64) [64,128), rope logits [128,192) [192,256), O [256,512).  An
 //   N-wide accumulator of a pair MMA takes N/2 columns: lanes 0-63 are the CTA's heads
@@ -66,10 +66,12 @@
 // comes back from the L2 (24 bytes are, outside the loops' chains).  The code is kept small
 // (rolled loops, short waits): with 98 KB of it every role ran from a cold instruction cache.
 //
-// Measured (2048 selected rows, 128 heads): 1177 us for 2048 queries, 992 TFLOP/s of the
-// 1926 measured; 54.0 us for 64 (one cluster a query: 128 of 152 SMs), 12.4 us for one (a
-// tile each for 16 clusters: latencies).  A tile takes 4300 clocks where its MMAs need 2176: they,
-// the producers' stores and the loads pass 4100 wavefronts of 128 bytes through the one pipe.
+// Measured (2048 selected rows, 128 heads): 1178 us for 2048 queries, 992 TFLOP/s of the
+// 1926 measured; 53.5 us for 64 (one cluster a query: 128 of 152 SMs), 12.4 us for one (a
+// tile each for 16 clusters: latencies).  A tile takes 4300 clocks where its MMAs need 2176: two
+// are in flight, each a chain own rows - Q K^T - other rows - P V, and the links slow one another
+// (of the loop's clocks the load/store pipe has a wavefront in 73 %, tensor operands are read
+// in 45 %, issue slots are taken in 54 %).
 // The 48-row kernel of attn.cu's kind, which widens every row in both CTAs: 2171, 100 and 11.7.
 #include <algorithm>
 #include <atomic>
@@ -472,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
           }
           ++a;
         } else {
-          __nanosleep(32);
+          __nanosleep(160);
           if ((++idle & 31u) == 0u) {
             until = wait_until(abort_flag, until, wlim);
             if (__any_sync(0xffffffffu, until == 1)) break;
