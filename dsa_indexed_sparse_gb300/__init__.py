@@ -146,15 +146,15 @@ _current_device = torch._C._cuda_getDevice      # for callers that have seen a C
 _FLOAT_CODES = {torch.float32: DSA_F32, torch.bfloat16: DSA_BF16}
 
 
-def _stream(stream) -> int:
+def _stream(stream, dev: Optional[int] = None) -> int:
     if stream is None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(torch.cuda.current_device() if dev is None else dev)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _rows(t: torch.Tensor, name: str) -> int:
-    """Data pointer of a tensor whose values are contiguous along its last dim, on the current GPU."""
-    if not t.is_cuda or t.get_device() != _current_device():
+def _rows(t: torch.Tensor, name: str, dev: int) -> int:
+    """Data pointer of a tensor whose values are contiguous along its last dim, on GPU dev."""
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be on the current CUDA device, not on {t.device}")
     if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"the last dim of {name} must be contiguous")
@@ -171,6 +171,26 @@ def _dtype_code(t: torch.Tensor) -> int:
     raise ValueError(f"unsupported dtype {t.dtype}")
 
 
+def _cache_ptr(t: torch.Tensor, name: str, dev: int) -> int:
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to libdsa must be contiguous")
+    return _rows(t, name, dev)
+
+
+def _on_current(*records: "_CachedDesc") -> int:
+    """The current GPU's index.  Refuses records with tensors off it (a descriptor holds their addresses)."""
+    dev = records[0]._gpu
+    if dev is None:
+        dev = records[0].gpu()
+    if dev >= 0 and dev == _current_device():
+        for r in records:
+            if r._gpu != dev and r.gpu() != dev:
+                break
+        else:
+            return dev
+    raise ValueError("the tensors of a call must be on the current CUDA device")
+
+
 class _CachedDesc:
     """The C descriptor is built on first use and kept until a field is reassigned
     (a step call then costs no Python-side struct building).  Tensors are
@@ -180,7 +200,17 @@ class _CachedDesc:
     def __setattr__(self, name, value):
         if name != "_desc":
             object.__setattr__(self, "_desc", None)
+            object.__setattr__(self, "_gpu", None)
         object.__setattr__(self, name, value)
+
+    def gpu(self) -> int:
+        """The index of the GPU that every tensor of the record is on, or -1."""
+        g = self.__dict__.get("_gpu")
+        if g is None:
+            on = {v.get_device() for v in vars(self).values() if isinstance(v, torch.Tensor)}
+            g = on.pop() if len(on) == 1 else -1
+            object.__setattr__(self, "_gpu", g)
+        return g
 
     def desc(self):
         d = self.__dict__.get("_desc")
@@ -291,7 +321,7 @@ class Rope(_CachedDesc):
             raise ValueError("turns must be int64 [d_rot / 2]")
         if not self.turns.is_contiguous():
             raise ValueError("turns must be contiguous")
-        return RopeDesc(self.d_rot, ROPE_LAYOUTS[self.layout], _rows(self.turns, "turns"), self.magnitude)
+        return RopeDesc(self.d_rot, ROPE_LAYOUTS[self.layout], self.turns.data_ptr(), self.magnitude)
 
 
 def rope(plan: Rope, pos: torch.Tensor, x: torch.Tensor, out: torch.Tensor, inverse: bool = False,
@@ -314,8 +344,9 @@ def rope(plan: Rope, pos: torch.Tensor, x: torch.Tensor, out: torch.Tensor, inve
         H, (xt, xh, _), (ot, oh, _) = shape[1], x.stride(), out.stride()
     else:
         H, xt, xh, ot, oh = 1, x.stride(0), 0, out.stride(0), 0
-    _check(_lib.dsa_rope(ctypes.byref(d), shape[0], H, _rows(pos, "pos"), dtype, _rows(x, "x"), xt, xh,
-                         _rows(out, "out"), ot, oh, 1 if inverse else 0, _stream(stream)))
+    dev = _on_current(plan)
+    _check(_lib.dsa_rope(ctypes.byref(d), shape[0], H, _rows(pos, "pos", dev), dtype, _rows(x, "x", dev), xt, xh,
+                         _rows(out, "out", dev), ot, oh, 1 if inverse else 0, _stream(stream, dev)))
     return out
 
 
@@ -420,9 +451,11 @@ def latent_cache_append_rope(seq: Seq, mla: Mla, plan: Rope, latent: torch.Tenso
         raise ValueError(f"latent and k_rope must be {want} for this cache")
     if latent.shape != (s.T, m.d_latent) or k_rope.shape != (s.T, m.d_rope):
         raise ValueError("latent must be [T, d_latent] and k_rope [T, d_rope]")
+    dev = _on_current(seq, mla, plan)
     _check(_lib.dsa_latent_cache_append_rope(ctypes.byref(s), ctypes.byref(m), ctypes.byref(r),
-                                             _rows(latent, "latent"), latent.stride(0), _rows(k_rope, "k_rope"),
-                                             k_rope.stride(0), m.kv_cache, _stream(stream)))
+                                             _rows(latent, "latent", dev), latent.stride(0),
+                                             _rows(k_rope, "k_rope", dev), k_rope.stride(0), m.kv_cache,
+                                             _stream(stream, dev)))
 
 
 def index_cache_append_rope(seq: Seq, plan: Rope, k_new: torch.Tensor, k_cache: torch.Tensor, k_scale: torch.Tensor,
@@ -433,10 +466,12 @@ def index_cache_append_rope(seq: Seq, plan: Rope, k_new: torch.Tensor, k_cache: 
     s, r = seq.desc(), plan.desc()
     if k_new.dim() != 2 or k_new.shape[0] != s.T:
         raise ValueError("k_new must be [T, D_I]")
+    dev = _on_current(seq, plan)
     _check(_lib.dsa_index_cache_append_rope(ctypes.byref(s), ctypes.byref(r), k_new.shape[1], offset,
                                             _dtype_code(k_new), DSA_MXFP8_E4M3 if mx else DSA_E4M3,
-                                            _rows(k_new, "k_new"), k_new.stride(0), _ptr(k_cache), _ptr(k_scale),
-                                            _stream(stream)))
+                                            _rows(k_new, "k_new", dev), k_new.stride(0),
+                                            _cache_ptr(k_cache, "k_cache", dev), _cache_ptr(k_scale, "k_scale", dev),
+                                            _stream(stream, dev)))
 
 
 def latent_cache_read(seq: Seq, mla: Mla, out: torch.Tensor, stream=None) -> torch.Tensor:
@@ -449,8 +484,9 @@ def latent_cache_read(seq: Seq, mla: Mla, out: torch.Tensor, stream=None) -> tor
     dtype = _FLOAT_CODES.get(out.dtype)
     if dtype is None:
         raise ValueError("out must be bfloat16 or float32")
-    _check(_lib.dsa_latent_cache_read(ctypes.byref(s), ctypes.byref(m), m.kv_cache, dtype, _rows(out, "out"),
-                                      out.stride(0), _stream(stream)))
+    dev = _on_current(seq, mla)
+    _check(_lib.dsa_latent_cache_read(ctypes.byref(s), ctypes.byref(m), m.kv_cache, dtype, _rows(out, "out", dev),
+                                      out.stride(0), _stream(stream, dev)))
     return out
 
 

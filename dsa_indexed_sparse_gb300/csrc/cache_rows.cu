@@ -14,10 +14,10 @@
 // next to nothing: the time is the latency of a launch and of the chain position
 // -> page -> row for a few tokens, and the bytes for many.  Writing 8192 bf16 rows
 // takes 3.7 us (5.2 TB/s; 4.5 with the values loaded after the chain), 64 4-bit rows or
-// 333 read ones 2 us; reading 65,536 4-bit rows into bf16 19.7 us (5.3 TB/s).  The next kernel may
-// launch as soon as a block has waited for the kernel before: it waits for this
-// grid before it reads a cache (and a query that it stages earlier was complete by
-// then).
+// 333 read ones 2 us; reading 65,536 4-bit rows into bf16 19.7 us (5.3 TB/s).  After a writer the
+// next kernel may launch as soon as a block has waited for the kernel before: it waits
+// for this grid before it reads a cache (and a query that it stages earlier was complete
+// by then).  Not so after the reader, whose output may be anything, a query among it.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
@@ -195,8 +195,9 @@ __global__ void __launch_bounds__(kRowWarps * 32) latent_write_kernel(SeqArgs se
   grid_dep_wait();
   grid_dep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = blockIdx.x * (blockDim.x >> 5) + warp;
-  if (t >= seq.T) return;
+  const int64_t tw = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp;
+  if (tw >= seq.T) return;
+  const int t = static_cast<int>(tw);
   const uint4* src = reinterpret_cast<const uint4*>(a.latent + t * a.latent_stride);
   const uint8_t* rsrc = a.k_rope + t * a.rope_stride;
   constexpr bool kF32 = kKind == MlaKind::kF32;
@@ -252,8 +253,9 @@ __global__ void __launch_bounds__(kIndexWarps * 32) index_write_kernel(SeqArgs s
   grid_dep_wait();
   grid_dep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = blockIdx.x * kIndexWarps + warp;
-  if (t >= seq.T) return;
+  const int64_t tw = static_cast<int64_t>(blockIdx.x) * kIndexWarps + warp;
+  if (tw >= seq.T) return;
+  const int t = static_cast<int>(tw);
   const int nq = a.D / 4;
   float4* v4 = reinterpret_cast<float4*>(rows[warp]);
   const uint8_t* src = a.k_new + t * a.stride;
@@ -345,12 +347,11 @@ __device__ __forceinline__ void store_values(uint8_t* dst, int i, const float (&
 template <MlaKind kKind, bool kF32Out, int kRows>
 __global__ void __launch_bounds__(kRowWarps * 32) latent_read_kernel(SeqArgs seq, LatentReadArgs a) {
   grid_dep_wait();
-  grid_dep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t0 = (blockIdx.x * (blockDim.x >> 5) + warp) * kRows;
+  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp) * kRows;
   if (t0 >= seq.T) return;
   int pos;
-  const int64_t mine = lane < kRows && t0 + lane < seq.T ? token_row(seq, t0 + lane, &pos) : -1;
+  const int64_t mine = lane < kRows && t0 + lane < seq.T ? token_row(seq, static_cast<int>(t0) + lane, &pos) : -1;
   int64_t row[kRows];
 #pragma unroll
   for (int r = 0; r < kRows; ++r) row[r] = __shfl_sync(0xffffffffu, mine, r);
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) latent_read_kernel(SeqArgs seq
 // Warps per block: one for a few tokens (they spread over the SMs), up to kRowWarps.
 int row_warps(int T, int num_sms) {
   int w = kRowWarps;
-  while (w > 1 && (T + w - 1) / w < num_sms) w /= 2;
+  while (w > 1 && (static_cast<int64_t>(T) + w - 1) / w < num_sms) w /= 2;
   return w;
 }
 
@@ -475,7 +476,7 @@ cudaError_t launch_latent_write(const SeqArgs& seq, const MlaArgs& a, const Rope
   const LatentWriteArgs w{rope, static_cast<const uint8_t*>(latent), latent_stride, static_cast<const uint8_t*>(k_rope),
                           rope_stride, static_cast<uint8_t*>(kv_cache), a.row_bytes, a.d_latent, a.d_rope};
   const int warps = row_warps(seq.T, env.num_sms);
-  const dim3 grid((seq.T + warps - 1) / warps), block(warps * 32);
+  const dim3 grid((static_cast<int64_t>(seq.T) + warps - 1) / warps), block(warps * 32);
   *plan += rope.turns ? "latent_append_rope<" : "latent_append<";
 #define DSA_WRITE_GO(KIND, NAME)  \
   *plan += NAME ">";              \
@@ -499,7 +500,7 @@ cudaError_t launch_index_write(const SeqArgs& seq, const RopeArgs& rope, int32_t
     return cudaSuccess;
   }
   const IndexWriteArgs a{rope, D, off, static_cast<const uint8_t*>(k_new), stride, k_cache, k_scale};
-  const dim3 grid((seq.T + kIndexWarps - 1) / kIndexWarps), block(kIndexWarps * 32);
+  const dim3 grid((static_cast<int64_t>(seq.T) + kIndexWarps - 1) / kIndexWarps), block(kIndexWarps * 32);
   *plan += mx ? "index_append_rope<mx," : "index_append_rope<e4m3,";
   *plan += bf16_in ? "bf16>" : "f32>";
   if (mx)
@@ -522,7 +523,7 @@ cudaError_t launch_latent_read(const SeqArgs& seq, const MlaArgs& a, const void*
   // warps.  Fewer rows take no longer with a warp each, and spread further.
   const bool many = seq.T > env.num_sms * 64;
   const int warps = many ? kReadWarps : row_warps(seq.T, env.num_sms), per_block = warps * (many ? kReadRows : 1);
-  const dim3 grid((seq.T + per_block - 1) / per_block), block(warps * 32);
+  const dim3 grid((static_cast<int64_t>(seq.T) + per_block - 1) / per_block), block(warps * 32);
   *plan += "latent_read<";
 #define DSA_READ_LAUNCH(KIND, F32, ROWS) \
   launch_kernel(latent_read_kernel<KIND, F32, ROWS>, grid, block, 0, env.stream, true, 1, seq, r)

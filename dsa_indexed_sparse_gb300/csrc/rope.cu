@@ -220,7 +220,7 @@ cudaError_t launch_rope(const RopeArgs& rope, int32_t T, int32_t H, const int32_
     a.heads = slots * rows;
   else
     a.tokens = std::max(1, std::min({slots * rows / H, T, kRopeMaxPairs * 8 / pairs}));
-  const dim3 grid((T + a.tokens - 1) / a.tokens, (H + a.heads - 1) / a.heads), block(a.units * slots);
+  const dim3 grid((static_cast<int64_t>(T) + a.tokens - 1) / a.tokens, (H + a.heads - 1) / a.heads), block(a.units * slots);
   const size_t smem = static_cast<size_t>(a.tokens) * pairs * sizeof(float2);
   *plan += aligned ? (rope.half ? "rope_vec<half," : "rope_vec<interleaved,") : "rope_scalar<";
   *plan += bf16 ? "bf16>" : "f32>";

@@ -332,7 +332,8 @@ dsa_status_t dsa_rope(const dsa_rope_desc_t* rope, int32_t T, int32_t H, const i
 /* Cache writers that rotate on the way: as dsa_latent_cache_append and
  * dsa_index_cache_append[_mx], with the rope part (index keys: dims
  * [rot_offset, rot_offset + d_rot)) rotated by the token's position q_pos[t]
- * in fp32 before it is rounded or quantised.
+ * in fp32 before it is rounded or quantised.  As there, the positions of one call
+ * must be distinct, and a position or page out of range is flagged and skipped.
  *
  * Latent rows: latent device [T, d_latent] and k_rope device [T, d_rope], bf16
  *   (fp32 when mla->dtype == DSA_F32), with strides between tokens in values

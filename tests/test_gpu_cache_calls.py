@@ -1,0 +1,166 @@
+"""The rotating writers and the cache reader as a program chains them: records whose tensors are not on the GPU, outputs
+that feed the next call at once, long lists of tokens, streams and graphs.  Values are compared bit for bit with the same
+calls made one by one, or with the oracle's rows."""
+import dataclasses
+
+import numpy as np
+import pytest
+import torch
+
+import dsa_indexed_sparse_gb300 as dsa
+from oracle import dsa_oracle as O
+from tests import parity as P
+from tests.test_gpu_e2m1 import _make, _selection
+
+pytestmark = pytest.mark.gpu
+
+
+def _cache(dev, B, ctx, row_bytes=432):
+    pages = (ctx + 63) // 64
+    table = torch.randperm(B * pages, generator=torch.Generator().manual_seed(B * ctx)).to(torch.int32).view(B, pages)
+    rows = B * pages * 64
+    return table.to(dev), rows, torch.zeros((rows, row_bytes), dtype=torch.uint8, device=dev)
+
+
+def _mla(kv, dtype=dsa.DSA_E2M1):
+    q = torch.zeros((1, 1, 576), dtype=torch.bfloat16, device=kv.device)
+    return dsa.Mla(q=q, kv_cache=kv, d_latent=512, d_rope=64, softmax_scale=1.0, dtype=dtype)
+
+
+def test_records_off_the_gpu_are_refused(dev):
+    table, rows, kv = _cache(dev, 2, 100)
+    seq = torch.tensor([0, 1], dtype=torch.int32, device=dev)
+    pos = torch.tensor([5, 7], dtype=torch.int32, device=dev)
+    plan = dsa.Rope.make(64)
+    new = torch.zeros((2, 576), dtype=torch.bfloat16, device=dev)
+    out = torch.zeros((2, 576), dtype=torch.bfloat16, device=dev)
+    key = torch.zeros((2, 128), dtype=torch.bfloat16, device=dev)
+    kc, ks = torch.zeros((rows, 128), dtype=torch.uint8, device=dev), torch.zeros(rows, device=dev)
+    good = dict(q_seq=seq, q_pos=pos, block_table=table, max_ctx=100, cache_rows=rows)
+    for field in ("q_seq", "q_pos", "block_table"):
+        s = dsa.Seq(**{**good, field: good[field].cpu()})
+        with pytest.raises(ValueError, match="CUDA device"):
+            dsa.latent_cache_read(s, _mla(kv), out)
+        with pytest.raises(ValueError, match="CUDA device"):
+            dsa.latent_cache_append_rope(s, _mla(kv), plan, new[:, :512], new[:, 512:])
+        with pytest.raises(ValueError, match="CUDA device"):
+            dsa.index_cache_append_rope(s, plan, key, kc, ks)
+    s = dsa.Seq(**good)
+    with pytest.raises(ValueError, match="CUDA device"):
+        dsa.latent_cache_read(s, _mla(kv.cpu()), out)
+    with pytest.raises(ValueError, match="CUDA device"):
+        dsa.index_cache_append_rope(s, plan, key, kc.cpu(), ks)
+    with pytest.raises(ValueError, match="CUDA device"):
+        dsa.rope(plan, pos.cpu(), new[:, 512:], new[:, 512:])
+    dsa.check_status()
+
+
+@pytest.mark.parametrize("T", [1, 9727, 9729, 30001])
+def test_append_then_read_of_many_tokens(dev, T):
+    """Every token of one long sequence written and read back at once, in a random order; the sizes around the number of
+    warps that the GPU holds, and an odd one."""
+    table, rows, kv = _cache(dev, 1, T)
+    g = torch.Generator(device=dev).manual_seed(T)
+    order = torch.randperm(T, generator=g, device=dev).to(torch.int32)
+    s = dsa.Seq(q_seq=torch.zeros(T, dtype=torch.int32, device=dev), q_pos=order, block_table=table, max_ctx=T, cache_rows=rows)
+    new = torch.randn((T, 576), generator=g, device=dev).to(torch.bfloat16)
+    plan = dsa.Rope.make(64, layout="half")
+    mla = _mla(kv)
+    dsa.latent_cache_append_rope(s, mla, plan, new[:, :512], new[:, 512:])
+    out = torch.full((T, 576), float("nan"), dtype=torch.bfloat16, device=dev)
+    dsa.latent_cache_read(s, mla, out)
+    pe = torch.empty((T, 64), dtype=torch.bfloat16, device=dev)
+    dsa.rope(plan, order, new[:, 512:], pe)
+    dsa.check_status()
+    assert torch.equal(out[:, 512:], pe)             # the writer's rotation is the rope call's, bit for bit
+    for t in {0, T // 2, T - 1}:
+        row = O.e2m1_row(new[t, :512].float().cpu().numpy(), np.zeros(64))
+        at = int(O.physical_rows(table[0].cpu().numpy(), 64, np.array([int(order[t])]))[0])
+        assert np.array_equal(kv[at, :304].cpu().numpy(), row[:304])
+    # a latent value is off by at most one unit of its block scale (codes 4 and 6 lie two units apart; beyond 6 a unit is
+    # not reached: the scale is rounded by 2^-4 of itself at most), which is at most amax / 6 (1 + 2^-4); exact in bf16
+    x = new[:, :512].float().view(T, 32, 16)
+    amax = x.abs().amax(-1, keepdim=True)
+    assert bool(((out[:, :512].float().view(T, 32, 16) - x).abs() <= 1.001 * amax / 6 * (1 + 2 ** -4)).all())
+
+
+def test_reader_feeds_the_next_call_at_once(dev):
+    """The reader's output rotated, appended to another cache of another format and read again, without a wait between,
+    eagerly and as a replayed graph on another stream."""
+    T = 700
+    table, rows, kv = _cache(dev, 1, T)
+    _, _, kv8 = _cache(dev, 1, T, 656)
+    g = torch.Generator(device=dev).manual_seed(3)
+    s = dsa.Seq(q_seq=torch.zeros(T, dtype=torch.int32, device=dev), q_pos=torch.arange(T, dtype=torch.int32, device=dev),
+                block_table=table, max_ctx=T, cache_rows=rows)
+    new = torch.randn((T, 576), generator=g, device=dev).to(torch.bfloat16)
+    plan = dsa.Rope.make(64)
+    m4, m8 = _mla(kv), _mla(kv8, dsa.DSA_E4M3)
+    a, b = (torch.empty((T, 576), dtype=torch.bfloat16, device=dev) for _ in range(2))
+
+    def run():
+        dsa.latent_cache_append_rope(s, m4, plan, new[:, :512], new[:, 512:])
+        dsa.latent_cache_read(s, m4, a)
+        dsa.rope(plan, s.q_pos, a[:, 512:], a[:, 512:], inverse=True)
+        dsa.latent_cache_append_rope(s, m8, plan, a[:, :512], a[:, 512:])
+        dsa.latent_cache_read(s, m8, b)
+
+    steps = []
+    for call in (lambda: dsa.latent_cache_append_rope(s, m4, plan, new[:, :512], new[:, 512:]),
+                 lambda: dsa.latent_cache_read(s, m4, a),
+                 lambda: dsa.rope(plan, s.q_pos, a[:, 512:], a[:, 512:], inverse=True),
+                 lambda: dsa.latent_cache_append_rope(s, m8, plan, a[:, :512], a[:, 512:]),
+                 lambda: dsa.latent_cache_read(s, m8, b)):
+        call()
+        torch.cuda.synchronize()
+    want = a.clone(), b.clone(), kv8.clone()
+    # rotated and turned back: two roundings to bf16, each at most 2^-8 of the pair's length (a little more in all)
+    pair = new[:, 512:].float().view(T, 32, 2).norm(dim=-1, keepdim=True)
+    assert bool(((a[:, 512:].float() - new[:, 512:].float()).view(T, 32, 2).abs() <= 2.01 * 2 ** -8 * pair).all())
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    for again in range(3):
+        for t in (a, b, kv, kv8):
+            t.zero_()
+        torch.cuda.synchronize()
+        if again == 0:
+            run()
+        else:
+            with torch.cuda.stream(st):
+                if again == 1:
+                    graph = torch.cuda.CUDAGraph()
+                    with torch.cuda.graph(graph, stream=st):
+                        run()
+                for _ in range(3):
+                    graph.replay()
+        torch.cuda.synchronize()
+        dsa.check_status()
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1]) and torch.equal(kv8, want[2])
+
+
+def test_read_query_feeds_a_decode_step_at_once(dev):
+    """The attention stages its query early in a decode step: here the call before has just written it."""
+    wl = _make(41, ctx=[900, 500, 800], K=128, H=1)
+    r = P.Run(wl, dev)
+    n = wl.T
+    src = torch.from_numpy(np.random.default_rng(42).normal(0, 1, (n, 576)).astype(np.float32)).to(torch.bfloat16).to(dev)
+    table, rows, kv = _cache(dev, 1, 64, 1152)
+    kv = kv.view(torch.bfloat16)
+    s = dsa.Seq(q_seq=torch.zeros(n, dtype=torch.int32, device=dev), q_pos=torch.arange(n, dtype=torch.int32, device=dev),
+                block_table=table, max_ctx=64, cache_rows=rows)
+    m = _mla(kv, dsa.DSA_BF16)
+    dsa.latent_cache_append(s, m, src)
+    q = r.mla.q.view(n, 576)
+    ws = torch.empty(dsa.decode_workspace_size(r.seq, r.idxr, r.mla, 128), dtype=torch.uint8, device=dev)
+    out = torch.empty((n, 1, 512), dtype=torch.bfloat16, device=dev)
+    q.copy_(src)
+    dsa.decode_step(r.seq, r.idxr, r.mla, 128, out, ws)
+    torch.cuda.synchronize()
+    want = out.clone()
+    for _ in range(50):
+        q.fill_(float("nan"))
+        dsa.latent_cache_read(s, m, q)
+        dsa.decode_step(r.seq, r.idxr, r.mla, 128, out, ws)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    dsa.check_status()
