@@ -53,6 +53,10 @@
 // query; the clusters that fit the GPU at once share the items out.  Tiles are counted through a
 // cluster's items, so the next item's rows, codes and first logits are on their way during
 // the last softmax and the output (with a cluster for each item 1290 us instead of 1177).
+// Tiles at an item's end that select nothing -- a context shorter than K -- are left out: the
+// row warps look for the last selected entry when they open an item and say with every tile
+// whether it is its item's first or last (400 queries on a context of 400, K = 2048: 88 us, 273
+// with all tiles).
 //
 // Warps.  0-15 producers, four own and four other rows of a tile each, whichever can go on
 // (in a fixed order the other rows wait for Q K^T of rows just written: 1496 us); codes, scales
@@ -62,12 +66,12 @@
 // tiles' cache rows, row scales and masks, two tiles ahead.  20-27 stage the query, then
 // softmax, a thread one head and 32 of the tile's rows; the four threads of a head agree on m
 // and g through shared memory, when one of them has to let them grow.  Registers are dealt out
-// by setmaxnreg: 224 KB of shared memory leave almost nothing of the L1, and a spilled word
-// comes back from the L2 (24 bytes are, outside the loops' chains).  The code is kept small
+// by setmaxnreg, so that no role spills: 224 KB of shared memory leave almost nothing of the
+// L1, and a spilled word comes back from the L2 (60 spilled bytes: 1155 us).  The code is kept small
 // (rolled loops, short waits): with 98 KB of it every role ran from a cold instruction cache.
 //
-// Measured (2048 selected rows, 128 heads): 1178 us for 2048 queries, 992 TFLOP/s of the
-// 1926 measured; 53.5 us for 64 (one cluster a query: 128 of 152 SMs), 12.4 us for one (a
+// Measured (2048 selected rows, 128 heads): 1144 us for 2048 queries, 1021 TFLOP/s of the
+// 1926 measured; 54.1 us for 64 (one cluster a query: 128 of 152 SMs), 11.6 us for one (a
 // tile each for 16 clusters: latencies).  A tile takes 4300 clocks where its MMAs need 2176: two
 // are in flight, each a chain own rows - Q K^T - other rows - P V, and the links slow one another
 // (of the loop's clocks the load/store pipe has a wavefront in 73 %, tensor operands are read
@@ -114,7 +118,11 @@ constexpr int kOffMask = kOffMax + 4 * kHeads * 2;       // uint32 [2][4] valid 
 constexpr int kOffRmax = kOffMask + 32;                  // float [2][2] largest row scale of a tile's halves
 constexpr int kOffOk = kOffRmax + 16;                    // int [8 softmax warps]
 constexpr int kOffExp = kOffOk + 32;                     // int8 [64 heads] a
-constexpr int kOffBar = kOffExp + kHeads;
+constexpr int kOffInfo = kOffExp + kHeads;               // uint32 [8] what a tile is (tile number mod 8)
+constexpr int kOffBar = kOffInfo + 32;
+// what a tile is: written before its rows are given out; the warps that read it are fewer than
+// eight tiles apart (rows of tile g + 2 wait for Q K^T of g - 1 and so for P V of g - 3)
+constexpr uint32_t kFirst = 1, kLast = 2, kEnd = 4, kThere = 8;   // of its item; last of all; a tile at all
 constexpr int kNumBars = 24;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;
 constexpr int kUsed = kOffMisc + 16;
@@ -291,6 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
   uint64_t* qfull = bars + 19;    // leader: both CTAs' queries staged and their a read
   uint64_t* pfull = bars + 20;    // leader: P written, both CTAs (one buffer: P V of the tile before is complete)
   uint64_t* drain = bars + 21;    // every MMA complete (teardown)
+  volatile uint32_t* info = reinterpret_cast<volatile uint32_t*>(sm + kOffInfo);
   uint64_t* edone = bars + 22;    // [2] an item's output has left the stage of its last tile
   uint32_t* misc = reinterpret_cast<uint32_t*>(sm + kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
@@ -303,15 +312,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
   // keys written and multiplied while this one's last tile is in its softmax.
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
   auto slice_of = [&](int item) -> int { return item - p.split(item) * p.n_split; };
-  auto tiles_of = [&](int item) -> int {
-    const int r0 = slice_of(item) * p.rows_per_split;
-    return (min(K, r0 + p.rows_per_split) - r0 + kTile - 1) / kTile;
-  };
-  auto tiles_in_all = [&]() -> int {
-    int n = 0;   // items: one for each cluster when there are slices
-    for (int item = first; item < p.items; item += step) n += tiles_of(item);
-    return n;
-  };
   auto query_of = [&](int item) -> int { return p.seq.T - 1 - p.heads(p.split(item)); };
   auto head_of = [&](int item) -> int {   // this CTA's first head
     const int i = p.split(item);
@@ -357,7 +357,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
     const int32_t* rows_sm = reinterpret_cast<const int32_t*>(sm + kOffRows);
     shrink_registers<kRegsProducer>();
     cluster_wait();
-    const int ntiles = tiles_in_all();
     const int sub = lane >> 4, blk = lane & 15, l8 = lane >> 3, b8 = lane & 7;
     // In registers.  Own: codes of block `lane` of the warp's four own rows; scale word and
     // rope chunk b8 of row l8.  Other: codes of block blk of this CTA's value dims of rows
@@ -425,21 +424,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
       fetch_v();
       // Own rows of tile a take the stage of a - 2: free once P V of that is complete or, when that
       // was an item's last tile, once the item's output, which goes through the stage, has been
-      // written.  (A cluster has more than one item only without slices, all of one length.)
-      const int per_item = tiles_of(first);
-      int a = 0, b = 0, after_last = per_item + 1, item_n = 0;
-      auto own_free = [&](int a) -> bool {
+      // written.  what: of tiles a, a - 1 and a - 2, four bits each.
+      int a = 0, b = 0, item_n = 0;
+      uint32_t what = info[0], idle = 0;
+      bool more_own = true, end_b = (what & kEnd) != 0;   // end_b: of tile b
+      auto own_free = [&]() -> bool {
         if (a < 2) return true;
-        return a == after_last ? mbar_test(&edone[item_n & 1], (item_n >> 1) & 1)
-                               : mbar_test(&pvdone[a & 1], ((a >> 1) - 1) & 1);
+        return (what >> 8) & kLast ? mbar_test(&edone[item_n & 1], (item_n >> 1) & 1)
+                                   : mbar_test(&pvdone[a & 1], ((a >> 1) - 1) & 1);
       };
-      uint32_t idle = 0;
       uint64_t until = 0;
 #pragma unroll 1
-      while (b < ntiles) {
+      while (true) {
         if (b < a && __all_sync(0xffffffffu, mbar_test(&sfull[b & 1], (b >> 1) & 1))) {
           const uint32_t at = vdst + static_cast<uint32_t>((b & 1) * kStage);
-          if (b + 1 < ntiles) rows_v(b + 1);   // rfull of b + 1: seen for own rows of b
+          const bool last = end_b;
+          if (!last) {
+            end_b = (info[(b + 1) & 7] & kEnd) != 0;
+            rows_v(b + 1);   // rfull of b + 1: seen for own rows of b
+          }
           vsc = vhave ? vsc : 0u;
           uint32_t w[2];
 #pragma unroll
@@ -449,13 +452,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) arrive_pair(leader_addr(&othfull[b & 1]));
-          if (b + 1 < ntiles) fetch_v();
+          if (last) break;
+          fetch_v();
           ++b;
-        } else if (a < ntiles && __all_sync(0xffffffffu, own_free(a))) {
+        } else if (more_own && __all_sync(0xffffffffu, own_free())) {
           const uint32_t st = static_cast<uint32_t>((a & 1) * kStage);
-          if (a + 1 < ntiles) {
+          if ((what >> 8) & kLast) ++item_n;   // a < 2: no such tile
+          more_own = !(what & kEnd);
+          what <<= 4;
+          if (more_own) {
             if (!wait(&rfull[(a + 1) & 1], (a + 1) >> 1)) break;
             rows_k(a + 1);
+            what |= info[(a + 1) & 7];
           }
           ksc = khave ? ksc : 0u;
           uint32_t w[4];
@@ -467,11 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0 && !(p.dbg_withhold && warp == 0 && a == 0)) arrive_pair(leader_addr(&ownfull[a & 1]));
-          if (a + 1 < ntiles) fetch_k();
-          if (a == after_last) {
-            after_last += per_item;
-            ++item_n;
-          }
+          if (more_own) fetch_k();
           ++a;
         } else {
           __nanosleep(160);
@@ -495,13 +499,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
       float rs1[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) pos[k] = pos1[k] = page[k] = row1[k] = -1;
-      // the tile that load_pos comes to next: its item and its number there; the query's position
-      // and sequence go with the tile from step to step
-      int item = first, gi0 = 0, gi1 = 0, qp1 = 0, b1 = 0;   // entries [gi0, gi1) of the item are left
+      // the tile that load_pos comes to next: entries [gi0, gi1) of the open item are left; the
+      // query's position and sequence, and what the tile is, go with it from step to step
+      int item = first, gi0 = 0, gi1 = 0, qp1 = 0, b1 = 0;
+      uint32_t what1 = 0, what = 0;
       const int32_t* idx = nullptr;
       uint32_t bad = 0;
       const int wrow = (warp - kWarpRows) * 64;
       auto load_pos = [&]() {
+        what1 = 0;
         if (gi0 >= gi1 && item < p.items) {
           const int t = query_of(item);
           gi0 = slice_of(item) * p.rows_per_split;
@@ -510,15 +516,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
           qp1 = __ldg(p.seq.q_pos + t);
           b1 = __ldg(p.seq.q_seq + t);
           item += step;
+          what1 = kFirst;
+        }
+        if (what1 & kFirst) {
+          // tiles at the end that select nothing (a context shorter than K) are left out, all but the
+          // item's first: the last 128 entries, then 512 at a time towards the first
+          const int top = gi1;   // most often the last tile's entries settle it
+          for (int e = top; e > gi0 + kTile;) {
+            const int from = max(gi0, e - (e == top ? kTile : 512));
+            int last = -1;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const int i = from + k * 32 + lane;
+              if (i < e && __ldg(idx + i) >= 0) last = i;
+            }
+            last = __reduce_max_sync(0xffffffffu, last);
+            gi1 = max(last + 1, min(gi1, gi0 + kTile));
+            e = last >= 0 ? 0 : from;
+          }
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int i = gi0 + wrow + k * 32 + lane;
           pos1[k] = i < gi1 ? __ldg(idx + i) : -1;
         }
+        if (gi0 < gi1) what1 |= kThere | (gi0 + kTile >= gi1 ? kLast | (item >= p.items ? kEnd : 0u) : 0u);
         gi0 += kTile;
       };
       auto load_page = [&]() {   // of pos <- pos1
+        what = what1;
         int qp = qp1, b = b1;
         if (qp < 0 || qp >= p.seq.max_ctx || b < 0 || b >= p.seq.B) {
           bad |= kDevBadPos;
@@ -547,15 +573,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
         }
       };
       // step j: scales and mask of tile j - 1 and rows of tile j given out, pages of j + 1 and
-      // positions of j + 2 loaded; step -1 only loads
-      load_pos();
-      const int todo = tiles_in_all();
+      // positions of j + 2 loaded; steps -2 and -1 only load
+      uint32_t given = 0;   // what tile j - 1 is
 #pragma unroll 1
-      for (int j = -1; j <= todo; ++j) {
+      for (int j = -2;; ++j) {
         asm volatile("" : "+r"(j));   // one copy of the loop's code
         if (j == 0) cluster_wait();
         const int st = j & 1;
-        if (j >= 1) {
+        if (given) {
           if (j >= 3 &&
               !__all_sync(0xffffffffu, wait_bar(&mfree[st ^ 1], (((j - 1) >> 1) - 1) & 1, abort_flag, wlim)))
             break;
@@ -576,13 +601,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&mfull[st ^ 1]);
+          if (given & kEnd) break;
         }
-        if (j >= 0 && j < todo) {
+        given = j >= 0 ? what : 0u;
+        if (given) {
           if (j >= 2 && !__all_sync(0xffffffffu, wait_bar(&rfree[st], ((j >> 1) - 1) & 1, abort_flag, wlim))) break;
           load_scale();
 #pragma unroll
           for (int k = 0; k < 2; ++k)
             reinterpret_cast<int32_t*>(sm + kOffRows)[st * kTile + wrow + k * 32 + lane] = row1[k];
+          if (warp == kWarpRows && lane == 0) info[j & 7] = given;
           __syncwarp();
           if (lane == 0) mbar_arrive(&rfull[st]);
         }
@@ -596,39 +624,38 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
       const uint32_t tmem = misc[0];
       const uint64_t dq = make_sdesc(smem_u32(sm + kOffQ), 16, 1024, kLayoutSw128);
       const uint64_t dk0 = make_sdesc(smem_u32(sm + kOffStage), 16, 1024, kLayoutSw128);
-      int g = 0, n = 0;   // tiles, items
-      bool ok = rank == 0;
+      int n = 0;   // items
+      bool ok = rank == 0, more = true;
 #pragma unroll 1
-      for (int item = first; item < p.items && ok; item += step, ++n) {
-        ok = __all_sync(0xffffffffu, wait_bar(qfull, n & 1, abort_flag, wlim));
-        const int end = g + tiles_of(item);
+      for (int g = 0; ok && more; ++g) {
+        const int sb = g & 1;
+        // the keys are there, the logit buffer is free and the query is the item's
+        ok = __all_sync(0xffffffffu, wait_bar(&ownfull[sb], (g >> 1) & 1, abort_flag, wlim));
+        if (!ok) break;
+        const uint32_t what = info[g & 7];
+        more = !(what & kEnd);
+        if (g >= 2) ok = __all_sync(0xffffffffu, wait_bar(&sfree[sb], ((g >> 1) - 1) & 1, abort_flag, wlim));
+        if (ok && (what & kFirst)) ok = __all_sync(0xffffffffu, wait_bar(qfull, n++ & 1, abort_flag, wlim));
+        if (!ok) break;
+        tc_fence_after();
+        fence_proxy_async_smem();
+        if (elect_one()) {
+          const uint32_t d = tmem + sb * 64;
+          const uint64_t dk = dk0 + static_cast<uint64_t>((sb * kStage) >> 4);
 #pragma unroll 1
-        for (; g < end && ok; ++g) {
-          const int sb = g & 1;
-          // the logit buffer is free and the keys are there
-          if (g >= 2) ok = __all_sync(0xffffffffu, wait_bar(&sfree[sb], ((g >> 1) - 1) & 1, abort_flag, wlim));
-          if (ok) ok = __all_sync(0xffffffffu, wait_bar(&ownfull[sb], (g >> 1) & 1, abort_flag, wlim));
-          if (!ok) break;
-          tc_fence_after();
-          fence_proxy_async_smem();
-          if (elect_one()) {
-            const uint32_t d = tmem + sb * 64;
-            const uint64_t dk = dk0 + static_cast<uint64_t>((sb * kStage) >> 4);
-#pragma unroll 1
-            for (int a = 0; a < 8; ++a) {   // 64 dims a turn
-              const uint64_t off = static_cast<uint64_t>((a * kAtom) >> 4);
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma_pair(d, dq + off + 2 * kk, dk + off + 2 * kk, kIdescLatent, static_cast<uint32_t>(a | kk));
-            }
-            constexpr uint64_t off = (8 * kAtom) >> 4;
+          for (int a = 0; a < 8; ++a) {   // 64 dims a turn
+            const uint64_t off = static_cast<uint64_t>((a * kAtom) >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              umma_pair(d + kColRope, dq + off + 2 * kk, dk + off + 2 * kk, kIdescRope, static_cast<uint32_t>(kk));
-            commit_pair(&sfull[sb]);
+              umma_pair(d, dq + off + 2 * kk, dk + off + 2 * kk, kIdescLatent, static_cast<uint32_t>(a | kk));
           }
-          __syncwarp();
+          constexpr uint64_t off = (8 * kAtom) >> 4;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_pair(d + kColRope, dq + off + 2 * kk, dk + off + 2 * kk, kIdescRope, static_cast<uint32_t>(kk));
+          commit_pair(&sfull[sb]);
         }
+        __syncwarp();
       }
     } else if (warp == kWarpPv) {
       cluster_wait();
@@ -637,33 +664,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
       const uint64_t dv0 = make_sdesc(smem_u32(sm + kOffStage), kAtom, 1024, kLayoutSw128);
       const uint64_t dp0 = make_sdesc(smem_u32(sm + kOffStage + 8 * kAtom), 16, 1024, kLayoutSw128);
       const uint64_t dp1 = make_sdesc(smem_u32(sm + kOffP1), 16, 1024, kLayoutSw128);
-      int g = 0;
-      bool ok = rank == 0;
+      bool ok = rank == 0, more = true;
 #pragma unroll 1
-      for (int item = first; item < p.items && ok; item += step) {
-        const int begin = g, end = g + tiles_of(item);
+      for (int g = 0; ok && more; ++g) {
+        ok = __all_sync(0xffffffffu, wait_bar(&othfull[g & 1], (g >> 1) & 1, abort_flag, wlim));
+        const uint32_t what = info[g & 7];
+        more = !(what & kEnd);
+        if (ok) ok = __all_sync(0xffffffffu, wait_bar(pfull, g & 1, abort_flag, wlim));
+        if (!ok) break;
+        tc_fence_after();
+        fence_proxy_async_smem();
+        if (elect_one()) {
+          const uint64_t st = static_cast<uint64_t>(((g & 1) * kStage) >> 4);
 #pragma unroll 1
-        for (; g < end && ok; ++g) {
-          ok = __all_sync(0xffffffffu, wait_bar(&othfull[g & 1], (g >> 1) & 1, abort_flag, wlim));
-          if (ok) ok = __all_sync(0xffffffffu, wait_bar(pfull, g & 1, abort_flag, wlim));
-          if (!ok) break;
-          tc_fence_after();
-          fence_proxy_async_smem();
-          if (elect_one()) {
-            const uint64_t st = static_cast<uint64_t>(((g & 1) * kStage) >> 4);
-#pragma unroll 1
-            for (int q = 0; q < 4; ++q) {   // value atoms 2 (q / 2), tile rows [64 (q & 1), 64 (q & 1) + 64)
-              const uint64_t da = (q & 1) ? dp1 : dp0 + st;
-              const uint64_t db = dv0 + st + static_cast<uint64_t>((((q & 1) * 4 + (q >> 1) * 2) * kAtom) >> 4);
+          for (int q = 0; q < 4; ++q) {   // value atoms 2 (q / 2), tile rows [64 (q & 1), 64 (q & 1) + 64)
+            const uint64_t da = (q & 1) ? dp1 : dp0 + st;
+            const uint64_t db = dv0 + st + static_cast<uint64_t>((((q & 1) * 4 + (q >> 1) * 2) * kAtom) >> 4);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma_pair(tmem + kColO + (q >> 1) * 128, da + 2 * kk, db + 128 * kk, kIdescPV,
-                          static_cast<uint32_t>((g - begin) | (q & 1) | kk));
-            }
-            commit_pair(&pvdone[g & 1]);
+            for (int kk = 0; kk < 4; ++kk)
+              umma_pair(tmem + kColO + (q >> 1) * 128, da + 2 * kk, db + 128 * kk, kIdescPV,
+                        static_cast<uint32_t>((~what & kFirst) | (q & 1) | kk));
           }
-          __syncwarp();
+          commit_pair(&pvdone[g & 1]);
         }
+        __syncwarp();
       }
     }
   } else {
@@ -850,11 +874,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
         if (lane == 0) mbar_arrive(&edone[done++ & 1]);
       }
       if (!more) break;
-      const int end = gt + tiles_of(item);
+      bool last_tile = false, stop = false;
       m = g = -INFINITY;
       l = 0.f;
 #pragma unroll 1
-      for (; gt < end; ++gt) {
+      for (; !last_tile; ++gt) {
         const int j = gt, st = j & 1;
         ok = ok && wait_bar(&mfull[st], (j >> 1) & 1, abort_flag, wlim) &&
              wait_bar(&sfull[st], (j >> 1) & 1, abort_flag, wlim);
@@ -886,6 +910,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
             fma2(x[i], x[i + 1], t0, t1, __uint_as_float(rs.x), __uint_as_float(rs.y));
             fma2(x[i + 2], x[i + 3], t2, t3, __uint_as_float(rs.z), __uint_as_float(rs.w));
           }
+          last_tile = (info[j & 7] & kLast) != 0;
           const uint32_t vmask = masks[st * 4 + rq];
           if (vmask != ~0u) {
 #pragma unroll
@@ -919,7 +944,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) ok = ok && oks[2 * k + (warp & 1)] != 0;
           named_bar_sync(head_bar, 128);
-          if (!ok) break;
+          if (!ok) {
+            stop = true;
+            break;
+          }
           const float gx = mx + lrmax;
           const bool need_m = mx > m + kRescaleM, need_g = gx > g + kRescaleG;
           // (g of -inf: nothing in O yet)
@@ -983,7 +1011,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
           mbar_arrive(&mfree[st]);
         }
       }
-      if (gt < end) break;
+      if (stop) break;
     }
   }
 

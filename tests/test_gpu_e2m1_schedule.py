@@ -49,6 +49,40 @@ def test_several_queries_per_cluster(dev, H, T, K):
     assert np.array_equal(out, again) and np.array_equal(lse, lse2)
 
 
+@pytest.mark.parametrize("K", [129, 640, 2000])
+def test_tiles_that_select_nothing(dev, K):
+    """Selections that end early: one entry at every distance from the ends, only the first or the last one, gaps of whole
+    tiles, and nothing; queries by the hundred, so that the ends differ from item to item of a cluster."""
+    T = 310
+    wl = _make(50 + K, ctx=[900], q_len=T, K=K)
+    rng = np.random.default_rng(K)
+    idx = np.full((T, K), -1, np.int32)
+    for t in range(T):
+        n = int(wl.q_pos[t]) + 1
+        kind = t % 7
+        if kind == 0:
+            idx[t, :rng.integers(1, min(K, n))] = 0
+            m = int((idx[t] == 0).sum())
+            idx[t, :m] = rng.choice(n, m, replace=False)
+        elif kind == 1:
+            idx[t, K - 1] = n - 1
+        elif kind == 2:
+            idx[t, 0] = 0
+        elif kind == 3:
+            idx[t, [0, K // 2, K - 1]] = [3, 1, 2]
+        elif kind == 4:
+            idx[t, int(rng.integers(0, K))] = int(rng.integers(0, n))
+        elif kind == 5:
+            at = np.sort(rng.choice(K, min(K, 90), replace=False))
+            idx[t, at] = rng.choice(n, len(at), replace=False)
+    out, lse, _ = P.Run(wl, dev).attn(idx)
+    _check(out, lse, wl, idx, ts=list(range(0, T, 3)))
+    few = dataclasses.replace(wl, T=9, q_per_seq=0, q_seq=wl.q_seq[:9], q_pos=wl.q_pos[:9], q=wl.q[:9])
+    for workspace in (True, False):                  # slices, some of them empty, and one slice
+        out, lse, _ = P.Run(few, dev).attn(idx[:9], workspace=workspace)
+        _check(out, lse, few, idx[:9])
+
+
 def test_maxima_do_not_reach_the_next_query(dev):
     """Every third query's selection has rows with logits hundreds of powers of two above the others', late in it."""
     T, K = 240, 300
