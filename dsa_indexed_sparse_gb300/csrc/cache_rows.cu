@@ -60,8 +60,11 @@ __device__ __forceinline__ float warp_max(float v) {
 __device__ __forceinline__ uint32_t e4m3_code(float v) {
   return static_cast<uint32_t>(__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3));
 }
+__device__ __forceinline__ uint32_t e4m3_code2(float a, float b) {
+  return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3));
+}
 __device__ __forceinline__ uint32_t e4m3_code4(float a, float b, float c, float d) {
-  return e4m3_code(a) | (e4m3_code(b) << 8) | (e4m3_code(c) << 16) | (e4m3_code(d) << 24);
+  return e4m3_code2(a, b) | (e4m3_code2(c, d) << 16);
 }
 // floor(log2 amax) - 8 clamped to [-127, 127]; -127 for 0 (the shared exponent of E4M3 blocks).
 __device__ __forceinline__ int mx_exponent(float amax) {
@@ -142,14 +145,20 @@ __device__ __forceinline__ void write_latent(const float (&v)[16], uint8_t* dst,
   for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v[i]));
   if constexpr (kKind == MlaKind::kE2M1) {
     const int e = e2m1_row_exponent(warp_max(amax));
-    // block scale and codes from exact power-of-two quotients; both divisions IEEE
-    const uint32_t sc = e4m3_code(__fdiv_rn(ldexpf(amax, -e), 6.f));
+    const float p = ldexpf(1.f, -e);   // x p: the power-of-two quotient, exact
+    const uint32_t sc = e4m3_code(__fdiv_rn(amax * p, 6.f));
     const float s = e4m3_to_float(static_cast<uint8_t>(sc));
     uint32_t w[2] = {0u, 0u};
     if (s > 0.f) {
+      // The quotients by s, which has four significant bits, of values with eight: one that is not
+      // half way between two codes differs from there by 2^-8 of itself at least, so the product
+      // with the rounded reciprocal, rounded to f16 (2^-11), falls on the same side, and one
+      // that is half way comes out so.  (With a division for each
+      // value writing and reading 16,384 rows took 17.9 us, so 15.7.)
+      const float r = __frcp_rn(s);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float2 q = make_float2(__fdiv_rn(ldexpf(v[2 * i], -e), s), __fdiv_rn(ldexpf(v[2 * i + 1], -e), s));
+        const float2 q = __half22float2(__floats2half2_rn(v[2 * i] * p * r, v[2 * i + 1] * p * r));
         w[i >> 2] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(q, __NV_E2M1, cudaRoundNearest)) << (8 * (i & 3));
       }
     }
@@ -168,8 +177,9 @@ __device__ __forceinline__ void write_latent(const float (&v)[16], uint8_t* dst,
 #pragma unroll
       for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       const int e = mx_exponent(amax);
+      const float p = ldexpf(1.f, -e);   // representable: -e is in [-127, 127]
 #pragma unroll
-      for (int i = 0; i < 16; ++i) q[i] = ldexpf(v[i], -e);
+      for (int i = 0; i < 16; ++i) q[i] = v[i] * p;
       if ((lane & 7) == 0) reinterpret_cast<float*>(dst + 512)[lane >> 3] = ldexpf(1.f, e);
     }
     reinterpret_cast<uint4*>(dst)[lane] =
@@ -292,8 +302,9 @@ __global__ void __launch_bounds__(kIndexWarps * 32) index_write_kernel(SeqArgs s
 #pragma unroll
       for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       const int e = mx_exponent(amax);
+      const float p = ldexpf(1.f, -e);
       if (c < nq) {
-        dst[c] = e4m3_code4(ldexpf(f.x, -e), ldexpf(f.y, -e), ldexpf(f.z, -e), ldexpf(f.w, -e));
+        dst[c] = e4m3_code4(f.x * p, f.y * p, f.z * p, f.w * p);
         if ((lane & 7) == 0) static_cast<uint8_t*>(a.k_scale)[row * (a.D / 32) + c / 8] = static_cast<uint8_t>(e + 127);
       }
     }
