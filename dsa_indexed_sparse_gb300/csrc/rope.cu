@@ -213,8 +213,8 @@ cudaError_t launch_rope(const RopeArgs& rope, int32_t T, int32_t H, const int32_
   const int slots = std::max(1, kRopeThreads / a.units);
   // A block takes up to eight rows a thread, four of two vectors in the half layout -- as many
   // as a thread loads at once (99.5 us for 16,384 x 128 bf16 heads with eight, 83.6 with four);
-  // the cosines are fetched once per thread and token -- fewer while the blocks do not fill the GPU twice: part of one token's
-  // heads, or the heads of several tokens.
+  // the cosines are fetched once per thread and token -- fewer while the blocks do not fill
+  // the GPU twice: part of one token's heads, or the heads of several tokens.
   int rows = rope.half && aligned ? 4 : 8;
   while (rows > 1 && static_cast<int64_t>(T) * H < 2ll * env.num_sms * slots * rows) rows /= 2;
   if (H > slots * rows)

@@ -164,3 +164,37 @@ def test_read_query_feeds_a_decode_step_at_once(dev):
         torch.cuda.synchronize()
         assert torch.equal(out, want)
     dsa.check_status()
+
+
+def test_codes_at_every_border(dev):
+    """For every block scale the values half way between two codes and their bf16 neighbours on both sides, of both signs:
+    the codes are the oracle's, computed from 64-bit quotients."""
+    scales = [v for v in O.decode_e4m3(np.arange(127, dtype=np.uint8)) if 0 < v <= 256]
+    blocks = []
+    for sc in scales:
+        vals = []
+        for mid in (0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0):
+            x = torch.tensor(mid * sc, dtype=torch.float64).to(torch.bfloat16)
+            assert float(x) == mid * sc                     # at most seven significant bits
+            bits = int(x.view(torch.int16))
+            for b in (bits - 1, bits, bits + 1):
+                v = float(torch.tensor(b, dtype=torch.int16).view(torch.bfloat16))
+                vals += [v, -v]
+        vals += [0.0, -0.0, 6 * sc]
+        for i in range(0, len(vals), 15):
+            blocks.append([6 * sc] + (vals[i:i + 15] + [0.0] * 15)[:15])   # the block's maximum: its scale is sc
+    top = [1536.0] + [0.0] * 15                             # the row's maximum: a row scale of 1
+    blocks += [top] * (-len(blocks) % 31)
+    rows = np.array([top + sum(blocks[i:i + 31], []) for i in range(0, len(blocks), 31)], np.float32)
+    T = len(rows)
+    table, n, kv = _cache(dev, 1, T)
+    s = dsa.Seq(q_seq=torch.zeros(T, dtype=torch.int32, device=dev), q_pos=torch.arange(T, dtype=torch.int32, device=dev),
+                block_table=table, max_ctx=T, cache_rows=n)
+    new = torch.cat([torch.from_numpy(rows), torch.zeros((T, 64))], dim=1).to(torch.bfloat16).to(dev)
+    dsa.latent_cache_append(s, _mla(kv), new)
+    dsa.check_status()
+    at = O.physical_rows(table[0].cpu().numpy(), 64, np.arange(T))
+    got = kv.cpu().numpy()[at]
+    for t in range(T):
+        want = O.e2m1_row(rows[t].astype(np.float64), np.zeros(64))
+        assert np.array_equal(got[t], want), (t, np.nonzero(got[t] != want)[0][:8])
