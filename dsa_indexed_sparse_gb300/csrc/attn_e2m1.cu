@@ -28,9 +28,11 @@
 // logits of its own, and the row scale, in fp32, where the two meet:
 //     x = (latent logit * 2^a) * row scale + rope logit.
 // P is f16 as well and carries the row scale: P = 2^(x c - m) * row scale * 2^(m - g),
-// c = scale * log2 e, with m a running bound of x c and g one of x c + log2(row
-// scale).  Both move only when they grow, m by more than 2^64 (l is fp32) and g by
-// more than 2^14 (P stays below 2^15; what falls under f16's 2^-24 is 2^-38 of it).
+// c = scale * log2 e, with m a running bound of x c and g one of x c + log2(row scale), less 7.
+// Both move only when they grow: m by more than 2^64 (l is fp32), g when P would pass 2^15.  P
+// of the largest term is 2^7 when g is set, and what falls under f16's 2^-24 is 2^-31 of
+// that: a value that is small because the rows with weight are 0 there is off by
+// 2^-32 of the other rows' magnitudes at most, each as if it had weight 1.
 // f16 rounds P by 2^-12 of itself, an eighth of bf16's, so the sum that normalises
 // the output is that of the unrounded weights, the one the log-sum-exp takes too.
 //
@@ -93,7 +95,8 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescaleM = 64.0f, kRescaleG = 14.0f;   // growth of m and g that is let pass, log2 units
+constexpr float kRescaleM = 64.0f;                       // growth of m that is let pass, log2 units
+constexpr float kPStart = 7.0f, kPMost = 15.0f;          // log2 of the largest P: when g is set, at most
 
 constexpr int kHeads = 64;            // heads per CTA
 constexpr int kTile = 128;            // selected rows per tile
@@ -493,8 +496,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
     if (warp >= kWarpRows) {
       // ------------------------------------------------ the tiles' rows, row scales and masks
       if (p.early_query) grid_dep_wait();   // the selected indices come from the kernel before
-      // Tile row 32 k + lane from wrow on, k = 0, 1.  A selected entry's way to its row, a tile's time between
-      // the steps: the position, its page id, the cache row, the row's scale.
+      // Tile row 32 k + lane from wrow on, k = 0, 1.  A selected entry's way to its row, a tile's
+      // time between the steps: the position, its page id, the cache row, the row's scale.
       int pos[2], pos1[2], page[2], row1[2];
       float rs1[2];
 #pragma unroll
@@ -589,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const float mine = row1[k] >= 0 ? rs1[k] : 0.f;
-            rmax = fmaxf(rmax, mine);
+            rmax = fmaxf(rmax, fabsf(mine));
             mask[k] = __ballot_sync(0xffffffffu, row1[k] >= 0);
             reinterpret_cast<float*>(sm + kOffScale)[(st ^ 1) * kTile + wrow + k * 32 + lane] = mine;
           }
@@ -604,6 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
           if (given & kEnd) break;
         }
         given = j >= 0 ? what : 0u;
+        if (j >= 0 && !given) break;   // not before the end
         if (given) {
           if (j >= 2 && !__all_sync(0xffffffffu, wait_bar(&rfree[st], ((j >> 1) - 1) & 1, abort_flag, wlim))) break;
           load_scale();
@@ -928,7 +932,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
         // to let m or g grow; only then (the first tile, and seldom after) do they exchange
         // their maxima.
         const float lrmax = __log2f(rmax);
-        const bool grow = named_bar_or(head_bar, 128, !ok || mx > m + kRescaleM || mx + lrmax > g + kRescaleG);
+        const bool grow = named_bar_or(head_bar, 128, !ok || mx > m + kRescaleM || mx + lrmax > g + kPMost);
         // P has one buffer and O may have to be rescaled: P V of the tile before is complete
         bool pv_ok = true;
         if (j >= 1 && ok) pv_ok = wait_bar(&pvdone[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, wlim);
@@ -948,8 +952,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
             stop = true;
             break;
           }
-          const float gx = mx + lrmax;
-          const bool need_m = mx > m + kRescaleM, need_g = gx > g + kRescaleG;
+          const float gx = mx + lrmax - kPStart;
+          const bool need_m = mx > m + kRescaleM, need_g = mx + lrmax > g + kPMost;
           // (g of -inf: nothing in O yet)
           if (__any_sync(0xffffffffu, need_g && g > -INFINITY)) {
             tc_fence_after();

@@ -202,3 +202,45 @@ def test_output_beside_other_rows(dev):
     dsa.check_status()
     assert np.array_equal(out.float().cpu().numpy(), want)
     assert bool((buf[:8] == 7).all()) and bool((buf[8 + n:] == 7).all())
+
+
+def test_row_scales_of_either_sign(dev):
+    """Row scales are any fp32 numbers to the reader: negative ones turn a row's latent part round, large and small ones mix."""
+    wl = _make(61, ctx=[700, 500], K=300)
+    kv = wl.kv.copy()
+    rs = kv[:, 288:292].copy().view("<f4")[:, 0]
+    rng = np.random.default_rng(62)
+    rs = rs * np.where(rng.random(len(rs)) < 0.5, -1.0, 1.0).astype("<f4") * 2.0 ** rng.integers(-6, 3, len(rs)).astype("<f4")
+    kv[:, 288:292] = rs.astype("<f4").view(np.uint8).reshape(-1, 4)
+    wl = dataclasses.replace(wl, kv=kv)
+    idx = _selection(rng, wl, 300, hole=0.1)
+    for workspace in (True, False):
+        out, lse, _ = P.Run(wl, dev).attn(idx, workspace=workspace)
+        _check(out, lse, wl, idx)
+    # Values of 2^18: what a weight in f16 loses shows beside outputs that are small because the rows with weight are 0
+    # there.  P = p rs 2^(m - g) is off by half of f16's smallest step, 2^-25, where it is below 2^-14, so an output by
+    # 2^(g - m) / l * sum_s 2^-25 |v_s / rs_s|.  g <= max(x) + log2 max(rs) - 7 with the maximum x (log2 units) rounded up
+    # by 2^-7 of itself at most, and l >= 2^(max(x) - m): 2^-32 max(rs) 2^(|max x| / 128) sum_s |v_s / rs_s|.
+    kv = kv.copy()
+    big = (-np.abs(rs) * np.float32(2.0 ** 18)).astype("<f4")
+    kv[:, 288:292] = big.view(np.uint8).reshape(-1, 4)
+    q = torch.from_numpy(O.decode_bf16(wl.q).astype(np.float32))
+    q[..., :512] *= 2.0 ** -18
+    wl = dataclasses.replace(wl, kv=kv, q=W._bf16_bits(q))
+    out, lse, _ = P.Run(wl, dev).attn(idx)
+    for t in range(wl.T):
+        sel = idx[t][idx[t] >= 0].astype(np.int64)
+        o_out, o_lse = O.sparse_mla_attn_row(wl, t, idx[t])
+        rows = O.physical_rows(wl.block_table[wl.q_seq[t]], wl.page_size, sel)
+        v = O.latent_rows(wl, rows)
+        logits = wl.softmax_scale * (O.mla_query(wl, t) @ v.T)
+        p = np.exp(logits - o_lse[:, None])
+        A = p @ np.abs(v[:, :512])
+        r = np.abs(big[rows].astype(np.float64))
+        lost = 2.0 ** -32 * r.max() * (np.abs(v[:, :512]) / r[:, None]).sum(0)
+        lost = lost[None] * 2.0 ** (np.abs(logits).max(1, keepdims=True) * 1.4427 / 128)
+        lse_tol = 576 * 2.0 ** -24 * abs(wl.softmax_scale) * (np.abs(O.mla_query(wl, t)) @ np.abs(v).T).max(1) + 1e-4
+        tol = 1.01 * 2.0 ** -8 * (2 * A + 2 * np.abs(o_out)) + 2 * lse_tol[:, None] * A + lost
+        err = np.abs(out[t] - o_out)
+        assert np.all(err <= tol), (t, float((err / tol).max()))
+        assert np.all(np.abs(lse[t] - o_lse) <= lse_tol)
