@@ -332,21 +332,24 @@ def rope(plan: Rope, pos: torch.Tensor, x: torch.Tensor, out: torch.Tensor, inve
     x (in place) or shares no value with it.  inverse: the transposed matrix -- the
     gradient of the rotation."""
     d = plan.desc()
-    shape = x.shape
-    if len(shape) not in (2, 3) or shape[-1] != d.d_rot or out.shape != shape:
+    shape, xs, os_ = x.shape, x.stride(), out.stride()
+    n = len(shape)
+    if n not in (2, 3) or shape[-1] != d.d_rot or out.shape != shape:
         raise ValueError("x and out must be [T, H, d_rot] or [T, d_rot]")
+    if xs[-1] != 1 or os_[-1] != 1:
+        raise ValueError("the last dim of x and out must be contiguous")
     dtype = _FLOAT_CODES.get(x.dtype)
     if dtype is None or out.dtype != x.dtype:
         raise ValueError("x and out must both be bfloat16 or float32")
-    if pos.dtype != torch.int32 or pos.shape != shape[:1] or not pos.is_contiguous():
+    T = shape[0]
+    if pos.dtype != torch.int32 or pos.dim() != 1 or pos.numel() != T or not pos.is_contiguous():
         raise ValueError("pos must be contiguous int32 [T]")
-    if len(shape) == 3:
-        H, (xt, xh, _), (ot, oh, _) = shape[1], x.stride(), out.stride()
-    else:
-        H, xt, xh, ot, oh = 1, x.stride(0), 0, out.stride(0), 0
     dev = _on_current(plan)
-    _check(_lib.dsa_rope(ctypes.byref(d), shape[0], H, _rows(pos, "pos", dev), dtype, _rows(x, "x", dev), xt, xh,
-                         _rows(out, "out", dev), ot, oh, 1 if inverse else 0, _stream(stream, dev)))
+    if pos.get_device() != dev or x.get_device() != dev or out.get_device() != dev:
+        raise ValueError("pos, x and out must be on the current CUDA device")
+    H, xh, oh = (shape[1], xs[1], os_[1]) if n == 3 else (1, 0, 0)
+    _check(_lib.dsa_rope(ctypes.byref(d), T, H, pos.data_ptr(), dtype, x.data_ptr(), xs[0], xh, out.data_ptr(),
+                         os_[0], oh, 1 if inverse else 0, _stream(stream, dev)))
     return out
 
 
@@ -449,13 +452,17 @@ def latent_cache_append_rope(seq: Seq, mla: Mla, plan: Rope, latent: torch.Tenso
     want = torch.float32 if m.dtype == DSA_F32 else torch.bfloat16
     if latent.dtype != want or k_rope.dtype != want:
         raise ValueError(f"latent and k_rope must be {want} for this cache")
-    if latent.shape != (s.T, m.d_latent) or k_rope.shape != (s.T, m.d_rope):
+    T = s.T
+    if latent.shape != (T, m.d_latent) or k_rope.shape != (T, m.d_rope):
         raise ValueError("latent must be [T, d_latent] and k_rope [T, d_rope]")
+    (lt, l1), (kt, k1) = latent.stride(), k_rope.stride()
+    if l1 != 1 or k1 != 1:
+        raise ValueError("the last dim of latent and k_rope must be contiguous")
     dev = _on_current(seq, mla, plan)
-    _check(_lib.dsa_latent_cache_append_rope(ctypes.byref(s), ctypes.byref(m), ctypes.byref(r),
-                                             _rows(latent, "latent", dev), latent.stride(0),
-                                             _rows(k_rope, "k_rope", dev), k_rope.stride(0), m.kv_cache,
-                                             _stream(stream, dev)))
+    if latent.get_device() != dev or k_rope.get_device() != dev:
+        raise ValueError("latent and k_rope must be on the current CUDA device")
+    _check(_lib.dsa_latent_cache_append_rope(ctypes.byref(s), ctypes.byref(m), ctypes.byref(r), latent.data_ptr(), lt,
+                                             k_rope.data_ptr(), kt, m.kv_cache, _stream(stream, dev)))
 
 
 def index_cache_append_rope(seq: Seq, plan: Rope, k_new: torch.Tensor, k_cache: torch.Tensor, k_scale: torch.Tensor,
@@ -484,9 +491,14 @@ def latent_cache_read(seq: Seq, mla: Mla, out: torch.Tensor, stream=None) -> tor
     dtype = _FLOAT_CODES.get(out.dtype)
     if dtype is None:
         raise ValueError("out must be bfloat16 or float32")
+    stride, last = out.stride()
+    if last != 1:
+        raise ValueError("the last dim of out must be contiguous")
     dev = _on_current(seq, mla)
-    _check(_lib.dsa_latent_cache_read(ctypes.byref(s), ctypes.byref(m), m.kv_cache, dtype, _rows(out, "out", dev),
-                                      out.stride(0), _stream(stream, dev)))
+    if out.get_device() != dev:
+        raise ValueError("out must be on the current CUDA device")
+    _check(_lib.dsa_latent_cache_read(ctypes.byref(s), ctypes.byref(m), m.kv_cache, dtype, out.data_ptr(), stride,
+                                      _stream(stream, dev)))
     return out
 
 
