@@ -198,3 +198,38 @@ def test_codes_at_every_border(dev):
     for t in range(T):
         want = O.e2m1_row(rows[t].astype(np.float64), np.zeros(64))
         assert np.array_equal(got[t], want), (t, np.nonzero(got[t] != want)[0][:8])
+
+
+def test_rows_beyond_32_bit_offsets(dev):
+    """A cache of more than 2^32 bytes whose used pages lie at both ends: the same rows, values and attention as in a
+    small cache, bit for bit."""
+    T, n_small = 200, 256
+    rows = ((1 << 32) // 432 // 64 + 80) * 64
+    big = torch.empty((rows, 432), dtype=torch.uint8, device=dev)
+    small = torch.zeros((n_small, 432), dtype=torch.uint8, device=dev)
+    last = rows // 64 - 1
+    tables = {"small": torch.tensor([[2, 0, 3, 1]], dtype=torch.int32, device=dev),
+              "big": torch.tensor([[last, 0, last - 1, last - 77]], dtype=torch.int32, device=dev)}
+    g = torch.Generator(device=dev).manual_seed(9)
+    new = torch.randn((T, 576), generator=g, device=dev).to(torch.bfloat16)
+    q = torch.randn((5, 128, 576), generator=g, device=dev).to(torch.bfloat16)
+    plan = dsa.Rope.make(64)
+    pos = torch.arange(T, dtype=torch.int32, device=dev)
+    idx = torch.stack([torch.randperm(150 + t, generator=g, device=dev)[:140] for t in range(5)]).to(torch.int32)
+    got = {}
+    for name, kv in (("small", small), ("big", big)):
+        common = dict(block_table=tables[name], max_ctx=256, cache_rows=kv.shape[0])
+        s = dsa.Seq(q_seq=torch.zeros(T, dtype=torch.int32, device=dev), q_pos=pos, **common)
+        m = dsa.Mla(q=q, kv_cache=kv, d_latent=512, d_rope=64, softmax_scale=0.07, dtype=dsa.DSA_E2M1)
+        dsa.latent_cache_append_rope(s, m, plan, new[:, :512], new[:, 512:])
+        vals = torch.empty((T, 576), device=dev)
+        dsa.latent_cache_read(s, m, vals)
+        queries = dsa.Seq(q_seq=torch.zeros(5, dtype=torch.int32, device=dev), q_pos=pos[150:155].clone(), **common)
+        out = torch.empty((5, 128, 512), dtype=torch.bfloat16, device=dev)
+        lse = torch.empty((5, 128), device=dev)
+        ws = torch.empty(max(16, dsa.sparse_mla_attn_workspace_size(queries, m, 140)), dtype=torch.uint8, device=dev)
+        dsa.sparse_mla_attn(queries, m, idx, 140, out, lse=lse, workspace=ws)
+        dsa.check_status()
+        got[name] = vals, out, lse
+    assert all(torch.equal(a, b) for a, b in zip(got["small"], got["big"]))
+    assert torch.equal(big[last * 64:], small[2 * 64:3 * 64])
