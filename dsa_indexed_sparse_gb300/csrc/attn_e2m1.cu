@@ -72,8 +72,8 @@
 // L1, and a spilled word comes back from the L2 (60 spilled bytes: 1155 us).  The code is kept small
 // (rolled loops, short waits): with 98 KB of it every role ran from a cold instruction cache.
 //
-// Measured (2048 selected rows, 128 heads): 1144 us for 2048 queries, 1021 TFLOP/s of the
-// 1926 measured; 54.1 us for 64 (one cluster a query: 128 of 152 SMs), 11.6 us for one (a
+// Measured (2048 selected rows, 128 heads): 1147 us for 2048 queries, 1018 TFLOP/s of the
+// 1926 measured; 54.4 us for 64 (one cluster a query: 128 of 152 SMs), 11.6 us for one (a
 // tile each for 16 clusters: latencies).  A tile takes 4300 clocks where its MMAs need 2176: two
 // are in flight, each a chain own rows - Q K^T - other rows - P V, and the links slow one another
 // (of the loop's clocks the load/store pipe has a wavefront in 73 %, tensor operands are read
