@@ -233,3 +233,24 @@ def test_rows_beyond_32_bit_offsets(dev):
         got[name] = vals, out, lse
     assert all(torch.equal(a, b) for a, b in zip(got["small"], got["big"]))
     assert torch.equal(big[last * 64:], small[2 * 64:3 * 64])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("T,d", [(1, 64), (37, 16), (1000, 32), (3001, 64), (700, 512)])
+def test_one_head_is_turned_as_one_of_many(dev, T, d, layout, dtype):
+    """One head's tokens (which take their cosines without the detour that many heads share) against the same values as
+    one of three heads, bit for bit; forwards, backwards and in place."""
+    g = torch.Generator(device=dev).manual_seed(T + d)
+    x = torch.randn((T, 3, d), generator=g, device=dev).to(dtype)
+    pos = torch.randint(0, 1 << 20, (T,), generator=g, device=dev, dtype=torch.int32)
+    plan = dsa.Rope.make(d, layout=layout, scaling="yarn", factor=8.0, original_ctx=4096)
+    for inverse in (False, True):
+        many = torch.empty_like(x)
+        dsa.rope(plan, pos, x, many, inverse=inverse)
+        one = torch.empty((T, d), dtype=dtype, device=dev)
+        dsa.rope(plan, pos, x[:, 1], one, inverse=inverse)
+        assert torch.equal(one, many[:, 1])
+        y = x[:, 2].clone()
+        dsa.rope(plan, pos, y, y, inverse=inverse)
+        assert torch.equal(y, many[:, 2])
