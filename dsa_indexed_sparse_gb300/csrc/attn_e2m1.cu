@@ -3,8 +3,7 @@
 // The mathematics is attn.cu's: for query t, head h and its selected rows S,
 //     logit_s = scale * q[t,h] . row_s[0:576],  out = sum_s softmax(logit)_s row_s[0:512],
 //     lse = log sum_s exp(logit_s),
-// with row_s the values the codes stand for, widened to bf16 (code * block scale *
-// row scale: at most six significant bits, so exact for a power-of-two row scale).
+// with row_s the values the codes stand for, code * block scale * row scale.
 //
 // What bounds it: a row is 432 bytes and 278,528 flop for 128 heads, 645 flop per
 // byte, so the tensor cores (284 flop per byte at this card's measured rates).  O of

@@ -244,3 +244,28 @@ def test_row_scales_of_either_sign(dev):
         err = np.abs(out[t] - o_out)
         assert np.all(err <= tol), (t, float((err / tol).max()))
         assert np.all(np.abs(lse[t] - o_lse) <= lse_tol)
+
+
+def test_two_streams_at_once(dev):
+    """Two calls with several queries per cluster and two with slices, again and again on two streams: the same bits."""
+    calls = []
+    for seed, T, K in ((71, 300, 200), (72, 4, 900)):
+        wl = _make(seed, ctx=[1100], q_len=T, K=K)
+        idx = torch.from_numpy(_selection(np.random.default_rng(seed), wl, K, hole=0.1)).to(dev)
+        for copy in range(2):
+            r = P.Run(wl, dev)
+            out = torch.empty((T, wl.H, 512), dtype=torch.bfloat16, device=dev)
+            ws = torch.empty(max(16, dsa.sparse_mla_attn_workspace_size(r.seq, r.mla, K)), dtype=torch.uint8, device=dev)
+            dsa.sparse_mla_attn(r.seq, r.mla, idx, K, out, workspace=ws)
+            torch.cuda.synchronize()
+            calls.append((r, idx, K, out, ws, out.clone(), torch.cuda.Stream()))
+    for _ in range(10):
+        for r, idx, K, out, ws, want, s in calls:
+            with torch.cuda.stream(s):
+                out.zero_()
+                for _ in range(5):
+                    dsa.sparse_mla_attn(r.seq, r.mla, idx, K, out, workspace=ws)
+        torch.cuda.synchronize()
+        for r, idx, K, out, ws, want, s in calls:
+            assert torch.equal(out, want)
+    dsa.check_status()
