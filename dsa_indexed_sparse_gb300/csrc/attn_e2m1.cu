@@ -64,20 +64,22 @@
 // and rope are loaded into registers a tile ahead, right after the registers' last use, a
 // row's whole 256 or 128 bytes by neighbouring lanes (32-byte pieces of eight rows took three
 // times as long).  16 Q K^T and 17 P V (rank 0 issues for both CTAs).  18 and 19 find the
-// tiles' cache rows, row scales and masks, two tiles ahead.  20-27 stage the query, then
-// softmax, a thread one head and 32 of the tile's rows; the four threads of a head agree on m
+// tiles' cache rows, row scales and masks, two tiles ahead.  20-27 turn the query, which the TMA
+// brings once Q K^T of the item before is complete, into f16; then softmax, a thread one head and 32 of the tile's rows; the four threads of a head agree on m
 // and g through shared memory, when one of them has to let them grow.  Registers are dealt out
 // by setmaxnreg, so that no role spills: 224 KB of shared memory leave almost nothing of the
-// L1, and a spilled word comes back from the L2 (60 spilled bytes: 1155 us).  The code is kept small
+// L1, and a spilled word comes back from the L2 (60 spilled bytes cost 1 %).  The code is kept small
 // (rolled loops, short waits): with 98 KB of it every role ran from a cold instruction cache.
 //
-// Measured (2048 selected rows, 128 heads): 1147 us for 2048 queries, 1018 TFLOP/s of the
-// 1926 measured; 54.4 us for 64 (one cluster a query: 128 of 152 SMs), 11.6 us for one (a
+// Measured (2048 selected rows, 128 heads): 1116 us for 2048 queries, 1047 TFLOP/s of the
+// 1926 measured; 54.7 us for 64 (one cluster a query: 128 of 152 SMs), 11.6 us for one (a
 // tile each for 16 clusters: latencies).  A tile takes 4300 clocks where its MMAs need 2176: two
 // are in flight, each a chain own rows - Q K^T - other rows - P V, and the links slow one another
 // (of the loop's clocks the load/store pipe has a wavefront in 73 %, tensor operands are read
 // in 45 %, issue slots are taken in 54 %).
 // The 48-row kernel of attn.cu's kind, which widens every row in both CTAs: 2171, 100 and 11.7.
+#include <cuda.h>
+
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -120,12 +122,12 @@ constexpr int kOffMask = kOffMax + 4 * kHeads * 2;       // uint32 [2][4] valid 
 constexpr int kOffRmax = kOffMask + 32;                  // float [2][2] largest row scale of a tile's halves
 constexpr int kOffOk = kOffRmax + 16;                    // int [8 softmax warps]
 constexpr int kOffExp = kOffOk + 32;                     // int8 [64 heads] a
-constexpr int kOffInfo = kOffExp + kHeads;               // uint32 [8] what a tile is (tile number mod 8)
-constexpr int kOffBar = kOffInfo + 32;
+constexpr int kOffInfo = kOffExp + kHeads;               // uint8 [8] what a tile is (tile number mod 8)
+constexpr int kOffBar = kOffInfo + 8;
 // what a tile is: written before its rows are given out; the warps that read it are fewer than
 // eight tiles apart (rows of tile g + 2 wait for Q K^T of g - 1 and so for P V of g - 3)
 constexpr uint32_t kFirst = 1, kLast = 2, kEnd = 4, kThere = 8;   // of its item; last of all; a tile at all
-constexpr int kNumBars = 24;
+constexpr int kNumBars = 25;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;
 constexpr int kUsed = kOffMisc + 16;
 constexpr int kSmemBytes = 232448;
@@ -275,7 +277,8 @@ __device__ __forceinline__ void widen_codes(uint2 u, uint32_t scale_code, uint32
   }
 }
 
-__global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_e2m1_kernel(const __grid_constant__ CUtensorMap qmap, PairParams p) {
   grid_dep_launch();   // the kernel after waits for this grid before it reads what this grid writes
   extern __shared__ __align__(1024) uint8_t sm_raw[];
   uint8_t* sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
@@ -301,10 +304,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
   uint64_t* qfull = bars + 19;    // leader: both CTAs' queries staged and their a read
   uint64_t* pfull = bars + 20;    // leader: P written, both CTAs (one buffer: P V of the tile before is complete)
   uint64_t* drain = bars + 21;    // every MMA complete (teardown)
-  volatile uint32_t* info = reinterpret_cast<volatile uint32_t*>(sm + kOffInfo);
+  volatile uint8_t* info = sm + kOffInfo;
   uint64_t* edone = bars + 22;    // [2] an item's output has left the stage of its last tile
+  uint64_t* qraw = bars + 24;     // an item's query has come
   uint32_t* misc = reinterpret_cast<uint32_t*>(sm + kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
+  volatile int* fetched = abort_flag + 1;   // the number of the cluster's item whose query was fetched last
   const uint64_t wlim = p.wait_limit_ns;
   const int K = p.a.K, H = p.a.H;
 
@@ -318,6 +323,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
   auto head_of = [&](int item) -> int {   // this CTA's first head
     const int i = p.split(item);
     return (i - p.heads(i) * p.head_blocks) * 128 + static_cast<int>(rank) * kHeads;
+  };
+
+  auto row_of = [&](int item) -> int { return query_of(item) * H + head_of(item); };   // < 2^31
+  // Fetches an item's query, 64 heads as they are (heads beyond H: the next token's, or zeros; nothing
+  // is written of them), into its nine swizzled atoms; one thread.
+  auto load_query = [&](int row) {
+    mbar_arrive_expect_tx(qraw, 9 * kAtom);
+#pragma unroll 1
+    for (int a = 0; a < 9; ++a) tma_load_2d(sm + kOffQ + a * kAtom, &qmap, qraw, a * 64, row);
   };
 
   // Warps set out as soon as they can: only what reaches the other CTA, the barriers or TMEM
@@ -338,8 +352,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
     mbar_init(pfull, 16);
     mbar_init(drain, 2);
     mbar_init(qstaged, 8);
+    mbar_init(qraw, 1);
     mbar_init(qfull, 16);
     *abort_flag = 0;
+    *fetched = 0;
     fence_mbar_init();
   }
   __syncwarp();
@@ -494,6 +510,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
     shrink_registers<kRegsMma>();
     if (warp >= kWarpRows) {
       // ------------------------------------------------ the tiles' rows, row scales and masks
+      if (warp == kWarpRows && lane == 0) load_query(row_of(first));   // its thread made the barrier
+      __syncwarp();
       if (p.early_query) grid_dep_wait();   // the selected indices come from the kernel before
       // Tile row 32 k + lane from wrow on, k = 0, 1.  A selected entry's way to its row, a tile's
       // time between the steps: the position, its page id, the cache row, the row's scale.
@@ -613,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
 #pragma unroll
           for (int k = 0; k < 2; ++k)
             reinterpret_cast<int32_t*>(sm + kOffRows)[st * kTile + wrow + k * 32 + lane] = row1[k];
-          if (warp == kWarpRows && lane == 0) info[j & 7] = given;
+          if (warp == kWarpRows && lane == 0) info[j & 7] = static_cast<uint8_t>(given);
           __syncwarp();
           if (lane == 0) mbar_arrive(&rfull[st]);
         }
@@ -712,29 +730,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
     const volatile uint32_t* masks = reinterpret_cast<const volatile uint32_t*>(sm + kOffMask);
     const uint32_t prow0 = smem_u32(sm + (half ? kOffP1 : kOffStage + 8 * kAtom)) + static_cast<uint32_t>(hl * 128);
     const uint32_t pstep = half ? 0u : static_cast<uint32_t>(kStage);   // rows 0-63: the stage's rope atom
-    // The query: eight heads a warp, copied as they are and, the latent part, turned in place
-    // into f16 with a power of two per head.  Loops, not straight code: this runs once an item, from
+    // The query: eight heads a warp, their latent part turned in place into f16 with a power of
+    // two per head.  Loops, not straight code: this runs once an item, from
     // a cold instruction cache.
     const uint32_t qsm = smem_u32(sm + kOffQ);
-    auto stage_query = [&](int item) {
-      const int t = query_of(item), h0 = head_of(item), w8 = (warp - kWarpSoft) * 8;
-      const uint4* qg = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.a.q) +
-                                                       (static_cast<int64_t>(t) * H + h0 + w8) * kDqk);
-#pragma unroll 1
-      for (int h = 0; h < 8; ++h, qg += kDqk / 8) {
-        const uint32_t have = h0 + w8 + h < H ? 16u : 0u;   // else zeros
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          const int c = lane + 32 * k;   // chunk c & 7 of atom c / 8
-          const uint32_t dst = qsm + static_cast<uint32_t>((c >> 3) * kAtom + (w8 + h) * 128 + (((c ^ h) & 7) << 4));
-          if (k < 2 || lane < 8)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
-                         "l"(have ? qg + c : static_cast<const uint4*>(p.a.q)), "r"(have)
-                         : "memory");
-        }
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      __syncwarp();
+    auto stage_query = [&](int n, bool& ok) {
+      const int w8 = (warp - kWarpSoft) * 8;
+      ok = __all_sync(0xffffffffu, wait_bar(qraw, n & 1, abort_flag, wlim)) && ok;
       // head lane & 7, atoms 2 (lane / 8) and the next
       const int h = lane & 7;
       const uint32_t at = qsm + static_cast<uint32_t>((lane >> 3) * 2 * kAtom + (w8 + h) * 128);
@@ -798,7 +800,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
     };
     // Turn by turn: the next item's query is staged (Q K^T of the last tile is complete), the
     // last item's output written, the next item's tiles taken.
-    uint32_t tmem = 0;
+    cluster_wait();
+    tc_fence_after();
+    const uint32_t tmem = misc[0] + lane_off;
     bool ok = true;
     float m = -INFINITY, g = -INFINITY, l = 0.f, qexp = 0.f;
     int gt = 0, n = 0, done = 0;   // tiles, items staged and done
@@ -806,12 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
     for (int item = first;; item += step) {
       const bool more = item < p.items;
       if (more) {
-        stage_query(item);
-        if (item == first) {
-          cluster_wait();
-          tc_fence_after();
-          tmem = misc[0] + lane_off;
-        }
+        stage_query(n, ok);
         qexp = query_exp(n++, ok);
       }
       if (item != first) {
@@ -877,6 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
         if (lane == 0) mbar_arrive(&edone[done++ & 1]);
       }
       if (!more) break;
+      const int next_row = row_of(min(item + step, p.items - 1));
       bool last_tile = false, stop = false;
       m = g = -INFINITY;
       l = 0.f;
@@ -887,6 +887,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
              wait_bar(&sfull[st], (j >> 1) & 1, abort_flag, wlim);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
+        // Q K^T of the item's last tile is complete: the next item's query may come
+        if (ok && warp == kWarpSoft && (info[j & 7] & (kLast | kEnd)) == kLast) {
+          if (lane == 0) {
+            load_query(next_row);
+            *fetched = n;
+          }
+          __syncwarp();
+        }
         const uint32_t scales = smem_u32(sm + kOffScale) + static_cast<uint32_t>((st * kTile + rq * 32) * 4);
         float x[32];
         float mx = -INFINITY, rmax = 0.f;
@@ -1018,6 +1026,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_e2m1_kernel(PairParams p) {
     }
   }
 
+  // The last query fetched has come (after an abort it may not have been waited for).
+  if (warp == kWarpSoft) mbar_drain(qraw, *fetched & 1, &g_status_attn_e2m1, p.wait_limit_ns);
   // Every MMA has finished in both CTAs before either releases its TMEM or leaves (after
   // an abort some may still be running).
   if (rank == 0 && (warp == kWarpQk || warp == kWarpPv)) {
@@ -1106,9 +1116,14 @@ cudaError_t launch_attn_e2m1(const SeqArgs& seq, const MlaArgs& a, void* workspa
   }
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(attn_e2m1_kernel), kSmemBytes, env.device);
   if (e != cudaSuccess) return e;
+  alignas(64) CUtensorMap qmap;   // the queries' heads as rows; boxes of 64 dims of 64 heads
+  std::string why;
+  if (static_cast<int64_t>(seq.T) * a.H > 0x7FFFFF00ll ||
+      !encode_tmap_2d(&qmap, a.q, 2, kDqk, static_cast<uint64_t>(seq.T) * a.H, kDqk * 2, 64, kHeads, &why))
+    return cudaErrorInvalidValue;
   const int64_t grid = 2 * std::min<int64_t>(items, resident_clusters(env.num_sms));
   e = launch_kernel(attn_e2m1_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmemBytes, env.stream, true,
-                    2, p);
+                    2, qmap, p);
   if (e != cudaSuccess) return e;
   char buf[96];
   snprintf(buf, sizeof(buf), "attn_tc<e2m1x128>[split=%d,grid=%lld]", split, static_cast<long long>(grid));
