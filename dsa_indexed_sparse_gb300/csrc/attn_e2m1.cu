@@ -64,11 +64,12 @@
 // and rope are loaded into registers a tile ahead, right after the registers' last use, a
 // row's whole 256 or 128 bytes by neighbouring lanes (32-byte pieces of eight rows took three
 // times as long).  16 Q K^T and 17 P V (rank 0 issues for both CTAs).  18 and 19 find the
-// tiles' cache rows, row scales and masks, two tiles ahead.  20-27 turn the query, which the TMA
-// brings once Q K^T of the item before is complete, into f16; then softmax, a thread one head and 32 of the tile's rows; the four threads of a head agree on m
-// and g through shared memory, when one of them has to let them grow.  Registers are dealt out
-// by setmaxnreg, so that no role spills: 224 KB of shared memory leave almost nothing of the
-// L1, and a spilled word comes back from the L2 (60 spilled bytes cost 1 %).  The code is kept small
+// tiles' cache rows, row scales and masks, two tiles ahead.  20-27 turn the query, which the
+// TMA brings once Q K^T of the item before is complete, into f16; then softmax, a thread
+// one head and 32 of the tile's rows; the four threads of a head agree on m and g through
+// shared memory, when one of them has to let them grow.  Registers are dealt out by
+// setmaxnreg, so that no role spills: 224 KB of shared memory leave almost nothing of the L1,
+// and a spilled word comes back from the L2 (60 spilled bytes cost 1 %).  The code is kept small
 // (rolled loops, short waits): with 98 KB of it every role ran from a cold instruction cache.
 //
 // Measured (2048 selected rows, 128 heads): 1116 us for 2048 queries, 1047 TFLOP/s of the
