@@ -76,8 +76,8 @@
 // 1926 measured; 54.7 us for 64 (one cluster a query: 128 of 152 SMs), 11.6 us for one (a
 // tile each for 16 clusters: latencies).  A tile takes 4300 clocks where its MMAs need 2176: two
 // are in flight, each a chain own rows - Q K^T - other rows - P V, and the links slow one another
-// (of the loop's clocks the load/store pipe has a wavefront in 73 %, tensor operands are read
-// in 45 %, issue slots are taken in 54 %).
+// (of the loop's clocks the load/store pipe has a wavefront in 69 %, tensor operands are read
+// in 45 %, issue slots are taken in 51 %).
 // The 48-row kernel of attn.cu's kind, which widens every row in both CTAs: 2171, 100 and 11.7.
 #include <cuda.h>
 
