@@ -118,8 +118,8 @@ constexpr int kOffStage = kOffQ + 9 * kAtom;             // [2]
 constexpr int kOffP1 = kOffStage + 2 * kStage;           // P of tile rows 64-127
 constexpr int kOffScale = kOffP1 + kAtom;                 // float [2][128] row scales
 constexpr int kOffRows = kOffScale + 2 * kTile * 4;      // int [2][128] cache rows, -1 for none
-constexpr int kOffMax = kOffRows + 2 * kTile * 4;        // for 32 heads each: bf16 [4 row quarters][32], float [2][32]
-constexpr int kOffMask = kOffMax + 4 * kHeads * 2;       // uint32 [2][4] valid rows
+constexpr int kOffSum = kOffRows + 2 * kTile * 4;        // for 32 heads each: float [2][32]
+constexpr int kOffMask = kOffSum + 2 * kHeads * 4;       // uint32 [2][4] valid rows
 constexpr int kOffRmax = kOffMask + 32;                  // float [2][2] largest row scale of a tile's halves
 constexpr int kOffOk = kOffRmax + 16;                    // int [8 softmax warps]
 constexpr int kOffExp = kOffOk + 32;                     // int8 [64 heads] a
@@ -724,9 +724,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // a scale of 0 becomes a tiny one, so that it leaves a masked logit at -inf
     const float sl2 = fmaxf(fabsf(p.a.softmax_scale) * kLog2e, 1e-30f);
     const uint32_t head_bar = 2 + (quarter & 1);   // the 128 threads of 32 heads
-    // the space in which the four threads of a head exchange maxima (xmax) and sums
-    uint8_t* exchange = sm + kOffMax + (quarter & 1) * 256;
-    __nv_bfloat16* xmax = reinterpret_cast<__nv_bfloat16*>(exchange) + lane;
+    // where the four threads of a head exchange sums, and maxima: [4 row quarters][32], in that part of
+    // the P buffer that these threads write (P V of the tile before is complete, this tile's P not begun)
+    float* sums = reinterpret_cast<float*>(sm + kOffSum + (quarter & 1) * 256) + lane;
+    float* xmax = reinterpret_cast<float*>(sm + kOffP1 + (quarter & 1) * 4096) + lane;
     volatile int* oks = reinterpret_cast<volatile int*>(sm + kOffOk);
     const volatile uint32_t* masks = reinterpret_cast<const volatile uint32_t*>(sm + kOffMask);
     const uint32_t prow0 = smem_u32(sm + (half ? kOffP1 : kOffStage + 8 * kAtom)) + static_cast<uint32_t>(hl * 128);
@@ -818,7 +819,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int last = item - step;
         ok = __all_sync(0xffffffffu, ok && wait_bar(&pvdone[(gt - 1) & 1], ((gt - 1) >> 1) & 1, abort_flag, wlim));
         // the sums of a head's four threads
-        float* sums = reinterpret_cast<float*>(exchange) + lane;
         if (rq >= 2) sums[(rq - 2) * 32] = l;
         named_bar_sync(head_bar, 128);
         if (rq < 2) sums[rq * 32] += l;
@@ -945,13 +945,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool pv_ok = true;
         if (j >= 1 && ok) pv_ok = wait_bar(&pvdone[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, wlim);
         if (grow) {
-          const __nv_bfloat16 mxb = __float2bfloat16_ru(mx);   // a bound is enough, rounded up
-          xmax[rq * 32] = mxb;
-          mx = __bfloat162float(mxb);
+          xmax[rq * 32] = mx;
           if (lane == 0) oks[warp - kWarpSoft] = ok ? 1 : 0;
           named_bar_sync(head_bar, 128);
 #pragma unroll
-          for (int k = 1; k < 4; ++k) mx = fmaxf(mx, __bfloat162float(xmax[(rq ^ k) * 32]));
+          for (int k = 1; k < 4; ++k) mx = fmaxf(mx, xmax[(rq ^ k) * 32]);
           // the four warps: those whose number is as odd as this one's
 #pragma unroll
           for (int k = 0; k < 4; ++k) ok = ok && oks[2 * k + (warp & 1)] != 0;

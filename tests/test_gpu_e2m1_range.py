@@ -1,0 +1,89 @@
+"""The attention over 4-bit rows where the range of its 16-bit weights shows: far maxima, rows of very unequal scale, rows
+that are all zero.  Against the float64 oracle.
+
+Tolerances, derived from the kernel's types (all sums in fp32; n selected rows, p_s the softmax weights):
+* a logit: the tensor cores' fp32 sums, of N products, are off by at most N 2^-23 of the sum of their magnitudes, whatever
+  the order and whether bits are rounded or cut off (a lone product of two bf16 values is exact); then the scale,
+  scale * log2 e, the sum of latent and rope part and the exponent's argument, a rounding each: 2^-22 of the logit in all;
+* a weight: twice the largest logit error (its own and the shift's), 2^-20 for the exponential and three fp32 products, 2^-11
+  for its rounding to f16; below f16's normal range, where the rounding is absolute, 2^-25.  The largest weight times
+  row scale starts at 2^7 or is allowed to have grown since, so the latter is at most 2^-32 max_s(p_s |rs_s|) of
+  each row's value over its scale, rs_s being the row scale of a row that holds any value (0 if it holds none);
+* sums over the rows: n 2^-23 of the sum of magnitudes A = sum_s p_s |v_s|;
+* the output's rounding to bf16: 2^-8 of it."""
+import dataclasses
+
+import numpy as np
+import pytest
+import torch
+
+import dsa_workloads as W
+from oracle import dsa_oracle as O
+from tests import parity as P
+from tests.test_gpu_e2m1 import _make, _selection
+
+pytestmark = pytest.mark.gpu
+
+LOG2E = 1.4426950408889634
+
+
+def _check_tight(out, lse, wl, idx, ts=None):
+    for t in range(wl.T) if ts is None else ts:
+        sel = idx[t][idx[t] >= 0].astype(np.int64)
+        o_out, o_lse = O.sparse_mla_attn_row(wl, t, idx[t])
+        rows = O.physical_rows(wl.block_table[wl.q_seq[t]], wl.page_size, sel)
+        kv, q, n, s = O.latent_rows(wl, rows), O.mla_query(wl, t), len(sel), abs(float(wl.softmax_scale))
+        rs = np.abs(wl.kv[rows, 288:292].copy().view("<f4")[:, 0].astype(np.float64))
+        rs[~(wl.kv[rows, 256:288] & 0x7F).any(axis=1)] = 0.0
+        logits = wl.softmax_scale * (q @ kv.T)
+        lat = s * (np.abs(q[:, :512]) @ np.abs(kv[:, :512]).T).max(axis=1)
+        rope = s * (np.abs(q[:, 512:]) @ np.abs(kv[:, 512:]).T).max(axis=1)
+        n_rope = (q[:, 512:] != 0).sum(axis=1)
+        e = 2.0 ** -23 * (512 * lat + np.maximum(n_rope - 1, 0) * rope) + 2.0 ** -22 * np.abs(logits).max(axis=1)
+        p = np.exp(logits - o_lse[:, None])
+        A = p @ np.abs(kv[:, :512])
+        v_over = np.divide(np.abs(kv[:, :512]), rs[:, None], out=np.zeros_like(kv[:, :512]), where=rs[:, None] > 0).sum(axis=0)
+        lost = 2.0 ** -32 * (p * rs).max(axis=1)[:, None] * v_over
+        before = (2 * e[:, None] + 2.0 ** -20 + 2.0 ** -11 + n * 2.0 ** -23) * A + lost
+        tol = 1.01 * (before + 2.0 ** -8 * (np.abs(o_out) + before))
+        assert np.all(np.isfinite(out[t])), t
+        err = np.abs(out[t] - o_out)
+        assert np.all(err <= tol), (t, float((err / np.maximum(tol, 1e-300)).max()))
+        lse_tol = e + 2.0 ** -20 + n * 2.0 ** -23 + 2.0 ** -22 * np.abs(o_lse)
+        assert np.all(np.abs(lse[t] - o_lse) <= lse_tol), (t, float((np.abs(lse[t] - o_lse) / lse_tol).max()))
+
+
+def _lift(wl, key, query, latent=2.0 ** -4):
+    """The workload with rope dim 0 of every cache row (key: [cache_rows]) and of the queries (query: [H]) set and the
+    other rope dims of the queries 0, so that a logit moves by softmax_scale * key * query exactly; query latents scaled."""
+    kv = wl.kv.copy()
+    bits = kv[:, 304:432].copy().view("<u2")
+    bits[:, 0] = W._bf16_bits(torch.from_numpy(np.asarray(key, np.float32)))
+    kv[:, 304:432] = bits.view(np.uint8).reshape(wl.cache_rows, 128)
+    q = torch.from_numpy(O.decode_bf16(wl.q).astype(np.float32))
+    q[..., :512] *= latent
+    q[..., 512:] = 0.0
+    q[..., 512] = torch.from_numpy(np.asarray(query, np.float32))
+    return dataclasses.replace(wl, kv=kv, q=W._bf16_bits(q))
+
+
+def _set_scales(wl, factor):
+    """Row scales times factor [cache_rows] (powers of two)."""
+    kv = wl.kv.copy()
+    rs = kv[:, 288:292].copy().view("<f4")[:, 0] * np.asarray(factor, np.float32)
+    kv[:, 288:292] = rs.astype("<f4").view(np.uint8).reshape(-1, 4)
+    return dataclasses.replace(wl, kv=kv)
+
+
+@pytest.mark.parametrize("workspace", [True, False])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("base", [600.0, 4100.0, 8200.0, 30000.0])
+def test_far_maxima(dev, base, sign, workspace):
+    """All logits of a head far from 0, by base and up to one and a half times that (log2 units) from head to head; among one
+    another they differ by little."""
+    wl = _make(101, ctx=[700, 650], K=300)
+    per = float(wl.softmax_scale) * LOG2E * 128.0
+    wl = _lift(wl, np.full(wl.cache_rows, 128.0), sign * base / per * (1 + np.arange(wl.H) % 64 / 128))
+    idx = _selection(np.random.default_rng(102), wl, 300, hole=0.1)
+    out, lse, _ = P.Run(wl, dev).attn(idx, workspace=workspace)
+    _check_tight(out, lse, wl, idx)
