@@ -520,6 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // time between the steps: the position, its page id, the cache row, the row's scale.
       int pos[2], pos1[2], page[2], row1[2];
       float rs1[2];
+      uint32_t sc1[2];   // its last four block scales
 #pragma unroll
       for (int k = 0; k < 2; ++k) pos[k] = pos1[k] = page[k] = row1[k] = -1;
       // the tile that load_pos comes to next: entries [gi0, gi1) of the open item are left; the
@@ -585,14 +586,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           page[k] = pos[k] >= 0 ? __ldg(bt + p.page(pos[k])) : -1;
         }
       };
-      auto load_scale = [&]() {   // row1, rs1 of pos, page
+      auto row_at = [&](int row) { return kv + static_cast<uint64_t>(static_cast<uint32_t>(max(row, 0))) * row_bytes; };
+      auto load_scale = [&]() {   // row1, rs1, sc1 of pos, page
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const bool good = page[k] >= 0 && page[k] < p.seq.n_pages;
           if (pos[k] >= 0 && !good) bad |= kDevBadIndex;
           row1[k] = good ? (page[k] - p.page(pos[k])) * p.seq.page_size + pos[k] : -1;   // < cache_rows < 2^31
-          const uint8_t* rp = kv + static_cast<uint64_t>(static_cast<uint32_t>(max(row1[k], 0))) * row_bytes;
+          const uint8_t* rp = row_at(row1[k]);
           rs1[k] = __ldg(reinterpret_cast<const float*>(rp + kE2m1RowScale));
+          sc1[k] = __ldg(reinterpret_cast<const uint32_t*>(rp + kE2m1RowScale) - 1);
         }
       };
       // step j: scales and mask of tile j - 1 and rows of tile j given out, pages of j + 1 and
@@ -611,7 +614,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t mask[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float mine = row1[k] >= 0 ? rs1[k] : 0.f;
+            float mine = row1[k] >= 0 ? rs1[k] : 0.f;
+            // A row whose block scales are all zero has no values, and its row scale (1, where the writer has
+            // stored it) must not stand for any: it takes part with 0.  Seldom more than a look at four scales
+            // (64 queries 55.3 us, 54.3 without it; the chunk the same).
+            constexpr uint32_t kAbs = 0x7F7F7F7Fu;
+            const bool look = row1[k] >= 0 && (sc1[k] & kAbs) == 0u;
+            if (__any_sync(0xffffffffu, look) && look) {
+              const uint4* sp = reinterpret_cast<const uint4*>(row_at(row1[k]) + kE2m1Scales);
+              const uint4 a = __ldg(sp), c = __ldg(sp + 1);
+              if (((a.x | a.y | a.z | a.w | c.x | c.y | c.z | c.w) & kAbs) == 0u) mine = 0.f;
+            }
             const uint32_t bits = __float_as_uint(mine) & 0x7FFFFFFFu;
             rmax = max(rmax, bits);
             rmin = min(rmin, bits ? bits : rmin);

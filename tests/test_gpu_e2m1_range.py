@@ -127,3 +127,34 @@ def test_roundings_of_the_output(dev, K, workspace):
     assert ("split=1," in plan) == (K <= 128 or not workspace)
     _check_tight(out, lse, wl, idx, slices="split=1," not in plan)
 
+
+
+@pytest.mark.parametrize("workspace", [True, False])
+@pytest.mark.parametrize("lift", [-20.0, 0.0, 20.0])
+@pytest.mark.parametrize("size", [0, -20, -30])
+def test_zero_rows(dev, size, lift, workspace):
+    """All-zero latent rows as the writer stores them (row scale 1) among rows of latents around 2^size, one alone, a few and
+    more than a tile of them, their logits below, beside and above the others' (log2 units): they weigh in the sum and
+    have no values.  Rows that hold something in one block alone, the first or the last, are no zero rows."""
+    wl = _make(121, ctx=[700, 650, 600, 520], K=500)
+    wl = _set_scales(wl, np.full(wl.cache_rows, 2.0 ** size))
+    key = np.zeros(wl.cache_rows)
+    kv = wl.kv.copy()
+    row = np.zeros(432, np.uint8)
+    row[288:292] = np.frombuffer(np.float32(1.0).tobytes(), np.uint8)
+    for t, where in enumerate(([250], [0, 1, 200, 499], list(range(0, 140)), list(range(256, 500)))):
+        rows = O.physical_rows(wl.block_table[t], 64, np.array(where))
+        rope = kv[rows, 304:].copy()
+        kv[rows] = row
+        kv[rows, 304:] = rope
+        key[rows] = lift
+        for at, block in ((150, 0), (151, 31), (152, 28), (153, 27)):
+            if at not in where:
+                one = O.physical_rows(wl.block_table[t], 64, np.array([at]))
+                kv[one, 256:288] = 0
+                kv[one, 256 + block] = 0x78
+    wl = dataclasses.replace(wl, kv=kv)
+    wl = _lift(wl, key, np.full(wl.H, 1.0 / (float(wl.softmax_scale) * LOG2E)), latent=2.0 ** (-4 - size))
+    idx = np.tile(np.arange(500, dtype=np.int32), (wl.T, 1))
+    out, lse, _ = P.Run(wl, dev).attn(idx, workspace=workspace)
+    _check_tight(out, lse, wl, idx, slices=workspace)
