@@ -1006,8 +1006,9 @@ __global__ void __launch_bounds__(32 * SW * HPC)
     ll = fmaf(fw[w], s_l[w0 + w], ll);
   }
   const int i0 = threadIdx.x - w0 * 32;   // thread within the head's warps
-  if (i0 == 0 && lse_out) lse_out[th] = ll > 0.f ? mm + logf(ll) : -INFINITY;
-  const float inv = ll > 0.f ? 1.f / ll : 0.f;
+  // ll is NaN where a slice's LSE is (the 4-bit rows' kernel)
+  if (i0 == 0 && lse_out) lse_out[th] = ll == 0.f ? -INFINITY : mm + logf(ll);
+  const float inv = ll == 0.f ? 0.f : 1.f / ll;
   uint2* dst = reinterpret_cast<uint2*>(out + th * kDv);
   // quad q holds dims [4q, 4q + 4): lane (q mod 64) / 2 of the warps, slots
   // 8 * (q / 64) + 4 * (q mod 2) .. + 3

@@ -845,8 +845,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) {
           tc_fence_after();
           // O holds sum p rs 2^(m - g) v over l = sum p
-          const float inv = l > 0.f ? exp2f(fminf(fmaxf(g - m, -126.f), 126.f)) / l : 0.f;
-          const float lse = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+          const float inv = l == 0.f ? 0.f : exp2f(fminf(fmaxf(g - m, -126.f), 126.f)) / l;   // l may be NaN
+          const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
           const int t = query_of(last), h0 = head_of(last);
           const int heads = min(32, H - (h0 + (quarter & 1) * 32));   // of this warp's 32 that exist
           const bool part = p.n_split > 1;

@@ -158,3 +158,31 @@ def test_zero_rows(dev, size, lift, workspace):
     idx = np.tile(np.arange(500, dtype=np.int32), (wl.T, 1))
     out, lse, _ = P.Run(wl, dev).attn(idx, workspace=workspace)
     _check_tight(out, lse, wl, idx, slices=workspace)
+
+
+@pytest.mark.parametrize("workspace", [True, False])
+@pytest.mark.parametrize("where", ["rope", "block scale", "row scale", "query latent", "query rope"])
+def test_nan_that_is_selected(dev, where, workspace):
+    """A NaN in a selected row makes its query's outputs and log-sum-exps NaN, one in a query's head that head's; the others
+    are what they are."""
+    wl = _make(131, ctx=[700, 650, 620], K=600)
+    idx = _selection(np.random.default_rng(132), wl, 600, hole=0.1)
+    want, want_lse, _ = P.Run(wl, dev).attn(idx, workspace=workspace)
+    kv, q = wl.kv.copy(), wl.q.copy()
+    bad = np.zeros((wl.T, wl.H), bool)
+    if where.startswith("query"):
+        q[1, 77, 5 if where == "query latent" else 520] = 0x7FC0
+        bad[1, 77] = True
+    else:
+        pos = idx[1][idx[1] >= 0][333]
+        row = O.physical_rows(wl.block_table[1], 64, np.array([pos]))[0]
+        if where == "rope":
+            kv[row, 304:306] = (0xC0, 0x7F)
+        elif where == "block scale":
+            kv[row, 270] = 0x7F
+        else:
+            kv[row, 288:292] = np.frombuffer(np.float32(np.nan).tobytes(), np.uint8)
+        bad[1] = True
+    out, lse, _ = P.Run(dataclasses.replace(wl, kv=kv, q=q), dev).attn(idx, workspace=workspace)
+    assert np.isnan(lse[bad]).all() and np.isnan(out[bad]).all()
+    assert np.array_equal(out[~bad], want[~bad]) and np.array_equal(lse[~bad], want_lse[~bad])
