@@ -141,8 +141,9 @@ def _ptr(t: Optional[torch.Tensor]):
 
 # The current stream's handle without a Stream object around it: 0.1 us against 2.9, of
 # the 3.4 that a small step's C call takes.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice      # for callers that have seen a CUDA tensor
+# Both are there in a torch with CUDA; one without still imports this module.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device   # once a CUDA tensor was seen
 _FLOAT_CODES = {torch.float32: DSA_F32, torch.bfloat16: DSA_BF16}
 
 
