@@ -474,8 +474,13 @@ def index_cache_append_rope(seq: Seq, plan: Rope, k_new: torch.Tensor, k_cache: 
     s, r = seq.desc(), plan.desc()
     if k_new.dim() != 2 or k_new.shape[0] != s.T:
         raise ValueError("k_new must be [T, D_I]")
+    D = k_new.shape[1]
+    if k_cache.element_size() != 1 or k_cache.numel() < s.cache_rows * D:
+        raise ValueError("k_cache must be one-byte codes [cache_rows, D_I]")
+    if k_scale.element_size() != (1 if mx else 4) or k_scale.numel() < s.cache_rows * (D // 32 if mx else 1):
+        raise ValueError("k_scale must be fp32 [cache_rows], or with mx uint8 [cache_rows, D_I / 32]")
     dev = _on_current(seq, plan)
-    _check(_lib.dsa_index_cache_append_rope(ctypes.byref(s), ctypes.byref(r), k_new.shape[1], offset,
+    _check(_lib.dsa_index_cache_append_rope(ctypes.byref(s), ctypes.byref(r), D, offset,
                                             _dtype_code(k_new), DSA_MXFP8_E4M3 if mx else DSA_E4M3,
                                             _rows(k_new, "k_new", dev), k_new.stride(0),
                                             _cache_ptr(k_cache, "k_cache", dev), _cache_ptr(k_scale, "k_scale", dev),
