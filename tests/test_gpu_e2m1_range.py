@@ -71,7 +71,7 @@ def _lift(wl, key, query, latent=2.0 ** -4):
 
 
 def _set_scales(wl, factor):
-    """Row scales times factor [cache_rows] (powers of two)."""
+    """Row scales times factor [cache_rows]."""
     kv = wl.kv.copy()
     rs = kv[:, 288:292].copy().view("<f4")[:, 0] * np.asarray(factor, np.float32)
     kv[:, 288:292] = rs.astype("<f4").view(np.uint8).reshape(-1, 4)
@@ -186,3 +186,17 @@ def test_nan_that_is_selected(dev, where, workspace):
     out, lse, _ = P.Run(dataclasses.replace(wl, kv=kv, q=q), dev).attn(idx, workspace=workspace)
     assert np.isnan(lse[bad]).all() and np.isnan(out[bad]).all()
     assert np.array_equal(out[~bad], want[~bad]) and np.array_equal(lse[~bad], want_lse[~bad])
+
+
+@pytest.mark.parametrize("H,T,K,workspace", [(128, 1, 1, True), (128, 3, 129, False), (16, 2, 777, False), (130, 150, 300, True),
+                                             (128, 2, 2048, False), (128, 2, 2048, True), (5, 300, 200, True)])
+@pytest.mark.parametrize("scales", ["powers of two", "any"])
+def test_ordinary_rows_and_any_row_scale(dev, H, T, K, workspace, scales):
+    """Ordinary queries and rows, with holes.  Row scales enter in fp32: one that is no power of two rounds no value."""
+    wl = _make(160 + H + T + K, ctx=[T + 2200], q_len=T, K=K, H=H)
+    rng = np.random.default_rng(K)
+    if scales == "any":
+        wl = _set_scales(wl, rng.uniform(0.6, 1.7, wl.cache_rows))
+    idx = _selection(rng, wl, K, hole=0.1 if K > 1 else 0.0)
+    out, lse, plan = P.Run(wl, dev).attn(idx, workspace=workspace)
+    _check_tight(out, lse, wl, idx, ts=sorted({0, T // 2, T - 1}), slices="split=1," not in plan)
