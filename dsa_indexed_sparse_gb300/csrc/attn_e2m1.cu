@@ -168,6 +168,7 @@ struct PairParams {
   uint64_t wait_limit_ns;
   uint32_t dbg_withhold;
   Divisor page, split, heads;   // by the page size, n_split, head_blocks
+  float scale_log2;         // |softmax scale| * log2 e; tiny for 0, so that it leaves a masked logit at -inf
   uint32_t early_query;     // the query was complete before the kernel before this one let it launch
 };
 
@@ -738,8 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int part32 = (warp - kWarpSoft) >> 2; // this thread's [32 part32, 32 part32 + 32)
     const int rq = half * 2 + part32;           // row quarter of the tile
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    // a scale of 0 becomes a tiny one, so that it leaves a masked logit at -inf
-    const float sl2 = fmaxf(fabsf(p.a.softmax_scale) * kLog2e, 1e-30f);
+    const float sl2 = p.scale_log2;
     const uint32_t head_bar = 2 + (quarter & 1);   // the 128 threads of 32 heads
     // where the four threads of a head exchange sums, and maxima: [2][4 row quarters][32], in that part
     // of the P buffer that these threads write (P V of the tile before is complete, this tile's P not begun)
@@ -1142,9 +1142,11 @@ cudaError_t launch_attn_e2m1(const SeqArgs& seq, const MlaArgs& a, void* workspa
   const int head_blocks = (a.H + 127) / 128;
   const int64_t items = static_cast<int64_t>(seq.T) * head_blocks * split;
   if (items > 0x3FFFFFFFll) return cudaErrorInvalidConfiguration;
+  float scale_log2 = std::fabs(a.softmax_scale) * kLog2e;
+  if (scale_log2 < 1e-30f) scale_log2 = 1e-30f;   // NaN stays
   PairParams p{seq,     a,  split,        rps,  head_blocks, static_cast<int32_t>(items),
                nullptr, nullptr, kWaitLimitNs, 0u, Divisor(seq.page_size), Divisor(split), Divisor(head_blocks),
-               env.chained ? 1u : 0u};
+               scale_log2, env.chained ? 1u : 0u};
   debug_wait_state(&p.wait_limit_ns, &p.dbg_withhold);
   if (split > 1) {
     const size_t o = static_cast<size_t>(split) * seq.T * a.H * kDv * sizeof(uint16_t);

@@ -200,3 +200,10 @@ def test_ordinary_rows_and_any_row_scale(dev, H, T, K, workspace, scales):
     idx = _selection(rng, wl, K, hole=0.1 if K > 1 else 0.0)
     out, lse, plan = P.Run(wl, dev).attn(idx, workspace=workspace)
     _check_tight(out, lse, wl, idx, ts=sorted({0, T // 2, T - 1}), slices="split=1," not in plan)
+
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf")])
+def test_softmax_scale_that_is_no_number(dev, scale):
+    wl = dataclasses.replace(_make(171, ctx=[300, 200], K=150), softmax_scale=scale)
+    out, lse, _ = P.Run(wl, dev).attn(_selection(np.random.default_rng(172), wl, 150))
+    assert np.isnan(out).all() and np.isnan(lse).all()
