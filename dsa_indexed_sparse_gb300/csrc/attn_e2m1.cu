@@ -73,12 +73,12 @@
 // and a spilled word comes back from the L2 (60 spilled bytes cost 1 %).  The code is kept small
 // (rolled loops, short waits): with 98 KB of it every role ran from a cold instruction cache.
 //
-// Measured (2048 selected rows, 128 heads): 1116 us for 2048 queries, 1047 TFLOP/s of the
-// 1926 measured; 54.7 us for 64 (one cluster a query: 128 of 152 SMs), 11.6 us for one (a
+// Measured (2048 selected rows, 128 heads): 1115 us for 2048 queries, 1047 TFLOP/s of the
+// 1926 measured; 55.3 us for 64 (one cluster a query: 128 of 152 SMs), 11.6 us for one (a
 // tile each for 16 clusters: latencies).  A tile takes 4300 clocks where its MMAs need 2176: two
 // are in flight, each a chain own rows - Q K^T - other rows - P V, and the links slow one another
-// (of the loop's clocks the load/store pipe has a wavefront in 69 %, tensor operands are read
-// in 45 %, issue slots are taken in 51 %).
+// (of the loop's clocks the load/store pipe has a wavefront in 71 %, tensor operands are read
+// in 45 %, issue slots are taken in 49 %).
 // The 48-row kernel of attn.cu's kind, which widens every row in both CTAs: 2171, 100 and 11.7.
 #include <cuda.h>
 
@@ -163,7 +163,11 @@ struct PairParams {
   int32_t rows_per_split;   // a multiple of kTile
   int32_t head_blocks;      // blocks of 128 heads
   int32_t items;            // T * head_blocks * n_split, shared out among the clusters
-  uint16_t* ws_o;           // [n_split, T, H, 512] bf16 partials (n_split > 1), each normalised by its own sum
+  // Partials (n_split > 1), each normalised by its own sum, in bf16 as attn.cu's are: 2^-8 of a partial besides the
+  // output's own rounding, where more than one slice is taken (relative error of the outputs 0.0021 instead of
+  // 0.0016 for one query).  A choice: in fp32 one query takes 13.0 us instead of 11.5, 16 queries 25.9
+  // instead of 22.0; in f16 with an exponent for every 128 dims 12.4 and 22.9.
+  uint16_t* ws_o;           // [n_split, T, H, 512]
   float* ws_lse;            // [n_split, T, H]
   uint64_t wait_limit_ns;
   uint32_t dbg_withhold;
@@ -1112,7 +1116,12 @@ int resident_clusters(int num_sms) {
 }
 
 // Row slices per query: one cluster for each while the GPU holds them all at once, a
-// slice at least one tile.
+// slice at least one tile.  Measured with other numbers of slices (us, 2048 rows a query, this
+// rule's first): 1 query 16 slices 11.7, 8 14.0, 1 43.7; 16 queries 4 slices 22.7, 3 27.2, 8 28.5,
+// 1 47.6; 38 queries 2 slices 37.7, 4 41.7, 1 54.5; 40 queries 1 slice 54.4, 2 63.4, 3 53.1; 64
+// queries 1 slice 55.6, 2 66.6, 3 70.0; 80 queries 1 slice 102, 2 93.5, 4 91.6; 160 queries 1 slice
+// 151, 2 155.  An item costs its query's staging, its output and a share of the merge besides its
+// tiles, so slices that fill the last clusters gain 10 % at 77 to 100 queries and lose elsewhere.
 int choose_split(const SeqArgs& seq, const MlaArgs& a, int num_sms) {
   const int tiles = (a.K + kTile - 1) / kTile;
   const int64_t clusters = static_cast<int64_t>(seq.T) * ((a.H + 127) / 128);

@@ -147,10 +147,16 @@ typedef struct dsa_mla_desc {
                              /*   dims [16 b, 16 b + 16); [288,292) the fp32 row   */
                              /*   scale; [292,304) reserved; [304,432) 64 bf16     */
                              /*   rope values.  Value = code * scale * row scale.  */
-                             /*   The tensor-core path widens values to bf16:      */
-                             /*   exact when the row scale is a power of two (as   */
-                             /*   the cache writers store it), rounded otherwise.  */
-                             /*   row_bytes a multiple of 16.                      */
+                             /*   row_bytes a multiple of 16.  The attention holds */
+                             /*   code * scale in f16, exactly, and multiplies     */
+                             /*   logits and weights by the row scale, any fp32    */
+                             /*   number, in fp32: no value is rounded.  Weight *  */
+                             /*   row scale goes to f16, 2^-11 of it; where it is  */
+                             /*   far below the head's largest one, an error of    */
+                             /*   2^-29 of that instead (times code * scale).  So a */
+                             /*   row scale should be about as large as its row's  */
+                             /*   values ask for, as the writers store it.  Rows   */
+                             /*   whose 32 scales are all zero count as row scale 0.*/
                              /*  DSA_F32 : row = d_latent+d_rope fp32 values       */
   const void* q;             /* device [T, H, d_latent+d_rope]: bf16, or fp32 when */
                              /* dtype == DSA_F32                                   */
@@ -189,10 +195,12 @@ dsa_status_t dsa_topk(const dsa_seq_desc_t* seq, const float* scores, int64_t ld
  *   out[t,h,:] = sum_s softmax(logit)_s * row_s[0 : d_latent]
  *   lse[t,h]   = log sum_s exp(logit_s)      (natural log; -inf if S is empty)
  * Entries -1 are skipped wherever they appear; an entry > q_pos[t] is skipped and
- * flagged.  1 <= K <= 16384.  out: device [T, H, d_latent], bf16 (fp32 when dtype == DSA_F32);
+ * flagged.  Over DSA_E2M1 rows a NaN in a selected row or a query head makes their out
+ * and lse NaN.  1 <= K <= 16384.  out: device [T, H, d_latent], bf16 (fp32 when dtype == DSA_F32);
  * lse: device fp32 [T, H] or NULL.  workspace may be NULL when
  * dsa_sparse_mla_attn_workspace_size() returns 0; a larger workspace lets the
- * call split each query's rows across more CTAs. */
+ * call split each query's rows across more CTAs (the tensor-core paths round each
+ * part's output to bf16 before they join them). */
 size_t dsa_sparse_mla_attn_workspace_size(const dsa_seq_desc_t* seq, const dsa_mla_desc_t* mla,
                                           int32_t K);
 dsa_status_t dsa_sparse_mla_attn(const dsa_seq_desc_t* seq, const dsa_mla_desc_t* mla,
@@ -279,7 +287,7 @@ dsa_status_t dsa_index_cache_append_mx(const dsa_seq_desc_t* seq, int32_t D_I, d
  *      to latent * 2**-e / s_b (fp32 quotient), ties to the even code, magnitudes
  *      beyond 6 saturated; zero codes where s_b is 0; zero bytes at [292,304); the
  *      rope copied to [304,432).  Latent values must be finite (an infinity is
- *      stored as the largest magnitude of its row, a NaN as one of them). */
+ *      stored as the largest magnitude of its row, a NaN as the largest of its block). */
 dsa_status_t dsa_latent_cache_append(const dsa_seq_desc_t* seq, const dsa_mla_desc_t* mla, const void* kv_new,
                                      void* kv_cache, dsa_stream_t stream);
 
