@@ -153,10 +153,10 @@ typedef struct dsa_mla_desc {
                              /*   number, in fp32: no value is rounded.  Weight *  */
                              /*   row scale goes to f16, 2^-11 of it; where it is  */
                              /*   far below the head's largest one, an error of    */
-                             /*   2^-29 of that instead (times code * scale).  So a */
+                             /*   2^-29 of that instead (times code * scale): a    */
                              /*   row scale should be about as large as its row's  */
                              /*   values ask for, as the writers store it.  Rows   */
-                             /*   whose 32 scales are all zero count as row scale 0.*/
+                             /*   whose 32 scales are all 0 count as row scale 0.  */
                              /*  DSA_F32 : row = d_latent+d_rope fp32 values       */
   const void* q;             /* device [T, H, d_latent+d_rope]: bf16, or fp32 when */
                              /* dtype == DSA_F32                                   */
