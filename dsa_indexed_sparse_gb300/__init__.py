@@ -20,7 +20,7 @@ LIB_PATH = os.path.join(_HERE, "libdsa.so")
 DSA_OK = 0
 STATUS_NAMES = {0: "DSA_OK", 1: "DSA_ERR_INVALID_ARG", 2: "DSA_ERR_UNSUPPORTED", 3: "DSA_ERR_WORKSPACE",
                 4: "DSA_ERR_CUDA", 5: "DSA_ERR_TIMEOUT", 6: "DSA_ERR_DEVICE_CHECK"}
-DSA_F32, DSA_BF16, DSA_E4M3, DSA_MXFP8_E4M3, DSA_E4M3_T128, DSA_E2M1 = 0, 1, 2, 3, 4, 5
+DSA_F32, DSA_BF16, DSA_E4M3, DSA_MXFP8_E4M3, DSA_E4M3_T128, DSA_E2M1, DSA_MXFP4_E2M1 = 0, 1, 2, 3, 4, 5, 6
 E2M1_ROW_BYTES = 432                # a DSA_E2M1 latent row
 ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
@@ -32,7 +32,8 @@ EXPORTED = ("dsa_abi_version", "dsa_status_string", "dsa_last_error", "dsa_last_
             "dsa_latent_cache_append", "dsa_debug_withhold_arrival",
             "dsa_indexer_prolog_workspace_size", "dsa_indexer_prolog",
             "dsa_rope_turns", "dsa_rope", "dsa_latent_cache_append_rope", "dsa_index_cache_append_rope",
-            "dsa_latent_cache_read", "dsa_check_status")
+            "dsa_latent_cache_read", "dsa_index_cache_append_mx4", "dsa_index_query_quantize", "dsa_index_cache_read",
+            "dsa_check_status")
 STATIC_WORKSPACE_BYTES = 32 << 20   # DSA_STATIC_WORKSPACE_BYTES
 
 
@@ -103,6 +104,10 @@ def _load() -> ctypes.CDLL:
         "dsa_latent_cache_append_rope": (C, [P, P, P, P, ctypes.c_int64, P, ctypes.c_int64, P, P]),
         "dsa_index_cache_append_rope": (C, [P, P, ctypes.c_int32, ctypes.c_int32, C, C, P, ctypes.c_int64, P, P, P]),
         "dsa_latent_cache_read": (C, [P, P, P, C, P, ctypes.c_int64, P]),
+        "dsa_index_cache_append_mx4": (C, [P, ctypes.c_int32, C, P, P, P, P]),
+        "dsa_index_query_quantize": (C, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, C, C, P, ctypes.c_int64,
+                                         ctypes.c_int64, P, P, P]),
+        "dsa_index_cache_read": (C, [P, ctypes.c_int32, C, P, P, C, P, ctypes.c_int64, P]),
         "dsa_check_status": (C, [P]),
     }
     for name, (res, args) in sig.items():
@@ -241,16 +246,23 @@ class Seq(_CachedDesc):
 @dataclasses.dataclass
 class Indexer(_CachedDesc):
     """Lightning-indexer inputs; see dsa_indexer_desc_t."""
-    q: torch.Tensor                    # [T, H_I, D_I] e4m3 codes (uint8) or fp32
+    q: torch.Tensor                    # [T, H_I, D_I] e4m3 codes (uint8) or fp32; MXFP4: uint8 [T, H_I, D_I/2]
     w: torch.Tensor                    # [T, H_I] fp32
-    k_cache: torch.Tensor              # [cache_rows, D_I]
-    q_scale: Optional[torch.Tensor] = None   # fp32 [T, H_I], or uint8 E8M0 [T, H_I, D_I/32] (MXFP8)
-    k_scale: Optional[torch.Tensor] = None   # fp32 [cache_rows], or uint8 E8M0 [cache_rows, D_I/32] (MXFP8)
-    dtype: Optional[int] = None              # DSA_MXFP8_E4M3 for MXFP8 codes; else from k_cache
+    k_cache: torch.Tensor              # [cache_rows, D_I]; MXFP4: uint8 [cache_rows, D_I/2]
+    q_scale: Optional[torch.Tensor] = None   # fp32 [T, H_I], or uint8 E8M0 [T, H_I, D_I/32] (MXFP8, MXFP4)
+    k_scale: Optional[torch.Tensor] = None   # fp32 [cache_rows], or uint8 E8M0 [cache_rows, D_I/32] (MXFP8, MXFP4)
+    dtype: Optional[int] = None              # DSA_MXFP8_E4M3 or DSA_MXFP4_E2M1 for such codes; else from k_cache
 
     def _build_desc(self) -> IndexerDesc:
         _, H_I, D_I = self.q.shape
         dt = self.dtype if self.dtype is not None else _dtype_code(self.k_cache)
+        if dt == DSA_MXFP4_E2M1:
+            T, rows, D_I = self.q.shape[0], self.k_cache.shape[0], 2 * D_I
+            want = ((self.q, (T, H_I, D_I // 2)), (self.q_scale, (T, H_I, D_I // 32)),
+                    (self.k_cache, (rows, D_I // 2)), (self.k_scale, (rows, D_I // 32)))
+            if any(t is None or t.dtype != torch.uint8 or t.shape != n for t, n in want):
+                raise ValueError("MXFP4: q and k_cache must be uint8 [T, H_I, D_I/2] and [cache_rows, D_I/2], their "
+                                 "scales uint8 [T, H_I, D_I/32] and [cache_rows, D_I/32]")
         return IndexerDesc(H_I, D_I, dt, _ptr(self.q), _ptr(self.q_scale),
                            _ptr(self.w), _ptr(self.k_cache), _ptr(self.k_scale))
 
@@ -424,16 +436,79 @@ def decode_step_static_ws(seq: Seq, idx: Indexer, mla: Mla, K: int, out: torch.T
     return out
 
 
+def _codes_check(dtype: int, D: int, rows: int, codes: torch.Tensor, scale: Optional[torch.Tensor], names: str) -> None:
+    """Codes and scales of at least `rows` index vectors of D values in the format dtype."""
+    if dtype not in (DSA_E4M3, DSA_MXFP8_E4M3, DSA_MXFP4_E2M1):
+        raise ValueError("dtype must be DSA_E4M3, DSA_MXFP8_E4M3 or DSA_MXFP4_E2M1")
+    per = D // 2 if dtype == DSA_MXFP4_E2M1 else D
+    if codes.element_size() != 1 or codes.numel() < rows * per:
+        raise ValueError(f"{names}: codes must be one-byte [{rows}, {per}]")
+    if scale is None:
+        if dtype != DSA_E4M3:
+            raise ValueError(f"{names}: scales are required")
+    elif scale.element_size() != (4 if dtype == DSA_E4M3 else 1) or scale.numel() < rows * (1 if dtype == DSA_E4M3 else D // 32):
+        raise ValueError(f"{names}: scales must be fp32 [{rows}] (DSA_E4M3) or uint8 [{rows}, D_I / 32]")
+
+
 def index_cache_append(seq: Seq, k_new: torch.Tensor, k_cache: torch.Tensor, k_scale: torch.Tensor,
-                       stream=None, mx: bool = False) -> None:
+                       stream=None, mx: bool = False, dtype: Optional[int] = None) -> None:
     """Quantises the new tokens' index keys k_new [T, D_I] (fp32 or bf16) to e4m3
     + per-token fp32 scale (k_scale [cache_rows]), or with mx to MXFP8 (k_scale
     uint8 [cache_rows, D_I / 32] E8M0 bytes), and writes them at their
-    positions' cache rows."""
+    positions' cache rows.  dtype (DSA_E4M3, DSA_MXFP8_E4M3 or DSA_MXFP4_E2M1:
+    k_cache uint8 [cache_rows, D_I / 2]) names the format instead of mx."""
     s = seq.desc()
-    fn = _lib.dsa_index_cache_append_mx if mx else _lib.dsa_index_cache_append
+    if dtype == DSA_MXFP4_E2M1:
+        if k_new.dim() != 2 or k_new.shape[0] != s.T or k_new.dtype not in _FLOAT_CODES:
+            raise ValueError("k_new must be float32 or bfloat16 [T, D_I]")
+        _codes_check(dtype, k_new.shape[1], s.cache_rows, k_cache, k_scale, "k_cache, k_scale")
+        dev = _on_current(seq)
+        _check(_lib.dsa_index_cache_append_mx4(ctypes.byref(s), k_new.shape[1], _FLOAT_CODES[k_new.dtype],
+                                               _cache_ptr(k_new, "k_new", dev), _cache_ptr(k_cache, "k_cache", dev),
+                                               _cache_ptr(k_scale, "k_scale", dev), _stream(stream, dev)))
+        return
+    if dtype not in (None, DSA_E4M3, DSA_MXFP8_E4M3):
+        raise ValueError("dtype must be DSA_E4M3, DSA_MXFP8_E4M3 or DSA_MXFP4_E2M1")
+    fn = _lib.dsa_index_cache_append_mx if (mx if dtype is None else dtype == DSA_MXFP8_E4M3) else _lib.dsa_index_cache_append
     _check(fn(ctypes.byref(s), k_new.shape[1], _dtype_code(k_new), _ptr(k_new), _ptr(k_cache), _ptr(k_scale),
               _stream(stream)))
+
+
+def index_query_quantize(q: torch.Tensor, codes: torch.Tensor, scale: torch.Tensor, dtype: int = DSA_E4M3,
+                         stream=None) -> None:
+    """Query heads q [T, H_I, D_I] (fp32 or bf16; a strided view whose last dim is
+    contiguous is fine) to the codes and scales that Indexer takes as q and q_scale:
+    codes uint8 [T, H_I, D_I] ([T, H_I, D_I / 2] for DSA_MXFP4_E2M1), scale fp32
+    [T, H_I] (DSA_E4M3) or uint8 [T, H_I, D_I / 32]."""
+    if q.dim() != 3 or q.dtype not in _FLOAT_CODES:
+        raise ValueError("q must be float32 or bfloat16 [T, H_I, D_I]")
+    T, H, D = q.shape
+    _codes_check(dtype, D, T * H, codes, scale, "codes, scale")
+    if scale is None:
+        raise ValueError("scale is required")
+    dev = q.get_device()
+    if dev < 0 or dev != _current_device():
+        raise ValueError("q must be on the current CUDA device")
+    _check(_lib.dsa_index_query_quantize(T, H, D, _FLOAT_CODES[q.dtype], dtype, _rows(q, "q", dev), q.stride(0),
+                                         q.stride(1), _cache_ptr(codes, "codes", dev), _cache_ptr(scale, "scale", dev),
+                                         _stream(stream, dev)))
+
+
+def index_cache_read(seq: Seq, k_cache: torch.Tensor, k_scale: Optional[torch.Tensor], out: torch.Tensor,
+                     dtype: int = DSA_E4M3, stream=None) -> torch.Tensor:
+    """The cached index keys of the positions of seq (q_seq, q_pos) as the values they
+    stand for: out [T, D_I], bf16 or fp32 (a row-strided view is fine)."""
+    s = seq.desc()
+    if out.dim() != 2 or out.shape[0] != s.T or out.dtype not in _FLOAT_CODES:
+        raise ValueError("out must be float32 or bfloat16 [T, D_I]")
+    D = out.shape[1]
+    _codes_check(dtype, D, s.cache_rows, k_cache, k_scale, "k_cache, k_scale")
+    dev = _on_current(seq)
+    _check(_lib.dsa_index_cache_read(ctypes.byref(s), D, dtype, _cache_ptr(k_cache, "k_cache", dev),
+                                     None if k_scale is None else _cache_ptr(k_scale, "k_scale", dev),
+                                     _FLOAT_CODES[out.dtype], _rows(out, "out", dev), out.stride(0),
+                                     _stream(stream, dev)))
+    return out
 
 
 def latent_cache_append(seq: Seq, mla: Mla, kv_new: torch.Tensor, stream=None) -> None:
@@ -467,7 +542,7 @@ def latent_cache_append_rope(seq: Seq, mla: Mla, plan: Rope, latent: torch.Tenso
 
 
 def index_cache_append_rope(seq: Seq, plan: Rope, k_new: torch.Tensor, k_cache: torch.Tensor, k_scale: torch.Tensor,
-                            offset: int = 0, stream=None, mx: bool = False) -> None:
+                            offset: int = 0, stream=None, mx: bool = False, dtype: Optional[int] = None) -> None:
     """index_cache_append with dims [offset, offset + d_rot) of every new key
     rotated by the token's position before it is quantised (k_new may be a
     row-strided view)."""
@@ -475,13 +550,16 @@ def index_cache_append_rope(seq: Seq, plan: Rope, k_new: torch.Tensor, k_cache: 
     if k_new.dim() != 2 or k_new.shape[0] != s.T:
         raise ValueError("k_new must be [T, D_I]")
     D = k_new.shape[1]
-    if k_cache.element_size() != 1 or k_cache.numel() < s.cache_rows * D:
-        raise ValueError("k_cache must be one-byte codes [cache_rows, D_I]")
-    if k_scale.element_size() != (1 if mx else 4) or k_scale.numel() < s.cache_rows * (D // 32 if mx else 1):
+    fmt = (DSA_MXFP8_E4M3 if mx else DSA_E4M3) if dtype is None else dtype
+    per = D // 2 if fmt == DSA_MXFP4_E2M1 else D
+    if k_cache.element_size() != 1 or k_cache.numel() < s.cache_rows * per:
+        raise ValueError("k_cache must be one-byte codes [cache_rows, D_I] (MXFP4: [cache_rows, D_I / 2])")
+    blocks = fmt != DSA_E4M3
+    if k_scale.element_size() != (1 if blocks else 4) or k_scale.numel() < s.cache_rows * (D // 32 if blocks else 1):
         raise ValueError("k_scale must be fp32 [cache_rows], or with mx uint8 [cache_rows, D_I / 32]")
     dev = _on_current(seq, plan)
     _check(_lib.dsa_index_cache_append_rope(ctypes.byref(s), ctypes.byref(r), D, offset,
-                                            _dtype_code(k_new), DSA_MXFP8_E4M3 if mx else DSA_E4M3,
+                                            _dtype_code(k_new), fmt,
                                             _rows(k_new, "k_new", dev), k_new.stride(0),
                                             _cache_ptr(k_cache, "k_cache", dev), _cache_ptr(k_scale, "k_scale", dev),
                                             _stream(stream, dev)))

@@ -78,26 +78,40 @@ dsa_status_t check_seq(const dsa_seq_desc_t* s, dsa::SeqArgs* out) {
   return DSA_OK;
 }
 
+bool index_kind(dsa_dtype_t dtype, dsa::IndexKind* kind) {
+  switch (dtype) {
+    case DSA_F32: *kind = dsa::IndexKind::kF32; return true;
+    case DSA_E4M3: *kind = dsa::IndexKind::kE4M3; return true;
+    case DSA_MXFP8_E4M3: *kind = dsa::IndexKind::kMx8; return true;
+    case DSA_MXFP4_E2M1: *kind = dsa::IndexKind::kMx4; return true;
+    default: return false;
+  }
+}
+
+// One E8M0 scale per 32 values.
+bool block_scaled(dsa::IndexKind kind) { return kind == dsa::IndexKind::kMx8 || kind == dsa::IndexKind::kMx4; }
+
 dsa_status_t check_indexer(const dsa_seq_desc_t* s, const dsa_indexer_desc_t* x, const float* scores,
                            int64_t ld, dsa::IndexerArgs* out) {
   if (!x) return fail(DSA_ERR_INVALID_ARG, "indexer descriptor is NULL");
   if (x->H_I < 1 || x->D_I < 1) return fail(DSA_ERR_INVALID_ARG, "H_I and D_I must be >= 1");
-  if (x->dtype != DSA_E4M3 && x->dtype != DSA_F32 && x->dtype != DSA_MXFP8_E4M3)
-    return fail(DSA_ERR_UNSUPPORTED, "indexer dtype must be DSA_E4M3, DSA_MXFP8_E4M3 or DSA_F32");
-  const bool mx = x->dtype == DSA_MXFP8_E4M3;
-  if (mx && x->D_I % 32 != 0) return fail(DSA_ERR_UNSUPPORTED, "MXFP8 index keys need D_I a multiple of 32");
+  dsa::IndexKind kind;
+  if (!index_kind(x->dtype, &kind))
+    return fail(DSA_ERR_UNSUPPORTED, "indexer dtype must be DSA_E4M3, DSA_MXFP8_E4M3, DSA_MXFP4_E2M1 or DSA_F32");
+  const bool mx = block_scaled(kind);
+  if (mx && x->D_I % 32 != 0) return fail(DSA_ERR_UNSUPPORTED, "MXFP8 and MXFP4 index keys need D_I a multiple of 32");
   if (s->T > 0 && (!x->q || !x->w || !x->k_cache))
     return fail(DSA_ERR_INVALID_ARG, "indexer q, w and k_cache must be non-NULL");
   if (s->T > 0 && mx && (!x->q_scale || !x->k_scale))
-    return fail(DSA_ERR_INVALID_ARG, "MXFP8 index keys need q_scale and k_scale");
+    return fail(DSA_ERR_INVALID_ARG, "MXFP8 and MXFP4 index keys need q_scale and k_scale");
   if (!aligned16(x->q) || !aligned16(x->k_cache) || !aligned16(x->w) || !aligned16(x->q_scale) ||
       !aligned16(x->k_scale))
     return fail(DSA_ERR_INVALID_ARG, "indexer pointers must be 16-byte aligned");
   if (ld < s->max_ctx || ld % 4 != 0) return fail(DSA_ERR_INVALID_ARG, "ld must be >= max_ctx and a multiple of 4");
   if (s->T > 0 && (!scores || !aligned16(scores)))
     return fail(DSA_ERR_INVALID_ARG, "scores must be non-NULL and 16-byte aligned");
-  *out = dsa::IndexerArgs{x->H_I, x->D_I, x->dtype != DSA_F32, mx, x->q, x->q_scale, x->w,
-                          x->k_cache, x->k_scale, const_cast<float*>(scores), ld};
+  *out = dsa::IndexerArgs{x->H_I, x->D_I, kind, x->q, x->q_scale, x->w, x->k_cache,
+                          x->k_scale, const_cast<float*>(scores), ld};
   return DSA_OK;
 }
 
@@ -256,7 +270,7 @@ bool encode_tmap_2d(void* tmap_out, const void* base, int elem_bytes, uint64_t i
   const CUtensorMapDataType dt = elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const CUresult r = fn(static_cast<CUtensorMap*>(tmap_out), dt, 2,
                         const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        box_inner * elem_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     char buf[96];
@@ -585,6 +599,17 @@ dsa_status_t check_rope(const dsa_rope_desc_t* r, bool used, dsa::RopeArgs* out)
   return DSA_OK;
 }
 
+// Codes and scales of index vectors: the format, and what lengths it has.
+dsa_status_t check_codes(dsa_dtype_t dtype, int32_t D_I, dsa::IndexKind* kind) {
+  if (!index_kind(dtype, kind) || *kind == dsa::IndexKind::kF32)
+    return fail(DSA_ERR_UNSUPPORTED, "index codes are DSA_E4M3, DSA_MXFP8_E4M3 or DSA_MXFP4_E2M1");
+  const bool mx = block_scaled(*kind);
+  if (mx ? (D_I < 32 || D_I > 1024 || D_I % 32 != 0) : (D_I < 4 || D_I > 1024 || D_I % 4 != 0))
+    return fail(DSA_ERR_UNSUPPORTED, mx ? "MXFP8 and MXFP4 index vectors need D_I in [32, 1024], a multiple of 32"
+                                        : "E4M3 index vectors need D_I in [4, 1024], a multiple of 4");
+  return DSA_OK;
+}
+
 // Whether rows of n values at t * st + h * sh are pairwise disjoint.
 bool rows_disjoint(int64_t T, int64_t st, int64_t H, int64_t sh, int64_t n) {
   if (T <= 1 && H <= 1) return true;
@@ -695,12 +720,8 @@ dsa_status_t dsa_index_cache_append_rope(const dsa_seq_desc_t* seq, const dsa_ro
     dsa::RopeArgs r;
     dsa_status_t st = check_seq(seq, &s);
     if (st != DSA_OK) return st;
-    if (key_dtype != DSA_E4M3 && key_dtype != DSA_MXFP8_E4M3)
-      return fail(DSA_ERR_UNSUPPORTED, "index keys are cached as DSA_E4M3 or DSA_MXFP8_E4M3");
-    const bool mx = key_dtype == DSA_MXFP8_E4M3;
-    if (mx ? (D_I < 32 || D_I > 1024 || D_I % 32 != 0) : (D_I < 4 || D_I > 1024 || D_I % 4 != 0))
-      return fail(DSA_ERR_UNSUPPORTED, mx ? "MXFP8 index-key append needs D_I in [32, 1024], a multiple of 32"
-                                          : "index-key append needs D_I in [4, 1024], a multiple of 4");
+    dsa::IndexKind kind;
+    if ((st = check_codes(key_dtype, D_I, &kind)) != DSA_OK) return st;
     if (src_dtype != DSA_F32 && src_dtype != DSA_BF16)
       return fail(DSA_ERR_UNSUPPORTED, "new index keys must be DSA_F32 or DSA_BF16");
     if ((st = check_rope(rope, s.T > 0, &r)) != DSA_OK) return st;
@@ -716,9 +737,99 @@ dsa_status_t dsa_index_cache_append_rope(const dsa_seq_desc_t* seq, const dsa_ro
     dsa::LaunchEnv env;
     if ((st = make_env(stream, &env)) != DSA_OK) return st;
     std::string plan;
-    const cudaError_t e = dsa::launch_index_write(s, r, D_I, rot_offset, src_dtype == DSA_BF16, mx, k_new, k_stride * es,
+    const cudaError_t e = dsa::launch_index_write(s, r, D_I, rot_offset, src_dtype == DSA_BF16, kind, k_new, k_stride * es,
                                                   k_cache, k_scale, env, &plan);
     if (e != cudaSuccess) return cuda_fail(e, "index-key append launch");
+    g_last_plan = plan;
+    return DSA_OK;
+  } catch (...) {
+    return fail(DSA_ERR_CUDA, "unexpected host exception");
+  }
+}
+
+dsa_status_t dsa_index_cache_append_mx4(const dsa_seq_desc_t* seq, int32_t D_I, dsa_dtype_t src_dtype,
+                                        const void* k_new, uint8_t* k_cache, uint8_t* k_exp, dsa_stream_t stream) {
+  try {
+    dsa::SeqArgs s;
+    dsa_status_t st = check_seq(seq, &s);
+    if (st != DSA_OK) return st;
+    dsa::IndexKind kind;
+    if ((st = check_codes(DSA_MXFP4_E2M1, D_I, &kind)) != DSA_OK) return st;
+    if (src_dtype != DSA_F32 && src_dtype != DSA_BF16)
+      return fail(DSA_ERR_UNSUPPORTED, "new index keys must be DSA_F32 or DSA_BF16");
+    if (s.T > 0 && (!k_new || !k_cache || !k_exp))
+      return fail(DSA_ERR_INVALID_ARG, "k_new, k_cache and k_exp must be non-NULL");
+    if (!aligned16(k_new) || !aligned16(k_cache) || !aligned16(k_exp))
+      return fail(DSA_ERR_INVALID_ARG, "k_new, k_cache and k_exp must be 16-byte aligned");
+    dsa::LaunchEnv env;
+    if ((st = make_env(stream, &env)) != DSA_OK) return st;
+    std::string plan;
+    const cudaError_t e = dsa::launch_index_append_mx4(s, D_I, src_dtype == DSA_BF16, k_new, k_cache, k_exp, env, &plan);
+    if (e != cudaSuccess) return cuda_fail(e, "index-key append launch");
+    g_last_plan = plan;
+    return DSA_OK;
+  } catch (...) {
+    return fail(DSA_ERR_CUDA, "unexpected host exception");
+  }
+}
+
+dsa_status_t dsa_index_query_quantize(int32_t T, int32_t H_I, int32_t D_I, dsa_dtype_t src_dtype,
+                                      dsa_dtype_t code_dtype, const void* q, int64_t stride_t, int64_t stride_h,
+                                      uint8_t* codes, void* scale, dsa_stream_t stream) {
+  try {
+    if (T < 0 || H_I < 0) return fail(DSA_ERR_INVALID_ARG, "need T >= 0 and H_I >= 0");
+    dsa::IndexKind kind;
+    dsa_status_t st = check_codes(code_dtype, D_I, &kind);
+    if (st != DSA_OK) return st;
+    if (src_dtype != DSA_F32 && src_dtype != DSA_BF16)
+      return fail(DSA_ERR_UNSUPPORTED, "query heads must be DSA_F32 or DSA_BF16");
+    if (static_cast<int64_t>(T) * H_I > 0x7FFFFFFFll) return fail(DSA_ERR_INVALID_ARG, "T * H_I >= 2^31");
+    const bool used = T > 0 && H_I > 0;
+    if (used && (!q || !codes || !scale)) return fail(DSA_ERR_INVALID_ARG, "q, codes and scale must be non-NULL");
+    if (!aligned16(q) || !aligned16(codes) || !aligned16(scale))
+      return fail(DSA_ERR_INVALID_ARG, "q, codes and scale must be 16-byte aligned");
+    // a load is four values of E4M3 vectors (8 bytes of bf16), else 16 bytes
+    const int64_t es = src_dtype == DSA_F32 ? 4 : 2, unit = kind == dsa::IndexKind::kE4M3 ? 4 : 16 / es;
+    if (stride_t < 0 || stride_h < 0 || stride_t % unit != 0 || stride_h % unit != 0)
+      return fail(DSA_ERR_INVALID_ARG, "strides of q must be >= 0 and multiples of 16 bytes (DSA_E4M3: of 4 values)");
+    dsa::LaunchEnv env;
+    if ((st = make_env(stream, &env)) != DSA_OK) return st;
+    std::string plan;
+    const cudaError_t e = dsa::launch_query_quantize(T, H_I, D_I, src_dtype == DSA_BF16, kind, q, stride_t * es,
+                                                     stride_h * es, codes, scale, env, &plan);
+    if (e != cudaSuccess) return cuda_fail(e, "query quantisation launch");
+    g_last_plan = plan;
+    return DSA_OK;
+  } catch (...) {
+    return fail(DSA_ERR_CUDA, "unexpected host exception");
+  }
+}
+
+dsa_status_t dsa_index_cache_read(const dsa_seq_desc_t* seq, int32_t D_I, dsa_dtype_t key_dtype, const void* k_cache,
+                                  const void* k_scale, dsa_dtype_t out_dtype, void* out, int64_t out_stride,
+                                  dsa_stream_t stream) {
+  try {
+    dsa::SeqArgs s;
+    dsa_status_t st = check_seq(seq, &s);
+    if (st != DSA_OK) return st;
+    dsa::IndexKind kind;
+    if ((st = check_codes(key_dtype, D_I, &kind)) != DSA_OK) return st;
+    if (out_dtype != DSA_F32 && out_dtype != DSA_BF16)
+      return fail(DSA_ERR_UNSUPPORTED, "keys are read as DSA_F32 or DSA_BF16");
+    if (s.T > 0 && (!k_cache || !out)) return fail(DSA_ERR_INVALID_ARG, "k_cache and out must be non-NULL");
+    if (s.T > 0 && !k_scale && block_scaled(kind)) return fail(DSA_ERR_INVALID_ARG, "k_scale must be non-NULL");
+    if (!aligned16(k_cache) || !aligned16(k_scale) || !aligned16(out))
+      return fail(DSA_ERR_INVALID_ARG, "k_cache, k_scale and out must be 16-byte aligned");
+    // a store is four values of E4M3 keys (8 bytes of bf16), else 16 bytes
+    const int64_t es = out_dtype == DSA_F32 ? 4 : 2, unit = kind == dsa::IndexKind::kE4M3 ? 4 : 16 / es;
+    if (s.T > 1 && (out_stride < D_I || out_stride % unit != 0))
+      return fail(DSA_ERR_INVALID_ARG, "the stride of out must hold a key and be a multiple of 16 bytes (DSA_E4M3: of 4 values)");
+    dsa::LaunchEnv env;
+    if ((st = make_env(stream, &env)) != DSA_OK) return st;
+    std::string plan;
+    const cudaError_t e = dsa::launch_index_read(s, kind, D_I, k_cache, k_scale, out_dtype == DSA_F32, out,
+                                                 out_stride * es, env, &plan);
+    if (e != cudaSuccess) return cuda_fail(e, "index-key read launch");
     g_last_plan = plan;
     return DSA_OK;
   } catch (...) {
@@ -831,7 +942,7 @@ dsa_status_t dsa_check_status(dsa_stream_t stream) {
     const uint32_t f = dsa_status_read_clear_indexer() | dsa_status_read_clear_topk() |
                        dsa_status_read_clear_attn() | dsa_status_read_clear_cache() |
                        dsa_status_read_clear_prolog() | dsa_status_read_clear_rows() |
-                       dsa_status_read_clear_attn_e2m1();
+                       dsa_status_read_clear_attn_e2m1() | dsa_status_read_clear_index_keys();
     if (f == 0) return DSA_OK;
     if (f == 0xFFFFFFFFu) return fail(DSA_ERR_CUDA, "could not read the device status word");
     std::string msg = "device flags:";

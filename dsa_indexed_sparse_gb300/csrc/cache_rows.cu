@@ -66,10 +66,12 @@ __device__ __forceinline__ uint32_t e4m3_code2(float a, float b) {
 __device__ __forceinline__ uint32_t e4m3_code4(float a, float b, float c, float d) {
   return e4m3_code2(a, b) | (e4m3_code2(c, d) << 16);
 }
-// floor(log2 amax) - 8 clamped to [-127, 127]; -127 for 0 (the shared exponent of E4M3 blocks).
+// floor(log2 amax) - kTop clamped to [-127, 127]; -127 for 0: the shared exponent of blocks
+// of codes whose largest number has exponent kTop (8 for E4M3, 2 for E2M1).
+template <int kTop = 8>
 __device__ __forceinline__ int mx_exponent(float amax) {
   if (!(amax > 0.f)) return -127;
-  return max(-127, min(127, ilogbf(amax) - 8));
+  return max(-127, min(127, ilogbf(amax) - kTop));
 }
 
 // Pair i of a row of rope values as they are given (loaded) or held (stored).
@@ -257,7 +259,7 @@ struct IndexWriteArgs {
   void* k_scale;            // fp32 [rows], or E8M0 uint8 [rows, D / 32]
 };
 
-template <bool kBf16In, bool kMx>
+template <bool kBf16In, IndexKind kKind>
 __global__ void __launch_bounds__(kIndexWarps * 32) index_write_kernel(SeqArgs seq, IndexWriteArgs a) {
   __shared__ __align__(16) float rows[kIndexWarps][1024];
   grid_dep_wait();
@@ -293,7 +295,8 @@ __global__ void __launch_bounds__(kIndexWarps * 32) index_write_kernel(SeqArgs s
   }
   __syncwarp();
   uint32_t* dst = reinterpret_cast<uint32_t*>(a.k_cache + row * a.D);
-  if constexpr (kMx) {
+  if constexpr (kKind == IndexKind::kMx8 || kKind == IndexKind::kMx4) {
+    constexpr bool kFp4 = kKind == IndexKind::kMx4;
     // blocks of 32 values: the 4-value chunks of 8 consecutive lanes (nq is a multiple of 8)
     for (int c0 = 0; c0 < nq; c0 += 32) {
       const int c = c0 + lane;
@@ -301,10 +304,16 @@ __global__ void __launch_bounds__(kIndexWarps * 32) index_write_kernel(SeqArgs s
       float amax = fmaxf(fmaxf(fabsf(f.x), fabsf(f.y)), fmaxf(fabsf(f.z), fabsf(f.w)));
 #pragma unroll
       for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      const int e = mx_exponent(amax);
+      const int e = kFp4 ? mx_exponent<2>(amax) : mx_exponent<8>(amax);
       const float p = ldexpf(1.f, -e);
       if (c < nq) {
-        dst[c] = e4m3_code4(f.x * p, f.y * p, f.z * p, f.w * p);
+        if constexpr (kFp4) {
+          const uint32_t lo = __nv_cvt_float2_to_fp4x2(make_float2(f.x * p, f.y * p), __NV_E2M1, cudaRoundNearest);
+          const uint32_t hi = __nv_cvt_float2_to_fp4x2(make_float2(f.z * p, f.w * p), __NV_E2M1, cudaRoundNearest);
+          reinterpret_cast<uint16_t*>(a.k_cache + row * (a.D / 2))[c] = static_cast<uint16_t>(lo | (hi << 8));
+        } else {
+          dst[c] = e4m3_code4(f.x * p, f.y * p, f.z * p, f.w * p);
+        }
         if ((lane & 7) == 0) static_cast<uint8_t*>(a.k_scale)[row * (a.D / 32) + c / 8] = static_cast<uint8_t>(e + 127);
       }
     }
@@ -503,7 +512,7 @@ cudaError_t launch_latent_write(const SeqArgs& seq, const MlaArgs& a, const Rope
   return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_index_write(const SeqArgs& seq, const RopeArgs& rope, int32_t D, int32_t off, bool bf16_in, bool mx,
+cudaError_t launch_index_write(const SeqArgs& seq, const RopeArgs& rope, int32_t D, int32_t off, bool bf16_in, IndexKind kind,
                                const void* k_new, int64_t stride, uint8_t* k_cache, void* k_scale,
                                const LaunchEnv& env, std::string* plan) {
   if (seq.T == 0) {
@@ -512,13 +521,15 @@ cudaError_t launch_index_write(const SeqArgs& seq, const RopeArgs& rope, int32_t
   }
   const IndexWriteArgs a{rope, D, off, static_cast<const uint8_t*>(k_new), stride, k_cache, k_scale};
   const dim3 grid((static_cast<int64_t>(seq.T) + kIndexWarps - 1) / kIndexWarps), block(kIndexWarps * 32);
-  *plan += mx ? "index_append_rope<mx," : "index_append_rope<e4m3,";
+  *plan += kind == IndexKind::kMx4 ? "index_append_rope<mxfp4," : (kind == IndexKind::kMx8 ? "index_append_rope<mx," : "index_append_rope<e4m3,");
   *plan += bf16_in ? "bf16>" : "f32>";
-  if (mx)
-    return bf16_in ? launch_kernel(index_write_kernel<true, true>, grid, block, 0, env.stream, true, 1, seq, a)
-                   : launch_kernel(index_write_kernel<false, true>, grid, block, 0, env.stream, true, 1, seq, a);
-  return bf16_in ? launch_kernel(index_write_kernel<true, false>, grid, block, 0, env.stream, true, 1, seq, a)
-                 : launch_kernel(index_write_kernel<false, false>, grid, block, 0, env.stream, true, 1, seq, a);
+#define DSA_INDEX_GO(KIND)                                                                                         \
+  return bf16_in ? launch_kernel(index_write_kernel<true, KIND>, grid, block, 0, env.stream, true, 1, seq, a)     \
+                 : launch_kernel(index_write_kernel<false, KIND>, grid, block, 0, env.stream, true, 1, seq, a)
+  if (kind == IndexKind::kMx4) DSA_INDEX_GO(IndexKind::kMx4);
+  if (kind == IndexKind::kMx8) DSA_INDEX_GO(IndexKind::kMx8);
+  DSA_INDEX_GO(IndexKind::kE4M3);
+#undef DSA_INDEX_GO
 }
 
 cudaError_t launch_latent_read(const SeqArgs& seq, const MlaArgs& a, const void* kv_cache, bool f32_out, void* out,

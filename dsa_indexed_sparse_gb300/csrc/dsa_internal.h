@@ -23,15 +23,17 @@ struct SeqArgs {
   int64_t n_pages;  // cache_rows / page_size
 };
 
+// fp32 values; E4M3 codes with an fp32 scale a vector; E4M3 or E2M1 codes with an E8M0 scale per 32 values
+enum class IndexKind { kF32 = 0, kE4M3 = 1, kMx8 = 2, kMx4 = 3 };
+
 struct IndexerArgs {
   int32_t H_I, D_I;
-  bool e4m3;  // e4m3 codes (else fp32 values)
-  bool mx;    // e4m3 codes with E8M0 scales per 32 elements (q_scale/k_scale uint8)
+  IndexKind kind;
   const void* q;
-  const void* q_scale;  // fp32 [T, H_I] (may be null) or uint8 [T, H_I, D_I/32] (mx)
+  const void* q_scale;  // fp32 [T, H_I] (may be null) or uint8 [T, H_I, D_I/32] (kMx8, kMx4)
   const float* w;
   const void* k;
-  const void* k_scale;  // fp32 [rows] (may be null) or uint8 [rows, D_I/32] (mx)
+  const void* k_scale;  // fp32 [rows] (may be null) or uint8 [rows, D_I/32] (kMx8, kMx4)
   float* scores;
   int64_t ld;
 };
@@ -165,11 +167,21 @@ void rope_turns(int32_t d_rot, double theta, int scaling, double factor, double 
 cudaError_t launch_latent_write(const SeqArgs& seq, const MlaArgs& a, const RopeArgs& rope, const void* latent,
                                 int64_t latent_stride, const void* k_rope, int64_t rope_stride, void* kv_cache,
                                 const LaunchEnv& env, std::string* plan);
-cudaError_t launch_index_write(const SeqArgs& seq, const RopeArgs& rope, int32_t D, int32_t off, bool bf16_in, bool mx,
+cudaError_t launch_index_write(const SeqArgs& seq, const RopeArgs& rope, int32_t D, int32_t off, bool bf16_in, IndexKind kind,
                                const void* k_new, int64_t stride, uint8_t* k_cache, void* k_scale,
                                const LaunchEnv& env, std::string* plan);
 cudaError_t launch_latent_read(const SeqArgs& seq, const MlaArgs& a, const void* kv_cache, bool f32_out, void* out,
                                int64_t out_stride, const LaunchEnv& env, std::string* plan);
+
+// MXFP4 index keys, query heads to codes and scales (kind: kE4M3, kMx8, kMx4), and the
+// reader of cached index keys.  Strides in bytes.
+cudaError_t launch_index_append_mx4(const SeqArgs& seq, int32_t D, bool bf16_in, const void* k_new, uint8_t* k_cache,
+                                    uint8_t* k_exp, const LaunchEnv& env, std::string* plan);
+cudaError_t launch_query_quantize(int64_t T, int32_t H, int32_t D, bool bf16_in, IndexKind kind, const void* q,
+                                  int64_t stride_t, int64_t stride_h, uint8_t* codes, void* scale, const LaunchEnv& env,
+                                  std::string* plan);
+cudaError_t launch_index_read(const SeqArgs& seq, IndexKind kind, int32_t D, const void* codes, const void* scale,
+                              bool f32_out, void* out, int64_t out_stride, const LaunchEnv& env, std::string* plan);
 
 // Sets the text dsa_last_error() returns on the calling thread.
 void set_last_error(const std::string& msg);
@@ -196,7 +208,8 @@ dsa_status_t decode_workspace_need(const dsa_seq_desc_t* seq, const dsa_mla_desc
 bool encode_tmap_2d_u8(void* tmap_out, const void* base, uint64_t inner, uint64_t rows,
                        uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows,
                        std::string* why);
-// Same for 1- or 2-byte elements (inner / box_inner counted in elements), 128-byte swizzle.
+// Same for 1- or 2-byte elements (inner / box_inner counted in elements); the swizzle is
+// that of the box's row, 128 or 64 bytes.
 bool encode_tmap_2d(void* tmap_out, const void* base, int elem_bytes, uint64_t inner, uint64_t rows,
                     uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows, std::string* why);
 
@@ -210,3 +223,4 @@ uint32_t dsa_status_read_clear_cache();
 uint32_t dsa_status_read_clear_prolog();
 uint32_t dsa_status_read_clear_rows();
 uint32_t dsa_status_read_clear_attn_e2m1();
+uint32_t dsa_status_read_clear_index_keys();

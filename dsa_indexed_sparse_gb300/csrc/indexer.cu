@@ -28,6 +28,7 @@
 
 #include "dsa_device.cuh"
 #include "dsa_internal.h"
+#include "latent_e2m1.cuh"
 #include "topk_select.cuh"
 
 DSA_DEFINE_STATUS_WORD(indexer)
@@ -38,17 +39,27 @@ namespace {
 // =============================================================== generic kernel
 constexpr int kGenThreads = 256;
 
-// kFmt: 0 fp32 values, 1 e4m3 codes with fp32 per-token / per-head scales,
-// 2 MXFP8 (e4m3 codes, E8M0 scale per 32 elements: the query is dequantised
-// into shared memory and each key element is dequantised as it is read; both
-// are exact in fp32).
-template <int kFmt>
+// kF32: fp32 values; kE4M3: codes with fp32 per-token / per-head scales; kMx8 and
+// kMx4 (E4M3 or E2M1 codes, E8M0 scale per 32 elements): the query is dequantised
+// into shared memory and each key element is dequantised as it is read; both are
+// exact in fp32.
+template <IndexKind kKind>
 __global__ void __launch_bounds__(kGenThreads)
     indexer_generic_kernel(SeqArgs seq, IndexerArgs a) {
   grid_dep_wait();
+  constexpr bool kMx = kKind == IndexKind::kMx8 || kKind == IndexKind::kMx4;
+  // element i of the vector whose codes start at `codes`
+  auto code_value = [](const uint8_t* codes, int i) -> float {
+    if (kKind == IndexKind::kMx4) {
+      const float2 v = e2m1x2_to_float2(codes[i >> 1]);
+      return (i & 1) ? v.y : v.x;
+    }
+    return e4m3_to_float(codes[i]);
+  };
+  const int row_codes = kKind == IndexKind::kMx4 ? a.D_I / 2 : a.D_I;   // bytes of a vector
   extern __shared__ float sm_gen[];
-  float* qf = sm_gen;                   // [H_I * D_I] query values (codes for kFmt 1)
-  float* wq = sm_gen + a.H_I * a.D_I;  // [H_I] w * q_scale (w for MXFP8)
+  float* qf = sm_gen;                   // [H_I * D_I] query values (codes for kE4M3)
+  float* wq = sm_gen + a.H_I * a.D_I;  // [H_I] w * q_scale (w for block scales)
   const int t = blockIdx.y;
   const int qpos = __ldg(seq.q_pos + t);
   const int b = __ldg(seq.q_seq + t);
@@ -57,14 +68,15 @@ __global__ void __launch_bounds__(kGenThreads)
     return;
   }
   const int HD = a.H_I * a.D_I;
-  const int nb = a.D_I / 32;            // MXFP8 blocks per vector
+  const int nb = a.D_I / 32;            // blocks per vector
   for (int i = threadIdx.x; i < HD; i += blockDim.x) {
-    if (kFmt == 0) {
+    if (kKind == IndexKind::kF32) {
       qf[i] = static_cast<const float*>(a.q)[static_cast<int64_t>(t) * HD + i];
     } else {
-      float v = e4m3_to_float(static_cast<const uint8_t*>(a.q)[static_cast<int64_t>(t) * HD + i]);
-      if (kFmt == 2) {
-        const int h = i / a.D_I, blk = (i % a.D_I) / 32;
+      const int h = i / a.D_I;
+      float v = code_value(static_cast<const uint8_t*>(a.q) + (static_cast<int64_t>(t) * a.H_I + h) * row_codes, i % a.D_I);
+      if (kMx) {
+        const int blk = (i % a.D_I) / 32;
         const int e = static_cast<const uint8_t*>(a.q_scale)[(static_cast<int64_t>(t) * a.H_I + h) * nb + blk];
         v = ldexpf(v, e - 127);
       }
@@ -72,7 +84,7 @@ __global__ void __launch_bounds__(kGenThreads)
     }
   }
   for (int h = threadIdx.x; h < a.H_I; h += blockDim.x) {
-    const float sq = (kFmt != 2 && a.q_scale)
+    const float sq = (!kMx && a.q_scale)
                          ? __ldg(static_cast<const float*>(a.q_scale) + static_cast<int64_t>(t) * a.H_I + h)
                          : 1.f;
     wq[h] = __ldg(a.w + static_cast<int64_t>(t) * a.H_I + h) * sq;
@@ -86,21 +98,21 @@ __global__ void __launch_bounds__(kGenThreads)
   float acc = 0.f;
   for (int h = 0; h < a.H_I; ++h) {
     float d = 0.f;
-    if (kFmt == 0) {
+    if (kKind == IndexKind::kF32) {
       const float* kr = static_cast<const float*>(a.k) + row * a.D_I;
       for (int i = 0; i < a.D_I; ++i) d = fmaf(qf[h * a.D_I + i], kr[i], d);
-    } else if (kFmt == 1) {
+    } else if (!kMx) {
       const uint8_t* kr = static_cast<const uint8_t*>(a.k) + row * a.D_I;
       for (int i = 0; i < a.D_I; ++i) d = fmaf(qf[h * a.D_I + i], e4m3_to_float(kr[i]), d);
     } else {
-      const uint8_t* kr = static_cast<const uint8_t*>(a.k) + row * a.D_I;
+      const uint8_t* kr = static_cast<const uint8_t*>(a.k) + row * row_codes;
       const uint8_t* ke = static_cast<const uint8_t*>(a.k_scale) + row * nb;
       for (int i = 0; i < a.D_I; ++i)
-        d = fmaf(qf[h * a.D_I + i], ldexpf(e4m3_to_float(kr[i]), static_cast<int>(ke[i / 32]) - 127), d);
+        d = fmaf(qf[h * a.D_I + i], ldexpf(code_value(kr, i), static_cast<int>(ke[i / 32]) - 127), d);
     }
     acc = fmaf(wq[h], fmaxf(d, 0.f), acc);
   }
-  const float sk = (kFmt != 2 && a.k_scale) ? __ldg(static_cast<const float*>(a.k_scale) + row) : 1.f;
+  const float sk = (!kMx && a.k_scale) ? __ldg(static_cast<const float*>(a.k_scale) + row) : 1.f;
   a.scores[static_cast<int64_t>(t) * a.ld + s] = acc * sk;
 }
 
@@ -128,9 +140,9 @@ constexpr uint32_t kSleepNs = 1000;
 // cp.async; the MMAs: barrier waits, descriptors, four MMAs, two commits), which
 // capped an SM at ~37 GB/s of keys: kProd producer warps and kMmaWarps issuing
 // warps take the tiles in turn as the epilogue groups do.
-template <int G, bool kMx = false>
+template <int G, IndexKind kKind = IndexKind::kE4M3>
 struct TcWarps {
-  static constexpr int kRot = G == 1 ? (kMx ? 2 : 3) : 1;
+  static constexpr int kRot = G == 1 ? (kKind == IndexKind::kMx8 ? 2 : 3) : 1;
   static constexpr int kProd = 2;                  // divides kTcStages
   static constexpr int kMmaWarps = G == 1 ? 2 : 1;
   static constexpr int kMma = kProd;               // the first MMA-issuing warp (also allocates TMEM)
@@ -143,17 +155,35 @@ struct TcWarps {
 // blocks of the K = 128 dot product go to four separate accumulators (one
 // MMA each, no accumulation), which the epilogue scales by the two blocks'
 // power-of-two factors and sums: d = sum_b 2^(eq_b + ek_b - 254) * D_b.
-template <int G, bool kMx = false>
+//
+// kMx4: MXFP4 keys and queries on the block-scaled MMA, which multiplies each 32-wide
+// block's products by both powers of two itself: one accumulator, two MMAs (K = 64
+// each).  Its scales lie in TMEM, a word per key and per query head, brought there by
+// tcgen05.cp from shared memory.  With four queries a group, two accumulators of all
+// 256 columns would leave no room for them, so every query has MMAs (N = 64) and
+// accumulators of its own: a ring of seven 64-column slots, slot (tile * G + query) % 7.
+template <int G, IndexKind kKind = IndexKind::kE4M3>
 struct TcCfg {
+  static constexpr bool kMx = kKind == IndexKind::kMx8, kMx4 = kKind == IndexKind::kMx4;
   static_assert(!kMx || G == 1, "MXFP8 keys run one query per group");
-  static constexpr int N = kTcHeads * G;                 // UMMA N
+  static constexpr int N = kTcHeads * G;                 // UMMA N (kMx4: of all of the tile's MMAs)
   static constexpr int kBlocks = kMx ? kTcDim / 32 : 1;  // accumulators per tile
-  static constexpr int kAccCols = kBlocks * N;           // TMEM columns per tile
-  static constexpr int kStageBytes = kTcKeys * kTcDim;   // 16384
-  static constexpr int kQBytes = N * kTcDim;             // one query-group buffer
-  // accumulator buffers: two, or one per rotation group
-  static constexpr int kAccBufs = TcWarps<G, kMx>::kRot > 2 ? TcWarps<G, kMx>::kRot : 2;
-  static constexpr int kTmemNeed = kAccBufs * kAccCols;
+  static constexpr int kAccCols = kMx4 ? kTcHeads : kBlocks * N;   // TMEM columns per tile (kMx4: per slot)
+  static constexpr int kRowBytes = kMx4 ? kTcDim / 2 : kTcDim;     // codes of a key or query head
+  static constexpr int kStageBytes = kTcKeys * kRowBytes;
+  static constexpr int kQBytes = N * kRowBytes;          // one query-group buffer
+  // accumulator buffers: two, or one per rotation group; or the slots
+  static constexpr int kAccBufs = kMx4 && G > 1 ? 7 : (TcWarps<G, kKind>::kRot > 2 ? TcWarps<G, kKind>::kRot : 2);
+  // kMx4, behind the accumulators: the keys' scale words, four columns a tile, for as many
+  // tiles as there are accumulators, or four (before a tile's are copied, its first slot has
+  // come round, so the MMAs of the tile before the last three are done); then the heads', two
+  // columns a query, for each issuing warp and query-group buffer (four for a single query:
+  // a copy writes four)
+  static constexpr int kKeyScaleCol = kAccBufs * kAccCols;
+  static constexpr int kQScaleCols = kMx4 ? (G > 1 ? 2 * G : 4) : 0;
+  static constexpr int kQScaleCol = kKeyScaleCol + 16;
+  static constexpr int kTmemNeed =
+      kMx4 ? kQScaleCol + 2 * TcWarps<G, kKind>::kMmaWarps * kQScaleCols : kAccBufs * kAccCols;
   static_assert(kTmemNeed <= 512, "TMEM plan");
   static constexpr uint32_t kTmemCols = kTmemNeed <= 128 ? 128u : (kTmemNeed <= 256 ? 256u : 512u);
   // per epilogue warp: w / 2 for its 64 heads, then (MXFP8) the query's block
@@ -163,8 +193,13 @@ struct TcCfg {
   static constexpr int kOffQ = kOffStages + kTcStages * kStageBytes;
   static constexpr int kOffWq = kOffQ + 2 * kQBytes;      // float [4G][kSlice]: each epilogue warp's slice
   // key scales: 4 bytes per key (an fp32 scale, or MXFP8's four E8M0 bytes)
-  static constexpr int kOffScale = kOffWq + TcWarps<G, kMx>::kEpiWarps * kSlice * 4;
-  static constexpr int kOffValid = kOffScale + kTcStages * kTcKeys * 4;  // uint32 [stages]
+  // (kMx4: as tcgen05.cp takes them, 16 bytes for keys i, i + 32, i + 64, i + 96)
+  static constexpr int kOffScale = kOffWq + TcWarps<G, kKind>::kEpiWarps * kSlice * 4;
+  // kMx4: the query heads' scale words, 16 bytes for heads i, i + 32 of two queries
+  static constexpr int kQScaleBytes = kQScaleCols * 128;
+  static constexpr int kOffQScale = kOffScale + kTcStages * kTcKeys * 4;
+  static_assert(kOffScale % 128 == 0 && kOffQScale % 128 == 0, "scale words as MMA operands");
+  static constexpr int kOffValid = kOffQScale + 2 * kQScaleBytes;  // uint32 [stages]
   static constexpr int kOffBar = kOffValid + kTcStages * 4 + 8;
   // barriers: full[S], empty[S], qfull[2], qempty[2], accfull[A], accempty[A], drain
   static constexpr int kNumBars = 2 * kTcStages + 4 + 2 * kAccBufs + 1;
@@ -176,6 +211,7 @@ struct TcCfg {
   static constexpr int kOffKeys = (kOffSel + static_cast<int>(sizeof(SelectSmem)) + 127) / 128 * 128;
   static_assert(kOffKeys % 16 == 0 && kOffSel % 16 == 0, "aligned fused-plan regions");
   static constexpr uint32_t kIdesc = make_idesc(kFmtE4M3, kFmtE4M3, false, false, kTcKeys, N);
+  static constexpr uint32_t kIdescLo = make_idesc_mxf4(kTcKeys, kTcHeads, 0), kIdescHi = make_idesc_mxf4(kTcKeys, kTcHeads, 2);
 };
 
 // Keys of one query a CTA of the fused plan holds in shared memory at most.
@@ -252,18 +288,20 @@ __device__ __forceinline__ int block_sum(int v, int* red) {
 // global memory) and counts it into the first histogram; once the cluster's
 // keys are complete the CTAs select the Top-K together and only the index row
 // leaves the SM.
-template <int G, bool kMx, bool kFused>
-__global__ void __launch_bounds__(TcWarps<G, kMx>::kThreads, 1)
+template <int G, IndexKind kKind, bool kFused>
+__global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
     indexer_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap kmap2,
                       const __grid_constant__ CUtensorMap qmap, TcParams p) {
   static_assert(!kFused || G == 1, "the fused plan runs one query per group");
-  using C = TcCfg<G, kMx>;
-  constexpr int kTcThreads = TcWarps<G, kMx>::kThreads;
-  constexpr int kRot = TcWarps<G, kMx>::kRot;
-  constexpr int kProd = TcWarps<G, kMx>::kProd;
-  constexpr int kMmaWarp = TcWarps<G, kMx>::kMma;
-  constexpr int kMmaWarps = TcWarps<G, kMx>::kMmaWarps;
-  constexpr int kEpi0 = TcWarps<G, kMx>::kEpi0;
+  using C = TcCfg<G, kKind>;
+  using W = TcWarps<G, kKind>;
+  constexpr bool kMx = C::kMx, kMx4 = C::kMx4;
+  constexpr int kTcThreads = W::kThreads;
+  constexpr int kRot = W::kRot;
+  constexpr int kProd = W::kProd;
+  constexpr int kMmaWarp = W::kMma;
+  constexpr int kMmaWarps = W::kMmaWarps;
+  constexpr int kEpi0 = W::kEpi0;
   static_assert(kTcStages % kProd == 0, "each producer owns every kProd-th stage");
   constexpr int kGroupWarps = 4 * G;           // epilogue warps that share one tile
   constexpr int NB = C::kAccBufs;
@@ -380,12 +418,12 @@ __global__ void __launch_bounds__(TcWarps<G, kMx>::kThreads, 1)
       mbar_init(&empty[i], 1 + kGroupWarps);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&qfull[i], 1);
+      mbar_init(&qfull[i], kMx4 ? 33 : 1);   // kMx4: and a lane's copies of scale words
       mbar_init(&qempty[i], kMmaWarps);   // each issuing warp releases a group's Q
     }
     for (int i = 0; i < NB; ++i) {
       mbar_init(&accfull[i], 1);
-      mbar_init(&accempty[i], kGroupWarps);
+      mbar_init(&accempty[i], kMx4 ? 4 : kGroupWarps);   // kMx4: a slot is one query's
     }
     mbar_init(drain, kMmaWarps);
     *abort_flag = 0;
@@ -464,6 +502,18 @@ __global__ void __launch_bounds__(TcWarps<G, kMx>::kThreads, 1)
             mbar_arrive_expect_tx(&qfull[qb], C::kQBytes);
             tma_load_2d(sm + C::kOffQ + qb * C::kQBytes, &qmap, &qfull[qb], 0, w.g * G * kTcHeads);
           }
+          if constexpr (kMx4) {
+            const uint8_t* src = static_cast<const uint8_t*>(p.a.q_scale);
+            const uint32_t dst = smem_u32(sm + C::kOffQScale + qb * C::kQScaleBytes) + lane * 16;
+#pragma unroll
+            for (int i = 0; i < 2 * G; ++i) {   // heads 32 (i % 2) + lane of query i / 2
+              const int t = w.g * G + (i >> 1);
+              if (t < p.seq.T)
+                cp_async4(dst + (i >> 2) * 512 + (i & 3) * 4,
+                          src + (static_cast<int64_t>(t) * kTcHeads + (i & 1) * 32 + lane) * 4);
+            }
+            cp_async_mbar_arrive(&qfull[qb]);
+          }
         }
         q_mine = mine ? (q_mine | (1u << qb)) : (q_mine & ~(1u << qb));
         const int b = w.g == pre_g ? pre_b : __ldg(p.seq.q_seq + w.g * G);
@@ -509,7 +559,18 @@ __global__ void __launch_bounds__(TcWarps<G, kMx>::kThreads, 1)
           if (pid1 >= 0) tma_load_2d(dst + C::kStageBytes / 2, &kmap, &full[st], 0, pid1 * kTcPage);
         }
       }
-      if (p.a.k_scale != nullptr) {
+      if constexpr (kMx4) {
+        // key 32 c + lane of the tile: word c of the lane's 16 bytes
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int32_t pid = c < 2 ? pid0 : pid1;
+          if (pid >= 0)
+            cp_async4(smem_u32(scale_s + st * kTcKeys) + lane * 16 + c * 4,
+                      static_cast<const uint8_t*>(p.a.k_scale) +
+                          (static_cast<int64_t>(pid) * kTcPage + (c & 1) * 32 + lane) * 4);
+        }
+        cp_async_mbar_arrive(&full[st]);
+      } else if (p.a.k_scale != nullptr) {
         // lanes 0-15: the 64 scales of the first page, lanes 16-31: the second (16 B each)
         const int half = lane >> 4;
         const int32_t pid = half ? pid1 : pid0;
@@ -551,6 +612,16 @@ __global__ void __launch_bounds__(TcWarps<G, kMx>::kThreads, 1)
         qb = qcount & 1;
         const bool ok = mbar_wait(&qfull[qb], (qcount >> 1) & 1, &g_status_indexer, abort_flag, kWaitLimitNs, kSleepNs);
         if (!__all_sync(0xffffffffu, ok)) break;
+        if constexpr (kMx4) {
+          fence_proxy_async_smem();   // the scale words were written by cp.async
+          if (elect_one()) {
+            const uint64_t ds = make_sdesc(smem_u32(sm + C::kOffQScale + qb * C::kQScaleBytes), 0, 128, kLayoutNone);
+#pragma unroll
+            for (int i = 0; i < C::kQScaleCols / 4; ++i)
+              tmem_copy_scales(tmem + C::kQScaleCol + (mw * 2 + qb) * C::kQScaleCols + 4 * i, ds + 32 * i);
+          }
+          __syncwarp();
+        }
         cur_g = w.g;
         ++qcount;
       }
@@ -558,6 +629,34 @@ __global__ void __launch_bounds__(TcWarps<G, kMx>::kThreads, 1)
       const int st = it % kTcStages;
       bool ok = mbar_wait(&full[st], (it / kTcStages) & 1, &g_status_indexer, abort_flag, kWaitLimitNs, kSleepNs);
       if (!__all_sync(0xffffffffu, ok)) break;
+      if constexpr (kMx4) {
+        const uint32_t ksc = tmem + C::kKeyScaleCol + (G == 1 ? it % NB : it & 3) * 4;
+        const uint32_t qsc = tmem + C::kQScaleCol + (mw * 2 + qb) * C::kQScaleCols;
+        const uint64_t dka = make_sdesc(smem_u32(sm + C::kOffStages + st * C::kStageBytes), 16, 512, kLayoutSw64);
+        const uint64_t dqb = make_sdesc(smem_u32(sm + C::kOffQ + qb * C::kQBytes), 16, 512, kLayoutSw64);
+        const uint64_t dks = make_sdesc(smem_u32(sm + C::kOffScale + st * kTcKeys * 4), 0, 128, kLayoutNone);
+        fence_proxy_async_smem();   // the scale words were written by cp.async
+        for (int j = 0; j < G; ++j) {
+          const int u = it * G + j, slot = u % NB;
+          if (u >= NB) {
+            ok = mbar_wait(&accempty[slot], ((u / NB) - 1) & 1, &g_status_indexer, abort_flag, kWaitLimitNs, kSleepNs);
+            if (!__all_sync(0xffffffffu, ok)) break;
+          }
+          tc_fence_after();
+          if (elect_one()) {
+            if (j == 0) tmem_copy_scales(ksc, dks);
+            const uint64_t db = dqb + static_cast<uint64_t>(j * (kTcHeads * C::kRowBytes / 16));
+            const uint32_t d = tmem + slot * C::kAccCols;
+            umma_mxf4(d, dka, db, C::kIdescLo, ksc, qsc + 2 * j, 0u);
+            umma_mxf4(d, dka + 2, db + 2, C::kIdescHi, ksc, qsc + 2 * j, 1u);
+            if (j == G - 1) umma_commit(&empty[st]);
+            umma_commit(&accfull[slot]);
+          }
+          __syncwarp();
+        }
+        if (!__all_sync(0xffffffffu, ok)) break;
+        continue;
+      }
       const int ab = it % NB;
       if (it >= NB) {
         ok = mbar_wait(&accempty[ab], ((it / NB) - 1) & 1, &g_status_indexer, abort_flag, kWaitLimitNs, kSleepNs);
@@ -630,7 +729,7 @@ __global__ void __launch_bounds__(TcWarps<G, kMx>::kThreads, 1)
         if (kMx) {
           pf_e0 = __ldg(static_cast<const uint32_t*>(p.a.q_scale) + o);
           pf_e1 = __ldg(static_cast<const uint32_t*>(p.a.q_scale) + o + 1);
-        } else if (p.a.q_scale) {
+        } else if (!kMx4 && p.a.q_scale) {
           pf_s0 = __ldg(static_cast<const float*>(p.a.q_scale) + o);
           pf_s1 = __ldg(static_cast<const float*>(p.a.q_scale) + o + 1);
         }
@@ -665,8 +764,9 @@ __global__ void __launch_bounds__(TcWarps<G, kMx>::kThreads, 1)
         cur_g = w.g;
         if (w.g + 1 < p.n_groups) prefetch(w.g + 1);
       }
-      const int ab = it % NB;
-      bool ok = mbar_wait(&accfull[ab], (it / NB) & 1, &g_status_indexer, abort_flag, kWaitLimitNs, kSleepNs);
+      const int au = kMx4 ? it * G + j : it;   // the accumulator's number
+      const int ab = au % NB;
+      bool ok = mbar_wait(&accfull[ab], (au / NB) & 1, &g_status_indexer, abort_flag, kWaitLimitNs, kSleepNs);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       // the stage (keys, scales, page validity) is still this tile's: the
@@ -682,7 +782,7 @@ __global__ void __launch_bounds__(TcWarps<G, kMx>::kThreads, 1)
       uint32_t ek = 0;   // MXFP8: this key's four E8M0 bytes
       if (kMx)
         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(ek) : "r"(scale_addr + st * (kTcKeys * 4)) : "memory");
-      else if (p.a.k_scale)
+      else if (!kMx4 && p.a.k_scale)
         asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sk) : "r"(scale_addr + st * (kTcKeys * 4)) : "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
@@ -733,7 +833,7 @@ __global__ void __launch_bounds__(TcWarps<G, kMx>::kThreads, 1)
       } else {
         // the 64 heads in two halves of 32 columns (fewer live registers: 18 warps
         // leave 96 a thread); head weights as 16-byte broadcast loads
-        const uint32_t col = tmem + lane_off + ab * C::N + j * kTcHeads;
+        const uint32_t col = tmem + lane_off + ab * C::kAccCols + (kMx4 ? 0 : j * kTcHeads);
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           uint32_t v[32];
@@ -790,17 +890,26 @@ __global__ void __launch_bounds__(TcWarps<G, kMx>::kThreads, 1)
   }
 }
 
-template <int G, bool kMx = false>
+// Tensor maps of the keys (one page, two pages) and of a group's query heads.
+template <typename C>
+bool encode_maps(const SeqArgs& seq, const IndexerArgs& a, CUtensorMap* kmap, CUtensorMap* kmap2, CUtensorMap* qmap,
+                 std::string* why) {
+  constexpr int n = C::kRowBytes;
+  return encode_tmap_2d_u8(kmap, a.k, n, static_cast<uint64_t>(seq.cache_rows), n, n, kTcPage, why) &&
+         encode_tmap_2d_u8(kmap2, a.k, n, static_cast<uint64_t>(seq.cache_rows), n, n, 2 * kTcPage, why) &&
+         encode_tmap_2d_u8(qmap, a.q, n, static_cast<uint64_t>(seq.T) * kTcHeads, n, n, C::N, why);
+}
+
+constexpr const char* kind_name(IndexKind kind) {
+  return kind == IndexKind::kMx4 ? "mxfp4" : (kind == IndexKind::kMx8 ? "mxfp8" : "e4m3");
+}
+
+template <int G, IndexKind kKind = IndexKind::kE4M3>
 cudaError_t launch_tc(const SeqArgs& seq, const IndexerArgs& a, const LaunchEnv& env,
                       std::string* plan, bool* unsupported, std::string* why) {
-  using C = TcCfg<G, kMx>;
+  using C = TcCfg<G, kKind>;
   alignas(64) CUtensorMap kmap, kmap2, qmap;
-  if (!encode_tmap_2d_u8(&kmap, a.k, kTcDim, static_cast<uint64_t>(seq.cache_rows), kTcDim,
-                         kTcDim, kTcPage, why) ||
-      !encode_tmap_2d_u8(&kmap2, a.k, kTcDim, static_cast<uint64_t>(seq.cache_rows), kTcDim,
-                         kTcDim, 2 * kTcPage, why) ||
-      !encode_tmap_2d_u8(&qmap, a.q, kTcDim, static_cast<uint64_t>(seq.T) * kTcHeads, kTcDim,
-                         kTcDim, C::N, why)) {
+  if (!encode_maps<C>(seq, a, &kmap, &kmap2, &qmap, why)) {
     *unsupported = true;
     return cudaSuccess;
   }
@@ -809,14 +918,15 @@ cudaError_t launch_tc(const SeqArgs& seq, const IndexerArgs& a, const LaunchEnv&
       static_cast<int64_t>(p.n_groups) * ((seq.max_ctx + kTcKeys - 1) / kTcKeys);
   const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(tiles_ub, env.num_sms)));
   const cudaError_t attr_err =
-      ensure_smem_limit(reinterpret_cast<const void*>(indexer_tc_kernel<G, kMx, false>), C::kSmemBytes, env.device);
+      ensure_smem_limit(reinterpret_cast<const void*>(indexer_tc_kernel<G, kKind, false>), C::kSmemBytes, env.device);
   if (attr_err != cudaSuccess) return attr_err;
-  const cudaError_t le = launch_kernel(indexer_tc_kernel<G, kMx, false>, dim3(grid), dim3(TcWarps<G, kMx>::kThreads), C::kSmemBytes,
+  const cudaError_t le = launch_kernel(indexer_tc_kernel<G, kKind, false>, dim3(grid), dim3(TcWarps<G, kKind>::kThreads), C::kSmemBytes,
                                        env.stream, true, 1,
                                     kmap, kmap2, qmap, p);
   if (le != cudaSuccess) return le;
   char buf[160];
-  snprintf(buf, sizeof(buf), "indexer_tc<G=%d%s>[grid=%d,tiles<=%lld]", G, kMx ? ",mxfp8" : "", grid,
+  snprintf(buf, sizeof(buf), "indexer_tc<G=%d%s%s>[grid=%d,tiles<=%lld]", G, kKind == IndexKind::kE4M3 ? "" : ",",
+           kKind == IndexKind::kE4M3 ? "" : kind_name(kKind), grid,
            static_cast<long long>(tiles_ub));
   *plan += buf;
   return cudaGetLastError();
@@ -826,7 +936,7 @@ cudaError_t launch_tc(const SeqArgs& seq, const IndexerArgs& a, const LaunchEnv&
 // CTAs, one cluster per query.  CL: the whole GPU in one wave at small batch
 // (up to 16 CTAs per query, non-portable cluster size), and enough CTAs that a
 // slice's keys fit kFusedMaxKeys.  Returns CL, or 0 when the plan does not apply.
-template <bool kMx>
+template <IndexKind kKind>
 int fused_cluster(const SeqArgs& seq, const LaunchEnv& env, int max_cl) {
   const int need = (seq.max_ctx + kFusedMaxKeys - 1) / kFusedMaxKeys;
   int cl = 1;
@@ -835,40 +945,37 @@ int fused_cluster(const SeqArgs& seq, const LaunchEnv& env, int max_cl) {
   if (cl > 16 || cl > max_cl) return 0;
   // every cluster of the launch resident at once is not required, but a cluster
   // of this size must fit on the GPU
-  using C = TcCfg<1, kMx>;
+  using C = TcCfg<1, kKind>;
   const int keys = (((seq.max_ctx + kTcKeys - 1) / kTcKeys + cl - 1) / cl) * kTcKeys;
   const size_t smem = static_cast<size_t>(C::kOffKeys) + static_cast<size_t>(keys) * 4 + 1024;
-  void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, TcParams) = indexer_tc_kernel<1, kMx, true>;
+  void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, TcParams) = indexer_tc_kernel<1, kKind, true>;
   if (ensure_smem_limit(reinterpret_cast<const void*>(kern),
                         C::kOffKeys + kFusedMaxKeys * 4 + 1024, env.device) != cudaSuccess)
     return 0;
-  while (cl > 1 && !cluster_fits(reinterpret_cast<const void*>(kern), env.device, cl, TcWarps<1, kMx>::kThreads, smem)) {
+  while (cl > 1 && !cluster_fits(reinterpret_cast<const void*>(kern), env.device, cl, TcWarps<1, kKind>::kThreads, smem)) {
     cl /= 2;
     if (cl < need) return 0;
   }
   return cl;
 }
 
-template <bool kMx>
+template <IndexKind kKind>
 cudaError_t launch_fused(const SeqArgs& seq, const IndexerArgs& a, int32_t K, int32_t* idx, int cl,
                          const LaunchEnv& env, std::string* plan, std::string* why, bool* unsupported) {
-  using C = TcCfg<1, kMx>;
+  using C = TcCfg<1, kKind>;
   alignas(64) CUtensorMap kmap, kmap2, qmap;
-  if (!encode_tmap_2d_u8(&kmap, a.k, kTcDim, static_cast<uint64_t>(seq.cache_rows), kTcDim, kTcDim, kTcPage, why) ||
-      !encode_tmap_2d_u8(&kmap2, a.k, kTcDim, static_cast<uint64_t>(seq.cache_rows), kTcDim, kTcDim, 2 * kTcPage,
-                         why) ||
-      !encode_tmap_2d_u8(&qmap, a.q, kTcDim, static_cast<uint64_t>(seq.T) * kTcHeads, kTcDim, kTcDim, C::N, why)) {
+  if (!encode_maps<C>(seq, a, &kmap, &kmap2, &qmap, why)) {
     *unsupported = true;
     return cudaSuccess;
   }
   TcParams p{seq, a, seq.T, K, idx};
   const int keys = (((seq.max_ctx + kTcKeys - 1) / kTcKeys + cl - 1) / cl) * kTcKeys;
   const size_t smem = static_cast<size_t>(C::kOffKeys) + static_cast<size_t>(keys) * 4 + 1024;
-  const cudaError_t le = launch_kernel(indexer_tc_kernel<1, kMx, true>, dim3(seq.T * cl), dim3(TcWarps<1, kMx>::kThreads),
+  const cudaError_t le = launch_kernel(indexer_tc_kernel<1, kKind, true>, dim3(seq.T * cl), dim3(TcWarps<1, kKind>::kThreads),
                                        smem, env.stream, true, cl, kmap, kmap2, qmap, p);
   if (le != cudaSuccess) return le;
   char buf[160];
-  snprintf(buf, sizeof(buf), "indexer_topk_fused<%s>[cluster=%d,grid=%d]", kMx ? "mxfp8" : "e4m3", cl, seq.T * cl);
+  snprintf(buf, sizeof(buf), "indexer_topk_fused<%s>[cluster=%d,grid=%d]", kind_name(kKind), cl, seq.T * cl);
   *plan += buf;
   return cudaGetLastError();
 }
@@ -879,11 +986,13 @@ cudaError_t launch_decode_fused(const SeqArgs& seq, const IndexerArgs& a, int32_
                                 const LaunchEnv& env, std::string* plan, bool* unsupported, std::string* why) {
   *unsupported = true;
   if (seq.T == 0 || K < 1) return cudaSuccess;
-  const bool tc_ok = a.e4m3 && a.H_I == kTcHeads && a.D_I == kTcDim && seq.page_size == kTcPage &&
+  const bool tc_ok = a.kind != IndexKind::kF32 && a.H_I == kTcHeads && a.D_I == kTcDim && seq.page_size == kTcPage &&
                      (reinterpret_cast<uintptr_t>(a.k) % 16 == 0) && (reinterpret_cast<uintptr_t>(a.q) % 16 == 0);
   // several queries of one sequence share their key reads in the chained plan
   if (!tc_ok || seq.q_per_seq > 1 || seq.T > env.num_sms) return cudaSuccess;
-  const int cl = a.mx ? fused_cluster<true>(seq, env, kFusedMaxCluster) : fused_cluster<false>(seq, env, kFusedMaxCluster);
+  const int cl = a.kind == IndexKind::kMx4   ? fused_cluster<IndexKind::kMx4>(seq, env, kFusedMaxCluster)
+                 : a.kind == IndexKind::kMx8 ? fused_cluster<IndexKind::kMx8>(seq, env, kFusedMaxCluster)
+                                             : fused_cluster<IndexKind::kE4M3>(seq, env, kFusedMaxCluster);
   // Measured on GB300: with one or two CTAs per query (a batch of >= num_sms / 4
   // queries) the fused kernel beats the chained indexer + Top-K (decode batch 64:
   // 81.0 vs 83.7 us a step); with more CTAs per query the selection's exchanges
@@ -891,8 +1000,9 @@ cudaError_t launch_decode_fused(const SeqArgs& seq, const IndexerArgs& a, int32_
   // batch 1: 25.9 vs 25.7 us; batch 4 at 131072 positions: 61.1 vs 55.8 us).
   if (cl < 1 || cl > kFusedMaxCluster) return cudaSuccess;
   *unsupported = false;
-  return a.mx ? launch_fused<true>(seq, a, K, idx, cl, env, plan, why, unsupported)
-              : launch_fused<false>(seq, a, K, idx, cl, env, plan, why, unsupported);
+  return a.kind == IndexKind::kMx4   ? launch_fused<IndexKind::kMx4>(seq, a, K, idx, cl, env, plan, why, unsupported)
+         : a.kind == IndexKind::kMx8 ? launch_fused<IndexKind::kMx8>(seq, a, K, idx, cl, env, plan, why, unsupported)
+                                     : launch_fused<IndexKind::kE4M3>(seq, a, K, idx, cl, env, plan, why, unsupported);
 }
 
 cudaError_t launch_indexer(const SeqArgs& seq, const IndexerArgs& a, const LaunchEnv& env,
@@ -902,12 +1012,15 @@ cudaError_t launch_indexer(const SeqArgs& seq, const IndexerArgs& a, const Launc
     *plan += "indexer[empty]";
     return cudaSuccess;
   }
-  const bool tc_ok = a.e4m3 && a.H_I == kTcHeads && a.D_I == kTcDim && seq.page_size == kTcPage &&
+  const bool tc_ok = a.kind != IndexKind::kF32 && a.H_I == kTcHeads && a.D_I == kTcDim && seq.page_size == kTcPage &&
                      (reinterpret_cast<uintptr_t>(a.k) % 16 == 0) &&
                      (reinterpret_cast<uintptr_t>(a.q) % 16 == 0);
   if (tc_ok) {
-    if (a.mx) return launch_tc<1, true>(seq, a, env, plan, unsupported, why);
+    if (a.kind == IndexKind::kMx8) return launch_tc<1, IndexKind::kMx8>(seq, a, env, plan, unsupported, why);
     const int qps = seq.q_per_seq;
+    if (a.kind == IndexKind::kMx4)
+      return qps > 0 && qps % 4 == 0 ? launch_tc<4, IndexKind::kMx4>(seq, a, env, plan, unsupported, why)
+                                     : launch_tc<1, IndexKind::kMx4>(seq, a, env, plan, unsupported, why);
     if (qps > 0 && qps % 4 == 0) return launch_tc<4>(seq, a, env, plan, unsupported, why);
     if (qps > 0 && qps % 2 == 0) return launch_tc<2>(seq, a, env, plan, unsupported, why);
     return launch_tc<1>(seq, a, env, plan, unsupported, why);
@@ -919,16 +1032,19 @@ cudaError_t launch_indexer(const SeqArgs& seq, const IndexerArgs& a, const Launc
     return cudaSuccess;
   }
   dim3 grid((seq.max_ctx + kGenThreads - 1) / kGenThreads, seq.T);
-  const int fmt = a.mx ? 2 : (a.e4m3 ? 1 : 0);
-  void (*kern)(SeqArgs, IndexerArgs) = fmt == 2 ? indexer_generic_kernel<2>
-                                       : (fmt == 1 ? indexer_generic_kernel<1> : indexer_generic_kernel<0>);
+  void (*kern)(SeqArgs, IndexerArgs) = a.kind == IndexKind::kMx4    ? indexer_generic_kernel<IndexKind::kMx4>
+                                       : a.kind == IndexKind::kMx8  ? indexer_generic_kernel<IndexKind::kMx8>
+                                       : a.kind == IndexKind::kE4M3 ? indexer_generic_kernel<IndexKind::kE4M3>
+                                                                    : indexer_generic_kernel<IndexKind::kF32>;
   if (smem > 48 * 1024) {
     const cudaError_t ae = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (ae != cudaSuccess) return ae;
   }
   const cudaError_t le = launch_kernel(kern, grid, dim3(kGenThreads), smem, env.stream, true, 1, seq, a);
   if (le != cudaSuccess) return le;
-  *plan += fmt == 2 ? "indexer_generic<mxfp8>" : (fmt == 1 ? "indexer_generic<e4m3>" : "indexer_generic<f32>");
+  *plan += "indexer_generic<";
+  *plan += a.kind == IndexKind::kF32 ? "f32" : kind_name(a.kind);
+  *plan += ">";
   return cudaGetLastError();
 }
 

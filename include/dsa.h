@@ -66,10 +66,14 @@ typedef enum dsa_dtype {
                              /* only)                                              */
   DSA_E4M3_T128 = 4,         /* MLA cache only: 656-byte FP8 rows with one fp32    */
                              /* scale per 128 latent dims (layout below)           */
-  DSA_E2M1 = 5               /* MLA cache only: 432-byte rows of 4-bit E2M1 codes  */
+  DSA_E2M1 = 5,              /* MLA cache only: 432-byte rows of 4-bit E2M1 codes  */
                              /* (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives)   */
                              /* with one E4M3 scale per 16 latent dims and one fp32*/
                              /* scale per row (layout below)                       */
+  DSA_MXFP4_E2M1 = 6         /* OCP MXFP4: E2M1 codes, two a byte (element 2 i in   */
+                             /* the low nibble of byte i), one E8M0 scale byte      */
+                             /* 2**(e - 127) per 32 consecutive elements (indexer   */
+                             /* only)                                               */
 } dsa_dtype_t;
 
 typedef void* dsa_stream_t;  /* cudaStream_t */
@@ -107,16 +111,19 @@ typedef struct dsa_seq_desc {
  *   DSA_MXFP8_E4M3: q_scale uint8 [T, H_I, D_I/32], k_scale uint8
  *                   [cache_rows, D_I/32]: E8M0 exponents, element i of a vector
  *                   is code * 2**(scale[i / 32] - 127); both required; D_I a
- *                   multiple of 32.
+ *                   multiple of 32.  Byte 255 stands for no number.
+ *   DSA_MXFP4_E2M1: q uint8 [T, H_I, D_I/2], k_cache uint8 [cache_rows, D_I/2],
+ *                   scales as for DSA_MXFP8_E4M3.
  *   DSA_F32:        q and k_cache hold fp32 values; scales as for DSA_E4M3. */
 typedef struct dsa_indexer_desc {
   int32_t H_I;               /* indexer heads                                      */
   int32_t D_I;               /* indexer head dim                                   */
-  dsa_dtype_t dtype;         /* DSA_E4M3, DSA_MXFP8_E4M3 or DSA_F32 (q and k_cache) */
-  const void* q;             /* device [T, H_I, D_I]                               */
+  dsa_dtype_t dtype;         /* DSA_E4M3, DSA_MXFP8_E4M3, DSA_MXFP4_E2M1 or DSA_F32 */
+                             /* (q and k_cache)                                    */
+  const void* q;             /* device [T, H_I, D_I] (MXFP4: D_I / 2 bytes a head) */
   const void* q_scale;       /* device query scales (layout by dtype, above)       */
   const float* w;            /* device fp32 [T, H_I] head weights                  */
-  const void* k_cache;       /* device [cache_rows, D_I]                           */
+  const void* k_cache;       /* device [cache_rows, D_I] (MXFP4: D_I / 2 bytes)    */
   const void* k_scale;       /* device key scales (layout by dtype, above)         */
 } dsa_indexer_desc_t;
 
@@ -267,6 +274,24 @@ dsa_status_t dsa_index_cache_append(const dsa_seq_desc_t* seq, int32_t D_I, dsa_
  *   D_I % 32 == 0; k_new, k_cache and k_exp 16-byte aligned. */
 dsa_status_t dsa_index_cache_append_mx(const dsa_seq_desc_t* seq, int32_t D_I, dsa_dtype_t src_dtype,
                                        const void* k_new, uint8_t* k_cache, uint8_t* k_exp, dsa_stream_t stream);
+/* MXFP4 index keys (the DSA_MXFP4_E2M1 format): as dsa_index_cache_append_mx with
+ *   x_b = floor(log2 max_i |k_new[t, 32 b + i]|) - 2 (2 is the exponent of E2M1's
+ *   largest number, 6 = 1.5 * 2**2) and code_i = the E2M1 value nearest to
+ *   k_new[t, i] * 2**-x_b, ties to the even code, magnitudes beyond 6 saturated.
+ *   k_cache: device uint8 [cache_rows, D_I / 2]; k_exp: device uint8 [cache_rows,
+ *   D_I / 32].  Values must be finite. */
+dsa_status_t dsa_index_cache_append_mx4(const dsa_seq_desc_t* seq, int32_t D_I, dsa_dtype_t src_dtype,
+                                        const void* k_new, uint8_t* k_cache, uint8_t* k_exp, dsa_stream_t stream);
+/* Query heads to the codes and scales that dsa_indexer_scores reads beside such keys:
+ *   q device [T, H_I, D_I] fp32 or bf16 (src_dtype), value (t, h, i) at t * stride_t +
+ *   h * stride_h + i (strides in values, multiples of 16 bytes, DSA_E4M3: of 4
+ *   values), every head quantised as the cache writers quantise a key to code_dtype;
+ *   codes device uint8 [T, H_I, D_I] (DSA_MXFP4_E2M1: D_I / 2 bytes a head), scale
+ *   device fp32 [T, H_I] (DSA_E4M3) or uint8 [T, H_I, D_I / 32].  The outputs share
+ *   no memory with q. */
+dsa_status_t dsa_index_query_quantize(int32_t T, int32_t H_I, int32_t D_I, dsa_dtype_t src_dtype,
+                                      dsa_dtype_t code_dtype, const void* q, int64_t stride_t, int64_t stride_h,
+                                      uint8_t* codes, void* scale, dsa_stream_t stream);
 /* Latent rows: kv_new device [T, d_latent + d_rope], bf16 (fp32 when
  *   mla->dtype == DSA_F32); mla gives d_latent, d_rope, the cache dtype and
  *   row_bytes (its q and kv_cache fields are not used); the rows are written to
@@ -353,7 +378,8 @@ dsa_status_t dsa_latent_cache_append_rope(const dsa_seq_desc_t* seq, const dsa_m
                                           dsa_stream_t stream);
 /* Index keys: k_new device [T, D_I] fp32 or bf16 (src_dtype) with a stride between
  *   tokens in values (a multiple of 4); key_dtype DSA_E4M3 (k_scale fp32
- *   [cache_rows]) or DSA_MXFP8_E4M3 (k_scale uint8 [cache_rows, D_I / 32]). */
+ *   [cache_rows]), DSA_MXFP8_E4M3 or DSA_MXFP4_E2M1 (k_scale uint8 [cache_rows,
+ *   D_I / 32]). */
 dsa_status_t dsa_index_cache_append_rope(const dsa_seq_desc_t* seq, const dsa_rope_desc_t* rope, int32_t D_I,
                                          int32_t rot_offset, dsa_dtype_t src_dtype, dsa_dtype_t key_dtype,
                                          const void* k_new, int64_t k_stride, uint8_t* k_cache, void* k_scale,
@@ -368,6 +394,15 @@ dsa_status_t dsa_index_cache_append_rope(const dsa_seq_desc_t* seq, const dsa_ro
  * again, moving rows between formats, and looking at what a cache holds. */
 dsa_status_t dsa_latent_cache_read(const dsa_seq_desc_t* seq, const dsa_mla_desc_t* mla, const void* kv_cache,
                                    dsa_dtype_t out_dtype, void* out, int64_t out_stride, dsa_stream_t stream);
+
+/* The same for index keys: out[t, :] = the D_I values that the cached key of position
+ * q_pos[t] of sequence q_seq[t] stands for (key_dtype DSA_E4M3, k_scale may be NULL for
+ * all-ones, DSA_MXFP8_E4M3 or DSA_MXFP4_E2M1), code * scale as fp32, or rounded to bf16;
+ * out_stride values between rows (multiples of 16 bytes, DSA_E4M3: of 4 values).  A
+ * position or page out of range is flagged and its row of out is left as it was. */
+dsa_status_t dsa_index_cache_read(const dsa_seq_desc_t* seq, int32_t D_I, dsa_dtype_t key_dtype, const void* k_cache,
+                                  const void* k_scale, dsa_dtype_t out_dtype, void* out, int64_t out_stride,
+                                  dsa_stream_t stream);
 
 /* Testing aid for the failure-detection path; the pages have no counterpart.
  * Every pipeline wait in the kernels is bounded: a wait that gives up sets a

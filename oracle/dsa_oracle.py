@@ -209,6 +209,26 @@ def e2m1_row(latent, rope_bits) -> np.ndarray:
     return row
 
 
+def quantize_mx_e2m1(x) -> tuple:
+    """OCP MXFP4 along the last axis: for each block of 32 values, exponent floor(log2(amax)) - 2 (2: the exponent of
+    E2M1's largest number, 6 = 1.5 * 2**2; -127 for an all-zero block, clamped to [-127, 127]), scale byte = exponent +
+    127, codes = e2m1_encode of x / 2**exponent (exact), two a byte with the even value in the low nibble.
+    Returns (uint8 codes [..., D / 2], uint8 scale bytes [..., D / 32])."""
+    x = np.asarray(x, dtype=np.float64)
+    xb = x.reshape(*x.shape[:-1], x.shape[-1] // 32, 32)
+    amax = np.max(np.abs(xb), axis=-1, keepdims=True)
+    exp = np.where(amax > 0, np.clip(np.frexp(amax)[1] - 1 - 2, -127, 127), -127).astype(np.int64)
+    codes = e2m1_encode(np.ldexp(xb, -exp)).reshape(x.shape)
+    return (codes[..., 0::2] | (codes[..., 1::2] << 4)).astype(np.uint8), (exp + 127).astype(np.uint8)[..., 0]
+
+
+def dequantize_mx_e2m1(codes, scales) -> np.ndarray:
+    """float64 values of MXFP4 data: code value * 2**(e - 127) of its block of 32."""
+    codes = np.asarray(codes)
+    v = decode_e2m1(np.stack([codes & 15, codes >> 4], axis=-1)).reshape(*codes.shape[:-1], -1, 32)
+    return (v * decode_e8m0(scales)[..., None]).reshape(*codes.shape[:-1], 2 * codes.shape[-1])
+
+
 def rope_frequencies(d_rot, theta=10000.0, scaling="none", factor=1.0, original_ctx=0.0, beta_fast=32.0,
                      beta_slow=1.0):
     """(angular frequency of each of the d_rot / 2 pairs, factor on cosine and sine), float64."""
