@@ -33,7 +33,8 @@ EXPORTED = ("dsa_abi_version", "dsa_status_string", "dsa_last_error", "dsa_last_
             "dsa_indexer_prolog_workspace_size", "dsa_indexer_prolog",
             "dsa_rope_turns", "dsa_rope", "dsa_latent_cache_append_rope", "dsa_index_cache_append_rope",
             "dsa_latent_cache_read", "dsa_index_cache_append_mx4", "dsa_index_query_quantize", "dsa_index_cache_read",
-            "dsa_check_status")
+            "dsa_block_topk", "dsa_block_mla_attn_workspace_size", "dsa_block_mla_attn",
+            "dsa_block_decode_workspace_size", "dsa_block_decode_step", "dsa_check_status")
 STATIC_WORKSPACE_BYTES = 32 << 20   # DSA_STATIC_WORKSPACE_BYTES
 
 
@@ -108,6 +109,12 @@ def _load() -> ctypes.CDLL:
         "dsa_index_query_quantize": (C, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, C, C, P, ctypes.c_int64,
                                          ctypes.c_int64, P, P, P]),
         "dsa_index_cache_read": (C, [P, ctypes.c_int32, C, P, P, C, P, ctypes.c_int64, P]),
+        "dsa_block_topk": (C, [P, P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, P, P]),
+        "dsa_block_mla_attn_workspace_size": (ctypes.c_size_t, [P, P, ctypes.c_int32]),
+        "dsa_block_mla_attn": (C, [P, P, P, ctypes.c_int32, P, P, P, ctypes.c_size_t, P]),
+        "dsa_block_decode_workspace_size": (ctypes.c_size_t, [P, P, ctypes.c_int32]),
+        "dsa_block_decode_step": (C, [P, P, P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, P, P, P, P,
+                                      ctypes.c_size_t, P]),
         "dsa_check_status": (C, [P]),
     }
     for name, (res, args) in sig.items():
@@ -448,6 +455,79 @@ def _codes_check(dtype: int, D: int, rows: int, codes: torch.Tensor, scale: Opti
             raise ValueError(f"{names}: scales are required")
     elif scale.element_size() != (4 if dtype == DSA_E4M3 else 1) or scale.numel() < rows * (1 if dtype == DSA_E4M3 else D // 32):
         raise ValueError(f"{names}: scales must be fp32 [{rows}] (DSA_E4M3) or uint8 [{rows}, D_I / 32]")
+
+
+def _dense(t: torch.Tensor, name: str, dev: int, dtype: torch.dtype, shape) -> int:
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}")
+    return _cache_ptr(t, name, dev)
+
+
+def _outputs(s: SeqDesc, m: MlaDesc, out: torch.Tensor, lse: Optional[torch.Tensor], dev: int):
+    """Pointers of an attention's out [T, H, d_latent] and lse [T, H] (or None)."""
+    o = _dense(out, "out", dev, torch.float32 if m.dtype == DSA_F32 else torch.bfloat16, (s.T, m.H, m.d_latent))
+    return o, None if lse is None else _dense(lse, "lse", dev, torch.float32, (s.T, m.H))
+
+
+def _scratch(workspace: Optional[torch.Tensor], dev: int):
+    if workspace is None:
+        return None, 0
+    return _cache_ptr(workspace, "workspace", dev), workspace.numel() * workspace.element_size()
+
+
+def block_topk(seq: Seq, scores: torch.Tensor, n_blocks: int, out: torch.Tensor, first: int = 1, last: int = 1,
+               stream=None) -> torch.Tensor:
+    """The n_blocks blocks (pages) of each query with the best score in each (scores:
+    fp32 [T, ld], of indexer_scores), the `first` first and `last` last ones always
+    among them: out int32 [T, n_blocks], ascending, -1 behind them."""
+    s = seq.desc()
+    dev = _on_current(seq)
+    if scores.dim() != 2 or scores.dtype != torch.float32 or scores.shape[0] != s.T:
+        raise ValueError("scores must be float32 [T, ld]")
+    _check(_lib.dsa_block_topk(ctypes.byref(s), _cache_ptr(scores, "scores", dev), scores.shape[1], n_blocks, first, last,
+                               _dense(out, "out", dev, torch.int32, (s.T, n_blocks)), _stream(stream, dev)))
+    return out
+
+
+def block_mla_attn_workspace_size(seq: Seq, mla: Mla, n_blocks: int) -> int:
+    s, m = seq.desc(), mla.desc()
+    return _lib.dsa_block_mla_attn_workspace_size(ctypes.byref(s), ctypes.byref(m), n_blocks)
+
+
+def block_mla_attn(seq: Seq, mla: Mla, block_idx: torch.Tensor, out: torch.Tensor, lse: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """sparse_mla_attn over whole blocks: block_idx int32 [T, n_blocks] names pages of
+    each query's sequence (-1: none), of which the positions up to the query's own count."""
+    s, m = seq.desc(), mla.desc()
+    if block_idx.dim() != 2:
+        raise ValueError("block_idx must be int32 [T, n_blocks]")
+    dev = _on_current(seq, mla)
+    o, l = _outputs(s, m, out, lse, dev)
+    ws, ws_bytes = _scratch(workspace, dev)
+    n = block_idx.shape[1]
+    _check(_lib.dsa_block_mla_attn(ctypes.byref(s), ctypes.byref(m), _dense(block_idx, "block_idx", dev, torch.int32, (s.T, n)),
+                                   n, o, l, ws, ws_bytes, _stream(stream, dev)))
+    return out
+
+
+def block_decode_workspace_size(seq: Seq, mla: Mla, n_blocks: int) -> int:
+    s, m = seq.desc(), mla.desc()
+    return _lib.dsa_block_decode_workspace_size(ctypes.byref(s), ctypes.byref(m), n_blocks)
+
+
+def block_decode_step(seq: Seq, idx: Indexer, mla: Mla, n_blocks: int, out: torch.Tensor, workspace: torch.Tensor,
+                      first: int = 1, last: int = 1, lse: Optional[torch.Tensor] = None,
+                      block_idx_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """indexer_scores, block_topk and block_mla_attn in one call (scratch:
+    block_decode_workspace_size bytes)."""
+    s, x, m = seq.desc(), idx.desc(), mla.desc()
+    dev = _on_current(seq, idx, mla)
+    o, l = _outputs(s, m, out, lse, dev)
+    sel = None if block_idx_out is None else _dense(block_idx_out, "block_idx_out", dev, torch.int32, (s.T, n_blocks))
+    ws, ws_bytes = _scratch(workspace, dev)
+    _check(_lib.dsa_block_decode_step(ctypes.byref(s), ctypes.byref(x), ctypes.byref(m), n_blocks, first, last, o, l, sel, ws,
+                                      ws_bytes, _stream(stream, dev)))
+    return out
 
 
 def index_cache_append(seq: Seq, k_new: torch.Tensor, k_cache: torch.Tensor, k_scale: torch.Tensor,

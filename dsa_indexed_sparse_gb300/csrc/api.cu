@@ -867,6 +867,181 @@ dsa_status_t dsa_latent_cache_read(const dsa_seq_desc_t* seq, const dsa_mla_desc
 }
 
 namespace {
+
+// Arguments of the choice of blocks.
+dsa_status_t check_blocks(int32_t n_blocks, int32_t n_first, int32_t n_last) {
+  if (n_blocks < 1 || n_blocks > 65536) return fail(DSA_ERR_UNSUPPORTED, "n_blocks must be in [1, 65536]");
+  if (n_first < 0 || n_last < 0 || static_cast<int64_t>(n_first) + n_last > n_blocks)
+    return fail(DSA_ERR_INVALID_ARG, "n_first and n_last must be >= 0 and together at most n_blocks");
+  return DSA_OK;
+}
+
+// Shape checks of the attention over blocks; K of *a is n_blocks.
+dsa_status_t check_block_shape(const dsa::SeqArgs& s, const dsa_mla_desc_t* mla, int32_t n_blocks, dsa::MlaArgs* a) {
+  dsa_status_t st = check_mla_shape(mla, 1, a);
+  if (st != DSA_OK) return st;
+  if ((st = check_blocks(n_blocks, 0, 0)) != DSA_OK) return st;
+  a->K = n_blocks;
+  if (dsa::attn_block_positions(s, *a) && static_cast<int64_t>(n_blocks) * s.page_size > 16384)
+    return fail(DSA_ERR_UNSUPPORTED, "n_blocks * page_size must be at most 16384 but for bf16 rows of 512 + 64 dims in pages of 64");
+  return DSA_OK;
+}
+
+// Workspace of the chained block step: [scores T x ld fp32][blocks T x n_blocks int32][attention].
+size_t block_ws_layout(const dsa::SeqArgs& s, const dsa::MlaArgs& a, int num_sms, int64_t* ld, size_t* off_idx,
+                       size_t* off_attn) {
+  *ld = (static_cast<int64_t>(s.max_ctx) + 3) / 4 * 4;
+  *off_idx = align256(static_cast<size_t>(s.T) * *ld * sizeof(float));
+  *off_attn = *off_idx + align256(static_cast<size_t>(s.T) * a.K * sizeof(int32_t));
+  return *off_attn + dsa::attn_block_workspace_bytes(s, a, num_sms);
+}
+
+dsa_status_t workspace_fail(size_t got, size_t need) {
+  char buf[128];
+  snprintf(buf, sizeof(buf), "workspace too small: %zu < %zu bytes", got, need);
+  return fail(DSA_ERR_WORKSPACE, buf);
+}
+
+}  // namespace
+
+dsa_status_t dsa_block_topk(const dsa_seq_desc_t* seq, const float* scores, int64_t ld, int32_t n_blocks,
+                            int32_t n_first, int32_t n_last, int32_t* block_idx, dsa_stream_t stream) {
+  try {
+    dsa::SeqArgs s;
+    dsa_status_t st = check_seq(seq, &s);
+    if (st != DSA_OK) return st;
+    if ((st = check_blocks(n_blocks, n_first, n_last)) != DSA_OK) return st;
+    if (ld < s.max_ctx || ld % 4 != 0) return fail(DSA_ERR_INVALID_ARG, "ld must be >= max_ctx and a multiple of 4");
+    if (s.T > 0 && (!scores || !block_idx)) return fail(DSA_ERR_INVALID_ARG, "scores and block_idx must be non-NULL");
+    if (!aligned16(scores) || !aligned16(block_idx))
+      return fail(DSA_ERR_INVALID_ARG, "scores and block_idx must be 16-byte aligned");
+    dsa::LaunchEnv env;
+    if ((st = make_env(stream, &env)) != DSA_OK) return st;
+    std::string plan, why;
+    bool unsupported = false;
+    const cudaError_t e = dsa::launch_block_topk(s, scores, ld, n_blocks, n_first, n_last, block_idx, env, &plan,
+                                                 &unsupported, &why);
+    if (unsupported) return fail(DSA_ERR_UNSUPPORTED, why);
+    if (e != cudaSuccess) return cuda_fail(e, "block top-k launch");
+    g_last_plan = plan;
+    return DSA_OK;
+  } catch (...) {
+    return fail(DSA_ERR_CUDA, "unexpected host exception");
+  }
+}
+
+size_t dsa_block_mla_attn_workspace_size(const dsa_seq_desc_t* seq, const dsa_mla_desc_t* mla, int32_t n_blocks) {
+  try {
+    dsa::SeqArgs s;
+    dsa::MlaArgs a;
+    if (check_seq(seq, &s) != DSA_OK) return 0;
+    if (check_block_shape(s, mla, n_blocks, &a) != DSA_OK) return 0;
+    dsa::LaunchEnv env;
+    if (make_env(nullptr, &env) != DSA_OK) return 0;
+    return dsa::attn_block_workspace_bytes(s, a, env.num_sms);
+  } catch (...) {
+    return 0;
+  }
+}
+
+dsa_status_t dsa_block_mla_attn(const dsa_seq_desc_t* seq, const dsa_mla_desc_t* mla, const int32_t* block_idx,
+                                int32_t n_blocks, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                dsa_stream_t stream) {
+  try {
+    dsa::SeqArgs s;
+    dsa::MlaArgs a;
+    dsa_status_t st = check_seq(seq, &s);
+    if (st != DSA_OK) return st;
+    if ((st = check_mla(seq, mla, block_idx, 1, out, lse, &a)) != DSA_OK) return st;
+    if ((st = check_block_shape(s, mla, n_blocks, &a)) != DSA_OK) return st;
+    a.idx = block_idx;
+    a.out = out;
+    a.lse = lse;
+    if (workspace && !aligned16(workspace)) return fail(DSA_ERR_WORKSPACE, "workspace must be 16-byte aligned");
+    dsa::LaunchEnv env;
+    if ((st = make_env(stream, &env)) != DSA_OK) return st;
+    if (!workspace) workspace_bytes = 0;
+    if (dsa::attn_block_positions(s, a)) {   // the blocks' positions need their room
+      const size_t need = dsa::attn_block_workspace_bytes(s, a, env.num_sms);
+      if (workspace_bytes < need) return workspace_fail(workspace_bytes, need);
+    }
+    std::string plan, why;
+    bool unsupported = false;
+    const cudaError_t e = dsa::launch_attn_block(s, a, workspace, workspace_bytes, env, &plan, &unsupported, &why);
+    if (unsupported) return fail(DSA_ERR_UNSUPPORTED, why);
+    if (e != cudaSuccess) return cuda_fail(e, "block attention launch");
+    g_last_plan = plan;
+    return DSA_OK;
+  } catch (...) {
+    return fail(DSA_ERR_CUDA, "unexpected host exception");
+  }
+}
+
+size_t dsa_block_decode_workspace_size(const dsa_seq_desc_t* seq, const dsa_mla_desc_t* mla, int32_t n_blocks) {
+  try {
+    dsa::SeqArgs s;
+    dsa::MlaArgs a;
+    if (check_seq(seq, &s) != DSA_OK) return 0;
+    if (check_block_shape(s, mla, n_blocks, &a) != DSA_OK) return 0;
+    dsa::LaunchEnv env;
+    if (make_env(nullptr, &env) != DSA_OK) return 0;
+    int64_t ld;
+    size_t oi, oa;
+    return block_ws_layout(s, a, env.num_sms, &ld, &oi, &oa);
+  } catch (...) {
+    return 0;
+  }
+}
+
+dsa_status_t dsa_block_decode_step(const dsa_seq_desc_t* seq, const dsa_indexer_desc_t* idx, const dsa_mla_desc_t* mla,
+                                   int32_t n_blocks, int32_t n_first, int32_t n_last, void* out, float* lse,
+                                   int32_t* block_idx_out, void* workspace, size_t workspace_bytes,
+                                   dsa_stream_t stream) {
+  try {
+    dsa::SeqArgs s;
+    dsa::MlaArgs a;
+    dsa_status_t st = check_seq(seq, &s);
+    if (st != DSA_OK) return st;
+    if ((st = check_blocks(n_blocks, n_first, n_last)) != DSA_OK) return st;
+    if ((st = check_block_shape(s, mla, n_blocks, &a)) != DSA_OK) return st;
+    if (!workspace || !aligned16(workspace)) return fail(DSA_ERR_WORKSPACE, "workspace must be non-NULL and 16-byte aligned");
+    if (block_idx_out && !aligned16(block_idx_out)) return fail(DSA_ERR_INVALID_ARG, "block_idx_out must be 16-byte aligned");
+    dsa::LaunchEnv env;
+    if ((st = make_env(stream, &env)) != DSA_OK) return st;
+    int64_t ld;
+    size_t off_idx, off_attn;
+    const size_t need = block_ws_layout(s, a, env.num_sms, &ld, &off_idx, &off_attn);
+    if (workspace_bytes < need) return workspace_fail(workspace_bytes, need);
+    char* ws = static_cast<char*>(workspace);
+    float* scores = reinterpret_cast<float*>(ws);
+    int32_t* sel = block_idx_out ? block_idx_out : reinterpret_cast<int32_t*>(ws + off_idx);
+    dsa::IndexerArgs ia;
+    if ((st = check_indexer(seq, idx, scores, ld, &ia)) != DSA_OK) return st;
+    if ((st = check_mla(seq, mla, sel, 1, out, lse, &a)) != DSA_OK) return st;
+    a.K = n_blocks;
+    std::string plan, why;
+    bool unsupported = false;
+    if ((static_cast<int64_t>(s.max_ctx) + s.page_size - 1) / s.page_size > 32768)   // before anything is launched
+      return fail(DSA_ERR_UNSUPPORTED, "block top-k: more than 32768 blocks of max_ctx");
+    cudaError_t e = dsa::launch_indexer(s, ia, env, &plan, &unsupported, &why);
+    if (unsupported) return fail(DSA_ERR_UNSUPPORTED, why);
+    if (e != cudaSuccess) return cuda_fail(e, "indexer launch");
+    plan += " -> ";
+    e = dsa::launch_block_topk(s, scores, ld, n_blocks, n_first, n_last, sel, env, &plan, &unsupported, &why);
+    if (unsupported) return fail(DSA_ERR_UNSUPPORTED, why);
+    if (e != cudaSuccess) return cuda_fail(e, "block top-k launch");
+    plan += " -> ";
+    e = dsa::launch_attn_block(s, a, ws + off_attn, workspace_bytes - off_attn, env, &plan, &unsupported, &why);
+    if (unsupported) return fail(DSA_ERR_UNSUPPORTED, why);
+    if (e != cudaSuccess) return cuda_fail(e, "block attention launch");
+    g_last_plan = plan;
+    return DSA_OK;
+  } catch (...) {
+    return fail(DSA_ERR_CUDA, "unexpected host exception");
+  }
+}
+
+namespace {
 dsa_status_t check_prolog(const dsa_seq_desc_t* seq, const dsa_prolog_desc_t* pd, dsa::SeqArgs* s) {
   dsa_status_t st = check_seq(seq, s);
   if (st != DSA_OK) return st;
@@ -942,7 +1117,8 @@ dsa_status_t dsa_check_status(dsa_stream_t stream) {
     const uint32_t f = dsa_status_read_clear_indexer() | dsa_status_read_clear_topk() |
                        dsa_status_read_clear_attn() | dsa_status_read_clear_cache() |
                        dsa_status_read_clear_prolog() | dsa_status_read_clear_rows() |
-                       dsa_status_read_clear_attn_e2m1() | dsa_status_read_clear_index_keys();
+                       dsa_status_read_clear_attn_e2m1() | dsa_status_read_clear_index_keys() |
+                       dsa_status_read_clear_attn_block() | dsa_status_read_clear_block_topk();
     if (f == 0) return DSA_OK;
     if (f == 0xFFFFFFFFu) return fail(DSA_ERR_CUDA, "could not read the device status word");
     std::string msg = "device flags:";

@@ -1,0 +1,775 @@
+// Sparse MLA attention over selected blocks (pages of 64 positions) of bf16 latent rows, on
+// pairs of CTAs; and the form for every other cache: the blocks' positions written out for
+// the attention over single rows.
+//
+// The mathematics: for query t, head h and the positions S of its blocks, those up to its own,
+//     logit_s = scale * q[t,h] . row_s[0:576],  out = sum_s softmax(logit)_s row_s[0:512],
+//     lse = log sum_s exp(logit_s).
+//
+// What bounds it: a row is 1152 bytes and 278,528 flop for 128 heads, 242 flop per byte
+// (this card's measured rates: 289), so for one query a block HBM and the tensor cores are
+// about even, and where queries share rows the tensor cores.  The rows of a block lie one after
+// the other in the cache: a 64 x 64 box of a tensor map is an operand atom as the tensor cores
+// read it, so what attn.cu's producer warps gather row by row two threads ask the TMA for, and
+// nothing but the softmax is left for warps to do.
+//
+// As in attn_e2m1.cu the two CTAs of a cluster split the heads (64 each) and issue pair MMAs
+// (cta_group::2, M = 128): each supplies half of the B operand, so the logits are computed
+// once.  A tile is two blocks.  For Q K^T a CTA brings its own block in full, nine atoms: X =
+// dims [0, 256), Y = dims [256, 512), R = rope; for P V both need block 0 at one offset and
+// block 1 at another, each its own value dims: rank 0 (block 0, dims [0, 256)) has them in X
+// and lets the TMA put block 1's over Y, dead once Q K^T is complete, rank 1 (block 1, dims
+// [256, 512)) has them in Y and takes block 0's over X.  P of block 0 goes into R, dead as well, P
+// of block 1 into a buffer of its own.  36 + 16 MMAs a tile: 1152 + 1024 clocks.
+//   shared memory: Q 72 KB | stage 0, 72 KB | stage 1 | P of block 1, 8 KB | maxima, barriers
+//   TMEM: logits [0,64) [64,128), O [256,512).  An N-wide accumulator of a pair MMA takes N/2
+//   columns: lanes 0-63 are the CTA's heads for the first half of N, lanes 64-127 for the second.
+//
+// A block that reaches past the query's position is masked in the logits, and its rows behind
+// the position, which may hold anything, are zeroed in shared memory before P V: 0 * NaN is
+// not 0.  A tile's missing second block is a box outside the tensor map, which reads as zeros.
+//
+// P goes to bf16, the type of V: at most 2^-8 of a weight, half a step; what normalises the output is
+// the sum of the unrounded weights, the one the log-sum-exp takes.  m, a running bound of the
+// logits, moves only when it grows by more than 2^64: bf16 and fp32 have the exponents for it,
+// and O is rescaled for the first tile and hardly ever after.
+//
+// Work.  An item is a slice of the blocks (few queries: joined by attn_combine) of 128 heads
+// of a query; the clusters that fit the GPU at once share the items out, and tiles, buffers and
+// phases are counted through a cluster's items, so that the next item's rows, query and first
+// logits are on their way during the last softmax and the output.
+//
+// Warps.  0 finds the items' blocks (entries 32 at a time, those that select something moved
+// together) and loads own blocks; 1 loads the other block's values and the queries; 2 issues Q
+// K^T, 3 P V (rank 0 for both CTAs; those of rank 1 pass on that its copies have landed); the rest
+// are softmax and output.
+#include <cuda.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstdio>
+
+#include "dsa_device.cuh"
+#include "dsa_internal.h"
+#include "pair_mma.cuh"
+
+DSA_DEFINE_STATUS_WORD(attn_block)
+
+namespace dsa {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescaleM = 64.0f;   // growth of m that is let pass, log2 units
+
+constexpr int kHeads = 64;            // heads per CTA
+constexpr int kPage = 64;
+constexpr int kDqk = 576, kDv = 512;
+constexpr int kAtom = 64 * 128;       // bytes of a [64 rows x 64 dims] atom
+constexpr int kStage = 9 * kAtom;
+constexpr int kWarpOwn = 0, kWarpOther = 1, kWarpQk = 2, kWarpPv = 3, kWarpSoft = 4;
+constexpr int kParts = 2;             // threads that share a (head, block)'s logits
+constexpr int kCols = kPage / kParts; // logits a thread
+constexpr int kSoftWarps = 4 * kParts;
+constexpr int kThreads = 32 * (kWarpSoft + kSoftWarps);
+
+constexpr int kOffQ = 0;
+constexpr int kOffStage = kOffQ + 9 * kAtom;              // [2]
+constexpr int kOffP1 = kOffStage + 2 * kStage;            // P of block 1
+constexpr int kOffMax = kOffP1 + kAtom;                   // float [2][2 kParts][32]: of 32 heads' threads each
+constexpr int kOffInfo = kOffMax + 2 * 2 * kParts * 32 * 4;   // int4 [4]: what a tile is, by tile number mod 4
+constexpr int kOffOk = kOffInfo + 4 * 16;                 // int [kSoftWarps]
+constexpr int kOffBar = kOffOk + kSoftWarps * 4;
+// What a tile is, in info: x flags, y the other block's first cache row, z and w how many rows of
+// blocks 0 and 1 count.  Written before the tile's loads, that is after P V of the tile two before.
+constexpr int kFirst = 1, kLast = 2, kEnd = 4;            // of its item; last of all
+constexpr int kNumBars = 20;
+constexpr int kOffMisc = kOffBar + kNumBars * 8;
+constexpr int kUsed = kOffMisc + 16;
+constexpr int kSmemBytes = 232448;
+constexpr int kSlack = kSmemBytes - kUsed;                // for re-aligning the base to 1024 bytes
+static_assert(kSlack >= 128 && kOffBar % 8 == 0 && kOffInfo % 16 == 0, "shared memory layout");
+
+constexpr uint32_t kColO = 256;
+constexpr uint32_t kIdescQK = make_idesc(kFmtBF16, kFmtBF16, false, false, 128, 128);
+constexpr uint32_t kIdescPV = make_idesc(kFmtBF16, kFmtBF16, false, true, 128, 256);
+
+struct BlockParams {
+  SeqArgs seq;
+  MlaArgs a;                // idx: [T, K] blocks
+  int32_t n_split;          // slices per query
+  int32_t per_split;        // entries per slice, an even number
+  int32_t head_blocks;      // blocks of 128 heads
+  int32_t items;            // T * head_blocks * n_split, shared out among the clusters
+  uint16_t* ws_o;           // [n_split, T, H, 512] (n_split > 1)
+  float* ws_lse;            // [n_split, T, H]
+  uint64_t wait_limit_ns;
+  uint32_t dbg_withhold;
+  Divisor split, heads;     // by n_split, head_blocks
+  float scale_log2;         // softmax scale * log2 e
+};
+
+// Whether a wait must end (1): another thread of the CTA gave up, or the wait has been going
+// on for longer than the limit (which this sets the flags for).  Else when it must.
+__device__ __noinline__ uint64_t wait_until(volatile int* abort_flag, uint64_t until, uint64_t limit_ns) {
+  if (*abort_flag) return 1;
+  const uint64_t now = globaltimer_ns();
+  if (until == 0) return now + limit_ns;
+  if (now < until) return until;
+  atomicOr(&g_status_attn_block, kDevTimeout);
+  *abort_flag = 1;
+  return 1;
+}
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns) {
+  const uint32_t addr = smem_u32(bar);
+  uint64_t until = 0;
+  for (uint32_t it = 1; !mbar_try_wait(addr, parity); ++it)
+    if ((it & 63u) == 0u && (until = wait_until(abort_flag, until, limit_ns)) == 1) return false;
+  return true;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_block_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap, BlockParams p) {
+  grid_dep_launch();   // the kernel after waits for this grid before it reads what this grid writes
+  extern __shared__ __align__(1024) uint8_t sm_raw[];
+  uint8_t* sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  if (sm - sm_raw > kSlack) {   // the same in both CTAs: their shared windows have one layout
+    if (threadIdx.x == 0) atomicOr(&g_status_attn_block, kDevConfig);
+    return;
+  }
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kOffBar);
+  // Barriers in pairs belong to a tile's stage or logit buffer: nothing comes to one for the
+  // tile after next before its waiters have passed it for this one.
+  uint64_t* ownfull = bars;       // [2] own block landed
+  uint64_t* ownpair = bars + 2;   // [2] leader: and the other CTA's (its query too, at an item's first tile)
+  uint64_t* othfull = bars + 4;   // [2] the other block's values landed
+  uint64_t* othpair = bars + 6;   // [2] leader: in the other CTA as well
+  uint64_t* sfull = bars + 8;     // [2] Q K^T complete: logits there, half of the stage and its rope atom dead
+  uint64_t* sfree = bars + 10;    // [2] leader: logits read, both CTAs
+  uint64_t* pvdone = bars + 12;   // [2] P V complete: the tile's stage and P free
+  uint64_t* edone = bars + 14;    // [2] an item's output has left the stage of its last tile
+  uint64_t* pfull = bars + 16;    // leader: P written, both CTAs (one buffer: P V of the tile before is complete)
+  uint64_t* qraw = bars + 17;     // an item's query has come
+  uint64_t* drain = bars + 18;    // every MMA complete (teardown)
+  uint32_t* misc = reinterpret_cast<uint32_t*>(sm + kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
+  const volatile int* info = reinterpret_cast<const volatile int*>(sm + kOffInfo);
+  const uint64_t wlim = p.wait_limit_ns;
+  const int N = p.a.K, H = p.a.H;
+
+  // Work items, one after the other, the clusters in turn: a slice of 128 heads of a query, the
+  // last query first (longest causal history).
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  auto slice_of = [&](int item) -> int { return item - p.split(item) * p.n_split; };
+  auto query_of = [&](int item) -> int { return p.seq.T - 1 - p.heads(p.split(item)); };
+  auto head_of = [&](int item) -> int {   // this CTA's first head
+    const int i = p.split(item);
+    return (i - p.heads(i) * p.head_blocks) * 128 + static_cast<int>(rank) * kHeads;
+  };
+
+  if (warp == kWarpOwn && lane == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ownfull[i], 1);
+      mbar_init(&ownpair[i], 1);
+      mbar_init(&othfull[i], 1);
+      mbar_init(&othpair[i], 1);
+      mbar_init(&sfull[i], 1);
+      mbar_init(&sfree[i], 2 * kSoftWarps);
+      mbar_init(&pvdone[i], 1);
+      mbar_init(&edone[i], kSoftWarps);
+    }
+    mbar_init(pfull, 2 * kSoftWarps);
+    mbar_init(qraw, 1);
+    mbar_init(drain, 2);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWarpOther && lane == 0) {
+    tma_prefetch_desc(&qmap);
+    tma_prefetch_desc(&kmap);
+  }
+  __syncwarp();
+  if (warp == kWarpQk) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(misc)), "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  cluster_arrive();
+  grid_dep_wait();
+  cluster_wait();
+  tc_fence_after();
+  const uint32_t tmem0 = misc[0];
+  auto wait = [&](uint64_t* bar, int use) -> bool {   // the whole warp
+    return __all_sync(0xffffffffu, wait_bar(bar, use & 1, abort_flag, wlim));
+  };
+
+  if (warp == kWarpOwn) {
+    // ------------------------------------------------ the items' blocks, own blocks
+    const int none = static_cast<int>(p.seq.cache_rows);   // a box from here on reads as zeros
+    int item = first, e0 = 0, e1 = 0, qp = 0, b = 0;
+    bool fresh = false;      // the open item has given no blocks yet
+    uint32_t bad = 0;
+    // the next blocks: lane l holds the first cache row of block l of cnt, and how many rows of it count
+    int n_row = 0, n_rows = 0, n_cnt = 0;
+    bool n_there = false, n_first = false;
+    auto next_blocks = [&]() {
+      n_there = false;
+      n_cnt = 0;
+      for (;;) {
+        if (e0 >= e1) {
+          if (fresh) break;   // an item that selects nothing: one tile of no rows
+          if (item >= p.items) return;
+          const int t = query_of(item);
+          e0 = slice_of(item) * p.per_split;
+          e1 = min(N, e0 + p.per_split);
+          qp = __ldg(p.seq.q_pos + t);
+          b = __ldg(p.seq.q_seq + t);
+          if (qp < 0 || qp >= p.seq.max_ctx || b < 0 || b >= p.seq.B) {
+            bad |= kDevBadPos;
+            e1 = e0;
+          }
+          fresh = true;
+          item += step;
+          continue;
+        }
+        // (item has moved on: the open one is item - step)
+        const int i = e0 + lane;
+        int blk = i < e1 ? __ldg(p.a.idx + static_cast<int64_t>(query_of(item - step)) * N + i) : -1;
+        e0 += 32;
+        if (blk > (qp >> 6)) {
+          bad |= kDevBadIndex;
+          blk = -1;
+        }
+        int page = blk >= 0 ? __ldg(p.seq.block_table + static_cast<int64_t>(b) * p.seq.bt_stride + blk) : -1;
+        if (blk >= 0 && (page < 0 || page >= p.seq.n_pages)) {
+          bad |= kDevBadIndex;
+          page = -1;
+        }
+        const uint32_t mask = __ballot_sync(0xffffffffu, page >= 0);
+        if (mask == 0) continue;
+        n_cnt = __popc(mask);
+        n_row = page * kPage;
+        n_rows = min(kPage, qp + 1 - blk * kPage);
+        if (mask & (mask + 1)) {   // holes: lane l takes the l-th that selects something
+          const int src = static_cast<int>(__fns(mask, 0, lane + 1)) & 31;
+          n_row = __shfl_sync(0xffffffffu, n_row, src);
+          n_rows = __shfl_sync(0xffffffffu, n_rows, src);
+        }
+        break;
+      }
+      n_first = fresh;
+      fresh = false;
+      n_there = true;
+    };
+    int j = 0, ended = 0;        // tiles; items that have ended before tile j - 1
+    int last1 = 0, last2 = 0;    // whether tiles j - 1 and j - 2 ended an item
+    bool ok = true;
+    next_blocks();
+    while (ok && n_there) {
+      const int row = n_row, rows = n_rows, cnt = n_cnt, tiles = max(1, (n_cnt + 1) >> 1);
+      const bool starts = n_first;
+      // the next blocks are looked up behind two tiles under way, before the last tile: whether it
+      // ends the item depends on them
+      const int ahead = min(2, tiles - 1);
+      for (int k = 0; k < tiles; ++k, ++j) {
+        if (k == ahead) next_blocks();
+        const int row0 = __shfl_sync(0xffffffffu, row, (2 * k) & 31), row1 = __shfl_sync(0xffffffffu, row, (2 * k + 1) & 31);
+        const int c0 = __shfl_sync(0xffffffffu, rows, (2 * k) & 31), c1 = __shfl_sync(0xffffffffu, rows, (2 * k + 1) & 31);
+        const bool has0 = 2 * k < cnt, has1 = 2 * k + 1 < cnt;
+        const bool last = k == tiles - 1 && (!n_there || n_first);
+        const int flags = (starts && k == 0 ? kFirst : 0) | (last ? kLast | (n_there ? 0 : kEnd) : 0);
+        if (j >= 2) {
+          ok = wait(&pvdone[j & 1], (j >> 1) - 1);
+          if (ok && last2) {
+            ok = wait(&edone[ended & 1], ended >> 1);
+            ++ended;
+          }
+          if (!ok) break;
+        }
+        last2 = last1;
+        last1 = last ? 1 : 0;
+        if (lane == 0) {
+          const int at0 = has0 ? row0 : none, at1 = has1 ? row1 : none;
+          *reinterpret_cast<int4*>(sm + kOffInfo + (j & 3) * 16) =
+              make_int4(flags, rank ? at0 : at1, has0 ? c0 : 0, has1 ? c1 : 0);
+          mbar_arrive_expect_tx(&ownfull[j & 1], kStage);
+          uint8_t* dst = sm + kOffStage + (j & 1) * kStage;
+#pragma unroll 1
+          for (int a = 0; a < 9; ++a) tma_load_2d(dst + a * kAtom, &kmap, &ownfull[j & 1], a * 64, rank ? at1 : at0);
+        }
+        __syncwarp();
+      }
+    }
+    if (bad) atomicOr(&g_status_attn_block, bad);
+    // the last copies have landed before the CTA leaves
+    for (int k = max(0, j - 2); k < j; ++k) mbar_drain(&ownfull[k & 1], (k >> 1) & 1, &g_status_attn_block, wlim);
+  } else if (warp == kWarpOther) {
+    // ------------------------------------------------ queries, the other block's values
+    auto load_query = [&](int item) {
+      const int row = query_of(item) * H + head_of(item);   // < 2^31
+      if (lane == 0) {
+        mbar_arrive_expect_tx(qraw, 9 * kAtom);
+        // heads beyond H: the next token's, or zeros; nothing is written of them
+#pragma unroll 1
+        for (int a = 0; a < 9; ++a) tma_load_2d(sm + kOffQ + a * kAtom, &qmap, qraw, a * 64, row);
+      }
+      __syncwarp();
+    };
+    int item = first, g = 0, queries = 1;
+    load_query(item);
+    for (bool more = true; more; ++g) {
+      const int st = g & 1;
+      if (!wait(&ownfull[st], g >> 1) || !wait(&sfull[st], g >> 1)) break;
+      const int flags = info[(g & 3) * 4], at = info[(g & 3) * 4 + 1];
+      more = !(flags & kEnd);
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&othfull[st], 4 * kAtom);
+        uint8_t* dst = sm + kOffStage + st * kStage + (rank ? 0 : 4) * kAtom;
+#pragma unroll 1
+        for (int a = 0; a < 4; ++a)
+          tma_load_2d(dst + a * kAtom, &kmap, &othfull[st], static_cast<int>(rank) * 256 + a * 64, at);
+      }
+      __syncwarp();
+      if ((flags & (kLast | kEnd)) == kLast) {   // Q K^T of the item's last tile is complete
+        item += step;
+        load_query(item);
+        ++queries;
+      }
+    }
+    for (int k = max(0, g - 2); k < g; ++k) mbar_drain(&othfull[k & 1], (k >> 1) & 1, &g_status_attn_block, wlim);
+    mbar_drain(qraw, (queries - 1) & 1, &g_status_attn_block, wlim);
+  } else if (warp == kWarpQk) {
+    const uint64_t dq = make_sdesc(smem_u32(sm + kOffQ), 16, 1024, kLayoutSw128);
+    const uint64_t dk0 = make_sdesc(smem_u32(sm + kOffStage), 16, 1024, kLayoutSw128);
+    int n = 0;   // items
+    bool ok = true, more = true;
+#pragma unroll 1
+    for (int g = 0; ok && more; ++g) {
+      const int sb = g & 1;
+      ok = wait(&ownfull[sb], g >> 1);
+      if (!ok) break;
+      const int flags = info[(g & 3) * 4];
+      more = !(flags & kEnd);
+      if (flags & kFirst) ok = wait(qraw, n++);
+      if (rank) {   // passed on to the CTA that issues
+        if (ok && lane == 0 && !(p.dbg_withhold && g == 0)) arrive_pair(leader_addr(&ownpair[sb]));
+        __syncwarp();
+        continue;
+      }
+      if (ok) ok = wait(&ownpair[sb], g >> 1);
+      if (ok && g >= 2) ok = wait(&sfree[sb], (g >> 1) - 1);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t d = tmem0 + sb * 64;
+        const uint64_t dk = dk0 + static_cast<uint64_t>((sb * kStage) >> 4);
+#pragma unroll
+        for (int a = 0; a < 9; ++a) {   // 64 dims a turn
+          const uint64_t off = static_cast<uint64_t>((a * kAtom) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_pair(d, dq + off + 2 * kk, dk + off + 2 * kk, kIdescQK, static_cast<uint32_t>(a | kk));
+        }
+        commit_pair(&sfull[sb]);
+      }
+      __syncwarp();
+    }
+  } else if (warp == kWarpPv) {
+    const uint64_t dv0 = make_sdesc(smem_u32(sm + kOffStage), kAtom, 1024, kLayoutSw128);
+    const uint64_t dp0 = make_sdesc(smem_u32(sm + kOffStage + 8 * kAtom), 16, 1024, kLayoutSw128);
+    const uint64_t dp1 = make_sdesc(smem_u32(sm + kOffP1), 16, 1024, kLayoutSw128);
+    bool ok = true, more = true;
+#pragma unroll 1
+    for (int g = 0; ok && more; ++g) {
+      const int sb = g & 1;
+      ok = wait(&ownfull[sb], g >> 1) && wait(&othfull[sb], g >> 1);
+      if (!ok) break;
+      const int flags = info[(g & 3) * 4];
+      more = !(flags & kEnd);
+      if (rank) {
+        if (lane == 0) arrive_pair(leader_addr(&othpair[sb]));
+        __syncwarp();
+        continue;
+      }
+      ok = wait(&othpair[sb], g >> 1) && wait(pfull, g);
+      if (!ok) break;
+      tc_fence_after();
+      fence_proxy_async_smem();
+      if (elect_one()) {
+        const uint64_t st = static_cast<uint64_t>((sb * kStage) >> 4);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {   // value atoms 2 (q / 2), block q & 1
+          const uint64_t da = (q & 1) ? dp1 : dp0 + st;
+          const uint64_t db = dv0 + st + static_cast<uint64_t>((((q & 1) * 4 + (q >> 1) * 2) * kAtom) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_pair(tmem0 + kColO + (q >> 1) * 128, da + 2 * kk, db + 128 * kk, kIdescPV,
+                      static_cast<uint32_t>((~flags & kFirst) | (q & 1) | kk));
+        }
+        commit_pair(&pvdone[sb]);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------ softmax and output
+    const int sw = warp - kWarpSoft;
+    const int quarter = warp & 3;
+    const int hl = (quarter & 1) * 32 + lane;   // head within the CTA
+    const int half = quarter >> 1;              // block of the tile; of the output: half of the value dims
+    const int part = sw >> 2;                   // this thread's rows [kCols part, kCols part + kCols)
+    const int rq = half * kParts + part;
+    const uint32_t tmem = tmem0 + (static_cast<uint32_t>(quarter * 32) << 16);
+    const float sl2 = p.scale_log2;
+    const uint32_t head_bar = 2 + (quarter & 1);   // the threads of 32 heads
+    constexpr uint32_t kHeadThreads = 64 * kParts;
+    float* xmax = reinterpret_cast<float*>(sm + kOffMax) + (quarter & 1) * (2 * kParts * 32) + lane;   // [2 kParts][32]
+    volatile int* oks = reinterpret_cast<volatile int*>(sm + kOffOk);
+    const uint32_t prow0 = smem_u32(sm + (half ? kOffP1 : kOffStage + 8 * kAtom)) + static_cast<uint32_t>(hl * 128);
+    const uint32_t pstep = half ? 0u : static_cast<uint32_t>(kStage);   // block 0: the stage's rope atom
+    bool ok = true;
+    int j = 0, done = 0;   // tiles, items
+#pragma unroll 1
+    for (int item = first; item < p.items; item += step) {
+      float m = -INFINITY, l = 0.f;
+      bool last = false, stop = false;
+#pragma unroll 1
+      for (; !last; ++j) {
+        const int st = j & 1;
+        ok = ok && wait(&ownfull[st], j >> 1) && wait(&sfull[st], j >> 1);
+        tc_fence_after();
+        const uint32_t stage = smem_u32(sm + kOffStage) + static_cast<uint32_t>(st * kStage);
+        float x[kCols];
+        float mx = -INFINITY;
+        if (ok) {
+          uint32_t s[kCols];
+          tmem_ld32(tmem + st * 64 + part * kCols, s);
+          const int4 what = *reinterpret_cast<const int4*>(sm + kOffInfo + (j & 3) * 16);
+          last = (what.x & kLast) != 0;
+          const int mine = (half ? what.w : what.z) - part * kCols;   // of this thread's rows that count
+          tmem_ld_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_pair(leader_addr(&sfree[st]));   // the logit buffer has been read
+#pragma unroll
+          for (int i = 0; i < kCols; i += 2)
+            mul2(x[i], x[i + 1], __uint_as_float(s[i]), __uint_as_float(s[i + 1]), sl2, sl2);
+          if (mine < kCols) {
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) x[i] = i < mine ? x[i] : -INFINITY;
+          }
+          float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < kCols; i += 2) mq[(i >> 1) & 3] = fmax3(mq[(i >> 1) & 3], x[i], x[i + 1]);
+          mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+          // rows behind the query's position: nothing of them may reach O
+          if ((what.z & 63) | (what.w & 63)) {
+            ok = wait(&othfull[st], j >> 1);
+            if (ok) {
+#pragma unroll 1
+              for (int blk = 0; blk < 2; ++blk) {
+                const int from = blk ? what.w : what.z;
+                if (from == 0) continue;   // not there: zeros already
+                for (int i = sw * 32 + lane; i < (kPage - from) * 32; i += kSoftWarps * 32)
+                  st_shared_v4(stage + (blk * 4 + ((i >> 3) & 3)) * kAtom + (from + (i >> 5)) * 128 + (i & 7) * 16, 0u, 0u, 0u, 0u);
+              }
+            }
+          }
+        }
+        // The threads of a head share m, and their warps leave together when one has given up.  One
+        // barrier tells whether any of them has to let m grow (the first tile, and seldom after);
+        // only then do they exchange their maxima.
+        const bool grow = named_bar_or(head_bar, kHeadThreads, !ok || mx > m + kRescaleM);
+        // P of block 1 has one buffer and O may have to be rescaled: P V of the tile before is complete
+        const bool pv_ok = !(j >= 1 && ok) || wait(&pvdone[(j - 1) & 1], (j - 1) >> 1);
+        if (grow) {
+          xmax[rq * 32] = mx;
+          if (lane == 0) oks[sw] = ok ? 1 : 0;
+          named_bar_sync(head_bar, kHeadThreads);
+#pragma unroll
+          for (int k = 0; k < 2 * kParts; ++k) mx = fmaxf(mx, xmax[k * 32]);
+          // the warps whose number is as odd as this one's
+#pragma unroll
+          for (int k = 0; k < 2 * kParts; ++k) ok = ok && oks[2 * k + (sw & 1)] != 0;
+          named_bar_sync(head_bar, kHeadThreads);
+          if (!ok) {
+            stop = true;
+            break;
+          }
+          const bool need = mx > m + kRescaleM;
+          if (__any_sync(0xffffffffu, need && m > -INFINITY)) {   // (m of -inf: nothing in O yet)
+            tc_fence_after();
+            const float f = need && m > -INFINITY ? exp2f(m - mx) : 1.f;
+#pragma unroll 1
+            for (int cc = 0; cc < 256 / kParts / 16; ++cc) {   // this thread's share of the columns
+              uint32_t o[16];
+              const uint32_t at = tmem + kColO + part * (256 / kParts) + cc * 16;
+              tmem_ld16(at, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st16(at, o);
+            }
+            tmem_st_wait();
+          }
+          if (need) {
+            l *= exp2f(m - mx);
+            m = mx;
+          }
+        }
+        ok = pv_ok;
+        const float msub = (m == -INFINITY) ? 0.f : m;
+        const uint32_t prow = prow0 + (j & 1) * pstep;
+        float se[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < kCols / 8; ++c) {
+          uint32_t pk[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int i = 8 * c + 2 * k;
+            float d0, d1;
+            add2(d0, d1, x[i], x[i + 1], -msub, -msub);
+            const float p0 = fast_exp2(d0), p1 = fast_exp2(d1);
+            add2(se[2 * (k & 1)], se[2 * (k & 1) + 1], se[2 * (k & 1)], se[2 * (k & 1) + 1], p0, p1);
+            pk[k] = pack_bf16x2(p0, p1);
+          }
+          st_shared_v4(prow + static_cast<uint32_t>(((part * (kCols / 8) + c) ^ (hl & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
+        }
+        l += (se[0] + se[1]) + (se[2] + se[3]);
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_pair(leader_addr(pfull));
+      }
+      if (stop) break;
+      // ---- the output: O / l, log-sum-exp
+      ok = ok && wait(&pvdone[(j - 1) & 1], (j - 1) >> 1);
+      // the sums of a head's threads
+      xmax[rq * 32] = l;
+      named_bar_sync(head_bar, kHeadThreads);
+      l = 0.f;
+#pragma unroll
+      for (int k = 0; k < 2 * kParts; ++k) l += xmax[k * 32];
+      named_bar_sync(head_bar, kHeadThreads);
+      if (ok) {
+        tc_fence_after();
+        const float inv = l == 0.f ? 0.f : 1.f / l;   // l may be NaN
+        const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        const int t = query_of(item), h0 = head_of(item);
+        const int heads = min(32, H - (h0 + (quarter & 1) * 32));   // of this warp's 32 that exist
+        const bool split = p.n_split > 1;
+        const int64_t head0 =
+            (static_cast<int64_t>(split ? slice_of(item) : 0) * p.seq.T + t) * H + h0 + (quarter & 1) * 32;
+        uint8_t* out = reinterpret_cast<uint8_t*>(split ? p.ws_o : static_cast<uint16_t*>(p.a.out)) +
+                       (head0 * kDv + half * 256 + part * (256 / kParts)) * 2;
+        // through the last tile's stage, which P V has left and the loads leave alone till edone: a
+        // thread holds one head's values, and neighbouring lanes should store a head's
+        const uint32_t stg = smem_u32(sm + kOffStage) + ((j - 1) & 1) * kStage + sw * 4096;
+        if (heads > 0) {
+#pragma unroll 1
+          for (int cc = 0; cc < 256 / kParts / 64; ++cc) {
+#pragma unroll 1
+            for (int hf = 0; hf < 2; ++hf) {
+              uint32_t o[32];
+              tmem_ld32(tmem + kColO + part * (256 / kParts) + cc * 64 + hf * 32, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                st_shared_v4(stg + lane * 128 + (((hf * 4 + k) ^ (lane & 7)) << 4),
+                             pack_bf16x2(__uint_as_float(o[8 * k]) * inv, __uint_as_float(o[8 * k + 1]) * inv),
+                             pack_bf16x2(__uint_as_float(o[8 * k + 2]) * inv, __uint_as_float(o[8 * k + 3]) * inv),
+                             pack_bf16x2(__uint_as_float(o[8 * k + 4]) * inv, __uint_as_float(o[8 * k + 5]) * inv),
+                             pack_bf16x2(__uint_as_float(o[8 * k + 6]) * inv, __uint_as_float(o[8 * k + 7]) * inv));
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int row = i * 4 + (lane >> 3), c4 = lane & 7;
+              const uint4 v = ld_shared_v4(stg + row * 128 + ((c4 ^ (row & 7)) << 4));
+              if (row < heads)
+                *reinterpret_cast<uint4*>(out + static_cast<int64_t>(row) * kDv * 2 + cc * 128 + c4 * 16) = v;
+            }
+            __syncwarp();
+          }
+          if (rq == 0 && lane < heads) {
+            if (split)
+              p.ws_lse[head0 + lane] = lse;
+            else if (p.a.lse)
+              p.a.lse[head0 + lane] = lse;
+          }
+        }
+        tc_fence_before();
+      }
+      fence_proxy_async_smem();   // the stage goes back to the TMA
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&edone[done++ & 1]);
+    }
+  }
+
+  // Every MMA has finished in both CTAs before either releases its TMEM or leaves (after
+  // an abort some may still be running).
+  if (rank == 0 && (warp == kWarpQk || warp == kWarpPv)) {
+    if (elect_one()) commit_pair(drain);
+    __syncwarp();
+  }
+  if (warp == kWarpQk) mbar_drain(drain, 0, &g_status_attn_block, p.wait_limit_ns);
+  tc_fence_before();
+  __syncwarp();
+  cluster_arrive();
+  cluster_wait();
+  if (warp == kWarpQk) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem0), "r"(512u) : "memory");
+  }
+}
+
+// Blocks to positions, ascending within a block; -1 for what is masked.
+__global__ void __launch_bounds__(256) expand_blocks_kernel(SeqArgs seq, const int32_t* blocks, int32_t N, int32_t* idx) {
+  grid_dep_wait();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, per = static_cast<int64_t>(N) * seq.page_size;
+  const int64_t t = i / per;
+  if (t >= seq.T) return;
+  const int k = static_cast<int>(i - t * per), j = k / seq.page_size, inside = k - j * seq.page_size;
+  const int qp = __ldg(seq.q_pos + t);
+  const int blk = __ldg(blocks + t * N + j);
+  int pos = -1;
+  if (blk >= 0 && qp >= 0 && qp < seq.max_ctx) {   // a bad position is flagged by the attention
+    if (blk > qp / seq.page_size) {
+      if (inside == 0) atomicOr(&g_status_attn_block, kDevBadIndex);
+    } else if (blk * seq.page_size + inside <= qp) {
+      pos = blk * seq.page_size + inside;
+    }
+  }
+  idx[i] = pos;
+}
+
+// Clusters that the current device holds at once (its SMs need not pair up everywhere), asked once.
+int resident_clusters(int num_sms) {
+  static std::atomic<int> cache[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return std::max(1, num_sms / 2);
+  int n = cache[dev].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  const void* kernel = reinterpret_cast<const void*>(attn_block_kernel);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::max(2, num_sms & ~1)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (ensure_smem_limit(kernel, kSmemBytes, dev) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
+    static_cast<void>(cudaGetLastError());
+    return std::max(1, num_sms / 2);
+  }
+  cache[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// Slices per query: a cluster for each while the GPU holds them all at once, a slice at least
+// one tile.
+int choose_split(const SeqArgs& seq, const MlaArgs& a, int num_sms) {
+  const int tiles = (a.K + 1) / 2;
+  const int64_t clusters = static_cast<int64_t>(seq.T) * ((a.H + 127) / 128);
+  return static_cast<int>(
+      std::max<int64_t>(1, std::min<int64_t>(tiles, resident_clusters(num_sms) / std::max<int64_t>(1, clusters))));
+}
+
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Whether the blocks are boxes of a tensor map: bf16 rows of the tensor-core path's dims in pages of 64.
+bool boxes(const SeqArgs& seq, const MlaArgs& a) {
+  return a.kind == MlaKind::kBF16 && a.d_latent == kDv && a.d_rope == kDqk - kDv && seq.page_size == kPage &&
+         a.row_bytes % 16 == 0;
+}
+
+}  // namespace
+
+bool attn_block_positions(const SeqArgs& seq, const MlaArgs& a) { return !boxes(seq, a); }
+
+size_t attn_block_workspace_bytes(const SeqArgs& seq, const MlaArgs& a, int num_sms) {
+  if (seq.T == 0) return 0;
+  if (!boxes(seq, a)) {
+    MlaArgs rows = a;
+    rows.K = a.K * seq.page_size;
+    return align256(static_cast<size_t>(seq.T) * rows.K * sizeof(int32_t)) + attn_workspace_bytes(seq, rows, num_sms);
+  }
+  const int split = choose_split(seq, a, num_sms);
+  if (split <= 1) return 0;
+  return align256(static_cast<size_t>(split) * seq.T * a.H * kDv * sizeof(uint16_t)) +
+         align256(static_cast<size_t>(split) * seq.T * a.H * sizeof(float));
+}
+
+cudaError_t launch_attn_block(const SeqArgs& seq, const MlaArgs& a, void* workspace, size_t ws_bytes,
+                              const LaunchEnv& env, std::string* plan, bool* unsupported, std::string* why) {
+  *unsupported = false;
+  if (seq.T == 0) {
+    *plan += "attn_block[empty]";
+    return cudaSuccess;
+  }
+  if (!boxes(seq, a)) {
+    MlaArgs rows = a;
+    rows.K = a.K * seq.page_size;
+    int32_t* idx = static_cast<int32_t*>(workspace);
+    rows.idx = idx;
+    const size_t used = align256(static_cast<size_t>(seq.T) * rows.K * sizeof(int32_t));
+    const int64_t n = static_cast<int64_t>(seq.T) * rows.K;
+    const cudaError_t e = launch_kernel(expand_blocks_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0,
+                                        env.stream, true, 1, seq, a.idx, a.K, idx);
+    if (e != cudaSuccess) return e;
+    *plan += "expand_blocks -> ";
+    return launch_attn(seq, rows, static_cast<char*>(workspace) + used, ws_bytes - used, env, plan, unsupported, why);
+  }
+  int split = choose_split(seq, a, env.num_sms);
+  if (split > 1 && (workspace == nullptr || ws_bytes < attn_block_workspace_bytes(seq, a, env.num_sms)))
+    split = 1;   // no room for partials: one slice per query
+  const int tiles = (a.K + 1) / 2;
+  const int per = (tiles + split - 1) / split * 2;
+  split = (a.K + per - 1) / per;   // every slice non-empty
+  const int head_blocks = (a.H + 127) / 128;
+  const int64_t items = static_cast<int64_t>(seq.T) * head_blocks * split;
+  if (items > 0x3FFFFFFFll || static_cast<int64_t>(seq.T) * a.H > 0x7FFFFF00ll) return cudaErrorInvalidConfiguration;
+  BlockParams p{seq,     a,       split,        per, head_blocks,    static_cast<int32_t>(items),
+                nullptr, nullptr, kWaitLimitNs, 0u,  Divisor(split), Divisor(head_blocks),
+                a.softmax_scale * kLog2e};
+  debug_wait_state(&p.wait_limit_ns, &p.dbg_withhold);
+  if (split > 1) {
+    p.ws_o = static_cast<uint16_t*>(workspace);
+    p.ws_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                        align256(static_cast<size_t>(split) * seq.T * a.H * kDv * sizeof(uint16_t)));
+  }
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(attn_block_kernel), kSmemBytes, env.device);
+  if (e != cudaSuccess) return e;
+  alignas(64) CUtensorMap qmap, kmap;   // boxes of 64 dims of 64 rows: heads, cache rows
+  std::string reason;
+  if (!encode_tmap_2d(&qmap, a.q, 2, kDqk, static_cast<uint64_t>(seq.T) * a.H, kDqk * 2, 64, kHeads, &reason) ||
+      !encode_tmap_2d(&kmap, a.kv, 2, kDqk, static_cast<uint64_t>(seq.cache_rows), static_cast<uint64_t>(a.row_bytes), 64,
+                      kPage, &reason)) {
+    *unsupported = true;
+    *why = "block attention: " + reason;
+    return cudaSuccess;
+  }
+  const int64_t grid = 2 * std::min<int64_t>(items, resident_clusters(env.num_sms));
+  e = launch_kernel(attn_block_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmemBytes, env.stream, true,
+                    2, qmap, kmap, p);
+  if (e != cudaSuccess) return e;
+  char buf[96];
+  snprintf(buf, sizeof(buf), "attn_block<bf16>[split=%d,grid=%lld]", split, static_cast<long long>(grid));
+  *plan += buf;
+  if (split > 1) {
+    e = launch_attn_combine(p.ws_o, p.ws_lse, split, seq.T, a.H, a.out, a.lse, env);
+    if (e != cudaSuccess) return e;
+    *plan += "+attn_combine";
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace dsa

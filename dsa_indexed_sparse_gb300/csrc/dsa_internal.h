@@ -94,6 +94,17 @@ cudaError_t launch_attn_e2m1(const SeqArgs& seq, const MlaArgs& a, void* workspa
 cudaError_t launch_attn_combine(const uint16_t* ws_o, const float* ws_lse, int n_split, int T, int H, void* out,
                                 float* lse_out, const LaunchEnv& env);
 
+// Blocks by the best score in each, and the attention over blocks (a.idx: [T, a.K] blocks).
+// The workspace may be null (ws_bytes 0) unless attn_block_positions: then the blocks' positions
+// are written into it for launch_attn.
+cudaError_t launch_block_topk(const SeqArgs& seq, const float* scores, int64_t ld, int32_t N, int32_t n_first,
+                              int32_t n_last, int32_t* out, const LaunchEnv& env, std::string* plan, bool* unsupported,
+                              std::string* why);
+bool attn_block_positions(const SeqArgs& seq, const MlaArgs& a);
+size_t attn_block_workspace_bytes(const SeqArgs& seq, const MlaArgs& a, int num_sms);
+cudaError_t launch_attn_block(const SeqArgs& seq, const MlaArgs& a, void* workspace, size_t ws_bytes,
+                              const LaunchEnv& env, std::string* plan, bool* unsupported, std::string* why);
+
 // Launches a kernel, when `pdl` with programmatic stream serialization (it
 // may launch while the previous kernel on the stream is finishing; every
 // kernel of this library waits for its predecessor with griddepcontrol.wait
@@ -224,3 +235,5 @@ uint32_t dsa_status_read_clear_prolog();
 uint32_t dsa_status_read_clear_rows();
 uint32_t dsa_status_read_clear_attn_e2m1();
 uint32_t dsa_status_read_clear_index_keys();
+uint32_t dsa_status_read_clear_attn_block();
+uint32_t dsa_status_read_clear_block_topk();

@@ -225,6 +225,43 @@ dsa_status_t dsa_decode_step(const dsa_seq_desc_t* seq, const dsa_indexer_desc_t
                              int32_t* idx_out, void* workspace, size_t workspace_bytes,
                              dsa_stream_t stream);
 
+/* Attention over blocks.  A block is a page: positions [b * page_size, (b + 1) *
+ * page_size) of a sequence, whose cache rows lie one after the other.
+ *
+ * Choice -- from the scores of dsa_indexer_scores: block_idx[t * n_blocks + j] are
+ * min(n_blocks, q_pos[t] / page_size + 1) blocks of query t: the first n_first, the
+ * last n_last (the query's own block is the last), and of the others those with the
+ * largest max_s scores[t * ld + s] over their positions s <= q_pos[t] (compared as
+ * fp32, -0 == +0; a NaN is passed over, a block of nothing else counts as -inf), ties
+ * to the lower block, in ascending order, then -1 up to n_blocks.
+ * n_first + n_last <= n_blocks <= 65536; at most 32768 blocks of max_ctx (else
+ * DSA_ERR_UNSUPPORTED); ld and scores as for dsa_topk; block_idx device int32
+ * [T, n_blocks]. */
+dsa_status_t dsa_block_topk(const dsa_seq_desc_t* seq, const float* scores, int64_t ld, int32_t n_blocks,
+                            int32_t n_first, int32_t n_last, int32_t* block_idx, dsa_stream_t stream);
+/* Attention -- dsa_sparse_mla_attn over S = the positions s <= q_pos[t] of the blocks
+ * block_idx[t * n_blocks + j] >= 0, in any order; entries -1 are skipped wherever they
+ * appear, a block that starts behind q_pos[t] or whose page is out of range is skipped
+ * and flagged, and one that is given twice counts twice.  Rows behind q_pos[t] in its
+ * own block may hold anything.  Every cache format, page size and number of heads.
+ * DSA_BF16 rows of 512 + 64 dims in pages of 64 (row_bytes a multiple of 16) are read as
+ * whole blocks, workspace may be NULL (a larger one lets the call split each query's
+ * blocks across more CTAs, whose outputs are rounded to bf16 before they are joined);
+ * for the others the blocks' positions are written into the workspace, which has to
+ * have dsa_block_mla_attn_workspace_size() bytes, and n_blocks * page_size <= 16384. */
+size_t dsa_block_mla_attn_workspace_size(const dsa_seq_desc_t* seq, const dsa_mla_desc_t* mla, int32_t n_blocks);
+dsa_status_t dsa_block_mla_attn(const dsa_seq_desc_t* seq, const dsa_mla_desc_t* mla, const int32_t* block_idx,
+                                int32_t n_blocks, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                dsa_stream_t stream);
+/* dsa_indexer_scores, dsa_block_topk and dsa_block_mla_attn chained, as dsa_decode_step
+ * chains its three.  block_idx_out (device int32 [T, n_blocks]) receives the blocks when
+ * non-NULL.  workspace: >= dsa_block_decode_workspace_size() bytes. */
+size_t dsa_block_decode_workspace_size(const dsa_seq_desc_t* seq, const dsa_mla_desc_t* mla, int32_t n_blocks);
+dsa_status_t dsa_block_decode_step(const dsa_seq_desc_t* seq, const dsa_indexer_desc_t* idx, const dsa_mla_desc_t* mla,
+                                   int32_t n_blocks, int32_t n_first, int32_t n_last, void* out, float* lse,
+                                   int32_t* block_idx_out, void* workspace, size_t workspace_bytes,
+                                   dsa_stream_t stream);
+
 /* The decode step with its scratch memory in a device array the library owns,
  * for callers that cannot allocate device memory (for example a plugin inside
  * an engine that owns all device memory and offers plugins no allocator, or a
