@@ -244,8 +244,9 @@ bool encode_tmap_2d_u8(void* tmap_out, const void* base, uint64_t inner, uint64_
   return encode_tmap_2d(tmap_out, base, 1, inner, rows, row_stride_bytes, box_inner, box_rows, why);
 }
 
-bool encode_tmap_2d(void* tmap_out, const void* base, int elem_bytes, uint64_t inner, uint64_t rows,
-                    uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows, std::string* why) {
+namespace {
+bool encode_tmap(void* tmap_out, const void* base, CUtensorMapDataType type, uint32_t rank, const cuuint64_t* dims,
+                 const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle, std::string* why) {
   using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -263,14 +264,9 @@ bool encode_tmap_2d(void* tmap_out, const void* base, int elem_bytes, uint64_t i
     *why = "cuTensorMapEncodeTiled unavailable";
     return false;
   }
-  const cuuint64_t dims[2] = {inner, rows};
-  const cuuint64_t strides[1] = {row_stride_bytes};
-  const cuuint32_t box[2] = {box_inner, box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUtensorMapDataType dt = elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  const CUresult r = fn(static_cast<CUtensorMap*>(tmap_out), dt, 2,
-                        const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        box_inner * elem_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = fn(static_cast<CUtensorMap*>(tmap_out), type, rank, const_cast<void*>(base), dims, strides, box,
+                        estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     char buf[96];
@@ -279,6 +275,33 @@ bool encode_tmap_2d(void* tmap_out, const void* base, int elem_bytes, uint64_t i
     return false;
   }
   return true;
+}
+}  // namespace
+
+bool encode_tmap_2d(void* tmap_out, const void* base, int elem_bytes, uint64_t inner, uint64_t rows,
+                    uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows, std::string* why) {
+  const cuuint64_t dims[2] = {inner, rows};
+  const cuuint64_t strides[1] = {row_stride_bytes};
+  const cuuint32_t box[2] = {box_inner, box_rows};
+  return encode_tmap(tmap_out, base, elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+                     dims, strides, box,
+                     box_inner * elem_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, why);
+}
+
+bool encode_tmap_atoms(void* tmap_out, const void* base, uint32_t atoms, uint64_t rows, uint64_t row_stride_bytes,
+                       uint32_t box_rows, uint32_t box_atoms, std::string* why) {
+  const cuuint64_t dims[3] = {64, rows, atoms};
+  const cuuint64_t strides[2] = {row_stride_bytes, 128};
+  const cuuint32_t box[3] = {64, box_rows, box_atoms};
+  return encode_tmap(tmap_out, base, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B, why);
+}
+
+bool encode_tmap_heads(void* tmap_out, const void* base, uint32_t atoms, uint64_t heads, uint64_t tokens,
+                       uint32_t box_heads, std::string* why) {
+  const cuuint64_t dims[4] = {64, heads, tokens, atoms};
+  const cuuint64_t strides[3] = {atoms * 128ull, heads * atoms * 128ull, 128};
+  const cuuint32_t box[4] = {64, box_heads, 1, 1};
+  return encode_tmap(tmap_out, base, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B, why);
 }
 
 }  // namespace dsa

@@ -69,10 +69,12 @@ constexpr int kDqk = 576, kDv = 512;
 constexpr int kAtom = 64 * 128;       // bytes of a [64 rows x 64 dims] atom
 constexpr int kStage = 9 * kAtom;
 constexpr int kWarpOwn = 0, kWarpOther = 1, kWarpQk = 2, kWarpPv = 3, kWarpSoft = 4;
-constexpr int kParts = 2;             // threads that share a (head, block)'s logits
+constexpr int kParts = 4;             // threads that share a (head, block)'s logits
 constexpr int kCols = kPage / kParts; // logits a thread
 constexpr int kSoftWarps = 4 * kParts;
+static_assert(kParts == 4, "a thread's 64 columns of O are one atom of the output");
 constexpr int kThreads = 32 * (kWarpSoft + kSoftWarps);
+constexpr int kAhead = 2;             // tiles that the L2 is asked for a block before its load
 
 constexpr int kOffQ = 0;
 constexpr int kOffStage = kOffQ + 9 * kAtom;              // [2]
@@ -84,7 +86,7 @@ constexpr int kOffBar = kOffOk + kSoftWarps * 4;
 // What a tile is, in info: x flags, y the other block's first cache row, z and w how many rows of
 // blocks 0 and 1 count.  Written before the tile's loads, that is after P V of the tile two before.
 constexpr int kFirst = 1, kLast = 2, kEnd = 4;            // of its item; last of all
-constexpr int kNumBars = 20;
+constexpr int kNumBars = 24;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;
 constexpr int kUsed = kOffMisc + 16;
 constexpr int kSmemBytes = 232448;
@@ -108,6 +110,7 @@ struct BlockParams {
   uint32_t dbg_withhold;
   Divisor split, heads;     // by n_split, head_blocks
   float scale_log2;         // softmax scale * log2 e
+  uint32_t page_bytes;      // of a block from its first row to its last row's end; 0: rows too far apart to ask for it whole
 };
 
 // Whether a wait must end (1): another thread of the CTA gave up, or the wait has been going
@@ -130,7 +133,9 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_block_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap, BlockParams p) {
+    attn_block_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap2,
+                      const __grid_constant__ CUtensorMap kmap1, const __grid_constant__ CUtensorMap omap,
+                      BlockParams p) {
   grid_dep_launch();   // the kernel after waits for this grid before it reads what this grid writes
   extern __shared__ __align__(1024) uint8_t sm_raw[];
   uint8_t* sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
@@ -142,18 +147,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kOffBar);
   // Barriers in pairs belong to a tile's stage or logit buffer: nothing comes to one for the
-  // tile after next before its waiters have passed it for this one.
-  uint64_t* ownfull = bars;       // [2] own block landed
-  uint64_t* ownpair = bars + 2;   // [2] leader: and the other CTA's (its query too, at an item's first tile)
-  uint64_t* othfull = bars + 4;   // [2] the other block's values landed
-  uint64_t* othpair = bars + 6;   // [2] leader: in the other CTA as well
-  uint64_t* sfull = bars + 8;     // [2] Q K^T complete: logits there, half of the stage and its rope atom dead
-  uint64_t* sfree = bars + 10;    // [2] leader: logits read, both CTAs
-  uint64_t* pvdone = bars + 12;   // [2] P V complete: the tile's stage and P free
-  uint64_t* edone = bars + 14;    // [2] an item's output has left the stage of its last tile
-  uint64_t* pfull = bars + 16;    // leader: P written, both CTAs (one buffer: P V of the tile before is complete)
-  uint64_t* qraw = bars + 17;     // an item's query has come
-  uint64_t* drain = bars + 18;    // every MMA complete (teardown)
+  // tile after next before its waiters have passed it for this one.  What both CTAs load for an
+  // MMA is counted on one barrier of the leader, which issues it.
+  uint64_t* ifull = bars;         // [2] what the tile is has been written
+  uint64_t* own = bars + 2;       // [2][2] leader: own blocks landed in both CTAs, atoms 0, 1, 4, 5 and the rest
+  uint64_t* pvhalf = bars + 6;    // [2] P V complete as far as atoms 0, 1, 4, 5 go
+  uint64_t* oth = bars + 8;       // [2] leader: the other blocks' values landed in both CTAs
+  uint64_t* othpart = bars + 10;  // [2] they have landed in this CTA (tiles with rows to zero only)
+  uint64_t* sfull = bars + 12;    // [2] Q K^T complete: logits there, half of the stage and its rope atom dead
+  uint64_t* sfree = bars + 14;    // [2] leader: logits read, both CTAs
+  uint64_t* pvdone = bars + 16;   // [2] P V complete: the tile's stage and P free
+  uint64_t* edone = bars + 18;    // [2] an item's output has left the stage of its last tile
+  uint64_t* pfull = bars + 20;    // leader: P written, both CTAs (one buffer: P V of the tile before is complete)
+  uint64_t* qfull = bars + 21;    // leader: an item's query has come, both CTAs
+  uint64_t* drain = bars + 22;    // every MMA complete (teardown)
   uint32_t* misc = reinterpret_cast<uint32_t*>(sm + kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
   const volatile int* info = reinterpret_cast<const volatile int*>(sm + kOffInfo);
@@ -172,24 +179,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kWarpOwn && lane == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ownfull[i], 1);
-      mbar_init(&ownpair[i], 1);
-      mbar_init(&othfull[i], 1);
-      mbar_init(&othpair[i], 1);
+      mbar_init(&ifull[i], 1);
+      mbar_init(&own[2 * i], 1);
+      mbar_init(&own[2 * i + 1], 1);
+      mbar_init(&pvhalf[i], 1);
+      mbar_init(&oth[i], 2);
+      mbar_init(&othpart[i], 1);
       mbar_init(&sfull[i], 1);
       mbar_init(&sfree[i], 2 * kSoftWarps);
       mbar_init(&pvdone[i], 1);
       mbar_init(&edone[i], kSoftWarps);
     }
     mbar_init(pfull, 2 * kSoftWarps);
-    mbar_init(qraw, 1);
+    mbar_init(qfull, 1);
     mbar_init(drain, 2);
     *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == kWarpOther && lane == 0) {
     tma_prefetch_desc(&qmap);
-    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&kmap2);
+    tma_prefetch_desc(&kmap1);
   }
   __syncwarp();
   if (warp == kWarpQk) {
@@ -203,6 +213,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_wait();
   tc_fence_after();
   const uint32_t tmem0 = misc[0];
+  // Whether a tile holds rows behind its query's position, which have to be zeroed.
+  auto zeroes = [](const int4& what) -> bool { return ((what.z | what.w) & (kPage - 1)) != 0; };
   auto wait = [&](uint64_t* bar, int use) -> bool {   // the whole warp
     return __all_sync(0xffffffffu, wait_bar(bar, use & 1, abort_flag, wlim));
   };
@@ -267,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     int j = 0, ended = 0;        // tiles; items that have ended before tile j - 1
     int last1 = 0, last2 = 0;    // whether tiles j - 1 and j - 2 ended an item
-    bool ok = true;
+    bool ok = true, half_issued = false;
     next_blocks();
     while (ok && n_there) {
       const int row = n_row, rows = n_rows, cnt = n_cnt, tiles = max(1, (n_cnt + 1) >> 1);
@@ -283,119 +295,169 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool last = k == tiles - 1 && (!n_there || n_first);
         const int flags = (starts && k == 0 ? kFirst : 0) | (last ? kLast | (n_there ? 0 : kEnd) : 0);
         if (j >= 2) {
-          ok = wait(&pvdone[j & 1], (j >> 1) - 1);
-          if (ok && last2) {
-            ok = wait(&edone[ended & 1], ended >> 1);
-            ++ended;
-          }
+          // (an item's output leaves through the stage of its last tile)
+          if (last2) ok = wait(&edone[ended & 1], ended >> 1);
+          ended += last2;
+          if (ok) ok = wait(&pvhalf[j & 1], (j >> 1) - 1);
           if (!ok) break;
         }
         last2 = last1;
         last1 = last ? 1 : 0;
+        const int at0 = has0 ? row0 : none, at1 = has1 ? row1 : none, at = rank ? at1 : at0;
+        uint8_t* dst = sm + kOffStage + (j & 1) * kStage;
+        uint64_t* bar = &own[2 * (j & 1)];
         if (lane == 0) {
-          const int at0 = has0 ? row0 : none, at1 = has1 ? row1 : none;
           *reinterpret_cast<int4*>(sm + kOffInfo + (j & 3) * 16) =
               make_int4(flags, rank ? at0 : at1, has0 ? c0 : 0, has1 ? c1 : 0);
-          mbar_arrive_expect_tx(&ownfull[j & 1], kStage);
-          uint8_t* dst = sm + kOffStage + (j & 1) * kStage;
-#pragma unroll 1
-          for (int a = 0; a < 9; ++a) tma_load_2d(dst + a * kAtom, &kmap, &ownfull[j & 1], a * 64, rank ? at1 : at0);
+          if (!(p.dbg_withhold && j == 0)) mbar_arrive(&ifull[j & 1]);
+          if (rank == 0) mbar_arrive_expect_tx(bar, 2 * 4 * kAtom);
+          tma_load_atoms_pair(dst, &kmap2, leader_addr(bar), at, 0);
+          tma_load_atoms_pair(dst + 4 * kAtom, &kmap2, leader_addr(bar), at, 4);
+        }
+        __syncwarp();
+        if (j >= 2) ok = wait(&pvdone[j & 1], (j >> 1) - 1);
+        if (!ok) {
+          half_issued = true;
+          break;
+        }
+        if (lane == 0) {
+          if (rank == 0) mbar_arrive_expect_tx(bar + 1, 2 * 5 * kAtom);
+          tma_load_atoms_pair(dst + 2 * kAtom, &kmap2, leader_addr(bar + 1), at, 2);
+          tma_load_atoms_pair(dst + 6 * kAtom, &kmap2, leader_addr(bar + 1), at, 6);
+          tma_load_atoms_pair(dst + 8 * kAtom, &kmap1, leader_addr(bar + 1), at, 8);
+        }
+        // the L2 is asked for the own block of a tile some tiles on
+        if (p.page_bytes > 0) {
+          const int e = 2 * (k + kAhead) + static_cast<int>(rank);
+          const int from = __shfl_sync(0xffffffffu, row, e & 31);
+          if (lane == 0 && e < cnt)
+            prefetch_l2_bulk(static_cast<const uint8_t*>(p.a.kv) + static_cast<int64_t>(from) * p.a.row_bytes, p.page_bytes);
         }
         __syncwarp();
       }
     }
     if (bad) atomicOr(&g_status_attn_block, bad);
-    // the last copies have landed before the CTA leaves
-    for (int k = max(0, j - 2); k < j; ++k) mbar_drain(&ownfull[k & 1], (k >> 1) & 1, &g_status_attn_block, wlim);
+    // the last copies, of both CTAs, have landed before either leaves
+    for (int k = max(0, j - 2); k < j && rank == 0; ++k)
+      for (int i = 0; i < 2; ++i) mbar_drain(&own[2 * (k & 1) + i], (k >> 1) & 1, &g_status_attn_block, wlim);
+    if (half_issued && rank == 0) mbar_drain(&own[2 * (j & 1)], (j >> 1) & 1, &g_status_attn_block, wlim);
   } else if (warp == kWarpOther) {
     // ------------------------------------------------ queries, the other block's values
+    auto query_row = [&](int item) -> int { return query_of(item) * H + head_of(item); };   // < 2^31
     auto load_query = [&](int item) {
-      const int row = query_of(item) * H + head_of(item);   // < 2^31
       if (lane == 0) {
-        mbar_arrive_expect_tx(qraw, 9 * kAtom);
+        if (rank == 0) mbar_arrive_expect_tx(qfull, 2 * 9 * kAtom);
+        const uint32_t bar = leader_addr(qfull);
+        const int row = query_row(item);
         // heads beyond H: the next token's, or zeros; nothing is written of them
-#pragma unroll 1
-        for (int a = 0; a < 9; ++a) tma_load_2d(sm + kOffQ + a * kAtom, &qmap, qraw, a * 64, row);
+#pragma unroll
+        for (int k3 = 0; k3 < 3; ++k3) tma_load_atoms_pair(sm + kOffQ + 3 * k3 * kAtom, &qmap, bar, row, 3 * k3);
+        // the L2 is asked for the query after it
+        const int next = item + step;
+        if (next < p.items) {
+          const int64_t from = query_row(next), rows = min(static_cast<int64_t>(kHeads), static_cast<int64_t>(p.seq.T) * H - from);
+          if (rows > 0)
+            prefetch_l2_bulk(static_cast<const uint8_t*>(p.a.q) + from * (kDqk * 2), static_cast<uint32_t>(rows) * (kDqk * 2));
+        }
       }
       __syncwarp();
     };
     int item = first, g = 0, queries = 1;
+    int parts[2] = {0, 0};   // tiles with rows to zero, of either stage
     load_query(item);
     for (bool more = true; more; ++g) {
       const int st = g & 1;
-      if (!wait(&ownfull[st], g >> 1) || !wait(&sfull[st], g >> 1)) break;
-      const int flags = info[(g & 3) * 4], at = info[(g & 3) * 4 + 1];
-      more = !(flags & kEnd);
+      if (!wait(&ifull[st], g >> 1) || !wait(&sfull[st], g >> 1)) break;
+      const int4 what = *reinterpret_cast<const int4*>(sm + kOffInfo + (g & 3) * 16);
+      more = !(what.x & kEnd);
+      const bool zero = zeroes(what);
       if (lane == 0) {
-        mbar_arrive_expect_tx(&othfull[st], 4 * kAtom);
+        uint32_t bar = leader_addr(&oth[st]);
+        if (zero) {   // the copies are waited for in their own CTA
+          mbar_arrive_expect_tx(&othpart[st], 4 * kAtom);
+          bar = smem_u32(&othpart[st]);
+        } else if (rank == 0) {
+          mbar_arrive_expect_tx(&oth[st], 2 * 4 * kAtom);
+          mbar_arrive(&oth[st]);
+        }
         uint8_t* dst = sm + kOffStage + st * kStage + (rank ? 0 : 4) * kAtom;
-#pragma unroll 1
-        for (int a = 0; a < 4; ++a)
-          tma_load_2d(dst + a * kAtom, &kmap, &othfull[st], static_cast<int>(rank) * 256 + a * 64, at);
+        tma_load_atoms_pair(dst, &kmap2, bar, what.y, rank ? 4 : 0);
+        tma_load_atoms_pair(dst + 2 * kAtom, &kmap2, bar, what.y, rank ? 6 : 2);
       }
       __syncwarp();
-      if ((flags & (kLast | kEnd)) == kLast) {   // Q K^T of the item's last tile is complete
+      if ((what.x & (kLast | kEnd)) == kLast) {   // Q K^T of the item's last tile is complete
         item += step;
         load_query(item);
         ++queries;
       }
+      if (zero) {
+        if (!wait(&othpart[st], parts[st]++)) {
+          ++g;
+          break;
+        }
+        if (lane == 0) arrive_pair(leader_addr(&oth[st]));
+        __syncwarp();
+      }
     }
-    for (int k = max(0, g - 2); k < g; ++k) mbar_drain(&othfull[k & 1], (k >> 1) & 1, &g_status_attn_block, wlim);
-    mbar_drain(qraw, (queries - 1) & 1, &g_status_attn_block, wlim);
+    for (int st = 0; st < 2; ++st)
+      if (parts[st]) mbar_drain(&othpart[st], (parts[st] - 1) & 1, &g_status_attn_block, wlim);
+    if (rank == 0) {
+      for (int k = max(0, g - 2); k < g; ++k) mbar_drain(&oth[k & 1], (k >> 1) & 1, &g_status_attn_block, wlim);
+      mbar_drain(qfull, (queries - 1) & 1, &g_status_attn_block, wlim);
+    }
   } else if (warp == kWarpQk) {
     const uint64_t dq = make_sdesc(smem_u32(sm + kOffQ), 16, 1024, kLayoutSw128);
     const uint64_t dk0 = make_sdesc(smem_u32(sm + kOffStage), 16, 1024, kLayoutSw128);
     int n = 0;   // items
-    bool ok = true, more = true;
+    bool ok = rank == 0, more = true;
 #pragma unroll 1
     for (int g = 0; ok && more; ++g) {
       const int sb = g & 1;
-      ok = wait(&ownfull[sb], g >> 1);
+      ok = wait(&ifull[sb], g >> 1);
       if (!ok) break;
       const int flags = info[(g & 3) * 4];
       more = !(flags & kEnd);
-      if (flags & kFirst) ok = wait(qraw, n++);
-      if (rank) {   // passed on to the CTA that issues
-        if (ok && lane == 0 && !(p.dbg_withhold && g == 0)) arrive_pair(leader_addr(&ownpair[sb]));
-        __syncwarp();
-        continue;
-      }
-      if (ok) ok = wait(&ownpair[sb], g >> 1);
+      if (flags & kFirst) ok = wait(qfull, n++);
       if (ok && g >= 2) ok = wait(&sfree[sb], (g >> 1) - 1);
       if (!ok) break;
       tc_fence_after();
-      if (elect_one()) {
-        const uint32_t d = tmem0 + sb * 64;
-        const uint64_t dk = dk0 + static_cast<uint64_t>((sb * kStage) >> 4);
+      const uint32_t d = tmem0 + sb * 64;
+      const uint64_t dk = dk0 + static_cast<uint64_t>((sb * kStage) >> 4);
+      auto multiply = [&](int a) {   // 64 dims
+        const uint64_t off = static_cast<uint64_t>((a * kAtom) >> 4);
 #pragma unroll
-        for (int a = 0; a < 9; ++a) {   // 64 dims a turn
-          const uint64_t off = static_cast<uint64_t>((a * kAtom) >> 4);
+        for (int kk = 0; kk < 4; ++kk)
+          umma_pair(d, dq + off + 2 * kk, dk + off + 2 * kk, kIdescQK, static_cast<uint32_t>(a | kk));
+      };
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_pair(d, dq + off + 2 * kk, dk + off + 2 * kk, kIdescQK, static_cast<uint32_t>(a | kk));
+      for (int i = 0; ok && i < 2; ++i) {   // atoms 0, 1, 4, 5, then 2, 3, 6, 7, 8
+        ok = wait(&own[2 * sb + i], g >> 1);
+        if (ok && elect_one()) {
+          multiply(2 * i);
+          multiply(2 * i + 1);
+          multiply(2 * i + 4);
+          multiply(2 * i + 5);
+          if (i == 1) {
+            multiply(8);
+            commit_pair(&sfull[sb]);
+          }
         }
-        commit_pair(&sfull[sb]);
+        __syncwarp();
       }
-      __syncwarp();
     }
   } else if (warp == kWarpPv) {
     const uint64_t dv0 = make_sdesc(smem_u32(sm + kOffStage), kAtom, 1024, kLayoutSw128);
     const uint64_t dp0 = make_sdesc(smem_u32(sm + kOffStage + 8 * kAtom), 16, 1024, kLayoutSw128);
     const uint64_t dp1 = make_sdesc(smem_u32(sm + kOffP1), 16, 1024, kLayoutSw128);
-    bool ok = true, more = true;
+    bool ok = rank == 0, more = true;
 #pragma unroll 1
     for (int g = 0; ok && more; ++g) {
       const int sb = g & 1;
-      ok = wait(&ownfull[sb], g >> 1) && wait(&othfull[sb], g >> 1);
+      ok = wait(&ifull[sb], g >> 1);
       if (!ok) break;
       const int flags = info[(g & 3) * 4];
       more = !(flags & kEnd);
-      if (rank) {
-        if (lane == 0) arrive_pair(leader_addr(&othpair[sb]));
-        __syncwarp();
-        continue;
-      }
-      ok = wait(&othpair[sb], g >> 1) && wait(pfull, g);
+      ok = wait(&oth[sb], g >> 1) && wait(pfull, g);
       if (!ok) break;
       tc_fence_after();
       fence_proxy_async_smem();
@@ -409,6 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < 4; ++kk)
             umma_pair(tmem0 + kColO + (q >> 1) * 128, da + 2 * kk, db + 128 * kk, kIdescPV,
                       static_cast<uint32_t>((~flags & kFirst) | (q & 1) | kk));
+          if (q == 1) commit_pair(&pvhalf[sb]);
         }
         commit_pair(&pvdone[sb]);
       }
@@ -431,7 +494,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t prow0 = smem_u32(sm + (half ? kOffP1 : kOffStage + 8 * kAtom)) + static_cast<uint32_t>(hl * 128);
     const uint32_t pstep = half ? 0u : static_cast<uint32_t>(kStage);   // block 0: the stage's rope atom
     bool ok = true;
-    int j = 0, done = 0;   // tiles, items
+    int j = 0, done = 0;   // tiles, items whose output has left
+    bool stored = false;   // an item's output is on its way
+    int parts0 = 0, parts1 = 0;   // tiles with rows to zero, of either stage
 #pragma unroll 1
     for (int item = first; item < p.items; item += step) {
       float m = -INFINITY, l = 0.f;
@@ -439,14 +504,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (; !last; ++j) {
         const int st = j & 1;
-        ok = ok && wait(&ownfull[st], j >> 1) && wait(&sfull[st], j >> 1);
+        ok = ok && wait(&ifull[st], j >> 1) && wait(&sfull[st], j >> 1);
+        if (stored) {   // the last item's output has left its stage (seldom still to be waited for: loads went before it)
+          if (lane == 0) {
+            bulk_wait_read();
+            mbar_arrive(&edone[done & 1]);
+          }
+          __syncwarp();
+          ++done;
+          stored = false;
+        }
         tc_fence_after();
         const uint32_t stage = smem_u32(sm + kOffStage) + static_cast<uint32_t>(st * kStage);
         float x[kCols];
         float mx = -INFINITY;
         if (ok) {
           uint32_t s[kCols];
-          tmem_ld32(tmem + st * 64 + part * kCols, s);
+          tmem_ld16(tmem + st * 64 + part * kCols, s);
           const int4 what = *reinterpret_cast<const int4*>(sm + kOffInfo + (j & 3) * 16);
           last = (what.x & kLast) != 0;
           const int mine = (half ? what.w : what.z) - part * kCols;   // of this thread's rows that count
@@ -466,8 +540,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < kCols; i += 2) mq[(i >> 1) & 3] = fmax3(mq[(i >> 1) & 3], x[i], x[i + 1]);
           mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
           // rows behind the query's position: nothing of them may reach O
-          if ((what.z & 63) | (what.w & 63)) {
-            ok = wait(&othfull[st], j >> 1);
+          if (zeroes(what)) {
+            ok = wait(&othpart[st], st ? parts1++ : parts0++);
             if (ok) {
 #pragma unroll 1
               for (int blk = 0; blk < 2; ++blk) {
@@ -483,9 +557,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // barrier tells whether any of them has to let m grow (the first tile, and seldom after);
         // only then do they exchange their maxima.
         const bool grow = named_bar_or(head_bar, kHeadThreads, !ok || mx > m + kRescaleM);
-        // P of block 1 has one buffer and O may have to be rescaled: P V of the tile before is complete
-        const bool pv_ok = !(j >= 1 && ok) || wait(&pvdone[(j - 1) & 1], (j - 1) >> 1);
         if (grow) {
+          // O may have to be rescaled: P V of the tile before is complete
+          const bool pv_ok = !(j >= 1 && ok) || wait(&pvdone[(j - 1) & 1], (j - 1) >> 1);
+          ok = ok && pv_ok;
           xmax[rq * 32] = mx;
           if (lane == 0) oks[sw] = ok ? 1 : 0;
           named_bar_sync(head_bar, kHeadThreads);
@@ -520,24 +595,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = mx;
           }
         }
-        ok = pv_ok;
         const float msub = (m == -INFINITY) ? 0.f : m;
         const uint32_t prow = prow0 + (j & 1) * pstep;
         float se[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t pk[kCols / 2];
 #pragma unroll
-        for (int c = 0; c < kCols / 8; ++c) {
-          uint32_t pk[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int i = 8 * c + 2 * k;
-            float d0, d1;
-            add2(d0, d1, x[i], x[i + 1], -msub, -msub);
-            const float p0 = fast_exp2(d0), p1 = fast_exp2(d1);
-            add2(se[2 * (k & 1)], se[2 * (k & 1) + 1], se[2 * (k & 1)], se[2 * (k & 1) + 1], p0, p1);
-            pk[k] = pack_bf16x2(p0, p1);
-          }
-          st_shared_v4(prow + static_cast<uint32_t>(((part * (kCols / 8) + c) ^ (hl & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
+        for (int k = 0; k < kCols / 2; ++k) {
+          float d0, d1;
+          add2(d0, d1, x[2 * k], x[2 * k + 1], -msub, -msub);
+          const float p0 = fast_exp2(d0), p1 = fast_exp2(d1);
+          add2(se[2 * (k & 1)], se[2 * (k & 1) + 1], se[2 * (k & 1)], se[2 * (k & 1) + 1], p0, p1);
+          pk[k] = pack_bf16x2(p0, p1);
         }
+        // P of block 1 has one buffer: P V of the tile before is complete
+        if (half && j >= 1) ok = wait(&pvdone[(j - 1) & 1], (j - 1) >> 1);
+#pragma unroll
+        for (int c = 0; c < kCols / 8; ++c)
+          st_shared_v4(prow + static_cast<uint32_t>(((part * (kCols / 8) + c) ^ (hl & 7)) << 4), pk[4 * c], pk[4 * c + 1],
+                       pk[4 * c + 2], pk[4 * c + 3]);
         l += (se[0] + se[1]) + (se[2] + se[3]);
         fence_proxy_async_smem();
         tc_fence_before();
@@ -558,55 +633,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const float inv = l == 0.f ? 0.f : 1.f / l;   // l may be NaN
         const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-        const int t = query_of(item), h0 = head_of(item);
-        const int heads = min(32, H - (h0 + (quarter & 1) * 32));   // of this warp's 32 that exist
-        const bool split = p.n_split > 1;
-        const int64_t head0 =
-            (static_cast<int64_t>(split ? slice_of(item) : 0) * p.seq.T + t) * H + h0 + (quarter & 1) * 32;
-        uint8_t* out = reinterpret_cast<uint8_t*>(split ? p.ws_o : static_cast<uint16_t*>(p.a.out)) +
-                       (head0 * kDv + half * 256 + part * (256 / kParts)) * 2;
-        // through the last tile's stage, which P V has left and the loads leave alone till edone: a
-        // thread holds one head's values, and neighbouring lanes should store a head's
-        const uint32_t stg = smem_u32(sm + kOffStage) + ((j - 1) & 1) * kStage + sw * 4096;
-        if (heads > 0) {
+        const int t = query_of(item), h0 = head_of(item) + (quarter & 1) * 32;
+        // through the last tile's stage, which P V has left and the loads leave alone till edone: the
+        // warp's 32 heads x 64 dims, half an atom, as a box of a TMA store
+        uint8_t* out = sm + kOffStage + ((j - 1) & 1) * kStage + (half * 4 + part) * kAtom + (quarter & 1) * 4096;
+        const uint32_t stg = smem_u32(out) + lane * 128;
 #pragma unroll 1
-          for (int cc = 0; cc < 256 / kParts / 64; ++cc) {
-#pragma unroll 1
-            for (int hf = 0; hf < 2; ++hf) {
-              uint32_t o[32];
-              tmem_ld32(tmem + kColO + part * (256 / kParts) + cc * 64 + hf * 32, o);
-              tmem_ld_wait();
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t o[32];
+          tmem_ld32(tmem + kColO + part * 64 + hf * 32, o);
+          tmem_ld_wait();
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                st_shared_v4(stg + lane * 128 + (((hf * 4 + k) ^ (lane & 7)) << 4),
-                             pack_bf16x2(__uint_as_float(o[8 * k]) * inv, __uint_as_float(o[8 * k + 1]) * inv),
-                             pack_bf16x2(__uint_as_float(o[8 * k + 2]) * inv, __uint_as_float(o[8 * k + 3]) * inv),
-                             pack_bf16x2(__uint_as_float(o[8 * k + 4]) * inv, __uint_as_float(o[8 * k + 5]) * inv),
-                             pack_bf16x2(__uint_as_float(o[8 * k + 6]) * inv, __uint_as_float(o[8 * k + 7]) * inv));
-            }
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int row = i * 4 + (lane >> 3), c4 = lane & 7;
-              const uint4 v = ld_shared_v4(stg + row * 128 + ((c4 ^ (row & 7)) << 4));
-              if (row < heads)
-                *reinterpret_cast<uint4*>(out + static_cast<int64_t>(row) * kDv * 2 + cc * 128 + c4 * 16) = v;
-            }
-            __syncwarp();
-          }
-          if (rq == 0 && lane < heads) {
-            if (split)
-              p.ws_lse[head0 + lane] = lse;
-            else if (p.a.lse)
-              p.a.lse[head0 + lane] = lse;
-          }
+          for (int k = 0; k < 4; ++k)
+            st_shared_v4(stg + (((hf * 4 + k) ^ (lane & 7)) << 4),
+                         pack_bf16x2(__uint_as_float(o[8 * k]) * inv, __uint_as_float(o[8 * k + 1]) * inv),
+                         pack_bf16x2(__uint_as_float(o[8 * k + 2]) * inv, __uint_as_float(o[8 * k + 3]) * inv),
+                         pack_bf16x2(__uint_as_float(o[8 * k + 4]) * inv, __uint_as_float(o[8 * k + 5]) * inv),
+                         pack_bf16x2(__uint_as_float(o[8 * k + 6]) * inv, __uint_as_float(o[8 * k + 7]) * inv));
         }
         tc_fence_before();
+        fence_proxy_async_smem();
+        __syncwarp();
+        const int row = (p.n_split > 1 ? slice_of(item) * p.seq.T : 0) + t;
+        if (lane == 0 && h0 < H) tma_store_heads(&omap, out, h0, row, half * 4 + part);
+        if (rq == 0 && h0 + lane < H) {
+          const int64_t at = static_cast<int64_t>(row) * H + h0 + lane;
+          if (p.n_split > 1)
+            p.ws_lse[at] = lse;
+          else if (p.a.lse)
+            p.a.lse[at] = lse;
+        }
+        if (lane == 0) bulk_commit();
       }
-      fence_proxy_async_smem();   // the stage goes back to the TMA
       __syncwarp();
-      if (lane == 0) mbar_arrive(&edone[done++ & 1]);
+      stored = true;
     }
+    if (lane == 0) bulk_wait();
+    __syncwarp();
   }
 
   // Every MMA has finished in both CTAs before either releases its TMEM or leaves (after
@@ -739,7 +802,8 @@ cudaError_t launch_attn_block(const SeqArgs& seq, const MlaArgs& a, void* worksp
   if (items > 0x3FFFFFFFll || static_cast<int64_t>(seq.T) * a.H > 0x7FFFFF00ll) return cudaErrorInvalidConfiguration;
   BlockParams p{seq,     a,       split,        per, head_blocks,    static_cast<int32_t>(items),
                 nullptr, nullptr, kWaitLimitNs, 0u,  Divisor(split), Divisor(head_blocks),
-                a.softmax_scale * kLog2e};
+                a.softmax_scale * kLog2e,
+                a.row_bytes <= 2 * kDqk + 128 ? static_cast<uint32_t>((kPage - 1) * a.row_bytes + 2 * kDqk) : 0u};
   debug_wait_state(&p.wait_limit_ns, &p.dbg_withhold);
   if (split > 1) {
     p.ws_o = static_cast<uint16_t*>(workspace);
@@ -748,18 +812,21 @@ cudaError_t launch_attn_block(const SeqArgs& seq, const MlaArgs& a, void* worksp
   }
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(attn_block_kernel), kSmemBytes, env.device);
   if (e != cudaSuccess) return e;
-  alignas(64) CUtensorMap qmap, kmap;   // boxes of 64 dims of 64 rows: heads, cache rows
+  alignas(64) CUtensorMap qmap, kmap2, kmap1, omap;   // boxes of three atoms of 64 heads, of two and one of 64 cache rows, of one of 32 heads of the output
   std::string reason;
-  if (!encode_tmap_2d(&qmap, a.q, 2, kDqk, static_cast<uint64_t>(seq.T) * a.H, kDqk * 2, 64, kHeads, &reason) ||
-      !encode_tmap_2d(&kmap, a.kv, 2, kDqk, static_cast<uint64_t>(seq.cache_rows), static_cast<uint64_t>(a.row_bytes), 64,
-                      kPage, &reason)) {
+  const uint64_t rows = static_cast<uint64_t>(seq.cache_rows), row_bytes = static_cast<uint64_t>(a.row_bytes);
+  if (!encode_tmap_atoms(&qmap, a.q, 9, static_cast<uint64_t>(seq.T) * a.H, kDqk * 2, kHeads, 3, &reason) ||
+      !encode_tmap_atoms(&kmap2, a.kv, 9, rows, row_bytes, kPage, 2, &reason) ||
+      !encode_tmap_atoms(&kmap1, a.kv, 9, rows, row_bytes, kPage, 1, &reason) ||
+      !encode_tmap_heads(&omap, split > 1 ? static_cast<const void*>(p.ws_o) : a.out, 8, static_cast<uint64_t>(a.H),
+                         static_cast<uint64_t>(split) * seq.T, 32, &reason)) {
     *unsupported = true;
     *why = "block attention: " + reason;
     return cudaSuccess;
   }
   const int64_t grid = 2 * std::min<int64_t>(items, resident_clusters(env.num_sms));
   e = launch_kernel(attn_block_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmemBytes, env.stream, true,
-                    2, qmap, kmap, p);
+                    2, qmap, kmap2, kmap1, omap, p);
   if (e != cudaSuccess) return e;
   char buf[96];
   snprintf(buf, sizeof(buf), "attn_block<bf16>[split=%d,grid=%lld]", split, static_cast<long long>(grid));

@@ -223,6 +223,15 @@ bool encode_tmap_2d_u8(void* tmap_out, const void* base, uint64_t inner, uint64_
 // that of the box's row, 128 or 64 bytes.
 bool encode_tmap_2d(void* tmap_out, const void* base, int elem_bytes, uint64_t inner, uint64_t rows,
                     uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows, std::string* why);
+// Rows of `atoms` * 64 16-bit values as operand atoms: coordinates (0, row, atom), a box 64
+// values x box_rows rows x box_atoms atoms, which lands as so many [box_rows x 128 bytes] atoms
+// one behind the other, 128-byte swizzle.
+bool encode_tmap_atoms(void* tmap_out, const void* base, uint32_t atoms, uint64_t rows, uint64_t row_stride_bytes,
+                       uint32_t box_rows, uint32_t box_atoms, std::string* why);
+// Packed [tokens, heads, atoms * 64] 16-bit values in the same way, coordinates (0, head, token,
+// atom): a box is 64 values x box_heads heads of one token, one atom, and ends at the token's last head.
+bool encode_tmap_heads(void* tmap_out, const void* base, uint32_t atoms, uint64_t heads, uint64_t tokens,
+                       uint32_t box_heads, std::string* why);
 
 }  // namespace dsa
 

@@ -92,4 +92,32 @@ __device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t nthreads, boo
   return any != 0;
 }
 
+// Tiled load of 64 values of rows from `row` on, atoms (64 values each) from `atom` on, into this
+// CTA; its bytes are counted on a barrier of either CTA of the pair (bar: an address in the
+// cluster's window).
+__device__ __forceinline__ void tma_load_atoms_pair(void* smem_dst, const void* map, uint32_t bar, int32_t row, int32_t atom) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
+      "l"(map), "r"(bar), "r"(0), "r"(row), "r"(atom)
+      : "memory");
+}
+// Stores a box of one atom of heads from `head` on of a token, from shared memory; part of the
+// thread's bulk group.
+__device__ __forceinline__ void tma_store_heads(const void* map, const void* smem_src, int32_t head, int32_t token,
+                                                int32_t atom) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(map),
+               "r"(smem_u32(smem_src)), "r"(0), "r"(head), "r"(token), "r"(atom)
+               : "memory");
+}
+// Closes the thread's bulk group; waits until what its groups store has been read from shared
+// memory, or has been written.
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+// Asks the L2 for `bytes` (a multiple of 16) from a 16-byte boundary on.
+__device__ __forceinline__ void prefetch_l2_bulk(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 }  // namespace dsa
