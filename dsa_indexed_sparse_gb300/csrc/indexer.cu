@@ -144,7 +144,8 @@ template <int G, IndexKind kKind = IndexKind::kE4M3>
 struct TcWarps {
   static constexpr int kRot = G == 1 ? (kKind == IndexKind::kMx8 ? 2 : 3) : 1;
   static constexpr int kProd = 2;                  // divides kTcStages
-  static constexpr int kMmaWarps = G == 1 ? 2 : 1;
+  // four MXFP4 queries have MMAs and commits of their own: one warp 2048 queries x 8192 keys 200 us, two 143
+  static constexpr int kMmaWarps = G == 1 || kKind == IndexKind::kMx4 ? 2 : 1;
   static constexpr int kMma = kProd;               // the first MMA-issuing warp (also allocates TMEM)
   static constexpr int kEpi0 = kProd + kMmaWarps;  // first epilogue warp
   static constexpr int kEpiWarps = 4 * G * kRot;
@@ -175,8 +176,9 @@ struct TcCfg {
   // accumulator buffers: two, or one per rotation group; or the slots
   static constexpr int kAccBufs = kMx4 && G > 1 ? 7 : (TcWarps<G, kKind>::kRot > 2 ? TcWarps<G, kKind>::kRot : 2);
   // kMx4, behind the accumulators: the keys' scale words, four columns a tile, for as many
-  // tiles as there are accumulators, or four (before a tile's are copied, its first slot has
-  // come round, so the MMAs of the tile before the last three are done); then the heads', two
+  // tiles as there are accumulators, or four (before a tile's are copied its first slot has come
+  // round: the MMAs two tiles back, this warp's last, are complete and so is all that it issued
+  // before, tile four back included); then the heads', two
   // columns a query, for each issuing warp and query-group buffer (four for a single query:
   // a copy writes four)
   static constexpr int kKeyScaleCol = kAccBufs * kAccCols;
@@ -211,7 +213,7 @@ struct TcCfg {
   static constexpr int kOffKeys = (kOffSel + static_cast<int>(sizeof(SelectSmem)) + 127) / 128 * 128;
   static_assert(kOffKeys % 16 == 0 && kOffSel % 16 == 0, "aligned fused-plan regions");
   static constexpr uint32_t kIdesc = make_idesc(kFmtE4M3, kFmtE4M3, false, false, kTcKeys, N);
-  static constexpr uint32_t kIdescLo = make_idesc_mxf4(kTcKeys, kTcHeads, 0), kIdescHi = make_idesc_mxf4(kTcKeys, kTcHeads, 2);
+  static constexpr uint32_t idesc_mxf4(int half) { return make_idesc_mxf4(kTcKeys, kTcHeads, half ? 2 : 0); }
 };
 
 // Keys of one query a CTA of the fused plan holds in shared memory at most.
@@ -647,8 +649,8 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
             if (j == 0) tmem_copy_scales(ksc, dks);
             const uint64_t db = dqb + static_cast<uint64_t>(j * (kTcHeads * C::kRowBytes / 16));
             const uint32_t d = tmem + slot * C::kAccCols;
-            umma_mxf4(d, dka, db, C::kIdescLo, ksc, qsc + 2 * j, 0u);
-            umma_mxf4(d, dka + 2, db + 2, C::kIdescHi, ksc, qsc + 2 * j, 1u);
+            umma_mxf4(d, dka, db, C::idesc_mxf4(0), ksc, qsc + 2 * j, 0u);
+            umma_mxf4(d, dka + 2, db + 2, C::idesc_mxf4(1), ksc, qsc + 2 * j, 1u);
             if (j == G - 1) umma_commit(&empty[st]);
             umma_commit(&accfull[slot]);
           }
