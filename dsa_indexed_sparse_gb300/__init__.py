@@ -184,6 +184,15 @@ def _dtype_code(t: torch.Tensor) -> int:
     raise ValueError(f"unsupported dtype {t.dtype}")
 
 
+def _flat(t: torch.Tensor, name: str, dev: int) -> int:
+    """Data pointer of a contiguous tensor on GPU dev."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current CUDA device, not on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
 def _cache_ptr(t: torch.Tensor, name: str, dev: int) -> int:
     if not t.is_contiguous():
         raise ValueError("tensors passed to libdsa must be contiguous")
@@ -445,34 +454,40 @@ def decode_step_static_ws(seq: Seq, idx: Indexer, mla: Mla, K: int, out: torch.T
 
 def _codes_check(dtype: int, D: int, rows: int, codes: torch.Tensor, scale: Optional[torch.Tensor], names: str) -> None:
     """Codes and scales of at least `rows` index vectors of D values in the format dtype."""
-    if dtype not in (DSA_E4M3, DSA_MXFP8_E4M3, DSA_MXFP4_E2M1):
+    if dtype == DSA_MXFP4_E2M1:
+        per, size, scales = D // 2, 1, rows * (D // 32)
+    elif dtype == DSA_MXFP8_E4M3:
+        per, size, scales = D, 1, rows * (D // 32)
+    elif dtype == DSA_E4M3:
+        per, size, scales = D, 4, rows
+    else:
         raise ValueError("dtype must be DSA_E4M3, DSA_MXFP8_E4M3 or DSA_MXFP4_E2M1")
-    per = D // 2 if dtype == DSA_MXFP4_E2M1 else D
     if codes.element_size() != 1 or codes.numel() < rows * per:
         raise ValueError(f"{names}: codes must be one-byte [{rows}, {per}]")
     if scale is None:
-        if dtype != DSA_E4M3:
+        if size == 1:
             raise ValueError(f"{names}: scales are required")
-    elif scale.element_size() != (4 if dtype == DSA_E4M3 else 1) or scale.numel() < rows * (1 if dtype == DSA_E4M3 else D // 32):
+    elif scale.element_size() != size or scale.numel() < scales:
         raise ValueError(f"{names}: scales must be fp32 [{rows}] (DSA_E4M3) or uint8 [{rows}, D_I / 32]")
 
 
 def _dense(t: torch.Tensor, name: str, dev: int, dtype: torch.dtype, shape) -> int:
     if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} {list(shape)}")
-    return _cache_ptr(t, name, dev)
+    return _flat(t, name, dev)
 
 
 def _outputs(s: SeqDesc, m: MlaDesc, out: torch.Tensor, lse: Optional[torch.Tensor], dev: int):
     """Pointers of an attention's out [T, H, d_latent] and lse [T, H] (or None)."""
-    o = _dense(out, "out", dev, torch.float32 if m.dtype == DSA_F32 else torch.bfloat16, (s.T, m.H, m.d_latent))
-    return o, None if lse is None else _dense(lse, "lse", dev, torch.float32, (s.T, m.H))
+    T, H = s.T, m.H
+    o = _dense(out, "out", dev, torch.float32 if m.dtype == DSA_F32 else torch.bfloat16, (T, H, m.d_latent))
+    return o, None if lse is None else _dense(lse, "lse", dev, torch.float32, (T, H))
 
 
 def _scratch(workspace: Optional[torch.Tensor], dev: int):
     if workspace is None:
         return None, 0
-    return _cache_ptr(workspace, "workspace", dev), workspace.numel() * workspace.element_size()
+    return _flat(workspace, "workspace", dev), workspace.numel() * workspace.element_size()
 
 
 def block_topk(seq: Seq, scores: torch.Tensor, n_blocks: int, out: torch.Tensor, first: int = 1, last: int = 1,
@@ -481,11 +496,12 @@ def block_topk(seq: Seq, scores: torch.Tensor, n_blocks: int, out: torch.Tensor,
     fp32 [T, ld], of indexer_scores), the `first` first and `last` last ones always
     among them: out int32 [T, n_blocks], ascending, -1 behind them."""
     s = seq.desc()
-    dev = _on_current(seq)
-    if scores.dim() != 2 or scores.dtype != torch.float32 or scores.shape[0] != s.T:
+    T, shape = s.T, scores.shape
+    if len(shape) != 2 or scores.dtype != torch.float32 or shape[0] != T:
         raise ValueError("scores must be float32 [T, ld]")
-    _check(_lib.dsa_block_topk(ctypes.byref(s), _cache_ptr(scores, "scores", dev), scores.shape[1], n_blocks, first, last,
-                               _dense(out, "out", dev, torch.int32, (s.T, n_blocks)), _stream(stream, dev)))
+    dev = _on_current(seq)
+    _check(_lib.dsa_block_topk(ctypes.byref(s), _flat(scores, "scores", dev), shape[1], n_blocks, first, last,
+                               _dense(out, "out", dev, torch.int32, (T, n_blocks)), _stream(stream, dev)))
     return out
 
 
@@ -539,13 +555,15 @@ def index_cache_append(seq: Seq, k_new: torch.Tensor, k_cache: torch.Tensor, k_s
     k_cache uint8 [cache_rows, D_I / 2]) names the format instead of mx."""
     s = seq.desc()
     if dtype == DSA_MXFP4_E2M1:
-        if k_new.dim() != 2 or k_new.shape[0] != s.T or k_new.dtype not in _FLOAT_CODES:
+        shape, src = k_new.shape, _FLOAT_CODES.get(k_new.dtype)
+        if len(shape) != 2 or shape[0] != s.T or src is None:
             raise ValueError("k_new must be float32 or bfloat16 [T, D_I]")
-        _codes_check(dtype, k_new.shape[1], s.cache_rows, k_cache, k_scale, "k_cache, k_scale")
+        D = shape[1]
+        _codes_check(dtype, D, s.cache_rows, k_cache, k_scale, "k_cache, k_scale")
         dev = _on_current(seq)
-        _check(_lib.dsa_index_cache_append_mx4(ctypes.byref(s), k_new.shape[1], _FLOAT_CODES[k_new.dtype],
-                                               _cache_ptr(k_new, "k_new", dev), _cache_ptr(k_cache, "k_cache", dev),
-                                               _cache_ptr(k_scale, "k_scale", dev), _stream(stream, dev)))
+        _check(_lib.dsa_index_cache_append_mx4(ctypes.byref(s), D, src, _flat(k_new, "k_new", dev),
+                                               _flat(k_cache, "k_cache", dev), _flat(k_scale, "k_scale", dev),
+                                               _stream(stream, dev)))
         return
     if dtype not in (None, DSA_E4M3, DSA_MXFP8_E4M3):
         raise ValueError("dtype must be DSA_E4M3, DSA_MXFP8_E4M3 or DSA_MXFP4_E2M1")
@@ -560,18 +578,21 @@ def index_query_quantize(q: torch.Tensor, codes: torch.Tensor, scale: torch.Tens
     contiguous is fine) to the codes and scales that Indexer takes as q and q_scale:
     codes uint8 [T, H_I, D_I] ([T, H_I, D_I / 2] for DSA_MXFP4_E2M1), scale fp32
     [T, H_I] (DSA_E4M3) or uint8 [T, H_I, D_I / 32]."""
-    if q.dim() != 3 or q.dtype not in _FLOAT_CODES:
+    shape, src = q.shape, _FLOAT_CODES.get(q.dtype)
+    if len(shape) != 3 or src is None:
         raise ValueError("q must be float32 or bfloat16 [T, H_I, D_I]")
-    T, H, D = q.shape
-    _codes_check(dtype, D, T * H, codes, scale, "codes, scale")
     if scale is None:
         raise ValueError("scale is required")
+    T, H, D = shape
+    _codes_check(dtype, D, T * H, codes, scale, "codes, scale")
+    st, sh, last = q.stride()
+    if last != 1 and D > 1:
+        raise ValueError("the last dim of q must be contiguous")
     dev = q.get_device()
     if dev < 0 or dev != _current_device():
         raise ValueError("q must be on the current CUDA device")
-    _check(_lib.dsa_index_query_quantize(T, H, D, _FLOAT_CODES[q.dtype], dtype, _rows(q, "q", dev), q.stride(0),
-                                         q.stride(1), _cache_ptr(codes, "codes", dev), _cache_ptr(scale, "scale", dev),
-                                         _stream(stream, dev)))
+    _check(_lib.dsa_index_query_quantize(T, H, D, src, dtype, q.data_ptr(), st, sh, _flat(codes, "codes", dev),
+                                         _flat(scale, "scale", dev), _stream(stream, dev)))
 
 
 def index_cache_read(seq: Seq, k_cache: torch.Tensor, k_scale: Optional[torch.Tensor], out: torch.Tensor,
@@ -579,15 +600,20 @@ def index_cache_read(seq: Seq, k_cache: torch.Tensor, k_scale: Optional[torch.Te
     """The cached index keys of the positions of seq (q_seq, q_pos) as the values they
     stand for: out [T, D_I], bf16 or fp32 (a row-strided view is fine)."""
     s = seq.desc()
-    if out.dim() != 2 or out.shape[0] != s.T or out.dtype not in _FLOAT_CODES:
+    shape, kind = out.shape, _FLOAT_CODES.get(out.dtype)
+    if len(shape) != 2 or shape[0] != s.T or kind is None:
         raise ValueError("out must be float32 or bfloat16 [T, D_I]")
-    D = out.shape[1]
+    D = shape[1]
     _codes_check(dtype, D, s.cache_rows, k_cache, k_scale, "k_cache, k_scale")
+    stride, last = out.stride()
+    if last != 1 and D > 1:
+        raise ValueError("the last dim of out must be contiguous")
     dev = _on_current(seq)
-    _check(_lib.dsa_index_cache_read(ctypes.byref(s), D, dtype, _cache_ptr(k_cache, "k_cache", dev),
-                                     None if k_scale is None else _cache_ptr(k_scale, "k_scale", dev),
-                                     _FLOAT_CODES[out.dtype], _rows(out, "out", dev), out.stride(0),
-                                     _stream(stream, dev)))
+    if out.get_device() != dev:
+        raise ValueError("out must be on the current CUDA device")
+    _check(_lib.dsa_index_cache_read(ctypes.byref(s), D, dtype, _flat(k_cache, "k_cache", dev),
+                                     None if k_scale is None else _flat(k_scale, "k_scale", dev), kind, out.data_ptr(),
+                                     stride, _stream(stream, dev)))
     return out
 
 

@@ -14,9 +14,11 @@
 // a load; the maxima of 16 lanes are then exchanged so that each lane goes on with half of
 // its values: eight shuffles for 16 blocks instead of 64.
 //
-// The choice: the largest key bits that N keys reach, bit by bit from the top, with a count over
-// the CTA for each (one barrier that counts, where a thread holds one key); it ends early when
-// exactly N keys do.  Keys above are taken, of those equal to it the first ones.
+// The choice, among the blocks that are not taken in any case: a histogram of eight bits of key
+// minus smallest key, from the highest bit that their range has on (scores of one query share
+// their first bits, and atomics on few bins would wait for one another), says which bin holds the
+// last key to take; the bin's keys are looked at again by their next eight bits until all of them
+// are taken or one key is left.  Of keys equal to it the first ones are taken.
 #include <algorithm>
 #include <cstdio>
 
@@ -32,6 +34,7 @@ namespace {
 constexpr int kMaxThreads = 512;
 constexpr int kMaxBlocks = 32768;   // keys of a query in shared memory
 constexpr int kMaxCluster = 8;
+constexpr int kBins = 256;          // of a histogram: eight bits
 
 struct BlockTopkArgs {
   const float* scores;
@@ -41,27 +44,14 @@ struct BlockTopkArgs {
   int32_t* out;
 };
 
-// A block's key: above all others where it is taken in any case; -inf for scores of nothing but
-// NaN (the maximum of a NaN and a number is the number).
-__device__ __forceinline__ uint32_t block_key(const BlockTopkArgs& a, int blk, int n, float best) {
-  return blk < a.n_first || blk >= n - a.n_last ? 0xFFFFFFFFu : order_key(fmaxf(best, -INFINITY));
-}
-
-// Sum over the CTA of a value per thread; red: one word per warp, of two sets taken in turn.
-__device__ __forceinline__ int block_count(int v, int* red) {
-  v = __reduce_add_sync(0xffffffffu, v);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  const int lane = threadIdx.x & 31;
-  return __reduce_add_sync(0xffffffffu, lane < static_cast<int>(blockDim.x >> 5) ? red[lane] : 0);
-}
-
 template <bool kPage64>
-__global__ void __launch_bounds__(kMaxThreads) block_topk_kernel(BlockTopkArgs a) {
+__global__ void __launch_bounds__(kMaxThreads, 2) block_topk_kernel(BlockTopkArgs a) {
   grid_dep_wait();
   grid_dep_launch();   // the kernel after waits for this grid before it reads the blocks
   extern __shared__ uint32_t keys[];
-  __shared__ int red[2][32];
+  __shared__ uint32_t bins[4][kBins];
+  __shared__ uint32_t red[2][32];
+  __shared__ uint32_t pick[2][3];   // of a pass: digit, keys above its bin, keys in it
   const int CL = static_cast<int>(cl_size()), rank = static_cast<int>(cl_rank());
   const int t = a.T - 1 - static_cast<int>(blockIdx.x) / CL;   // longest causal histories first
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
@@ -80,8 +70,9 @@ __global__ void __launch_bounds__(kMaxThreads) block_topk_kernel(BlockTopkArgs a
   // ---- this CTA's blocks [lo, hi) to keys in the first CTA
   const float* row = a.scores + static_cast<int64_t>(t) * a.ld;
   const uint32_t dst = CL > 1 ? cl_map(smem_u32(keys), 0) : 0u;
+  for (int i = tid; i < 4 * kBins; i += nt) (&bins[0][0])[i] = 0u;
   auto put = [&](int blk, float best) {
-    const uint32_t k = block_key(a, blk, n, best);
+    const uint32_t k = order_key(fmaxf(best, -INFINITY));   // (a NaN only where there is nothing else)
     if (CL > 1)
       cl_store(dst + static_cast<uint32_t>(blk) * 4u, k);
     else
@@ -145,54 +136,92 @@ __global__ void __launch_bounds__(kMaxThreads) block_topk_kernel(BlockTopkArgs a
     __syncthreads();
   }
 
-  // ---- the largest bits that N keys reach
-  const bool one = n <= nt;   // one key a thread
-  const uint32_t mine = tid < n ? keys[tid] : 0u;
-  uint32_t best = 0u;
-  int reach = n, set = 0;
-  for (int b = 31; b >= 0 && reach != N; --b) {
-    const uint32_t cand = best | (1u << b);
-    int c;
-    if (one) {
-      c = __syncthreads_count(tid < n && mine >= cand);
-    } else {
-      c = 0;
-      for (int i = tid; i < n; i += nt) c += keys[i] >= cand ? 1 : 0;
-      c = block_count(c, red[set]);
-      set ^= 1;
+  // ---- the last key to take: T, an offset from the smallest key
+  auto forced = [&](int i) -> bool { return i < a.n_first || i >= n - a.n_last; };   // n > N: no block twice
+  uint32_t rem = static_cast<uint32_t>(N - a.n_first - a.n_last);   // of the others
+  const bool some = rem > 0;
+  uint32_t base = 0u, T = 0u;
+  bool exact = false;   // all keys from T on are taken; else those above, and `rem` equal ones
+  if (some) {
+    uint32_t lo_key = 0xFFFFFFFFu, hi_key = 0u;
+    for (int i = tid; i < n; i += nt) {
+      if (forced(i)) continue;
+      lo_key = min(lo_key, keys[i]);
+      hi_key = max(hi_key, keys[i]);
     }
-    if (c >= N) {
-      best = cand;
-      reach = c;
+    lo_key = __reduce_min_sync(0xffffffffu, lo_key);
+    hi_key = __reduce_max_sync(0xffffffffu, hi_key);
+    if (lane == 0) red[0][warp] = lo_key, red[1][warp] = hi_key;
+    __syncthreads();
+    const bool has = lane < (nt >> 5);
+    base = __reduce_min_sync(0xffffffffu, has ? red[0][lane] : 0xFFFFFFFFu);
+    const uint32_t range = __reduce_max_sync(0xffffffffu, has ? red[1][lane] : 0u) - base;
+    int shift = 32 - __clz(static_cast<int>(range));   // bits that are not settled
+    for (int pass = 0; shift > 0 && !exact; ++pass) {
+      const int above = shift, bits = min(8, shift);
+      shift -= bits;
+      for (int i = tid; i < n; i += nt) {
+        const uint32_t d = keys[i] - base;
+        if (!forced(i) && (pass == 0 || (d >> above) == (T >> above))) atomicAdd(&bins[pass][(d >> shift) & ((1u << bits) - 1u)], 1u);
+      }
+      __syncthreads();
+      if (warp == 0) {   // lane l: bins 255 - 8 l and the seven below
+        uint32_t c[8], sum = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum += c[k] = bins[pass][kBins - 1 - (8 * lane + k)];
+        uint32_t incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t u = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += u;
+        }
+        uint32_t before = incl - sum;
+        if (before < rem && incl >= rem) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            if (before < rem && before + c[k] >= rem) {
+              pick[pass & 1][0] = static_cast<uint32_t>(kBins - 1 - (8 * lane + k));
+              pick[pass & 1][1] = before;
+              pick[pass & 1][2] = c[k];
+              before = rem;   // found
+            } else {
+              before += c[k];
+            }
+          }
+        }
+      }
+      __syncthreads();
+      T |= pick[pass & 1][0] << shift;
+      rem -= pick[pass & 1][1];
+      exact = pick[pass & 1][2] == rem;
     }
   }
-  // ---- keys above it, and of the keys equal to it so many that there are N, in ascending order
-  int above = N;
-  if (reach != N) {   // best is a key: some equal ones are left out
-    int c = 0;
-    for (int i = tid; i < n; i += nt) c += keys[i] > best ? 1 : 0;
-    above = block_count(c, red[set]);
-    set ^= 1;
-  }
-  const int equal_most = reach == N ? n : N - above;
+  // ---- what is taken, in ascending order
+  const int equal_most = static_cast<int>(rem);
   int o = 0, equals = 0;   // written, equal ones met, in the chunks before
   for (int i0 = 0; i0 < n; i0 += nt) {
     const int i = i0 + tid;
-    const uint32_t k = i < n ? keys[i] : 0u;
-    const uint32_t gt = __ballot_sync(0xffffffffu, i < n && k > best), eq = __ballot_sync(0xffffffffu, i < n && k == best);
+    bool take = i < n && forced(i), same = false;
+    if (i < n && some && !take) {
+      const uint32_t d = keys[i] - base;
+      take = d > T || (exact && d == T);
+      same = !exact && d == T;
+    }
+    const uint32_t gt = __ballot_sync(0xffffffffu, take), eq = __ballot_sync(0xffffffffu, same);
     __syncthreads();
-    if (lane == 0) red[0][warp] = __popc(gt) | (__popc(eq) << 16);
+    if (lane == 0) red[0][warp] = static_cast<uint32_t>(__popc(gt) | (__popc(eq) << 16));
     __syncthreads();
-    const int v = lane < (nt >> 5) ? red[0][lane] : 0;
-    const int before = __reduce_add_sync(0xffffffffu, lane < warp ? v : 0), all = __reduce_add_sync(0xffffffffu, v);
+    const uint32_t v = lane < (nt >> 5) ? red[0][lane] : 0u;
+    const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? v : 0u), all = __reduce_add_sync(0xffffffffu, v);
     const uint32_t lt = (1u << lane) - 1u;
-    const int eq_before = equals + (before >> 16) + __popc(eq & lt);
-    const int gt_before = (before & 0xFFFF) + __popc(gt & lt);
+    const int eq_before = equals + static_cast<int>(before >> 16) + __popc(eq & lt);
+    const int gt_before = static_cast<int>(before & 0xFFFFu) + __popc(gt & lt);
     // of the equal ones before this key in the chunk, those that are taken
     const int eq_taken = min(eq_before, equal_most) - min(equals, equal_most);
-    if (((gt >> lane) & 1u) || (((eq >> lane) & 1u) && eq_before < equal_most)) out[o + gt_before + eq_taken] = i;
-    o += (all & 0xFFFF) + min(equals + (all >> 16), equal_most) - min(equals, equal_most);
-    equals += all >> 16;
+    if (take || (same && eq_before < equal_most)) out[o + gt_before + eq_taken] = i;
+    const int eq_all = equals + static_cast<int>(all >> 16);
+    o += static_cast<int>(all & 0xFFFFu) + min(eq_all, equal_most) - min(equals, equal_most);
+    equals = eq_all;
   }
 }
 
@@ -216,10 +245,14 @@ cudaError_t launch_block_topk(const SeqArgs& seq, const float* scores, int64_t l
   void (*kernel)(BlockTopkArgs) = page64 ? block_topk_kernel<true> : block_topk_kernel<false>;
   const cudaError_t ae = ensure_smem_limit(reinterpret_cast<const void*>(kernel), kMaxBlocks * 4, env.device);
   if (ae != cudaSuccess) return ae;
-  // few queries: as many CTAs a query as the GPU holds at once, 128 blocks each at least
+  // Few queries: as many CTAs a query as the GPU holds at once, 128 blocks each at least.  One query of 32768
+  // scores takes 4.5 us (4.9 with one CTA), one of 131072 6.4 (12.3 with two CTAs).
   const int want = std::max(1, env.num_sms / seq.T), feed = static_cast<int>(std::max<int64_t>(1, blocks / 128));
   const int cl = std::max(1, std::min(kMaxCluster, std::min(want, feed)));
-  const int threads = seq.T * cl > 2 * env.num_sms ? 256 : kMaxThreads;
+  // Many queries: small CTAs, whose loads and choices overlap on an SM.  4096 queries of 16384 scores take
+  // 46.4 us with 64 threads, 48.3 with 128, 51.9 with 256, 72 with 512; 2048 of 4096 8.2, 9.4, 15.3 and
+  // 27.9; 1024 of 65536 60.2, 47.0, 48.9 and 54.2.
+  const int threads = static_cast<int64_t>(seq.T) * cl > 2 * env.num_sms ? (blocks > 512 ? 128 : 64) : kMaxThreads;
   const BlockTopkArgs a{scores, ld, seq.q_pos, seq.T, seq.max_ctx, seq.page_size, N, n_first, n_last, out};
   const cudaError_t e = launch_kernel(kernel, dim3(static_cast<unsigned>(static_cast<int64_t>(seq.T) * cl)), dim3(threads),
                                       static_cast<size_t>(blocks) * 4, env.stream, true, cl, a);
