@@ -228,6 +228,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the next blocks: lane l holds the first cache row of block l of cnt, and how many rows of it count
     int n_row = 0, n_rows = 0, n_cnt = 0;
     bool n_there = false, n_first = false;
+    int opened = -1, fresh_at = -1;   // entries from fresh_at on, loaded already
+    auto load_blk = [&](int it, int e) -> int {
+      return e + lane < e1 ? __ldg(p.a.idx + static_cast<int64_t>(query_of(it)) * N + e + lane) : -1;
+    };
     auto next_blocks = [&]() {
       n_there = false;
       n_cnt = 0;
@@ -238,6 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int t = query_of(item);
           e0 = slice_of(item) * p.per_split;
           e1 = min(N, e0 + p.per_split);
+          opened = load_blk(item, e0);   // its first entries, beside the query's position and sequence
           qp = __ldg(p.seq.q_pos + t);
           b = __ldg(p.seq.q_seq + t);
           if (qp < 0 || qp >= p.seq.max_ctx || b < 0 || b >= p.seq.B) {
@@ -245,12 +250,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             e1 = e0;
           }
           fresh = true;
+          fresh_at = e0;
           item += step;
           continue;
         }
-        // (item has moved on: the open one is item - step)
-        const int i = e0 + lane;
-        int blk = i < e1 ? __ldg(p.a.idx + static_cast<int64_t>(query_of(item - step)) * N + i) : -1;
+        int blk = fresh_at == e0 ? opened : load_blk(item - step, e0);   // (item has moved on)
+        fresh_at = -1;
         e0 += 32;
         if (blk > (qp >> 6)) {
           bad |= kDevBadIndex;

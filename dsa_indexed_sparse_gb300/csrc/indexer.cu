@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kGenThreads)
 // =============================================================== tcgen05 kernel
 constexpr int kTcHeads = 64;       // H_I
 constexpr int kTcDim = 128;        // D_I (bytes per key row)
-constexpr int kTcKeys = 128;       // keys per tile = UMMA M
+constexpr int kTcKeys = 128;       // keys per UMMA (its M) and accumulator
 constexpr int kTcPage = 64;        // tokens per page
 constexpr int kTcStages = 6;       // key-tile ring depth (16 KB each)
 // Waiting warps sleep between polls (woken when the phase completes): spinning
@@ -162,7 +162,8 @@ struct TcWarps {
 // each).  Its scales lie in TMEM, a word per key and per query head, brought there by
 // tcgen05.cp from shared memory.  With four queries a group, two accumulators of all
 // 256 columns would leave no room for them, so every query has MMAs (N = 64) and
-// accumulators of its own: a ring of seven 64-column slots, slot (tile * G + query) % 7.
+// accumulators of its own: a ring of seven 64-column slots, slot (part * G + query) % 7,
+// parts of 128 keys counted through the tiles.
 template <int G, IndexKind kKind = IndexKind::kE4M3>
 struct TcCfg {
   static constexpr bool kMx = kKind == IndexKind::kMx8, kMx4 = kKind == IndexKind::kMx4;
@@ -171,19 +172,25 @@ struct TcCfg {
   static constexpr int kBlocks = kMx ? kTcDim / 32 : 1;  // accumulators per tile
   static constexpr int kAccCols = kMx4 ? kTcHeads : kBlocks * N;   // TMEM columns per tile (kMx4: per slot)
   static constexpr int kRowBytes = kMx4 ? kTcDim / 2 : kTcDim;     // codes of a key or query head
-  static constexpr int kStageBytes = kTcKeys * kRowBytes;
+  // keys per tile, what goes from role to role at a time: 16 KB of codes.  The roles' pace is a chain of
+  // issue steps a tile, so half the bytes a key make twice the keys a tile, in kSub parts of 128 (with one:
+  // 4 x 131072 keys 13.5 us, 12.3 with two; 2048 queries x 8192 keys 143 and 128.5).
+  static constexpr int kTile = kMx4 ? 2 * kTcKeys : kTcKeys;
+  static constexpr int kSub = kTile / kTcKeys, kPages = kTile / kTcPage;
+  static constexpr int kWindow = 32 / kPages;            // tiles whose page ids a producer warp holds
+  static constexpr int kStageBytes = kTile * kRowBytes;
   static constexpr int kQBytes = N * kRowBytes;          // one query-group buffer
-  // accumulator buffers: two, or one per rotation group; or the slots
-  static constexpr int kAccBufs = kMx4 && G > 1 ? 7 : (TcWarps<G, kKind>::kRot > 2 ? TcWarps<G, kKind>::kRot : 2);
-  // kMx4, behind the accumulators: the keys' scale words, four columns a tile, for as many
-  // tiles as there are accumulators, or four (before a tile's are copied its first slot has come
-  // round: the MMAs two tiles back, this warp's last, are complete and so is all that it issued
-  // before, tile four back included); then the heads', two
-  // columns a query, for each issuing warp and query-group buffer (four for a single query:
-  // a copy writes four)
+  // accumulator buffers: two, or one per rotation group (and part); or the slots
+  static constexpr int kAccBufs = kMx4 && G > 1 ? 7 : kSub * (TcWarps<G, kKind>::kRot > 2 ? TcWarps<G, kKind>::kRot : 2);
+  // kMx4, behind the accumulators: the keys' scale words, four columns a part.  As many parts as there
+  // are accumulators, whose being free says that the MMAs before are complete; or, of the slots, eight:
+  // an issuing warp's last wait for a tile's slots says that its own first MMAs of that tile are
+  // complete, and so is all that it issued for the tiles before.  Then the heads', two columns a query,
+  // for each issuing warp and query-group buffer (four for a single query: a copy writes four).
   static constexpr int kKeyScaleCol = kAccBufs * kAccCols;
+  static constexpr int kKeyScales = G == 1 ? kAccBufs : 8;
   static constexpr int kQScaleCols = kMx4 ? (G > 1 ? 2 * G : 4) : 0;
-  static constexpr int kQScaleCol = kKeyScaleCol + 16;
+  static constexpr int kQScaleCol = kKeyScaleCol + 4 * kKeyScales;
   static constexpr int kTmemNeed =
       kMx4 ? kQScaleCol + 2 * TcWarps<G, kKind>::kMmaWarps * kQScaleCols : kAccBufs * kAccCols;
   static_assert(kTmemNeed <= 512, "TMEM plan");
@@ -195,11 +202,11 @@ struct TcCfg {
   static constexpr int kOffQ = kOffStages + kTcStages * kStageBytes;
   static constexpr int kOffWq = kOffQ + 2 * kQBytes;      // float [4G][kSlice]: each epilogue warp's slice
   // key scales: 4 bytes per key (an fp32 scale, or MXFP8's four E8M0 bytes)
-  // (kMx4: as tcgen05.cp takes them, 16 bytes for keys i, i + 32, i + 64, i + 96)
+  // (kMx4: as tcgen05.cp takes them, 16 bytes for keys i, i + 32, i + 64, i + 96 of a part)
   static constexpr int kOffScale = kOffWq + TcWarps<G, kKind>::kEpiWarps * kSlice * 4;
   // kMx4: the query heads' scale words, 16 bytes for heads i, i + 32 of two queries
   static constexpr int kQScaleBytes = kQScaleCols * 128;
-  static constexpr int kOffQScale = kOffScale + kTcStages * kTcKeys * 4;
+  static constexpr int kOffQScale = kOffScale + kTcStages * kTile * 4;
   static_assert(kOffScale % 128 == 0 && kOffQScale % 128 == 0, "scale words as MMA operands");
   static constexpr int kOffValid = kOffQScale + 2 * kQScaleBytes;  // uint32 [stages]
   static constexpr int kOffBar = kOffValid + kTcStages * 4 + 8;
@@ -230,9 +237,9 @@ struct TcParams {
   int32_t* idx;
 };
 
-// Number of 128-key tiles of query group g (its longest causal history), with
+// Number of tiles of query group g (its longest causal history), with
 // q_pos validation.  Also returns the group's history length.
-template <int G>
+template <int G, int kTile>
 __device__ __forceinline__ int group_tiles(const TcParams& p, int g, int* n_hist) {
   int n = 0;
 #pragma unroll
@@ -248,24 +255,24 @@ __device__ __forceinline__ int group_tiles(const TcParams& p, int g, int* n_hist
     }
   }
   *n_hist = n;
-  return (n + kTcKeys - 1) / kTcKeys;
+  return (n + kTile - 1) / kTile;
 }
 
 // Walks the (group, key tile) list from a starting point.
-template <int G>
+template <int G, int kTile>
 struct TileWalker {
   int g, kt, ntiles, nhist;
   __device__ void init(const TcParams& p, int g0, int kt0) {
     g = g0;
     kt = kt0;
-    ntiles = group_tiles<G>(p, g, &nhist);
+    ntiles = group_tiles<G, kTile>(p, g, &nhist);
   }
   __device__ void advance(const TcParams& p) {
     ++kt;
     while (kt >= ntiles && g + 1 < p.n_groups) {
       ++g;
       kt = 0;
-      ntiles = group_tiles<G>(p, g, &nhist);
+      ntiles = group_tiles<G, kTile>(p, g, &nhist);
     }
   }
 };
@@ -298,6 +305,7 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
   using C = TcCfg<G, kKind>;
   using W = TcWarps<G, kKind>;
   constexpr bool kMx = C::kMx, kMx4 = C::kMx4;
+  constexpr int kTile = C::kTile, kSub = C::kSub, kPages = C::kPages;
   constexpr int kTcThreads = W::kThreads;
   constexpr int kRot = W::kRot;
   constexpr int kProd = W::kProd;
@@ -353,7 +361,7 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
       grid_dep_launch();
       return;
     }
-    const int tiles = (n + kTcKeys - 1) / kTcKeys;
+    const int tiles = (n + kTile - 1) / kTile;
     const int kt0 = static_cast<int>(static_cast<int64_t>(rank) * tiles / f_CL);
     const int kt1 = static_cast<int>(static_cast<int64_t>(rank + 1) * tiles / f_CL);
     if (threadIdx.x == 0) {
@@ -362,8 +370,8 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
     }
     begin = 0;
     end = kt1 - kt0;
-    f_lo = kt0 * kTcKeys;
-    f_len = max(0, min(n, kt1 * kTcKeys) - f_lo);
+    f_lo = kt0 * kTile;
+    f_len = max(0, min(n, kt1 * kTile) - f_lo);
     select_prepare<kTcThreads>(sel, f_CL);   // zeroes the histograms, arrives at the cluster barrier
   } else {
   // ---- work split: equal share of the global tile list -----------------
@@ -371,7 +379,7 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
   for (int g0 = 0; g0 < p.n_groups; g0 += kTcThreads) {
     const int g = g0 + threadIdx.x;
     int nh;
-    const int c = (g < p.n_groups) ? group_tiles<G>(p, g, &nh) : 0;
+    const int c = (g < p.n_groups) ? group_tiles<G, kTile>(p, g, &nh) : 0;
     total += block_sum<kTcThreads>(c, red);
   }
   begin = static_cast<int64_t>(blockIdx.x) * total / gridDim.x;
@@ -382,7 +390,7 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
     for (int g0 = 0; g0 < p.n_groups; g0 += kTcThreads) {
       const int g = g0 + threadIdx.x;
       int nh;
-      const int c = (g < p.n_groups) ? group_tiles<G>(p, g, &nh) : 0;
+      const int c = (g < p.n_groups) ? group_tiles<G, kTile>(p, g, &nh) : 0;
       // inclusive scan within the block
       int v = c;
 #pragma unroll
@@ -456,14 +464,14 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
   int pre_g = -1, pre_kt = -1, pre_b = 0, pre_npg = 0;
   int32_t pre_page = -1;
   if (warp < kProd && ntiles > 2) {
-    TileWalker<G> w0;
+    TileWalker<G, kTile> w0;
     w0.init(p, g_start, kt_start);
     for (int i = 0; i < warp; ++i) w0.advance(p);
     pre_g = w0.g;
     pre_kt = w0.kt;
     pre_b = __ldg(p.seq.q_seq + w0.g * G);
     pre_npg = (w0.nhist + kTcPage - 1) / kTcPage;
-    const int lp = 2 * (pre_kt + (lane >> 1) * kProd) + (lane & 1);
+    const int lp = kPages * (pre_kt + (lane / kPages) * kProd) + lane % kPages;
     if (pre_b >= 0 && pre_b < p.seq.B && lp < pre_npg)
       pre_page = __ldg(p.seq.block_table + static_cast<int64_t>(pre_b) * p.seq.bt_stride + lp);
   }
@@ -478,11 +486,11 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
     // scales.  A query group's own TMA load goes with the producer of the
     // group's first tile in this CTA.
     const int pw = warp;
-    TileWalker<G> w;
+    TileWalker<G, kTile> w;
     w.init(p, g_start, kt_start);
     int cur_g = -1, qcount = 0;
     int win_kt = -1;        // kt of the window's first tile; the window holds kt, kt + kProd, ...
-    int32_t my_page = -1;   // page id of window tile lane / 2, page lane % 2
+    int32_t my_page = -1;   // page id of window tile lane / kPages, page lane % kPages
     const int32_t* bt = p.seq.block_table;
     bool b_ok = false;
     int npg = 0;
@@ -527,21 +535,21 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
         ++qcount;
       }
       if (it % kProd != pw) continue;
-      if (win_kt < 0 || (w.kt - win_kt) / kProd >= 16) {
+      if (win_kt < 0 || (w.kt - win_kt) / kProd >= C::kWindow) {
         const bool pre = w.g == pre_g && w.kt == pre_kt;   // the window read before the wait
         pre_g = -1;
         win_kt = w.kt;
-        const int lp = 2 * (win_kt + (lane >> 1) * kProd) + (lane & 1);
+        const int lp = kPages * (win_kt + (lane / kPages) * kProd) + lane % kPages;
         my_page = (b_ok && lp < npg) ? (pre ? pre_page : __ldg(bt + lp)) : -1;
         if (lp < npg && (my_page < 0 || my_page >= p.seq.n_pages || !b_ok)) {
           atomicOr(&g_status_indexer, kDevBadIndex);
           my_page = -1;
         }
       }
-      const int wi = 2 * ((w.kt - win_kt) / kProd);
-      const int32_t pid0 = __shfl_sync(0xffffffffu, my_page, wi);
-      int32_t pid1 = __shfl_sync(0xffffffffu, my_page, wi + 1);
-      if (2 * w.kt + 1 >= npg) pid1 = -1;
+      const int wi = kPages * ((w.kt - win_kt) / kProd);
+      int32_t pid[kPages];   // -1: bad, or behind the history
+#pragma unroll
+      for (int i = 0; i < kPages; ++i) pid[i] = __shfl_sync(0xffffffffu, my_page, wi + i);
       const int st = it % kTcStages;
       if (it >= kTcStages) {
         const bool ok = mbar_wait(&empty[st], ((it / kTcStages) - 1) & 1, &g_status_indexer, abort_flag,
@@ -549,37 +557,43 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
         if (!__all_sync(0xffffffffu, ok)) break;
       }
       if (lane == 0) {
-        constexpr uint32_t per_page = C::kStageBytes / 2;
-        valid_s[st] = (pid0 >= 0 ? 1u : 0u) | (pid1 >= 0 ? 2u : 0u);
-        mbar_arrive_expect_tx(&full[st], (pid0 >= 0 ? per_page : 0u) + (pid1 >= 0 ? per_page : 0u));
-        uint8_t* dst = sm + C::kOffStages + st * C::kStageBytes;
-        // two adjacent pages go in one 128-row box (kmap2), the others one page each
-        if (pid0 >= 0 && pid1 == pid0 + 1) {
-          tma_load_2d(dst, &kmap2, &full[st], 0, pid0 * kTcPage);
-        } else {
-          if (pid0 >= 0) tma_load_2d(dst, &kmap, &full[st], 0, pid0 * kTcPage);
-          if (pid1 >= 0) tma_load_2d(dst + C::kStageBytes / 2, &kmap, &full[st], 0, pid1 * kTcPage);
+        constexpr uint32_t per_page = C::kStageBytes / kPages;
+        uint32_t valid = 0;
+#pragma unroll
+        for (int i = 0; i < kPages; ++i) valid |= pid[i] >= 0 ? 1u << i : 0u;
+        valid_s[st] = valid;
+        mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(__popc(valid)) * per_page);
+#pragma unroll
+        for (int i = 0; i < kPages; i += 2) {
+          uint8_t* dst = sm + C::kOffStages + st * C::kStageBytes + i * per_page;
+          // two adjacent pages go in one 128-row box (kmap2), the others one page each
+          if (pid[i] >= 0 && pid[i + 1] == pid[i] + 1) {
+            tma_load_2d(dst, &kmap2, &full[st], 0, pid[i] * kTcPage);
+          } else {
+            if (pid[i] >= 0) tma_load_2d(dst, &kmap, &full[st], 0, pid[i] * kTcPage);
+            if (pid[i + 1] >= 0) tma_load_2d(dst + per_page, &kmap, &full[st], 0, pid[i + 1] * kTcPage);
+          }
         }
       }
       if constexpr (kMx4) {
-        // key 32 c + lane of the tile: word c of the lane's 16 bytes
+        // key 32 c + lane of a part: word c of the lane's 16 bytes
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int32_t pid = c < 2 ? pid0 : pid1;
-          if (pid >= 0)
-            cp_async4(smem_u32(scale_s + st * kTcKeys) + lane * 16 + c * 4,
+        for (int i = 0; i < 4 * kSub; ++i) {
+          const int32_t page = pid[i >> 1];
+          if (page >= 0)
+            cp_async4(smem_u32(scale_s + st * kTile + (i >> 2) * kTcKeys) + lane * 16 + (i & 3) * 4,
                       static_cast<const uint8_t*>(p.a.k_scale) +
-                          (static_cast<int64_t>(pid) * kTcPage + (c & 1) * 32 + lane) * 4);
+                          (static_cast<int64_t>(page) * kTcPage + (i & 1) * 32 + lane) * 4);
         }
         cp_async_mbar_arrive(&full[st]);
       } else if (p.a.k_scale != nullptr) {
         // lanes 0-15: the 64 scales of the first page, lanes 16-31: the second (16 B each)
         const int half = lane >> 4;
-        const int32_t pid = half ? pid1 : pid0;
-        if (pid >= 0)
+        const int32_t page = half ? pid[1] : pid[0];
+        if (page >= 0)
           cp_async16(smem_u32(scale_s + st * kTcKeys + half * kTcPage + (lane & 15) * 4),
                      static_cast<const uint8_t*>(p.a.k_scale) +
-                         (static_cast<int64_t>(pid) * kTcPage + (lane & 15) * 4) * 4);
+                         (static_cast<int64_t>(page) * kTcPage + (lane & 15) * 4) * 4);
         cp_async_mbar_arrive(&full[st]);
       }
       ++issued;
@@ -602,7 +616,7 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
     // own MMAs on it are done), so no warp can release a buffer's next group
     // before that group's Q has landed.
     const int mw = warp - kMmaWarp;
-    TileWalker<G> w;
+    TileWalker<G, kTile> w;
     w.init(p, g_start, kt_start);
     int cur_g = -1, qcount = 0, qb = 0;
     for (int it = 0; it < ntiles; ++it, w.advance(p)) {
@@ -632,29 +646,34 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
       bool ok = mbar_wait(&full[st], (it / kTcStages) & 1, &g_status_indexer, abort_flag, kWaitLimitNs, kSleepNs);
       if (!__all_sync(0xffffffffu, ok)) break;
       if constexpr (kMx4) {
-        const uint32_t ksc = tmem + C::kKeyScaleCol + (G == 1 ? it % NB : it & 3) * 4;
         const uint32_t qsc = tmem + C::kQScaleCol + (mw * 2 + qb) * C::kQScaleCols;
-        const uint64_t dka = make_sdesc(smem_u32(sm + C::kOffStages + st * C::kStageBytes), 16, 512, kLayoutSw64);
         const uint64_t dqb = make_sdesc(smem_u32(sm + C::kOffQ + qb * C::kQBytes), 16, 512, kLayoutSw64);
-        const uint64_t dks = make_sdesc(smem_u32(sm + C::kOffScale + st * kTcKeys * 4), 0, 128, kLayoutNone);
         fence_proxy_async_smem();   // the scale words were written by cp.async
-        for (int j = 0; j < G; ++j) {
-          const int u = it * G + j, slot = u % NB;
-          if (u >= NB) {
-            ok = mbar_wait(&accempty[slot], ((u / NB) - 1) & 1, &g_status_indexer, abort_flag, kWaitLimitNs, kSleepNs);
-            if (!__all_sync(0xffffffffu, ok)) break;
+        for (int h = 0; h < kSub && ok; ++h) {
+          const int su = it * kSub + h;   // part
+          const uint32_t ksc = tmem + C::kKeyScaleCol + (su % C::kKeyScales) * 4;
+          const uint64_t dka =
+              make_sdesc(smem_u32(sm + C::kOffStages + st * C::kStageBytes + h * kTcKeys * C::kRowBytes), 16, 512, kLayoutSw64);
+          const uint64_t dks = make_sdesc(smem_u32(sm + C::kOffScale + (st * kTile + h * kTcKeys) * 4), 0, 128, kLayoutNone);
+          for (int j = 0; j < G; ++j) {
+            const int u = su * G + j, slot = u % NB;
+            if (u >= NB) {
+              ok = mbar_wait(&accempty[slot], ((u / NB) - 1) & 1, &g_status_indexer, abort_flag, kWaitLimitNs, kSleepNs);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+            }
+            tc_fence_after();
+            if (elect_one()) {
+              if (j == 0) tmem_copy_scales(ksc, dks);
+              const uint64_t db = dqb + static_cast<uint64_t>(j * (kTcHeads * C::kRowBytes / 16));
+              const uint32_t d = tmem + slot * C::kAccCols;
+              umma_mxf4(d, dka, db, C::idesc_mxf4(0), ksc, qsc + 2 * j, 0u);
+              umma_mxf4(d, dka + 2, db + 2, C::idesc_mxf4(1), ksc, qsc + 2 * j, 1u);
+              if (h == kSub - 1 && j == G - 1) umma_commit(&empty[st]);
+              umma_commit(&accfull[slot]);
+            }
+            __syncwarp();
           }
-          tc_fence_after();
-          if (elect_one()) {
-            if (j == 0) tmem_copy_scales(ksc, dks);
-            const uint64_t db = dqb + static_cast<uint64_t>(j * (kTcHeads * C::kRowBytes / 16));
-            const uint32_t d = tmem + slot * C::kAccCols;
-            umma_mxf4(d, dka, db, C::idesc_mxf4(0), ksc, qsc + 2 * j, 0u);
-            umma_mxf4(d, dka + 2, db + 2, C::idesc_mxf4(1), ksc, qsc + 2 * j, 1u);
-            if (j == G - 1) umma_commit(&empty[st]);
-            umma_commit(&accfull[slot]);
-          }
-          __syncwarp();
         }
         if (!__all_sync(0xffffffffu, ok)) break;
         continue;
@@ -703,7 +722,7 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     float* wq = wq_s + e * C::kSlice;
     float* cq = wq + kTcHeads;   // MXFP8: the query's block factors [4][64]
-    TileWalker<G> w;
+    TileWalker<G, kTile> w;
     w.init(p, g_start, kt_start);
     int cur_g = -1, qp = -1;
     float* srow = p.a.scores;   // this warp's query's score row
@@ -766,28 +785,35 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
         cur_g = w.g;
         if (w.g + 1 < p.n_groups) prefetch(w.g + 1);
       }
-      const int au = kMx4 ? it * G + j : it;   // the accumulator's number
+      uint32_t vmask = 0;
+      bool ok = true;
+#pragma unroll 1
+      for (int h = 0; h < kSub; ++h) {
+      const int au = kMx4 ? (it * kSub + h) * G + j : it;   // the accumulator's number
       const int ab = au % NB;
-      bool ok = mbar_wait(&accfull[ab], (au / NB) & 1, &g_status_indexer, abort_flag, kWaitLimitNs, kSleepNs);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      ok = mbar_wait(&accfull[ab], (au / NB) & 1, &g_status_indexer, abort_flag, kWaitLimitNs, kSleepNs);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
       tc_fence_after();
       // the stage (keys, scales, page validity) is still this tile's: the
       // producer refills it only after this warp's arrival on empty[st]
       const int st = it % kTcStages;
-      ok = mbar_wait(&full[st], (it / kTcStages) & 1, &g_status_indexer, abort_flag, kWaitLimitNs, kSleepNs);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      const int s = w.kt * kTcKeys + row;
-      uint32_t vmask;
-      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vmask) : "r"(valid_addr + st * 4) : "memory");
-      const bool key_ok = s < w.nhist && ((vmask >> (row >> 6)) & 1u);
       float sk = 1.f;
       uint32_t ek = 0;   // MXFP8: this key's four E8M0 bytes
-      if (kMx)
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(ek) : "r"(scale_addr + st * (kTcKeys * 4)) : "memory");
-      else if (!kMx4 && p.a.k_scale)
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sk) : "r"(scale_addr + st * (kTcKeys * 4)) : "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
+      if (h == 0) {
+        ok = mbar_wait(&full[st], (it / kTcStages) & 1, &g_status_indexer, abort_flag, kWaitLimitNs, kSleepNs);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vmask) : "r"(valid_addr + st * 4) : "memory");
+        if (kMx)
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(ek) : "r"(scale_addr + st * (kTcKeys * 4)) : "memory");
+        else if (!kMx4 && p.a.k_scale)
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sk) : "r"(scale_addr + st * (kTcKeys * 4)) : "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[st]);
+      }
+      const int s = w.kt * kTile + h * kTcKeys + row;
+      const bool key_ok = s < w.nhist && ((vmask >> (2 * h + (row >> 6))) & 1u);
       const float4* w4 = reinterpret_cast<const float4*>(wq);
       float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       if constexpr (kMx) {
@@ -873,6 +899,8 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
       } else {
         if (key_ok && s <= qp) srow[s] = sum * sk;
       }
+      }
+      if (!ok) break;
     }
   }
 
@@ -917,7 +945,7 @@ cudaError_t launch_tc(const SeqArgs& seq, const IndexerArgs& a, const LaunchEnv&
   }
   TcParams p{seq, a, (seq.T + G - 1) / G, 0, nullptr};
   const int64_t tiles_ub =
-      static_cast<int64_t>(p.n_groups) * ((seq.max_ctx + kTcKeys - 1) / kTcKeys);
+      static_cast<int64_t>(p.n_groups) * ((seq.max_ctx + C::kTile - 1) / C::kTile);
   const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(tiles_ub, env.num_sms)));
   const cudaError_t attr_err =
       ensure_smem_limit(reinterpret_cast<const void*>(indexer_tc_kernel<G, kKind, false>), C::kSmemBytes, env.device);
@@ -948,7 +976,7 @@ int fused_cluster(const SeqArgs& seq, const LaunchEnv& env, int max_cl) {
   // every cluster of the launch resident at once is not required, but a cluster
   // of this size must fit on the GPU
   using C = TcCfg<1, kKind>;
-  const int keys = (((seq.max_ctx + kTcKeys - 1) / kTcKeys + cl - 1) / cl) * kTcKeys;
+  const int keys = (((seq.max_ctx + C::kTile - 1) / C::kTile + cl - 1) / cl) * C::kTile;
   const size_t smem = static_cast<size_t>(C::kOffKeys) + static_cast<size_t>(keys) * 4 + 1024;
   void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, TcParams) = indexer_tc_kernel<1, kKind, true>;
   if (ensure_smem_limit(reinterpret_cast<const void*>(kern),
@@ -971,7 +999,7 @@ cudaError_t launch_fused(const SeqArgs& seq, const IndexerArgs& a, int32_t K, in
     return cudaSuccess;
   }
   TcParams p{seq, a, seq.T, K, idx};
-  const int keys = (((seq.max_ctx + kTcKeys - 1) / kTcKeys + cl - 1) / cl) * kTcKeys;
+  const int keys = (((seq.max_ctx + C::kTile - 1) / C::kTile + cl - 1) / cl) * C::kTile;
   const size_t smem = static_cast<size_t>(C::kOffKeys) + static_cast<size_t>(keys) * 4 + 1024;
   const cudaError_t le = launch_kernel(indexer_tc_kernel<1, kKind, true>, dim3(seq.T * cl), dim3(TcWarps<1, kKind>::kThreads),
                                        smem, env.stream, true, cl, kmap, kmap2, qmap, p);
