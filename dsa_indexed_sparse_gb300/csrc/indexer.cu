@@ -654,7 +654,8 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
           const uint32_t ksc = tmem + C::kKeyScaleCol + (su % C::kKeyScales) * 4;
           const uint64_t dka =
               make_sdesc(smem_u32(sm + C::kOffStages + st * C::kStageBytes + h * kTcKeys * C::kRowBytes), 16, 512, kLayoutSw64);
-          const uint64_t dks = make_sdesc(smem_u32(sm + C::kOffScale + (st * kTile + h * kTcKeys) * 4), 0, 128, kLayoutNone);
+          const uint64_t dks =
+              make_sdesc(smem_u32(sm + C::kOffScale + (st * kTile + h * kTcKeys) * 4), 0, 128, kLayoutNone);
           for (int j = 0; j < G; ++j) {
             const int u = su * G + j, slot = u % NB;
             if (u >= NB) {
@@ -788,117 +789,117 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
       uint32_t vmask = 0;
       bool ok = true;
 #pragma unroll 1
-      for (int h = 0; h < kSub; ++h) {
-      const int au = kMx4 ? (it * kSub + h) * G + j : it;   // the accumulator's number
-      const int ab = au % NB;
-      ok = mbar_wait(&accfull[ab], (au / NB) & 1, &g_status_indexer, abort_flag, kWaitLimitNs, kSleepNs);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      // the stage (keys, scales, page validity) is still this tile's: the
-      // producer refills it only after this warp's arrival on empty[st]
-      const int st = it % kTcStages;
-      float sk = 1.f;
-      uint32_t ek = 0;   // MXFP8: this key's four E8M0 bytes
-      if (h == 0) {
-        ok = mbar_wait(&full[st], (it / kTcStages) & 1, &g_status_indexer, abort_flag, kWaitLimitNs, kSleepNs);
+      for (int h = 0; h < kSub; ++h) {   // the tile's parts
+        const int au = kMx4 ? (it * kSub + h) * G + j : it;   // the accumulator's number
+        const int ab = au % NB;
+        ok = mbar_wait(&accfull[ab], (au / NB) & 1, &g_status_indexer, abort_flag, kWaitLimitNs, kSleepNs);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vmask) : "r"(valid_addr + st * 4) : "memory");
-        if (kMx)
-          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(ek) : "r"(scale_addr + st * (kTcKeys * 4)) : "memory");
-        else if (!kMx4 && p.a.k_scale)
-          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sk) : "r"(scale_addr + st * (kTcKeys * 4)) : "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[st]);
-      }
-      const int s = w.kt * kTile + h * kTcKeys + row;
-      const bool key_ok = s < w.nhist && ((vmask >> (2 * h + (row >> 6))) & 1u);
-      const float4* w4 = reinterpret_cast<const float4*>(wq);
-      float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if constexpr (kMx) {
-        // d[h] = sum_b D_b[h] * 2^(eq_b[h] - 127) * 2^(ek_b - 127), 32 heads at a time
-        const uint32_t col = tmem + lane_off + ab * C::kAccCols;
-        float kx[C::kBlocks];
+        tc_fence_after();
+        // the stage (keys, scales, page validity) is still this tile's: the
+        // producer refills it only after this warp's arrival on empty[st]
+        const int st = it % kTcStages;
+        float sk = 1.f;
+        uint32_t ek = 0;   // MXFP8: this key's four E8M0 bytes
+        if (h == 0) {
+          ok = mbar_wait(&full[st], (it / kTcStages) & 1, &g_status_indexer, abort_flag, kWaitLimitNs, kSleepNs);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vmask) : "r"(valid_addr + st * 4) : "memory");
+          if (kMx)
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(ek) : "r"(scale_addr + st * (kTcKeys * 4)) : "memory");
+          else if (!kMx4 && p.a.k_scale)
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sk) : "r"(scale_addr + st * (kTcKeys * 4)) : "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&empty[st]);
+        }
+        const int s = w.kt * kTile + h * kTcKeys + row;
+        const bool key_ok = s < w.nhist && ((vmask >> (2 * h + (row >> 6))) & 1u);
+        const float4* w4 = reinterpret_cast<const float4*>(wq);
+        float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if constexpr (kMx) {
+          // d[h] = sum_b D_b[h] * 2^(eq_b[h] - 127) * 2^(ek_b - 127), 32 heads at a time
+          const uint32_t col = tmem + lane_off + ab * C::kAccCols;
+          float kx[C::kBlocks];
 #pragma unroll
-        for (int bk = 0; bk < C::kBlocks; ++bk) kx[bk] = ldexpf(1.f, static_cast<int>((ek >> (8 * bk)) & 0xFFu) - 127);
+          for (int bk = 0; bk < C::kBlocks; ++bk) kx[bk] = ldexpf(1.f, static_cast<int>((ek >> (8 * bk)) & 0xFFu) - 127);
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          float d[32];
+          for (int hh = 0; hh < 2; ++hh) {
+            float d[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) d[i] = 0.f;
+            for (int i = 0; i < 32; ++i) d[i] = 0.f;
 #pragma unroll
-          for (int bk = 0; bk < C::kBlocks; ++bk) {
-            uint32_t v[32];
-            tmem_ld32(col + bk * C::N + 32 * hh, v);
-            tmem_ld_wait();
-            if (hh == 1 && bk == C::kBlocks - 1) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&accempty[ab]);   // the accumulators are in registers
+            for (int bk = 0; bk < C::kBlocks; ++bk) {
+              uint32_t v[32];
+              tmem_ld32(col + bk * C::N + 32 * hh, v);
+              tmem_ld_wait();
+              if (hh == 1 && bk == C::kBlocks - 1) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&accempty[ab]);   // the accumulators are in registers
+              }
+              // packed over head pairs: f = query factor * key factor, d += D * f
+              const float4* c4 = reinterpret_cast<const float4*>(cq + bk * kTcHeads + 32 * hh);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 cv = c4[i];
+                float f0, f1, f2, f3;
+                mul2(f0, f1, cv.x, cv.y, kx[bk], kx[bk]);
+                mul2(f2, f3, cv.z, cv.w, kx[bk], kx[bk]);
+                fma2(d[4 * i], d[4 * i + 1], __uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), f0, f1);
+                fma2(d[4 * i + 2], d[4 * i + 3], __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]), f2, f3);
+              }
             }
-            // packed over head pairs: f = query factor * key factor, d += D * f
-            const float4* c4 = reinterpret_cast<const float4*>(cq + bk * kTcHeads + 32 * hh);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const float4 cv = c4[i];
-              float f0, f1, f2, f3;
-              mul2(f0, f1, cv.x, cv.y, kx[bk], kx[bk]);
-              mul2(f2, f3, cv.z, cv.w, kx[bk], kx[bk]);
-              fma2(d[4 * i], d[4 * i + 1], __uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), f0, f1);
-              fma2(d[4 * i + 2], d[4 * i + 3], __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]), f2, f3);
+              const float4 wv = w4[8 * hh + i];
+              const int a = 4 * (i & 1);
+              fma2(acc[a], acc[a + 1], wv.x, wv.y, d[4 * i] + fabsf(d[4 * i]), d[4 * i + 1] + fabsf(d[4 * i + 1]));
+              fma2(acc[a + 2], acc[a + 3], wv.z, wv.w, d[4 * i + 2] + fabsf(d[4 * i + 2]),
+                   d[4 * i + 3] + fabsf(d[4 * i + 3]));
             }
           }
+        } else {
+          // the 64 heads in two halves of 32 columns (fewer live registers: 18 warps
+          // leave 96 a thread); head weights as 16-byte broadcast loads
+          const uint32_t col = tmem + lane_off + ab * C::kAccCols + (kMx4 ? 0 : j * kTcHeads);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 wv = w4[8 * hh + i];
-            const int a = 4 * (i & 1);
-            fma2(acc[a], acc[a + 1], wv.x, wv.y, d[4 * i] + fabsf(d[4 * i]), d[4 * i + 1] + fabsf(d[4 * i + 1]));
-            fma2(acc[a + 2], acc[a + 3], wv.z, wv.w, d[4 * i + 2] + fabsf(d[4 * i + 2]),
-                 d[4 * i + 3] + fabsf(d[4 * i + 3]));
-          }
-        }
-      } else {
-        // the 64 heads in two halves of 32 columns (fewer live registers: 18 warps
-        // leave 96 a thread); head weights as 16-byte broadcast loads
-        const uint32_t col = tmem + lane_off + ab * C::kAccCols + (kMx4 ? 0 : j * kTcHeads);
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          uint32_t v[32];
-          tmem_ld32(col + 32 * hh, v);
-          tmem_ld_wait();
-          if (hh == 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&accempty[ab]);   // the accumulator is in registers
-          }
-          // x + |x| per head, then packed fmas over head pairs: eight running sums
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 wv = w4[8 * hh + i];
-            const int a = 4 * (i & 1);
-            float y[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float x = __uint_as_float(v[4 * i + k]);
-              y[k] = x + fabsf(x);
+          for (int hh = 0; hh < 2; ++hh) {
+            uint32_t v[32];
+            tmem_ld32(col + 32 * hh, v);
+            tmem_ld_wait();
+            if (hh == 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&accempty[ab]);   // the accumulator is in registers
             }
-            fma2(acc[a], acc[a + 1], wv.x, wv.y, y[0], y[1]);
-            fma2(acc[a + 2], acc[a + 3], wv.z, wv.w, y[2], y[3]);
+            // x + |x| per head, then packed fmas over head pairs: eight running sums
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 wv = w4[8 * hh + i];
+              const int a = 4 * (i & 1);
+              float y[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float x = __uint_as_float(v[4 * i + k]);
+                y[k] = x + fabsf(x);
+              }
+              fma2(acc[a], acc[a + 1], wv.x, wv.y, y[0], y[1]);
+              fma2(acc[a + 2], acc[a + 3], wv.z, wv.w, y[2], y[3]);
+            }
           }
         }
-      }
-      const float sum = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
-      if constexpr (kFused) {
-        // a key on a bad page (flagged above) gets the lowest key of all
-        if (s <= qp) {
-          const uint32_t k = key_ok ? order_key(sum * sk) : 0u;
-          keys_s[s - f_lo] = k;
-          select_count0(sel, k);
+        const float sum = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
+        if constexpr (kFused) {
+          // a key on a bad page (flagged above) gets the lowest key of all
+          if (s <= qp) {
+            const uint32_t k = key_ok ? order_key(sum * sk) : 0u;
+            keys_s[s - f_lo] = k;
+            select_count0(sel, k);
+          }
+        } else {
+          if (key_ok && s <= qp) srow[s] = sum * sk;
         }
-      } else {
-        if (key_ok && s <= qp) srow[s] = sum * sk;
-      }
       }
       if (!ok) break;
     }
