@@ -10,7 +10,8 @@
 // (this card's measured rates: 289), so for one query a block HBM and the tensor cores are
 // about even, and where queries share rows the tensor cores.  The rows of a block lie one after
 // the other in the cache: a 64 x 64 box of a tensor map is an operand atom as the tensor cores
-// read it, so what attn.cu's producer warps gather row by row two threads ask the TMA for, and
+// read it, so what attn.cu's producer warps gather row by row a thread asks the TMA for, several
+// atoms a request (a request takes its warp 0.05 us, so one atom each paced the loads), and
 // nothing but the softmax is left for warps to do.
 //
 // As in attn_e2m1.cu the two CTAs of a cluster split the heads (64 each) and issue pair MMAs
@@ -20,7 +21,8 @@
 // block 1 at another, each its own value dims: rank 0 (block 0, dims [0, 256)) has them in X
 // and lets the TMA put block 1's over Y, dead once Q K^T is complete, rank 1 (block 1, dims
 // [256, 512)) has them in Y and takes block 0's over X.  P of block 0 goes into R, dead as well, P
-// of block 1 into a buffer of its own.  36 + 16 MMAs a tile: 1152 + 1024 clocks.
+// of block 1 into a buffer of its own.  P V leaves atoms 0, 1, 4 and 5 first, and the loads of the
+// tile after next begin there.  36 + 16 MMAs a tile: 1152 + 1024 clocks.
 //   shared memory: Q 72 KB | stage 0, 72 KB | stage 1 | P of block 1, 8 KB | maxima, barriers
 //   TMEM: logits [0,64) [64,128), O [256,512).  An N-wide accumulator of a pair MMA takes N/2
 //   columns: lanes 0-63 are the CTA's heads for the first half of N, lanes 64-127 for the second.
@@ -41,8 +43,17 @@
 //
 // Warps.  0 finds the items' blocks (entries 32 at a time, those that select something moved
 // together) and loads own blocks; 1 loads the other block's values and the queries; 2 issues Q
-// K^T, 3 P V (rank 0 for both CTAs; those of rank 1 pass on that its copies have landed); the rest
-// are softmax and output.
+// K^T, 3 P V (rank 0 for both CTAs).  What both CTAs load for an MMA is counted on a barrier of the
+// leader's (passing on an arrival took 500 clocks of a tile's 3200).  4-19 are softmax and output, a
+// thread 16 logits (with eight warps the chain was 300 clocks a tile longer).
+//
+// Measured (32 blocks a query, 128 heads): 775 us for a chunk of 2048 queries, 1500 TFLOP/s of the
+// 1926 measured (86 % of what the card holds over seconds: clocks fall to 1.8 GHz); 37.5 us for 64
+// queries, 10.2 for one (16 slices and their merge).  A tile takes 2900 clocks in the middle of a chunk
+// where its MMAs need 2176: shared memory moves 360 KB for it (240 for operands, 104 from the TMA, 16
+// of P), 2880 clocks of its 128 bytes a clock.  64 queries read their 151 MB at 6 TB/s once under way
+// (8 us are launch, dependent loads and output); asking the L2 for blocks two tiles ahead takes 38 us,
+// one tile 38, three 41, six 47, not asking 41.5.
 #include <cuda.h>
 
 #include <algorithm>
@@ -742,13 +753,18 @@ int resident_clusters(int num_sms) {
   return n;
 }
 
-// Slices per query: a cluster for each while the GPU holds them all at once, a slice at least
-// one tile.
+// Slices per query: a cluster for each while the GPU holds them all at once, a slice at least one
+// tile, or two where more than 32 slices would hold one each: their merge costs what it saves.
+// Measured with other numbers of slices (us, 32 blocks a query, this rule's first): 1 query 16 slices
+// 10.2, 8 11.0, 1 29.4; 4 queries 8 slices 11.7, 16 13.2, 4 14.1; 16 queries 4 slices 21.0, 2 23.8, 8
+// 24.0; 38 queries 2 slices 31.2, 1 34.4, 3 38.7; 40 queries 1 slice 34.5, 2 45.8; 64 queries 1 slice
+// 37.3, 2 48.3; 80 queries 1 slice 55.1, 2 63.4; 1 query of 128 blocks 32 slices 11.9, 64 15.3, 16 14.4.
 int choose_split(const SeqArgs& seq, const MlaArgs& a, int num_sms) {
-  const int tiles = (a.K + 1) / 2;
-  const int64_t clusters = static_cast<int64_t>(seq.T) * ((a.H + 127) / 128);
-  return static_cast<int>(
-      std::max<int64_t>(1, std::min<int64_t>(tiles, resident_clusters(num_sms) / std::max<int64_t>(1, clusters))));
+  const int64_t tiles = (a.K + 1) / 2;
+  const int64_t clusters = std::max<int64_t>(1, static_cast<int64_t>(seq.T) * ((a.H + 127) / 128));
+  const int64_t held = std::max<int64_t>(1, resident_clusters(num_sms) / clusters);
+  if (tiles <= held && clusters * tiles > 32) return static_cast<int>((tiles + 1) / 2);
+  return static_cast<int>(std::min(tiles, held));
 }
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
