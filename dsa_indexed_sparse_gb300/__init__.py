@@ -184,13 +184,13 @@ def _dtype_code(t: torch.Tensor) -> int:
     raise ValueError(f"unsupported dtype {t.dtype}")
 
 
-def _flat(t: torch.Tensor, name: str, dev: int) -> int:
-    """Data pointer of a contiguous tensor on GPU dev."""
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on the current CUDA device, not on {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+def _flat(dev: int, *tensors: torch.Tensor) -> None:
+    """Refuses tensors that are not contiguous or not on GPU dev."""
+    for t in tensors:
+        if t.get_device() != dev:
+            raise ValueError(f"the tensors of a call must be on the current CUDA device, not on {t.device}")
+        if not t.is_contiguous():
+            raise ValueError("tensors passed to libdsa must be contiguous")
 
 
 def _cache_ptr(t: torch.Tensor, name: str, dev: int) -> int:
@@ -474,7 +474,8 @@ def _codes_check(dtype: int, D: int, rows: int, codes: torch.Tensor, scale: Opti
 def _dense(t: torch.Tensor, name: str, dev: int, dtype: torch.dtype, shape) -> int:
     if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} {list(shape)}")
-    return _flat(t, name, dev)
+    _flat(dev, t)
+    return t.data_ptr()
 
 
 def _outputs(s: SeqDesc, m: MlaDesc, out: torch.Tensor, lse: Optional[torch.Tensor], dev: int):
@@ -487,7 +488,8 @@ def _outputs(s: SeqDesc, m: MlaDesc, out: torch.Tensor, lse: Optional[torch.Tens
 def _scratch(workspace: Optional[torch.Tensor], dev: int):
     if workspace is None:
         return None, 0
-    return _flat(workspace, "workspace", dev), workspace.numel() * workspace.element_size()
+    _flat(dev, workspace)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def block_topk(seq: Seq, scores: torch.Tensor, n_blocks: int, out: torch.Tensor, first: int = 1, last: int = 1,
@@ -500,8 +502,11 @@ def block_topk(seq: Seq, scores: torch.Tensor, n_blocks: int, out: torch.Tensor,
     if len(shape) != 2 or scores.dtype != torch.float32 or shape[0] != T:
         raise ValueError("scores must be float32 [T, ld]")
     dev = _on_current(seq)
-    _check(_lib.dsa_block_topk(ctypes.byref(s), _flat(scores, "scores", dev), shape[1], n_blocks, first, last,
-                               _dense(out, "out", dev, torch.int32, (T, n_blocks)), _stream(stream, dev)))
+    if out.dtype != torch.int32 or out.shape != (T, n_blocks):
+        raise ValueError("out must be int32 [T, n_blocks]")
+    _flat(dev, scores, out)
+    _check(_lib.dsa_block_topk(ctypes.byref(s), scores.data_ptr(), shape[1], n_blocks, first, last, out.data_ptr(),
+                               _stream(stream, dev)))
     return out
 
 
@@ -561,9 +566,9 @@ def index_cache_append(seq: Seq, k_new: torch.Tensor, k_cache: torch.Tensor, k_s
         D = shape[1]
         _codes_check(dtype, D, s.cache_rows, k_cache, k_scale, "k_cache, k_scale")
         dev = _on_current(seq)
-        _check(_lib.dsa_index_cache_append_mx4(ctypes.byref(s), D, src, _flat(k_new, "k_new", dev),
-                                               _flat(k_cache, "k_cache", dev), _flat(k_scale, "k_scale", dev),
-                                               _stream(stream, dev)))
+        _flat(dev, k_new, k_cache, k_scale)
+        _check(_lib.dsa_index_cache_append_mx4(ctypes.byref(s), D, src, k_new.data_ptr(), k_cache.data_ptr(),
+                                               k_scale.data_ptr(), _stream(stream, dev)))
         return
     if dtype not in (None, DSA_E4M3, DSA_MXFP8_E4M3):
         raise ValueError("dtype must be DSA_E4M3, DSA_MXFP8_E4M3 or DSA_MXFP4_E2M1")
@@ -591,8 +596,9 @@ def index_query_quantize(q: torch.Tensor, codes: torch.Tensor, scale: torch.Tens
     dev = q.get_device()
     if dev < 0 or dev != _current_device():
         raise ValueError("q must be on the current CUDA device")
-    _check(_lib.dsa_index_query_quantize(T, H, D, src, dtype, q.data_ptr(), st, sh, _flat(codes, "codes", dev),
-                                         _flat(scale, "scale", dev), _stream(stream, dev)))
+    _flat(dev, codes, scale)
+    _check(_lib.dsa_index_query_quantize(T, H, D, src, dtype, q.data_ptr(), st, sh, codes.data_ptr(), scale.data_ptr(),
+                                         _stream(stream, dev)))
 
 
 def index_cache_read(seq: Seq, k_cache: torch.Tensor, k_scale: Optional[torch.Tensor], out: torch.Tensor,
@@ -611,9 +617,13 @@ def index_cache_read(seq: Seq, k_cache: torch.Tensor, k_scale: Optional[torch.Te
     dev = _on_current(seq)
     if out.get_device() != dev:
         raise ValueError("out must be on the current CUDA device")
-    _check(_lib.dsa_index_cache_read(ctypes.byref(s), D, dtype, _flat(k_cache, "k_cache", dev),
-                                     None if k_scale is None else _flat(k_scale, "k_scale", dev), kind, out.data_ptr(),
-                                     stride, _stream(stream, dev)))
+    _flat(dev, k_cache)
+    scale = None
+    if k_scale is not None:
+        _flat(dev, k_scale)
+        scale = k_scale.data_ptr()
+    _check(_lib.dsa_index_cache_read(ctypes.byref(s), D, dtype, k_cache.data_ptr(), scale, kind, out.data_ptr(), stride,
+                                     _stream(stream, dev)))
     return out
 
 

@@ -11,7 +11,7 @@
 // about even, and where queries share rows the tensor cores.  The rows of a block lie one after
 // the other in the cache: a 64 x 64 box of a tensor map is an operand atom as the tensor cores
 // read it, so what attn.cu's producer warps gather row by row a thread asks the TMA for, several
-// atoms a request (a request takes its warp 0.05 us, so one atom each paced the loads), and
+// atoms a request (with one atom each the requests paced the loads: a chunk 800 us, 780), and
 // nothing but the softmax is left for warps to do.
 //
 // As in attn_e2m1.cu the two CTAs of a cluster split the heads (64 each) and issue pair MMAs
@@ -44,8 +44,7 @@
 // Warps.  0 finds the items' blocks (entries 32 at a time, those that select something moved
 // together) and loads own blocks; 1 loads the other block's values and the queries; 2 issues Q
 // K^T, 3 P V (rank 0 for both CTAs).  What both CTAs load for an MMA is counted on a barrier of the
-// leader's (passing on an arrival took 500 clocks of a tile's 3200).  4-19 are softmax and output, a
-// thread 16 logits (with eight warps the chain was 300 clocks a tile longer).
+// leader's (passing on an arrival took 500 clocks).  4-19 are softmax and output, a thread 16 logits.
 //
 // Measured (32 blocks a query, 128 heads): 775 us for a chunk of 2048 queries, 1500 TFLOP/s of the
 // 1926 measured (86 % of what the card holds over seconds: clocks fall to 1.8 GHz); 37.5 us for 64
