@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) block_topk_kernel(BlockTopkArg
     qp = -1;   // no block: all -1
   }
   const int n_tok = qp + 1, N = a.N;
-  const int n = kPage64 ? (n_tok + 63) >> 6 : (n_tok + a.page_size - 1) / a.page_size;
+  const int n = kPage64 ? (n_tok + 63) >> 6 : (n_tok > 0 ? qp / a.page_size + 1 : 0);
   int32_t* out = a.out + static_cast<int64_t>(t) * N;
   if (n <= N) {   // cluster-uniform
     for (int i = rank * nt + tid; i < N; i += CL * nt) out[i] = i < n ? i : -1;
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) block_topk_kernel(BlockTopkArg
   } else {
     for (int blk = lo + warp; blk < hi; blk += nt >> 5) {
       float best = -INFINITY;
-      const int end = min(n_tok, (blk + 1) * a.page_size);
+      const int end = blk == n - 1 ? n_tok : (blk + 1) * a.page_size;
       for (int pos = blk * a.page_size + lane; pos < end; pos += 32) best = fmaxf(best, __ldg(row + pos));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));

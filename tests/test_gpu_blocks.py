@@ -195,6 +195,33 @@ def test_nan_and_infinity_of_selected_rows(dev):
     assert not bool(torch.isnan(clean[0]).any())
 
 
+@pytest.mark.parametrize("workspace", [True, False])
+def test_nan_of_a_query_head_stays_with_it(dev, workspace):
+    s = Blocks(dev, [640, 200], per=1)
+    idx = s.choose(9)
+    s.q[0, 17, 5] = float("nan")
+    s.q[1, 127, 575] = float("inf")              # logits of both signs' infinity
+    out, lse = s.run(idx, workspace)
+    dsa.check_status()
+    assert bool(torch.isnan(out[0, 17]).all()) and bool(torch.isnan(lse[0, 17]))
+    assert bool(torch.isnan(out[1, 127]).all()) and bool(torch.isnan(lse[1, 127]))
+    s.q[0, 17, 5] = s.q[1, 127, 575] = 0.0
+    clean = s.run(idx, workspace)
+    s.check(clean, idx)
+    out[0, 17], out[1, 127], lse[0, 17], lse[1, 127] = clean[0][0, 17], clean[0][1, 127], clean[1][0, 17], clean[1][1, 127]
+    assert torch.equal(out, clean[0]) and torch.equal(lse, clean[1])
+
+
+def test_the_same_call_gives_the_same_bits(dev):
+    s = Blocks(dev, [5000, 3000, 2000], per=4, seed=12)
+    idx = s.choose(31, 0.1)
+    a = s.run(idx)
+    for _ in range(3):
+        b = s.run(idx)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    dsa.check_status()
+
+
 def test_bad_blocks_and_pages_are_flagged_and_skipped(dev):
     s = Blocks(dev, [640, 300], per=1)
     idx = torch.tensor([[0, 10, 3, 9], [2, 4, 1, 5]], dtype=torch.int32, device=dev)   # 10, 5: behind the position
@@ -388,6 +415,37 @@ def test_block_topk(dev, lens, per, page, N, first, last, kind):
     dsa.block_topk(seq, x.to(dev), N, out, first=first, last=last)
     dsa.check_status()
     assert np.array_equal(out.cpu().numpy(), _choice(x.numpy(), q_pos.numpy(), page, N, first, last))
+
+
+def test_block_topk_captured_and_on_two_streams(dev):
+    g = torch.Generator().manual_seed(7)
+    q_pos = torch.tensor([20000, 9000, 63, 64], dtype=torch.int32)
+    seq = dsa.Seq(q_seq=torch.zeros(4, dtype=torch.int32, device=dev), q_pos=q_pos.to(dev),
+                  block_table=torch.zeros((1, 313), dtype=torch.int32, device=dev), max_ctx=20001, cache_rows=64)
+    xs = [torch.randn((4, 20004), generator=g).to(dev) for _ in range(2)]
+    outs = [torch.full((4, 12), -7, dtype=torch.int32, device=dev) for _ in range(2)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        for x, o, st in zip(xs, outs, streams):
+            with torch.cuda.stream(st):
+                dsa.block_topk(seq, x, 12, o, first=2, last=1)
+    torch.cuda.synchronize()
+    for x, o in zip(xs, outs):
+        assert np.array_equal(o.cpu().numpy(), _choice(x.cpu().numpy(), q_pos.numpy(), 64, 12, 2, 1))
+    with torch.cuda.stream(streams[0]):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=streams[0]):
+            for x, o in zip(xs, outs):
+                dsa.block_topk(seq, x, 12, o, first=2, last=1)
+        for x in xs:
+            x.copy_(torch.randn(x.shape, generator=g))
+        graph.replay()
+    torch.cuda.synchronize()
+    dsa.check_status()
+    for x, o in zip(xs, outs):
+        assert np.array_equal(o.cpu().numpy(), _choice(x.cpu().numpy(), q_pos.numpy(), 64, 12, 2, 1))
 
 
 def test_block_topk_bad_position(dev):

@@ -305,6 +305,23 @@ def test_scores_of_far_exponents(dev):
     s.check(got)
 
 
+def test_scores_on_two_streams_are_the_same_bits(dev):
+    a, b = Scores(dev, [9000, 4100], 4, seed=1), Scores(dev, [20000], 1, seed=2)
+    want = a.run(), b.run()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(5):
+        for s, st in ((a, streams[0]), (b, streams[1])):
+            with torch.cuda.stream(st):
+                got.append(s.run())
+    torch.cuda.synchronize()
+    dsa.check_status()
+    for i, g in enumerate(got):
+        assert torch.equal(g, want[i % 2])
+
+
 def test_scores_bad_page_is_flagged(dev):
     s = Scores(dev, [300], 4)
     s.seq.block_table[0, 1] = -1
@@ -343,6 +360,11 @@ def test_decode_step(dev, lens, fused):
     dsa.sparse_mla_attn(s.seq, mla, idx, K, o2, workspace=ws)
     dsa.check_status()
     assert torch.equal(out, o2)
+    if ws.numel() <= dsa.STATIC_WORKSPACE_BYTES:   # the step with the library's own scratch
+        o2.fill_(7)
+        dsa.decode_step_static_ws(s.seq, s.idx, mla, K, o2, idx_out=idx.fill_(-7))
+        dsa.check_status()
+        assert torch.equal(out, o2) and torch.equal(sel, idx)
 
 
 def test_append_quantise_score_captured(dev):
