@@ -144,8 +144,9 @@ template <int G, IndexKind kKind = IndexKind::kE4M3>
 struct TcWarps {
   static constexpr int kRot = G == 1 ? (kKind == IndexKind::kMx8 ? 2 : 3) : 1;
   static constexpr int kProd = 2;                  // divides kTcStages
-  // four MXFP4 queries have MMAs and commits of their own: one warp 2048 queries x 8192 keys 200 us, two 143
-  static constexpr int kMmaWarps = G == 1 || kKind == IndexKind::kMx4 ? 2 : 1;
+  // four MXFP4 queries go in two pairs, each issued by a warp of its own in every tile
+  static constexpr bool kByPair = kKind == IndexKind::kMx4 && G > 1;
+  static constexpr int kMmaWarps = G == 1 || kByPair ? 2 : 1;
   static constexpr int kMma = kProd;               // the first MMA-issuing warp (also allocates TMEM)
   static constexpr int kEpi0 = kProd + kMmaWarps;  // first epilogue warp
   static constexpr int kEpiWarps = 4 * G * kRot;
@@ -161,16 +162,31 @@ struct TcWarps {
 // block's products by both powers of two itself: one accumulator, two MMAs (K = 64
 // each).  Its scales lie in TMEM, a word per key and per query head, brought there by
 // tcgen05.cp from shared memory.  With four queries a group, two accumulators of all
-// 256 columns would leave no room for them, so every query has MMAs (N = 64) and
-// accumulators of its own: a ring of seven 64-column slots, slot (part * G + query) % 7,
-// parts of 128 keys counted through the tiles.
+// 256 columns would leave no room for them, so each pair of queries has MMAs (N = 128)
+// and accumulators of its own, in a ring of three slots of 128 columns that the pairs
+// take in turn, part of 128 keys after part: unit v = 2 part + pair in slot v % 3.
+// Issuing warp i issues pair i.
+//
+// A wait by parity passes at once where the barrier is two phases behind the one meant,
+// so whoever waits has to know that the phase before is over.  A slot goes to and fro
+// between the pairs, each with a warp of its own, so every use of a slot has the other
+// of two sets of barriers than the use before: what a barrier counts is then always one
+// pair's.  The epilogue of unit v waits for a phase whose predecessor is unit v - 6, its
+// own; the issuing warp of v for the release of v - 3, whose predecessor v - 9 it waited
+// for before it issued v - 6.
+// (2048 queries x 8192 keys: one warp for both pairs 137 us, a warp each 134; slots of
+// 64 columns for single queries, seven for warps that take the tiles in turn 133, three
+// for each of two warps 144.)
 template <int G, IndexKind kKind = IndexKind::kE4M3>
 struct TcCfg {
   static constexpr bool kMx = kKind == IndexKind::kMx8, kMx4 = kKind == IndexKind::kMx4;
   static_assert(!kMx || G == 1, "MXFP8 keys run one query per group");
   static constexpr int N = kTcHeads * G;                 // UMMA N (kMx4: of all of the tile's MMAs)
   static constexpr int kBlocks = kMx ? kTcDim / 32 : 1;  // accumulators per tile
-  static constexpr int kAccCols = kMx4 ? kTcHeads : kBlocks * N;   // TMEM columns per tile (kMx4: per slot)
+  static constexpr bool kByPair = TcWarps<G, kKind>::kByPair;
+  static constexpr int kPairs = kByPair ? G / 2 : 1;     // an MMA's share of a group is all of it, or a pair of queries
+  static constexpr int kMmaN = N / kPairs;
+  static constexpr int kAccCols = kBlocks * kMmaN;       // TMEM columns per tile (kMx4: per slot)
   static constexpr int kRowBytes = kMx4 ? kTcDim / 2 : kTcDim;     // codes of a key or query head
   // keys per tile, what goes from role to role at a time: 16 KB of codes.  The roles' pace is a chain of
   // issue steps a tile, so half the bytes a key make twice the keys a tile, in kSub parts of 128 (with one:
@@ -181,16 +197,17 @@ struct TcCfg {
   static constexpr int kStageBytes = kTile * kRowBytes;
   static constexpr int kQBytes = N * kRowBytes;          // one query-group buffer
   // accumulator buffers: two, or one per rotation group (and part); or the slots
-  static constexpr int kAccBufs = kMx4 && G > 1 ? 7 : kSub * (TcWarps<G, kKind>::kRot > 2 ? TcWarps<G, kKind>::kRot : 2);
+  static constexpr int kAccSets = kByPair ? 2 : 1;       // sets of their barriers (above)
+  static constexpr int kAccBufs = kByPair ? 3 : kSub * (TcWarps<G, kKind>::kRot > 2 ? TcWarps<G, kKind>::kRot : 2);
+  static constexpr int kAccBars = kAccSets * kAccBufs;
   // kMx4, behind the accumulators: the keys' scale words, four columns a part.  As many parts as there
-  // are accumulators, whose being free says that the MMAs before are complete; or, of the slots, eight:
-  // an issuing warp's last wait for a tile's slots says that its own first MMAs of that tile are
-  // complete, and so is all that it issued for the tiles before.  Then the heads', two columns a query,
-  // for each issuing warp and query-group buffer (four for a single query: a copy writes four).
+  // are accumulators, whose being free says that the MMAs before are complete; or four for each issuing
+  // warp: its unit v is issued when v - 3 is released, which was issued when its own v - 6, three parts
+  // back, was.  Then the heads', four columns a query or pair, for each issuing warp and query-group buffer.
   static constexpr int kKeyScaleCol = kAccBufs * kAccCols;
-  static constexpr int kKeyScales = G == 1 ? kAccBufs : 8;
-  static constexpr int kQScaleCols = kMx4 ? (G > 1 ? 2 * G : 4) : 0;
-  static constexpr int kQScaleCol = kKeyScaleCol + 4 * kKeyScales;
+  static constexpr int kKeyScales = kByPair ? 4 : kAccBufs;
+  static constexpr int kQScaleCols = kMx4 ? 4 : 0;
+  static constexpr int kQScaleCol = kKeyScaleCol + 4 * kKeyScales * (kByPair ? TcWarps<G, kKind>::kMmaWarps : 1);
   static constexpr int kTmemNeed =
       kMx4 ? kQScaleCol + 2 * TcWarps<G, kKind>::kMmaWarps * kQScaleCols : kAccBufs * kAccCols;
   static_assert(kTmemNeed <= 512, "TMEM plan");
@@ -205,13 +222,13 @@ struct TcCfg {
   // (kMx4: as tcgen05.cp takes them, 16 bytes for keys i, i + 32, i + 64, i + 96 of a part)
   static constexpr int kOffScale = kOffWq + TcWarps<G, kKind>::kEpiWarps * kSlice * 4;
   // kMx4: the query heads' scale words, 16 bytes for heads i, i + 32 of two queries
-  static constexpr int kQScaleBytes = kQScaleCols * 128;
+  static constexpr int kQScaleBytes = kMx4 ? 512 * kPairs : 0;
   static constexpr int kOffQScale = kOffScale + kTcStages * kTile * 4;
   static_assert(kOffScale % 128 == 0 && kOffQScale % 128 == 0, "scale words as MMA operands");
   static constexpr int kOffValid = kOffQScale + 2 * kQScaleBytes;  // uint32 [stages]
   static constexpr int kOffBar = kOffValid + kTcStages * 4 + 8;
   // barriers: full[S], empty[S], qfull[2], qempty[2], accfull[A], accempty[A], drain
-  static constexpr int kNumBars = 2 * kTcStages + 4 + 2 * kAccBufs + 1;
+  static constexpr int kNumBars = 2 * kTcStages + 4 + 2 * kAccBars + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;  // tmem base, abort, sched[2], red[one per warp]
   static constexpr int kSmemBytes = kOffMisc + 256 + 1024;  // + alignment slack
   // fused decode plan: the selection's scratch, then this CTA's keys (read 16
@@ -220,7 +237,7 @@ struct TcCfg {
   static constexpr int kOffKeys = (kOffSel + static_cast<int>(sizeof(SelectSmem)) + 127) / 128 * 128;
   static_assert(kOffKeys % 16 == 0 && kOffSel % 16 == 0, "aligned fused-plan regions");
   static constexpr uint32_t kIdesc = make_idesc(kFmtE4M3, kFmtE4M3, false, false, kTcKeys, N);
-  static constexpr uint32_t idesc_mxf4(int half) { return make_idesc_mxf4(kTcKeys, kTcHeads, half ? 2 : 0); }
+  static constexpr uint32_t idesc_mxf4(int half) { return make_idesc_mxf4(kTcKeys, kMmaN, half ? 2 : 0); }
 };
 
 // Keys of one query a CTA of the fused plan holds in shared memory at most.
@@ -328,8 +345,8 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
   uint64_t* qfull = bars + 2 * kTcStages;
   uint64_t* qempty = qfull + 2;
   uint64_t* accfull = qfull + 4;
-  uint64_t* accempty = accfull + NB;
-  uint64_t* drain = accempty + NB;   // every MMA of the issuing warp complete (teardown)
+  uint64_t* accempty = accfull + C::kAccBars;
+  uint64_t* drain = accempty + C::kAccBars;   // every MMA of the issuing warp complete (teardown)
   uint32_t* misc = reinterpret_cast<uint32_t*>(sm + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
   int* sched = reinterpret_cast<int*>(misc + 2);   // g0, kt0
@@ -423,17 +440,17 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
     const uint32_t full_count = 1u + (p.a.k_scale != nullptr ? 32u : 0u);
     for (int i = 0; i < kTcStages; ++i) {
       mbar_init(&full[i], full_count);
-      // freed by the MMA (keys read) and by each epilogue warp of the tile's
+      // freed by the MMAs (keys read) and by each epilogue warp of the tile's
       // group (key scales read)
-      mbar_init(&empty[i], 1 + kGroupWarps);
+      mbar_init(&empty[i], (C::kByPair ? kMmaWarps : 1) + kGroupWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&qfull[i], kMx4 ? 33 : 1);   // kMx4: and a lane's copies of scale words
       mbar_init(&qempty[i], kMmaWarps);   // each issuing warp releases a group's Q
     }
-    for (int i = 0; i < NB; ++i) {
+    for (int i = 0; i < C::kAccBars; ++i) {
       mbar_init(&accfull[i], 1);
-      mbar_init(&accempty[i], kMx4 ? 4 : kGroupWarps);   // kMx4: a slot is one query's
+      mbar_init(&accempty[i], kGroupWarps / C::kPairs);
     }
     mbar_init(drain, kMmaWarps);
     *abort_flag = 0;
@@ -611,14 +628,24 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
       if ((q_mine >> (k & 1)) & 1u) mbar_drain(&qfull[k & 1], (k >> 1) & 1, &g_status_indexer);
   } else if (warp < kMmaWarp + kMmaWarps) {
     // ------------------------------------------------ MMA issuers (whole warps, an elected lane issues)
-    // Issuing warp mw takes the tiles it with it % kMmaWarps == mw.  Every issuing
-    // warp waits for each group's Q and releases it (its commit arrives once its
-    // own MMAs on it are done), so no warp can release a buffer's next group
-    // before that group's Q has landed.
+    // Issuing warp mw takes the tiles it with it % kMmaWarps == mw (kByPair: its pair of
+    // queries in every tile).  Every issuing warp waits for each group's Q and releases
+    // it (its commit arrives once its own MMAs on it are done), so no warp can release a
+    // buffer's next group before that group's Q has landed.
     const int mw = warp - kMmaWarp;
     TileWalker<G, kTile> w;
     w.init(p, g_start, kt_start);
     int cur_g = -1, qcount = 0, qb = 0;
+    // kMx4: the next unit's place in the ring of barriers and its phase, the next part's
+    // scale columns (counted on, and the step's loop unrolled: a step costs this warp, which
+    // shares its issue slots with the epilogue, far more than the tensor cores; 147.7 us
+    // where 137.6), descriptors of the first stage and query buffer
+    int ring = C::kByPair ? mw : mw * kSub, kscale = C::kByPair ? 0 : mw * kSub;
+    uint32_t ring_par = 0;
+    const uint64_t dka0 = make_sdesc(smem_u32(sm + C::kOffStages), 16, 512, kLayoutSw64);
+    const uint64_t dks0 = make_sdesc(smem_u32(sm + C::kOffScale), 0, 128, kLayoutNone);
+    const uint64_t dq0 =
+        make_sdesc(smem_u32(sm + C::kOffQ + (C::kByPair ? mw * C::kMmaN * C::kRowBytes : 0)), 16, 512, kLayoutSw64);
     for (int it = 0; it < ntiles; ++it, w.advance(p)) {
       if (w.g != cur_g) {
         if (qcount > 0) {
@@ -630,53 +657,58 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
         if (!__all_sync(0xffffffffu, ok)) break;
         if constexpr (kMx4) {
           fence_proxy_async_smem();   // the scale words were written by cp.async
-          if (elect_one()) {
-            const uint64_t ds = make_sdesc(smem_u32(sm + C::kOffQScale + qb * C::kQScaleBytes), 0, 128, kLayoutNone);
-#pragma unroll
-            for (int i = 0; i < C::kQScaleCols / 4; ++i)
-              tmem_copy_scales(tmem + C::kQScaleCol + (mw * 2 + qb) * C::kQScaleCols + 4 * i, ds + 32 * i);
-          }
+          if (elect_one())
+            tmem_copy_scales(tmem + C::kQScaleCol + (mw * 2 + qb) * C::kQScaleCols,
+                             make_sdesc(smem_u32(sm + C::kOffQScale + qb * C::kQScaleBytes) + (C::kByPair ? mw * 512 : 0),
+                                        0, 128, kLayoutNone));
           __syncwarp();
         }
         cur_g = w.g;
         ++qcount;
       }
-      if (kMmaWarps > 1 && it % kMmaWarps != mw) continue;
+      if (kMmaWarps > 1 && !C::kByPair && it % kMmaWarps != mw) continue;
       const int st = it % kTcStages;
       bool ok = mbar_wait(&full[st], (it / kTcStages) & 1, &g_status_indexer, abort_flag, kWaitLimitNs, kSleepNs);
       if (!__all_sync(0xffffffffu, ok)) break;
       if constexpr (kMx4) {
-        const uint32_t qsc = tmem + C::kQScaleCol + (mw * 2 + qb) * C::kQScaleCols;
-        const uint64_t dqb = make_sdesc(smem_u32(sm + C::kOffQ + qb * C::kQBytes), 16, 512, kLayoutSw64);
+        constexpr int kBars = C::kAccBars;
         fence_proxy_async_smem();   // the scale words were written by cp.async
-        for (int h = 0; h < kSub && ok; ++h) {
-          const int su = it * kSub + h;   // part
-          const uint32_t ksc = tmem + C::kKeyScaleCol + (su % C::kKeyScales) * 4;
-          const uint64_t dka =
-              make_sdesc(smem_u32(sm + C::kOffStages + st * C::kStageBytes + h * kTcKeys * C::kRowBytes), 16, 512, kLayoutSw64);
-          const uint64_t dks =
-              make_sdesc(smem_u32(sm + C::kOffScale + (st * kTile + h * kTcKeys) * 4), 0, 128, kLayoutNone);
-          for (int j = 0; j < G; ++j) {
-            const int u = su * G + j, slot = u % NB;
-            if (u >= NB) {
-              ok = mbar_wait(&accempty[slot], ((u / NB) - 1) & 1, &g_status_indexer, abort_flag, kWaitLimitNs, kSleepNs);
-              ok = __all_sync(0xffffffffu, ok);
-              if (!ok) break;
-            }
+        const uint64_t dka = dka0 + static_cast<uint64_t>(st * (C::kStageBytes / 16));
+        const uint64_t dks = dks0 + static_cast<uint64_t>(st * (kTile * 4 / 16));
+        const uint64_t db = dq0 + static_cast<uint64_t>(qb * (C::kQBytes / 16));
+        const uint32_t qsc = tmem + C::kQScaleCol + (mw * 2 + qb) * C::kQScaleCols;
+#pragma unroll
+        for (int h = 0; h < kSub; ++h) {   // the tile's parts
+          const int slot = ring >= NB ? ring - NB : ring;
+          // the use before: the other set's barrier of the slot, or the phase before
+          const int before = C::kAccSets == 1 || ring >= NB ? slot : slot + NB;
+          const uint32_t before_par = C::kAccSets > 1 && ring >= NB ? ring_par : ring_par ^ 1u;
+          ok = ok && mbar_wait(&accempty[before], before_par, &g_status_indexer, abort_flag, kWaitLimitNs, kSleepNs);
+          if (__all_sync(0xffffffffu, ok)) {
             tc_fence_after();
             if (elect_one()) {
-              if (j == 0) tmem_copy_scales(ksc, dks);
-              const uint64_t db = dqb + static_cast<uint64_t>(j * (kTcHeads * C::kRowBytes / 16));
               const uint32_t d = tmem + slot * C::kAccCols;
-              umma_mxf4(d, dka, db, C::idesc_mxf4(0), ksc, qsc + 2 * j, 0u);
-              umma_mxf4(d, dka + 2, db + 2, C::idesc_mxf4(1), ksc, qsc + 2 * j, 1u);
-              if (h == kSub - 1 && j == G - 1) umma_commit(&empty[st]);
-              umma_commit(&accfull[slot]);
+              const uint32_t ksc = tmem + C::kKeyScaleCol + ((C::kByPair ? mw * C::kKeyScales : 0) + kscale) * 4;
+              const uint64_t da = dka + h * (kTcKeys * C::kRowBytes / 16);
+              tmem_copy_scales(ksc, dks + h * (kTcKeys * 4 / 16));
+              umma_mxf4(d, da, db, C::idesc_mxf4(0), ksc, qsc, 0u);
+              umma_mxf4(d, da + 2, db + 2, C::idesc_mxf4(1), ksc, qsc, 1u);
+              if (h == kSub - 1) umma_commit(&empty[st]);
+              umma_commit(&accfull[ring]);
             }
             __syncwarp();
           }
+          ring += C::kPairs;
+          if (ring >= kBars) ring -= kBars, ring_par ^= 1u;
+          if (++kscale == C::kKeyScales) kscale = 0;
         }
         if (!__all_sync(0xffffffffu, ok)) break;
+        if constexpr (!C::kByPair) {   // the parts of the tile of the other issuing warp
+          ring += kSub;
+          if (ring >= kBars) ring -= kBars, ring_par ^= 1u;
+          kscale += kSub;
+          if (kscale >= C::kKeyScales) kscale -= C::kKeyScales;
+        }
         continue;
       }
       const int ab = it % NB;
@@ -727,6 +759,8 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
     w.init(p, g_start, kt_start);
     int cur_g = -1, qp = -1;
     float* srow = p.a.scores;   // this warp's query's score row
+    int ring = j / 2;   // kByPair: the next unit's place in the ring of barriers, and its phase
+    uint32_t ring_par = 0;
     const uint32_t valid_addr = smem_u32(sm + C::kOffValid);
     const uint32_t scale_addr = smem_u32(sm + C::kOffScale) + row * 4;
     // prefetched group: its first query's sequence, this warp's query's sequence
@@ -790,9 +824,20 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
       bool ok = true;
 #pragma unroll 1
       for (int h = 0; h < kSub; ++h) {   // the tile's parts
-        const int au = kMx4 ? (it * kSub + h) * G + j : it;   // the accumulator's number
-        const int ab = au % NB;
-        ok = mbar_wait(&accfull[ab], (au / NB) & 1, &g_status_indexer, abort_flag, kWaitLimitNs, kSleepNs);
+        int ab, abar;   // the accumulator, its barriers and their phase
+        uint32_t par;
+        if constexpr (C::kByPair) {
+          abar = ring;
+          ab = ring >= NB ? ring - NB : ring;
+          par = ring_par;
+          ring += C::kPairs;
+          if (ring >= C::kAccBars) ring -= C::kAccBars, ring_par ^= 1u;
+        } else {
+          const int au = kMx4 ? it * kSub + h : it;
+          ab = abar = au % NB;
+          par = (au / NB) & 1;
+        }
+        ok = mbar_wait(&accfull[abar], par, &g_status_indexer, abort_flag, kWaitLimitNs, kSleepNs);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -836,7 +881,7 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
               if (hh == 1 && bk == C::kBlocks - 1) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&accempty[ab]);   // the accumulators are in registers
+                if (lane == 0) mbar_arrive(&accempty[abar]);   // the accumulators are in registers
               }
               // packed over head pairs: f = query factor * key factor, d += D * f
               const float4* c4 = reinterpret_cast<const float4*>(cq + bk * kTcHeads + 32 * hh);
@@ -862,7 +907,7 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
         } else {
           // the 64 heads in two halves of 32 columns (fewer live registers: 18 warps
           // leave 96 a thread); head weights as 16-byte broadcast loads
-          const uint32_t col = tmem + lane_off + ab * C::kAccCols + (kMx4 ? 0 : j * kTcHeads);
+          const uint32_t col = tmem + lane_off + ab * C::kAccCols + (j % (G / C::kPairs)) * kTcHeads;
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
             uint32_t v[32];
@@ -871,7 +916,7 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
             if (hh == 1) {
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(&accempty[ab]);   // the accumulator is in registers
+              if (lane == 0) mbar_arrive(&accempty[abar]);   // the accumulator is in registers
             }
             // x + |x| per head, then packed fmas over head pairs: eight running sums
 #pragma unroll

@@ -285,6 +285,62 @@ def test_scores_many_tiles_a_cta(dev):
         s.check(got, ts=[0, s.T // 2, s.T - 1])
 
 
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8", "e4m3"])
+@pytest.mark.parametrize("per", [1, 4])
+def test_scores_of_many_short_histories(dev, fmt, per):
+    """Dozens of query groups a CTA, most of one tile, some of two to nine, in any order: query buffers, stages and
+    accumulators go from warp to warp at every turn.  Five runs, all of the same bits, the first against the formula.
+
+    Tolerance as above, with two roundings more for the weight times the query's scale and one for the key's."""
+    g = torch.Generator().manual_seed(per)
+    B, top, pages = 6000 // per, 1100, 256
+    lens = torch.where(torch.rand(B, generator=g) < 0.7, torch.randint(per, 140, (B,), generator=g),
+                       torch.randint(per, top + 1, (B,), generator=g))
+    lens[0] = top
+    table = torch.randint(0, pages, (B, (top + 63) // 64), generator=g).to(torch.int32)     # pages may be shared
+    T, rows = B * per, pages * 64
+
+    def codes(*n):
+        c = torch.randint(0, 256, (*n, 64 if fmt == "mxfp4" else 128), generator=g).to(torch.uint8)
+        return c if fmt == "mxfp4" else c & 0xF7                   # no NaN code
+    scale = (lambda *n: torch.rand(n, generator=g) + 0.5) if fmt == "e4m3" else \
+        (lambda *n: torch.randint(121, 134, (*n, 4), generator=g).to(torch.uint8))
+    q, qs, k, ks = codes(T, 64), scale(T, 64), codes(rows), scale(rows)
+    w = torch.randn((T, 64), generator=g)
+    pos = (lens[:, None] - per + torch.arange(per)).flatten().to(torch.int32)
+    seq = dsa.Seq(q_seq=torch.arange(B, dtype=torch.int32).repeat_interleave(per).to(dev), q_pos=pos.to(dev),
+                  block_table=table.to(dev), max_ctx=top, cache_rows=rows, q_per_seq=per)
+    idx = dsa.Indexer(q=q.to(dev), w=w.to(dev), k_cache=k.to(dev), q_scale=qs.to(dev), k_scale=ks.to(dev), dtype=FORMATS[fmt])
+    out = [torch.full((T, (top + 3) // 4 * 4), -77.0, device=dev) for _ in range(5)]
+    for o in out:
+        dsa.indexer_scores(seq, idx, o)
+    assert "indexer_tc" in dsa.last_plan()
+    dsa.check_status()
+    for o in out[1:]:
+        assert torch.equal(o, out[0])
+    got = out[0].cpu().numpy()
+    kd = _decode(k.numpy(), ks.numpy(), fmt)
+    for t in range(0, T, 3):
+        n = int(pos[t]) + 1
+        keys = kd[O.physical_rows(table[t // per].numpy(), 64, np.arange(n))]
+        qd, wd = _decode(q[t].numpy(), qs[t].numpy(), fmt), w[t].numpy().astype(np.float64)
+        want, mag = wd @ np.maximum(qd @ keys.T, 0.0), np.abs(wd) @ (np.abs(qd) @ np.abs(keys).T)
+        assert np.all(np.abs(got[t, :n] - want) <= 133 * 2.0 ** -23 * mag), t
+        assert np.all(got[t, n:] == -77.0)
+
+
+def test_scores_of_largest_products(dev):
+    """The largest dot products of either sign, which the ReLU keeps or takes to 0 whole, with weights of either sign."""
+    s = Scores(dev, [130, 64], 4, seed=9)
+    s.idx.q.fill_(0x77)                                            # 6
+    sign = torch.randint(0, 2, (s.rows, 1), generator=torch.Generator().manual_seed(4)).to(torch.uint8)
+    s.idx.k_cache.copy_((0x77 + 0x88 * sign).expand(-1, 64))       # all 6 or all -6
+    s.q, s.k = s.idx.q.cpu(), s.idx.k_cache.cpu()
+    got = s.run()
+    dsa.check_status()
+    s.check(got)
+
+
 @pytest.mark.parametrize("H, D, page", [(4, 32, 64), (64, 64, 64), (64, 128, 16), (3, 256, 64)])
 def test_scores_other_dims(dev, H, D, page):
     s = Scores(dev, [100, 37], 3, H=H, D=D, page=page)
