@@ -200,6 +200,11 @@ struct TcCfg {
   static constexpr int kAccSets = kByPair ? 2 : 1;       // sets of their barriers (above)
   static constexpr int kAccBufs = kByPair ? 3 : kSub * (TcWarps<G, kKind>::kRot > 2 ? TcWarps<G, kKind>::kRot : 2);
   static constexpr int kAccBars = kAccSets * kAccBufs;
+  // A slot whose rotation group's tiles are issued by either issuing warp: what the stage's release
+  // says covers the accumulators too, so that a tile's issuer, who waited for its keys, knows that
+  // the tile six before, which was the slot's last but one, has left it.
+  static constexpr bool kLateFree = !kByPair && TcWarps<G, kKind>::kRot % TcWarps<G, kKind>::kMmaWarps != 0;
+  static_assert(!kLateFree || 2 * TcWarps<G, kKind>::kRot == kTcStages, "the last use but one lay in the same stage");
   // kMx4, behind the accumulators: the keys' scale words, four columns a part.  As many parts as there
   // are accumulators, whose being free says that the MMAs before are complete; or four for each issuing
   // warp: its unit v is issued when v - 3 is released, which was issued when its own v - 6, three parts
@@ -856,7 +861,7 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
           else if (!kMx4 && p.a.k_scale)
             asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sk) : "r"(scale_addr + st * (kTcKeys * 4)) : "memory");
           __syncwarp();
-          if (lane == 0) mbar_arrive(&empty[st]);
+          if (!C::kLateFree && lane == 0) mbar_arrive(&empty[st]);
         }
         const int s = w.kt * kTile + h * kTcKeys + row;
         const bool key_ok = s < w.nhist && ((vmask >> (2 * h + (row >> 6))) & 1u);
@@ -917,6 +922,7 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive(&accempty[abar]);   // the accumulator is in registers
+              if (C::kLateFree && h == kSub - 1 && lane == 0) mbar_arrive(&empty[st]);
             }
             // x + |x| per head, then packed fmas over head pairs: eight running sums
 #pragma unroll
