@@ -174,8 +174,8 @@ struct TcWarps {
 // pair's.  The epilogue of unit v waits for a phase whose predecessor is unit v - 6, its
 // own; the issuing warp of v for the release of v - 3, whose predecessor v - 9 it waited
 // for before it issued v - 6.
-// (2048 queries x 8192 keys: one warp for both pairs 137 us, a warp each 134; slots of
-// 64 columns for single queries, seven for warps that take the tiles in turn 133, three
+// (2048 queries x 8192 keys: one warp for both pairs 137 us, a warp each 128; slots of
+// 64 columns for single queries, seven for warps that take the tiles in turn 132, three
 // for each of two warps 144.)
 template <int G, IndexKind kKind = IndexKind::kE4M3>
 struct TcCfg {
@@ -809,11 +809,12 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
           qp = -1;
         }
         // the previous group's tiles are done: this warp alone reads its slice.
-        // Half weights: w * ReLU(x) = (w / 2) * (x + |x|) exactly (the halving and
-        // doubling are exact), and x + |x| runs on the FMA pipe instead of a
-        // max on the half-rate ALU pipe.
-        wq[2 * lane] = 0.5f * (pf_w0 * pf_s0);
-        wq[2 * lane + 1] = 0.5f * (pf_w1 * pf_s1);
+        // MXFP8: half weights, w * ReLU(x) = (w / 2) * (x + |x|) exactly (the halving and
+        // doubling are exact), where x + |x| runs on the FMA pipe and a max on the
+        // half-rate ALU pipe.  The others have the FMA pipe's time to spare and take the max
+        // (2048 queries x 8192 keys: E4M3 145.1 us with x + |x|, 141.4; MXFP4 135, 130).
+        wq[2 * lane] = (kMx ? 0.5f : 1.f) * (pf_w0 * pf_s0);
+        wq[2 * lane + 1] = (kMx ? 0.5f : 1.f) * (pf_w1 * pf_s1);
         if (kMx) {
 #pragma unroll
           for (int bk = 0; bk < C::kBlocks; ++bk) {
@@ -924,17 +925,15 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
               if (lane == 0) mbar_arrive(&accempty[abar]);   // the accumulator is in registers
               if (C::kLateFree && h == kSub - 1 && lane == 0) mbar_arrive(&empty[st]);
             }
-            // x + |x| per head, then packed fmas over head pairs: eight running sums
+            // the ReLU (a NaN stays one), then packed fmas over head pairs: eight running sums
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float4 wv = w4[8 * hh + i];
               const int a = 4 * (i & 1);
               float y[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float x = __uint_as_float(v[4 * i + k]);
-                y[k] = x + fabsf(x);
-              }
+              for (int k = 0; k < 4; ++k)
+                asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y[k]) : "f"(__uint_as_float(v[4 * i + k])));
               fma2(acc[a], acc[a + 1], wv.x, wv.y, y[0], y[1]);
               fma2(acc[a + 2], acc[a + 3], wv.z, wv.w, y[2], y[3]);
             }
