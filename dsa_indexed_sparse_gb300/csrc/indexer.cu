@@ -505,8 +505,11 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
     // of the stages st with st % kProd == pw).  It keeps the page ids of its next
     // 16 tiles in registers (lane l: tile l / 2, page l % 2, loaded in parallel);
     // lane 0 issues the TMA tile loads, every lane one 16-byte copy of key
-    // scales.  A query group's own TMA load goes with the producer of the
-    // group's first tile in this CTA.
+    // scales.  The TMA loads into query buffer pw go with producer pw too,
+    // whichever of them has the group's first tile, so that a buffer's releases are
+    // waited for one by one: a producer that had not waited for the last but one
+    // could take it for the last.
+    static_assert(kProd == 2, "a producer for each of the two query buffers");
     const int pw = warp;
     TileWalker<G, kTile> w;
     w.init(p, g_start, kt_start);
@@ -519,12 +522,10 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
     uint32_t* valid_s = reinterpret_cast<uint32_t*>(sm + C::kOffValid);
     float* scale_s = reinterpret_cast<float*>(sm + C::kOffScale);
     int issued = 0, last_it = -1;   // tiles whose copies this warp issued, the last of them
-    uint32_t q_mine = 0;   // bit b: the last Q load into buffer b was issued by this warp
     for (int it = 0; it < ntiles; ++it, w.advance(p)) {
       if (w.g != cur_g) {
         const int qb = qcount & 1;
-        const bool mine = it % kProd == pw;
-        if (mine) {
+        if (qb == pw) {
           if (qcount >= 2) {
             const bool ok = mbar_wait(&qempty[qb], ((qcount >> 1) - 1) & 1, &g_status_indexer, abort_flag,
                                       kWaitLimitNs, kSleepNs);
@@ -547,7 +548,6 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
             cp_async_mbar_arrive(&qfull[qb]);
           }
         }
-        q_mine = mine ? (q_mine | (1u << qb)) : (q_mine & ~(1u << qb));
         const int b = w.g == pre_g ? pre_b : __ldg(p.seq.q_seq + w.g * G);
         b_ok = (b >= 0 && b < p.seq.B);
         bt = p.seq.block_table + static_cast<int64_t>(b_ok ? b : 0) * p.seq.bt_stride;
@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
       mbar_drain(&full[k % kTcStages], (k / kTcStages) & 1, &g_status_indexer);
     }
     for (int k = max(0, qcount - 2); k < qcount; ++k)
-      if ((q_mine >> (k & 1)) & 1u) mbar_drain(&qfull[k & 1], (k >> 1) & 1, &g_status_indexer);
+      if ((k & 1) == pw) mbar_drain(&qfull[k & 1], (k >> 1) & 1, &g_status_indexer);
   } else if (warp < kMmaWarp + kMmaWarps) {
     // ------------------------------------------------ MMA issuers (whole warps, an elected lane issues)
     // Issuing warp mw takes the tiles it with it % kMmaWarps == mw (kByPair: its pair of
