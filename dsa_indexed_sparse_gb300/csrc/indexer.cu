@@ -174,9 +174,13 @@ struct TcWarps {
 // pair's.  The epilogue of unit v waits for a phase whose predecessor is unit v - 6, its
 // own; the issuing warp of v for the release of v - 3, whose predecessor v - 9 it waited
 // for before it issued v - 6.
-// (2048 queries x 8192 keys: one warp for both pairs 137 us, a warp each 128; slots of
-// 64 columns for single queries, seven for warps that take the tiles in turn 132, three
-// for each of two warps 144.)
+// (2048 queries x 8192 keys, in one state of the rest: one warp for both pairs 137 us, a
+// warp each 128; slots of 64 columns for single queries, seven for warps that take the
+// tiles in turn 132, three for each of two warps 144.)
+//
+// What paces it then is the instructions of the head sums' warps, whose issue slots the
+// issuing warps share: parts unrolled, ring and stage counted on, one vote for two waits
+// and sums joined in pairs took 128 us to 116.
 template <int G, IndexKind kKind = IndexKind::kE4M3>
 struct TcCfg {
   static constexpr bool kMx = kKind == IndexKind::kMx8, kMx4 = kKind == IndexKind::kMx4;
@@ -689,7 +693,8 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
           const int before = C::kAccSets == 1 || ring >= NB ? slot : slot + NB;
           const uint32_t before_par = C::kAccSets > 1 && ring >= NB ? ring_par : ring_par ^ 1u;
           ok = ok && mbar_wait(&accempty[before], before_par, &g_status_indexer, abort_flag, kWaitLimitNs, kSleepNs);
-          if (__all_sync(0xffffffffu, ok)) {
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok) {
             tc_fence_after();
             if (elect_one()) {
               const uint32_t d = tmem + slot * C::kAccCols;
@@ -707,7 +712,7 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
           if (ring >= kBars) ring -= kBars, ring_par ^= 1u;
           if (++kscale == C::kKeyScales) kscale = 0;
         }
-        if (!__all_sync(0xffffffffu, ok)) break;
+        if (!ok) break;
         if constexpr (!C::kByPair) {   // the parts of the tile of the other issuing warp
           ring += kSub;
           if (ring >= kBars) ring -= kBars, ring_par ^= 1u;
@@ -764,8 +769,9 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
     w.init(p, g_start, kt_start);
     int cur_g = -1, qp = -1;
     float* srow = p.a.scores;   // this warp's query's score row
-    int ring = j / 2;   // kByPair: the next unit's place in the ring of barriers, and its phase
-    uint32_t ring_par = 0;
+    // kByPair: the next unit's place in the ring of barriers, the next tile's stage, and their phases
+    int ring = j / 2, st_next = 0;
+    uint32_t ring_par = 0, st_next_par = 0;
     const uint32_t valid_addr = smem_u32(sm + C::kOffValid);
     const uint32_t scale_addr = smem_u32(sm + C::kOffScale) + row * 4;
     // prefetched group: its first query's sequence, this warp's query's sequence
@@ -828,7 +834,10 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
       }
       uint32_t vmask = 0;
       bool ok = true;
-#pragma unroll 1
+      const int st = C::kByPair ? st_next : it % kTcStages;
+      const uint32_t st_par = C::kByPair ? st_next_par : (it / kTcStages) & 1;
+      if (++st_next == kTcStages) st_next = 0, st_next_par ^= 1u;
+#pragma unroll
       for (int h = 0; h < kSub; ++h) {   // the tile's parts
         int ab, abar;   // the accumulator, its barriers and their phase
         uint32_t par;
@@ -844,18 +853,15 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
           par = (au / NB) & 1;
         }
         ok = mbar_wait(&accfull[abar], par, &g_status_indexer, abort_flag, kWaitLimitNs, kSleepNs);
+        // the stage (keys, scales, page validity) is still this tile's: the
+        // producer refills it only after this warp's arrival on empty[st]
+        if (h == 0) ok = ok && mbar_wait(&full[st], st_par, &g_status_indexer, abort_flag, kWaitLimitNs, kSleepNs);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        // the stage (keys, scales, page validity) is still this tile's: the
-        // producer refills it only after this warp's arrival on empty[st]
-        const int st = it % kTcStages;
         float sk = 1.f;
         uint32_t ek = 0;   // MXFP8: this key's four E8M0 bytes
         if (h == 0) {
-          ok = mbar_wait(&full[st], (it / kTcStages) & 1, &g_status_indexer, abort_flag, kWaitLimitNs, kSleepNs);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
           asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vmask) : "r"(valid_addr + st * 4) : "memory");
           if (kMx)
             asm volatile("ld.shared.u32 %0, [%1];" : "=r"(ek) : "r"(scale_addr + st * (kTcKeys * 4)) : "memory");
@@ -865,7 +871,7 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
           if (!C::kLateFree && lane == 0) mbar_arrive(&empty[st]);
         }
         const int s = w.kt * kTile + h * kTcKeys + row;
-        const bool key_ok = s < w.nhist && ((vmask >> (2 * h + (row >> 6))) & 1u);
+        const bool key_ok = (vmask >> (2 * h + (row >> 6))) & 1u;   // (looked at for positions up to the query's)
         const float4* w4 = reinterpret_cast<const float4*>(wq);
         float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if constexpr (kMx) {
@@ -939,7 +945,15 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
             }
           }
         }
-        const float sum = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
+        float sum;
+        if constexpr (kMx4) {
+          add2(acc[0], acc[1], acc[0], acc[1], acc[4], acc[5]);
+          add2(acc[2], acc[3], acc[2], acc[3], acc[6], acc[7]);
+          add2(acc[0], acc[1], acc[0], acc[1], acc[2], acc[3]);
+          sum = acc[0] + acc[1];
+        } else {
+          sum = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
+        }
         if constexpr (kFused) {
           // a key on a bad page (flagged above) gets the lowest key of all
           if (s <= qp) {
