@@ -168,9 +168,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* sfree = bars + 14;    // [2] leader: logits read, both CTAs
   uint64_t* pvdone = bars + 16;   // [2] P V complete: the tile's stage and P free
   uint64_t* edone = bars + 18;    // [2] an item's output has left the stage of its last tile
-  uint64_t* pfull = bars + 20;    // leader: P written, both CTAs (one buffer: P V of the tile before is complete)
-  uint64_t* qfull = bars + 21;    // leader: an item's query has come, both CTAs
-  uint64_t* drain = bars + 22;    // every MMA complete (teardown)
+  // A pair too: the warps of block 0 write P without waiting for P V of the tile before, so some may
+  // arrive for a tile while others have yet to for the one before it; for the one after it none can,
+  // whose loads wait for this one's P V.
+  uint64_t* pfull = bars + 20;    // [2] leader: P written and rows zeroed, both CTAs
+  uint64_t* qfull = bars + 22;    // leader: an item's query has come, both CTAs
+  uint64_t* drain = bars + 23;    // every MMA complete (teardown)
   uint32_t* misc = reinterpret_cast<uint32_t*>(sm + kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
   const volatile int* info = reinterpret_cast<const volatile int*>(sm + kOffInfo);
@@ -199,8 +202,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sfree[i], 2 * kSoftWarps);
       mbar_init(&pvdone[i], 1);
       mbar_init(&edone[i], kSoftWarps);
+      mbar_init(&pfull[i], 2 * kSoftWarps);
     }
-    mbar_init(pfull, 2 * kSoftWarps);
     mbar_init(qfull, 1);
     mbar_init(drain, 2);
     *abort_flag = 0;
@@ -472,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       const int flags = info[(g & 3) * 4];
       more = !(flags & kEnd);
-      ok = wait(&oth[sb], g >> 1) && wait(pfull, g);
+      ok = wait(&oth[sb], g >> 1) && wait(&pfull[sb], g >> 1);
       if (!ok) break;
       tc_fence_after();
       fence_proxy_async_smem();
@@ -632,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_pair(leader_addr(pfull));
+        if (lane == 0) arrive_pair(leader_addr(&pfull[j & 1]));
       }
       if (stop) break;
       // ---- the output: O / l, log-sum-exp

@@ -222,6 +222,29 @@ def test_the_same_call_gives_the_same_bits(dev):
     dsa.check_status()
 
 
+@pytest.mark.parametrize("group", [0, 1, 2, 3])
+@pytest.mark.parametrize("per, N", [(700, 9), (150, 12), (3, 16)])
+def test_one_group_of_heads_behind_the_others(dev, group, per, N):
+    """Blocks in any order, so that the query's own, whose rows behind the position are zeroed, lies in any tile, and maxima
+    that jump for one group of 32 heads only, which then rescales O: the groups of either CTA pass a tile at different times,
+    and P V has to wait for the last of them.  Five runs of the same bits."""
+    s = Blocks(dev, [64 * 40 - 17], per=per, seed=20 + group)
+    u = torch.randn(D_ROW, generator=s.g, device=dev)
+    heads = slice(32 * group, 32 * group + 32)
+    s.q[:, heads] = (u + 0.5 * s.q[:, heads].float()).to(torch.bfloat16)
+    for i in range(40):                          # logits of these heads: about 5 f
+        row = s.table[0, i].long() * 64 + torch.arange(64, device=dev)
+        s.cache[row] = (s.cache[row].float() + float((i * 17) % 40 - 15) * u / 8).to(torch.bfloat16)
+    idx = s.choose(N, 0.1, order="any")
+    first = s.run(idx)
+    assert "attn_block" in dsa.last_plan()
+    for _ in range(4):
+        again = s.run(idx)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    dsa.check_status()
+    s.check(first, idx, ts=range(0, s.T, max(1, s.T // 40)))
+
+
 def test_bad_blocks_and_pages_are_flagged_and_skipped(dev):
     s = Blocks(dev, [640, 300], per=1)
     idx = torch.tensor([[0, 10, 3, 9], [2, 4, 1, 5]], dtype=torch.int32, device=dev)   # 10, 5: behind the position
