@@ -36,6 +36,13 @@ DSA_DEFINE_STATUS_WORD(indexer)
 namespace dsa {
 namespace {
 
+// max(x, 0); a NaN stays one.
+__device__ __forceinline__ float relu(float x) {
+  float y;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // =============================================================== generic kernel
 constexpr int kGenThreads = 256;
 
@@ -110,7 +117,7 @@ __global__ void __launch_bounds__(kGenThreads)
       for (int i = 0; i < a.D_I; ++i)
         d = fmaf(qf[h * a.D_I + i], ldexpf(code_value(kr, i), static_cast<int>(ke[i / 32]) - 127), d);
     }
-    acc = fmaf(wq[h], fmaxf(d, 0.f), acc);
+    acc = fmaf(wq[h], relu(d), acc);
   }
   const float sk = (!kMx && a.k_scale) ? __ldg(static_cast<const float*>(a.k_scale) + row) : 1.f;
   a.scores[static_cast<int64_t>(t) * a.ld + s] = acc * sk;
@@ -931,15 +938,14 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
               if (lane == 0) mbar_arrive(&accempty[abar]);   // the accumulator is in registers
               if (C::kLateFree && h == kSub - 1 && lane == 0) mbar_arrive(&empty[st]);
             }
-            // the ReLU (a NaN stays one), then packed fmas over head pairs: eight running sums
+            // the ReLU, then packed fmas over head pairs: eight running sums
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float4 wv = w4[8 * hh + i];
               const int a = 4 * (i & 1);
               float y[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y[k]) : "f"(__uint_as_float(v[4 * i + k])));
+              for (int k = 0; k < 4; ++k) y[k] = relu(__uint_as_float(v[4 * i + k]));
               fma2(acc[a], acc[a + 1], wv.x, wv.y, y[0], y[1]);
               fma2(acc[a + 2], acc[a + 3], wv.z, wv.w, y[2], y[3]);
             }
