@@ -457,6 +457,11 @@ __device__ __forceinline__ float bf16_bits_to_float(uint16_t b) {
   return __uint_as_float(static_cast<uint32_t>(b) << 16);
 }
 
+// An E8M0 scale byte: 2^(e - 127); 255 stands for no number.
+__device__ __forceinline__ float e8m0_to_float(uint32_t e) {
+  return __uint_as_float(e == 0u ? 0x00400000u : (e == 255u ? 0x7FC00000u : e << 23));
+}
+
 // Page-table translation: logical position s of the sequence whose table row
 // starts at `bt` -> physical cache row, or -1 (and kDevBadIndex) if the page id
 // is outside [0, n_pages).

@@ -170,11 +170,6 @@ struct IndexReadArgs {
   Divisor per, page;        // by the threads a key, by the page size
 };
 
-// 2^(e - 127); 255 stands for no number.
-__device__ __forceinline__ float e8m0_to_float(uint32_t e) {
-  return __uint_as_float(e == 0u ? 0x00400000u : (e == 255u ? 0x7FC00000u : e << 23));
-}
-
 template <IndexKind kKind, bool kF32Out>
 __global__ void __launch_bounds__(2 * kBlockThreads) index_read_kernel(SeqArgs seq, IndexReadArgs a) {
   grid_dep_wait();

@@ -47,9 +47,9 @@ __device__ __forceinline__ float relu(float x) {
 constexpr int kGenThreads = 256;
 
 // kF32: fp32 values; kE4M3: codes with fp32 per-token / per-head scales; kMx8 and
-// kMx4 (E4M3 or E2M1 codes, E8M0 scale per 32 elements): the query is dequantised
-// into shared memory and each key element is dequantised as it is read; both are
-// exact in fp32.
+// kMx4: E4M3 or E2M1 codes with an E8M0 scale per 32 elements.  Of these the codes of a
+// block are multiplied and summed, and the sum takes both blocks' powers of two at once,
+// as on the tensor cores: either factor alone could leave fp32's range.
 template <IndexKind kKind>
 __global__ void __launch_bounds__(kGenThreads)
     indexer_generic_kernel(SeqArgs seq, IndexerArgs a) {
@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kGenThreads)
   };
   const int row_codes = kKind == IndexKind::kMx4 ? a.D_I / 2 : a.D_I;   // bytes of a vector
   extern __shared__ float sm_gen[];
-  float* qf = sm_gen;                   // [H_I * D_I] query values (codes for kE4M3)
+  float* qf = sm_gen;                   // [H_I * D_I] query values (of codes, without their scales)
   float* wq = sm_gen + a.H_I * a.D_I;  // [H_I] w * q_scale (w for block scales)
   const int t = blockIdx.y;
   const int qpos = __ldg(seq.q_pos + t);
@@ -81,13 +81,7 @@ __global__ void __launch_bounds__(kGenThreads)
       qf[i] = static_cast<const float*>(a.q)[static_cast<int64_t>(t) * HD + i];
     } else {
       const int h = i / a.D_I;
-      float v = code_value(static_cast<const uint8_t*>(a.q) + (static_cast<int64_t>(t) * a.H_I + h) * row_codes, i % a.D_I);
-      if (kMx) {
-        const int blk = (i % a.D_I) / 32;
-        const int e = static_cast<const uint8_t*>(a.q_scale)[(static_cast<int64_t>(t) * a.H_I + h) * nb + blk];
-        v = ldexpf(v, e - 127);
-      }
-      qf[i] = v;
+      qf[i] = code_value(static_cast<const uint8_t*>(a.q) + (static_cast<int64_t>(t) * a.H_I + h) * row_codes, i % a.D_I);
     }
   }
   for (int h = threadIdx.x; h < a.H_I; h += blockDim.x) {
@@ -114,8 +108,13 @@ __global__ void __launch_bounds__(kGenThreads)
     } else {
       const uint8_t* kr = static_cast<const uint8_t*>(a.k) + row * row_codes;
       const uint8_t* ke = static_cast<const uint8_t*>(a.k_scale) + row * nb;
-      for (int i = 0; i < a.D_I; ++i)
-        d = fmaf(qf[h * a.D_I + i], ldexpf(code_value(kr, i), static_cast<int>(ke[i / 32]) - 127), d);
+      const uint8_t* qe = static_cast<const uint8_t*>(a.q_scale) + (static_cast<int64_t>(t) * a.H_I + h) * nb;
+      for (int blk = 0; blk < nb; ++blk) {
+        float part = 0.f;
+        for (int i = 32 * blk; i < 32 * blk + 32; ++i) part = fmaf(qf[h * a.D_I + i], code_value(kr, i), part);
+        const int eq = qe[blk], ek = ke[blk];
+        d += eq == 255 || ek == 255 ? __int_as_float(0x7FC00000) : ldexpf(part, eq + ek - 254);
+      }
     }
     acc = fmaf(wq[h], relu(d), acc);
   }
@@ -831,8 +830,8 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
         if (kMx) {
 #pragma unroll
           for (int bk = 0; bk < C::kBlocks; ++bk) {
-            cq[bk * kTcHeads + 2 * lane] = ldexpf(1.f, static_cast<int>((pf_e0 >> (8 * bk)) & 0xFFu) - 127);
-            cq[bk * kTcHeads + 2 * lane + 1] = ldexpf(1.f, static_cast<int>((pf_e1 >> (8 * bk)) & 0xFFu) - 127);
+            cq[bk * kTcHeads + 2 * lane] = e8m0_to_float((pf_e0 >> (8 * bk)) & 0xFFu);
+            cq[bk * kTcHeads + 2 * lane + 1] = e8m0_to_float((pf_e1 >> (8 * bk)) & 0xFFu);
           }
         }
         __syncwarp();
@@ -886,7 +885,7 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
           const uint32_t col = tmem + lane_off + ab * C::kAccCols;
           float kx[C::kBlocks];
 #pragma unroll
-          for (int bk = 0; bk < C::kBlocks; ++bk) kx[bk] = ldexpf(1.f, static_cast<int>((ek >> (8 * bk)) & 0xFFu) - 127);
+          for (int bk = 0; bk < C::kBlocks; ++bk) kx[bk] = e8m0_to_float((ek >> (8 * bk)) & 0xFFu);
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
             float d[32];

@@ -111,7 +111,8 @@ typedef struct dsa_seq_desc {
  *   DSA_MXFP8_E4M3: q_scale uint8 [T, H_I, D_I/32], k_scale uint8
  *                   [cache_rows, D_I/32]: E8M0 exponents, element i of a vector
  *                   is code * 2**(scale[i / 32] - 127); both required; D_I a
- *                   multiple of 32.  Byte 255 stands for no number.
+ *                   multiple of 32.  Byte 255 stands for no number: the scores of
+ *                   such a key, or query, are NaN, as with a code that is NaN.
  *   DSA_MXFP4_E2M1: q uint8 [T, H_I, D_I/2], k_cache uint8 [cache_rows, D_I/2],
  *                   scales as for DSA_MXFP8_E4M3.
  *   DSA_F32:        q and k_cache hold fp32 values; scales as for DSA_E4M3. */

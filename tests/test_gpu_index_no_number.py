@@ -1,4 +1,4 @@
-"""Index codes and scales that stand for no number: the same scores on every path.
+"""Index codes and scales that stand for no number, and scales far from one another: the same scores on every path.
 
 Tolerance as in test_gpu_index_mx4: 130 2^-23 of sum_h |w_h| sum_i |q_hi k_i| (products of MXFP4 and MXFP8 codes and
 powers of two are exact, 128 and fewer of them are added in fp32, then 64 and fewer weighted heads), with two roundings
@@ -77,6 +77,18 @@ class Case:
 
 
 @pytest.mark.parametrize("H, D, page, per", SHAPES)
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+def test_scale_byte_255_scores_nan(dev, fmt, H, D, page, per):
+    """A block of a key whose scale byte is 255 takes the key's score with it, of a query head all of the query's."""
+    c = Case(dev, fmt, H, D, page, per)
+    for s in (0, 77, 290):
+        c.ks[c.row(s), s % (D // 32)] = 255
+    c.check(c.run(), no_key=(0, 77, 290))
+    c.qs[per - 1, H - 1, D // 32 - 1] = 255
+    c.check(c.run(), no_key=(0, 77, 290), no_query=(per - 1,))
+
+
+@pytest.mark.parametrize("H, D, page, per", SHAPES)
 @pytest.mark.parametrize("fmt", ["e4m3", "mxfp8"])
 def test_nan_codes_score_nan(dev, fmt, H, D, page, per):
     c = Case(dev, fmt, H, D, page, per)
@@ -103,3 +115,12 @@ def test_nan_of_fp32_keys_scores_nan(dev):
     assert np.array_equal(got[11].numpy(), want[11].numpy(), equal_nan=True)    # infinities of one head or of several
     plain = [s for s in range(40) if s not in (9, 11)]
     assert bool(((got - want).abs() <= 30 * 2.0 ** -23 * mag)[plain].all()) and bool((got[40:] == -77.0).all())
+
+
+@pytest.mark.parametrize("exps", [((0, 8), (247, 255)), ((247, 255), (0, 8))])
+@pytest.mark.parametrize("H, D, page, per", SHAPES)
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+def test_only_the_sum_of_exponents_counts(dev, fmt, H, D, page, per, exps):
+    """Scales at the two ends of their range: a vector's values alone would leave fp32."""
+    c = Case(dev, fmt, H, D, page, per, exps=exps)
+    c.check(c.run())
