@@ -720,7 +720,7 @@ __global__ void __launch_bounds__(256) expand_blocks_kernel(SeqArgs seq, const i
   if (blk >= 0 && qp >= 0 && qp < seq.max_ctx) {   // a bad position is flagged by the attention
     if (blk > qp / seq.page_size) {
       if (inside == 0) atomicOr(&g_status_attn_block, kDevBadIndex);
-    } else if (blk * seq.page_size + inside <= qp) {
+    } else if (inside <= qp - blk * seq.page_size) {   // (the sum could pass 2^31)
       pos = blk * seq.page_size + inside;
     }
   }

@@ -28,3 +28,28 @@ def test_block_choice(dev, page):
     dsa.block_topk(_seq(dev, torch.zeros((1, n), dtype=torch.int32, device=dev), page, page, LAST), scores, N, out, first=0, last=0)
     dsa.check_status()
     assert torch.equal(out[0], want)
+
+
+@pytest.mark.parametrize("page", [10000, 16384])
+def test_block_attention_over_positions(dev, page):
+    """A last page that ends behind 2^31: its positions as dsa_sparse_mla_attn takes them."""
+    g = torch.Generator(device=dev).manual_seed(page)
+    blk, n = LAST // page, LAST // page + 1
+    table = torch.zeros((1, n), dtype=torch.int32, device=dev)
+    table[0, -1] = 1
+    cache = torch.randn((2 * page, 576), generator=g, device=dev).to(torch.bfloat16)
+    mla = dsa.Mla(q=torch.randn((1, 16, 576), generator=g, device=dev).to(torch.bfloat16), kv_cache=cache, d_latent=512, d_rope=64,
+                  softmax_scale=0.07)
+    seq = _seq(dev, table, page, 2 * page)
+    pos = torch.arange(page, device=dev) + blk * page
+    pos = torch.where(pos <= LAST, pos, -1).to(torch.int32)[None].contiguous()
+    outs = []
+    for size, call in ((dsa.block_mla_attn_workspace_size(seq, mla, 1), lambda o, l, ws: dsa.block_mla_attn(
+            seq, mla, torch.tensor([[blk]], dtype=torch.int32, device=dev), o, lse=l, workspace=ws)),
+                       (dsa.sparse_mla_attn_workspace_size(seq, mla, page), lambda o, l, ws: dsa.sparse_mla_attn(
+                           seq, mla, pos, page, o, lse=l, workspace=ws))):
+        out, lse = torch.empty((1, 16, 512), dtype=torch.bfloat16, device=dev), torch.empty((1, 16), device=dev)
+        call(out, lse, torch.empty(max(size, 16), dtype=torch.uint8, device=dev))
+        dsa.check_status()
+        outs.append((out, lse))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
