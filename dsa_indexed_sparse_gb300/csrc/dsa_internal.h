@@ -13,6 +13,11 @@
 
 namespace dsa {
 
+// Counts of n in d, the last one short; of 0 <= n < 2^31, without a sum that passes 2^31.
+__host__ __device__ constexpr int div_up(int n, int d) {
+  return static_cast<int>((static_cast<uint32_t>(n) + static_cast<uint32_t>(d) - 1u) / static_cast<uint32_t>(d));
+}
+
 struct SeqArgs {
   int32_t B, T, max_ctx, q_per_seq;
   const int32_t* q_seq;

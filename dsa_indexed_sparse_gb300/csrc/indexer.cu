@@ -287,7 +287,7 @@ __device__ __forceinline__ int group_tiles(const TcParams& p, int g, int* n_hist
     }
   }
   *n_hist = n;
-  return (n + kTile - 1) / kTile;
+  return div_up(n, kTile);
 }
 
 // Walks the (group, key tile) list from a starting point.
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
       grid_dep_launch();
       return;
     }
-    const int tiles = (n + kTile - 1) / kTile;
+    const int tiles = div_up(n, kTile);
     const int kt0 = static_cast<int>(static_cast<int64_t>(rank) * tiles / f_CL);
     const int kt1 = static_cast<int>(static_cast<int64_t>(rank + 1) * tiles / f_CL);
     if (threadIdx.x == 0) {
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
     pre_g = w0.g;
     pre_kt = w0.kt;
     pre_b = __ldg(p.seq.q_seq + w0.g * G);
-    pre_npg = (w0.nhist + kTcPage - 1) / kTcPage;
+    pre_npg = div_up(w0.nhist, kTcPage);
     const int lp = kPages * (pre_kt + (lane / kPages) * kProd) + lane % kPages;
     if (pre_b >= 0 && pre_b < p.seq.B && lp < pre_npg)
       pre_page = __ldg(p.seq.block_table + static_cast<int64_t>(pre_b) * p.seq.bt_stride + lp);
@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
         const int b = w.g == pre_g ? pre_b : __ldg(p.seq.q_seq + w.g * G);
         b_ok = (b >= 0 && b < p.seq.B);
         bt = p.seq.block_table + static_cast<int64_t>(b_ok ? b : 0) * p.seq.bt_stride;
-        npg = (w.nhist + kTcPage - 1) / kTcPage;
+        npg = div_up(w.nhist, kTcPage);
         win_kt = -1;
         cur_g = w.g;
         ++qcount;
@@ -1015,7 +1015,7 @@ cudaError_t launch_tc(const SeqArgs& seq, const IndexerArgs& a, const LaunchEnv&
   }
   TcParams p{seq, a, (seq.T + G - 1) / G, 0, nullptr};
   const int64_t tiles_ub =
-      static_cast<int64_t>(p.n_groups) * ((seq.max_ctx + C::kTile - 1) / C::kTile);
+      static_cast<int64_t>(p.n_groups) * div_up(seq.max_ctx, C::kTile);
   const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(tiles_ub, env.num_sms)));
   const cudaError_t attr_err =
       ensure_smem_limit(reinterpret_cast<const void*>(indexer_tc_kernel<G, kKind, false>), C::kSmemBytes, env.device);
@@ -1038,7 +1038,7 @@ cudaError_t launch_tc(const SeqArgs& seq, const IndexerArgs& a, const LaunchEnv&
 // slice's keys fit kFusedMaxKeys.  Returns CL, or 0 when the plan does not apply.
 template <IndexKind kKind>
 int fused_cluster(const SeqArgs& seq, const LaunchEnv& env, int max_cl) {
-  const int need = (seq.max_ctx + kFusedMaxKeys - 1) / kFusedMaxKeys;
+  const int need = div_up(seq.max_ctx, kFusedMaxKeys);
   int cl = 1;
   while (cl < 16 && static_cast<int64_t>(seq.T) * cl * 2 <= env.num_sms) cl *= 2;
   cl = std::max(cl, need);
@@ -1046,7 +1046,7 @@ int fused_cluster(const SeqArgs& seq, const LaunchEnv& env, int max_cl) {
   // every cluster of the launch resident at once is not required, but a cluster
   // of this size must fit on the GPU
   using C = TcCfg<1, kKind>;
-  const int keys = (((seq.max_ctx + C::kTile - 1) / C::kTile + cl - 1) / cl) * C::kTile;
+  const int keys = div_up(div_up(seq.max_ctx, C::kTile), cl) * C::kTile;
   const size_t smem = static_cast<size_t>(C::kOffKeys) + static_cast<size_t>(keys) * 4 + 1024;
   void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, TcParams) = indexer_tc_kernel<1, kKind, true>;
   if (ensure_smem_limit(reinterpret_cast<const void*>(kern),
@@ -1069,7 +1069,7 @@ cudaError_t launch_fused(const SeqArgs& seq, const IndexerArgs& a, int32_t K, in
     return cudaSuccess;
   }
   TcParams p{seq, a, seq.T, K, idx};
-  const int keys = (((seq.max_ctx + C::kTile - 1) / C::kTile + cl - 1) / cl) * C::kTile;
+  const int keys = div_up(div_up(seq.max_ctx, C::kTile), cl) * C::kTile;
   const size_t smem = static_cast<size_t>(C::kOffKeys) + static_cast<size_t>(keys) * 4 + 1024;
   const cudaError_t le = launch_kernel(indexer_tc_kernel<1, kKind, true>, dim3(seq.T * cl), dim3(TcWarps<1, kKind>::kThreads),
                                        smem, env.stream, true, cl, kmap, kmap2, qmap, p);
@@ -1131,7 +1131,7 @@ cudaError_t launch_indexer(const SeqArgs& seq, const IndexerArgs& a, const Launc
     *why = "indexer: H_I * D_I too large for the generic kernel";
     return cudaSuccess;
   }
-  dim3 grid((seq.max_ctx + kGenThreads - 1) / kGenThreads, seq.T);
+  dim3 grid(div_up(seq.max_ctx, kGenThreads), seq.T);
   void (*kern)(SeqArgs, IndexerArgs) = a.kind == IndexKind::kMx4    ? indexer_generic_kernel<IndexKind::kMx4>
                                        : a.kind == IndexKind::kMx8  ? indexer_generic_kernel<IndexKind::kMx8>
                                        : a.kind == IndexKind::kE4M3 ? indexer_generic_kernel<IndexKind::kE4M3>

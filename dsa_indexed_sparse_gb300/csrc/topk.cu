@@ -67,11 +67,11 @@ __global__ void __launch_bounds__(kThreads) topk_kernel(TopkArgs a) {
   }
   select_prepare<kThreads>(&sel, CL);
   // this CTA's slice [lo, hi) of the history (slice starts are multiples of 4)
-  const int slice = ((n + CL - 1) / CL + 3) & ~3;
-  const int lo = min(n, rank * slice), hi = min(n, lo + slice);
-  const int len = hi - lo;
+  const uint32_t slice = (static_cast<uint32_t>(div_up(n, CL)) + 3u) & ~3u;
+  const int lo = static_cast<int>(min(static_cast<uint32_t>(n), rank * slice));
+  const int len = static_cast<int>(min(static_cast<uint32_t>(n - lo), slice));
   const float* row = a.scores + static_cast<int64_t>(t) * a.ld + lo;
-  const bool cached = slice <= a.cache_keys;
+  const bool cached = slice <= static_cast<uint32_t>(a.cache_keys);
   if (cached) {
     // scores -> keys in shared memory (16-byte loads, several in flight per
     // thread), counted into the first histogram on the way
@@ -120,7 +120,7 @@ cudaError_t launch_topk(const SeqArgs& seq, const float* scores, int64_t ld, int
   // slice within the shared-memory key cache when the cluster can.
   const int want = std::max(1, env.num_sms / seq.T);   // one wave: T x cluster <= SMs
   const int feed = std::max(1, seq.max_ctx / kMinSliceKeys);
-  const int fit = (seq.max_ctx + kCacheKeys - 1) / kCacheKeys;
+  const int fit = div_up(seq.max_ctx, kCacheKeys);
   const cudaError_t attr_err =
       ensure_smem_limit(reinterpret_cast<const void*>(topk_kernel), kCacheKeys * 4, env.device);
   if (attr_err != cudaSuccess) return attr_err;
@@ -133,10 +133,10 @@ cudaError_t launch_topk(const SeqArgs& seq, const float* scores, int64_t ld, int
       cluster_fits(reinterpret_cast<const void*>(topk_kernel), env.device, kMaxClusterOne, kThreads, kCacheKeys * 4))
     max_cl = kMaxClusterOne;
   const int cl = std::max(1, std::min(max_cl, std::max(std::min(want, feed), fit)));
-  const int slice = ((seq.max_ctx + cl - 1) / cl + 3) & ~3;
+  const uint32_t slice = (static_cast<uint32_t>(div_up(seq.max_ctx, cl)) + 3u) & ~3u;
   const bool cached = slice <= kCacheKeys;
   const size_t smem = cached ? static_cast<size_t>(slice) * 4 : 0;
-  TopkArgs a{scores, ld, seq.q_pos, seq.max_ctx, K, idx, cached ? slice : 0, seq.T};
+  TopkArgs a{scores, ld, seq.q_pos, seq.max_ctx, K, idx, cached ? static_cast<int32_t>(slice) : 0, seq.T};
   // Programmatic dependent launch: the clusters are placed as the indexer's CTAs
   // finish (each triggers its dependents when its tiles are done) and wait for
   // the scores in griddepcontrol.wait, instead of launching after the indexer's
