@@ -813,7 +813,8 @@ dsa_status_t dsa_index_query_quantize(int32_t T, int32_t H_I, int32_t D_I, dsa_d
       return fail(DSA_ERR_INVALID_ARG, "q, codes and scale must be 16-byte aligned");
     // a load is four values of E4M3 vectors (8 bytes of bf16), else 16 bytes
     const int64_t es = src_dtype == DSA_F32 ? 4 : 2, unit = kind == dsa::IndexKind::kE4M3 ? 4 : 16 / es;
-    if (stride_t < 0 || stride_h < 0 || stride_t % unit != 0 || stride_h % unit != 0)
+    auto stride_ok = [&](int64_t stride, int32_t n) -> bool { return n <= 1 || (stride >= 0 && stride % unit == 0); };
+    if (!stride_ok(stride_t, T) || !stride_ok(stride_h, H_I))
       return fail(DSA_ERR_INVALID_ARG, "strides of q must be >= 0 and multiples of 16 bytes (DSA_E4M3: of 4 values)");
     dsa::LaunchEnv env;
     if ((st = make_env(stream, &env)) != DSA_OK) return st;

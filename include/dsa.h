@@ -323,7 +323,7 @@ dsa_status_t dsa_index_cache_append_mx4(const dsa_seq_desc_t* seq, int32_t D_I, 
 /* Query heads to the codes and scales that dsa_indexer_scores reads beside such keys:
  *   q device [T, H_I, D_I] fp32 or bf16 (src_dtype), value (t, h, i) at t * stride_t +
  *   h * stride_h + i (strides in values, multiples of 16 bytes, DSA_E4M3: of 4
- *   values), every head quantised as the cache writers quantise a key to code_dtype;
+ *   values; that of a dimension of one is not used), every head quantised as the cache writers quantise a key to code_dtype;
  *   codes device uint8 [T, H_I, D_I] (DSA_MXFP4_E2M1: D_I / 2 bytes a head), scale
  *   device fp32 [T, H_I] (DSA_E4M3) or uint8 [T, H_I, D_I / 32].  The outputs share
  *   no memory with q. */

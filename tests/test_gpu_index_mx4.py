@@ -470,3 +470,18 @@ def test_calls_of_no_tokens(dev):
                              torch.zeros((0, 64, 4), dtype=torch.uint8, device=dev), dtype=dsa.DSA_MXFP4_E2M1)
     dsa.check_status()
     assert torch.equal(before, s.idx.k_cache)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8", "e4m3"])
+@pytest.mark.parametrize("shape, strides", [((1, 64, 128), (8193, 128, 1)), ((5, 1, 128), (256, 7, 1)), ((1, 1, 128), (3, 5, 1))])
+def test_query_quantize_stride_of_one_token_or_head(dev, fmt, shape, strides):
+    """The stride of a dimension of one is whatever the view it came from has."""
+    base = torch.randn(8192 + 1024, generator=torch.Generator().manual_seed(6)).to(torch.bfloat16).to(dev)
+    x = base.as_strided(shape, strides)
+    n = shape[0] * shape[1]
+    codes, scale = _buffers(fmt, n, 128, dev, fill=9)
+    codes, scale = codes.view(*shape[:2], -1), scale.view(*shape[:2], -1) if fmt != "e4m3" else scale.view(*shape[:2])
+    dsa.index_query_quantize(x, codes, scale, dtype=FORMATS[fmt])
+    dsa.check_status()
+    c, s = _encode(x.float().cpu().numpy().reshape(n, 128), fmt)
+    assert np.array_equal(codes.cpu().numpy().reshape(c.shape), c) and np.array_equal(scale.cpu().numpy().reshape(s.shape), s)
