@@ -7,7 +7,7 @@
 // Adaptation and Performance Optimization for Kimi K3.1 Pro", section 4.  The
 // formats written are the ones the scoring and attention kernels read:
 //  * index keys: uint8 [cache_rows, D] e4m3 codes + fp32 [cache_rows] scales,
-//    scale = amax / 448 (1 for an all-zero vector), code = the E4M3 value
+//    scale = amax / 448 (1 where that is 0 in fp32), code = the E4M3 value
 //    nearest to x / scale (ties to even, saturated to +-448), both divisions
 //    IEEE round-to-nearest in fp32;
 //  * index keys, MXFP8: uint8 codes + uint8 [cache_rows, D/32] E8M0 bytes; block
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
     }
   }
   amax = warp_max(amax);
-  const float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+  const float scale = e4m3_scale(amax);
   uint32_t* dst = reinterpret_cast<uint32_t*>(k_cache + row * D);
 #pragma unroll
   for (int k = 0; k < kMaxChunks; ++k) {
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
 #pragma unroll
   for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v[i]));
   amax = warp_max(amax);
-  const float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+  const float scale = e4m3_scale(amax);
   uint32_t q[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)

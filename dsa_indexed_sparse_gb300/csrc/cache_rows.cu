@@ -171,7 +171,7 @@ __device__ __forceinline__ void write_latent(const float (&v)[16], uint8_t* dst,
     float q[16];
     if constexpr (kKind == MlaKind::kFP8Row) {
       amax = warp_max(amax);
-      const float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+      const float scale = e4m3_scale(amax);
 #pragma unroll
       for (int i = 0; i < 16; ++i) q[i] = __fdiv_rn(v[i], scale);
       if (lane < 4) reinterpret_cast<float*>(dst + 512)[lane] = lane == 0 ? scale : 0.f;
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kIndexWarps * 32) index_write_kernel(SeqArgs s
       amax = fmaxf(amax, fmaxf(fmaxf(fabsf(f.x), fabsf(f.y)), fmaxf(fabsf(f.z), fabsf(f.w))));
     }
     amax = warp_max(amax);
-    const float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+    const float scale = e4m3_scale(amax);
     for (int c = lane; c < nq; c += 32) {
       const float4 f = v4[c];
       dst[c] = e4m3_code4(__fdiv_rn(f.x, scale), __fdiv_rn(f.y, scale), __fdiv_rn(f.z, scale), __fdiv_rn(f.w, scale));

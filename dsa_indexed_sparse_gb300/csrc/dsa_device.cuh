@@ -457,6 +457,14 @@ __device__ __forceinline__ float bf16_bits_to_float(uint16_t b) {
   return __uint_as_float(static_cast<uint32_t>(b) << 16);
 }
 
+// The fp32 scale of the E4M3 codes of a vector whose largest magnitude is amax: amax / 448, or 1
+// where that is 0, for zeros and magnitudes up to 1.75 * 2^-142, whose codes are then 0 (and not
+// the NaN of 0 / 0).
+__device__ __forceinline__ float e4m3_scale(float amax) {
+  const float s = __fdiv_rn(amax, 448.f);
+  return s > 0.f ? s : 1.f;
+}
+
 // An E8M0 scale byte: 2^(e - 127); 255 stands for no number.
 __device__ __forceinline__ float e8m0_to_float(uint32_t e) {
   return __uint_as_float(e == 0u ? 0x00400000u : (e == 255u ? 0x7FC00000u : e << 23));

@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) quantize_row_kernel(QuantizeAr
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+  const float scale = e4m3_scale(amax);
   uint32_t* dst = reinterpret_cast<uint32_t*>(a.codes + r * a.D);
   for (int c = lane; c < nq; c += 32) {   // the second look comes from the L1
     const float4 f = load(c);

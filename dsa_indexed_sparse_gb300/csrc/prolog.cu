@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(32 * kEpiHeads) prolog_epilogue_kernel(EpiPara
     load_vec128(p.yq + static_cast<int64_t>(t) * HD + h * 128, static_cast<int64_t>(p.seq.T) * HD, p.split_q,
                 lane, v);
     const float amax = warp_max(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))));
-    const float scale = amax > 0.f ? amax / 448.f : 1.f;
+    const float scale = e4m3_scale(amax);
     uint8_t* dst = p.q_codes + (static_cast<int64_t>(t) * p.H_I + h) * 128;
 #pragma unroll
     for (int i = 0; i < 4; ++i) dst[lane + 32 * i] = to_e4m3(v[i] / scale);
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(32 * kEpiHeads) prolog_epilogue_kernel(EpiPara
     amax = fmaxf(amax, fabsf(v[i]));
   }
   amax = warp_max(amax);
-  const float scale = amax > 0.f ? amax / 448.f : 1.f;
+  const float scale = e4m3_scale(amax);
   const int qp = __ldg(p.seq.q_pos + t), b = __ldg(p.seq.q_seq + t);
   if (qp < 0 || qp >= p.seq.max_ctx || b < 0 || b >= p.seq.B) {
     if (lane == 0) atomicOr(&g_status_prolog, kDevBadPos);

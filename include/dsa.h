@@ -295,7 +295,8 @@ dsa_status_t dsa_decode_step_static_ws(const dsa_seq_desc_t* seq, const dsa_inde
  * skipped and flagged (dsa_check_status).
  *
  * Index keys: k_new device [T, D_I] fp32 or bf16 (src_dtype); per token
- *   scale = amax_i |k_new[t,i]| / 448 in fp32 (1 when the row is all zero),
+ *   scale = amax_i |k_new[t,i]| / 448 in fp32 (1 where that is 0: nothing in the
+ *   row is above 1.75 * 2**-142),
  *   code_i = the E4M3 value nearest to k_new[t,i] / scale (fp32 quotient), ties
  *   to the even code, magnitudes beyond 448 saturated;
  *   writes k_cache[row, 0:D_I] (uint8, row stride D_I) and k_scale[row] (fp32),
@@ -323,8 +324,8 @@ dsa_status_t dsa_index_cache_append_mx4(const dsa_seq_desc_t* seq, int32_t D_I, 
 /* Query heads to the codes and scales that dsa_indexer_scores reads beside such keys:
  *   q device [T, H_I, D_I] fp32 or bf16 (src_dtype), value (t, h, i) at t * stride_t +
  *   h * stride_h + i (strides in values, multiples of 16 bytes, DSA_E4M3: of 4
- *   values; that of a dimension of one is not used), every head quantised as the cache writers quantise a key to code_dtype;
- *   codes device uint8 [T, H_I, D_I] (DSA_MXFP4_E2M1: D_I / 2 bytes a head), scale
+ *   values; that of a dimension of one is not used), every head quantised as the
+ *   cache writers quantise a key to code_dtype; codes device uint8 [T, H_I, D_I] (DSA_MXFP4_E2M1: D_I / 2 bytes a head), scale
  *   device fp32 [T, H_I] (DSA_E4M3) or uint8 [T, H_I, D_I / 32].  The outputs share
  *   no memory with q. */
 dsa_status_t dsa_index_query_quantize(int32_t T, int32_t H_I, int32_t D_I, dsa_dtype_t src_dtype,

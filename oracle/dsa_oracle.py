@@ -150,11 +150,12 @@ def dequantize_mx_e4m3(codes, scales, block: int = 32) -> np.ndarray:
 
 def quantize_e4m3_row(x) -> tuple:
     """One token's vector -> (uint8 codes, float32 scale): scale = amax / 448 in
-    float32 (1 when the row is all zero), codes = e4m3_encode(x / scale) with the
-    quotient formed in float32."""
+    float32 (1 where that is 0: the row is all zero, or holds nothing above
+    1.75 * 2**-142), codes = e4m3_encode(x / scale) with the quotient formed in float32."""
     x = np.asarray(x, dtype=np.float32)
     amax = np.float32(np.max(np.abs(x))) if x.size else np.float32(0)
-    scale = np.float32(amax / np.float32(448.0)) if amax > 0 else np.float32(1.0)
+    scale = np.float32(amax / np.float32(448.0))
+    scale = scale if scale > 0 else np.float32(1.0)
     return e4m3_encode((x / scale).astype(np.float32)), scale
 
 

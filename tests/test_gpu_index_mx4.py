@@ -485,3 +485,29 @@ def test_query_quantize_stride_of_one_token_or_head(dev, fmt, shape, strides):
     dsa.check_status()
     c, s = _encode(x.float().cpu().numpy().reshape(n, 128), fmt)
     assert np.array_equal(codes.cpu().numpy().reshape(c.shape), c) and np.array_equal(scale.cpu().numpy().reshape(s.shape), s)
+
+
+def test_e4m3_vectors_whose_scale_would_be_zero(dev):
+    """fp32 vectors so small that amax / 448 is 0 in fp32 are stored as zeros, not as the NaN of 0 / 0, by every writer."""
+    edge = np.float32(1.75 * 2.0 ** -142)
+    tops = [np.float32(0), np.float32(1e-45), np.float32(1e-43), edge, np.nextafter(edge, np.float32(1)), np.float32(1e-42), np.float32(1e-38)]
+    x = np.zeros((len(tops), 128), np.float32)
+    x[:, 3], x[:, 70], x[:, 127] = tops, -np.array(tops) / np.float32(2), np.array(tops) / np.float32(3)
+    n = len(tops)
+    c, s = _encode(x, "e4m3")
+    assert np.all((c & 127) != 127) and np.all(s > 0) and np.all(s[:4] == 1) and s[4] < 1
+    t = torch.from_numpy(x).to(dev)
+    codes, scale = _buffers("e4m3", n, 128, dev, fill=9)
+    dsa.index_query_quantize(t.view(n, 1, 128), codes.view(n, 1, 128), scale.view(n, 1))
+    assert np.array_equal(codes.cpu().numpy(), c) and np.array_equal(scale.cpu().numpy(), s)
+    seq = dsa.Seq(q_seq=torch.zeros(n, dtype=torch.int32, device=dev), q_pos=torch.arange(n, dtype=torch.int32, device=dev),
+                  block_table=torch.zeros((1, 1), dtype=torch.int32, device=dev), max_ctx=64, cache_rows=64)
+    kc, ks = _buffers("e4m3", 64, 128, dev, fill=9)
+    dsa.index_cache_append(seq, t, kc, ks)
+    assert np.array_equal(kc[:n].cpu().numpy(), c) and np.array_equal(ks[:n].cpu().numpy(), s)
+    kc, ks = _buffers("e4m3", 64, 128, dev, fill=9)
+    dsa.index_cache_append_rope(seq, dsa.Rope.make(32), t, kc, ks, offset=80)      # dims 80 to 111: zeros
+    dsa.check_status()
+    kc, turned = kc[:n].cpu().numpy(), (np.arange(128) >= 80) & (np.arange(128) < 112)
+    assert np.array_equal(kc[:, ~turned], c[:, ~turned]) and np.all((kc[:, turned] & 127) == 0)
+    assert np.array_equal(ks[:n].cpu().numpy(), s)
