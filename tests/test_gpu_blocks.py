@@ -550,3 +550,87 @@ def test_calls_of_no_queries(dev):
     dsa.block_mla_attn(seq, mla, torch.empty((0, 4), dtype=torch.int32, device=dev), out)
     dsa.block_topk(seq, torch.empty((0, 100), device=dev), 4, torch.empty((0, 4), dtype=torch.int32, device=dev))
     dsa.check_status()
+
+
+# ------------------------------------------------------------------------------------------------- many queries, other caches
+
+@pytest.mark.parametrize("kind", ["equal", "special", "normal"])
+@pytest.mark.parametrize("ctx, page, N, first, last, threads", [(16384, 64, 33, 1, 2, 64), (40000, 64, 100, 0, 0, 128), (40000, 64, 600, 2, 5, 128),
+                                                               (3000, 16, 50, 1, 1, 64), (12000, 16, 90, 3, 0, 128), (5000, 7, 200, 1, 1, 128)])
+def test_block_topk_of_many_queries(dev, ctx, page, N, first, last, threads, kind):
+    """A prompt chunk's launches: small CTAs, each of which reads its blocks in several turns and writes its choice in several chunks."""
+    g = torch.Generator().manual_seed(ctx + N)
+    B, per = 40, 8
+    lens = [ctx - b * 97 % (ctx - 100) for b in range(B - 1)] + [page * N // 2]
+    q_pos = torch.cat([torch.arange(n - per, n) for n in lens]).to(torch.int32)
+    T, ld = B * per, (ctx + 3) // 4 * 4
+    x = _scores(g, T, ld, kind)
+    x[torch.arange(ld)[None, :] > q_pos[:, None]] = float("inf") if kind != "special" else float("nan")
+    seq = dsa.Seq(q_seq=torch.arange(B, dtype=torch.int32).repeat_interleave(per).to(dev), q_pos=q_pos.to(dev),
+                  block_table=torch.zeros((B, (ctx + page - 1) // page), dtype=torch.int32, device=dev), max_ctx=ctx,
+                  cache_rows=page, page_size=page, q_per_seq=per)
+    out = torch.full((T, N), -7, dtype=torch.int32, device=dev)
+    dsa.block_topk(seq, x.to(dev), N, out, first=first, last=last)
+    assert f"threads={threads}]" in dsa.last_plan()
+    dsa.check_status()
+    assert np.array_equal(out.cpu().numpy(), _choice(x.numpy(), q_pos.numpy(), page, N, first, last))
+
+
+@pytest.mark.parametrize("fmt, page, H", [("e4m3", 64, 128), ("e4m3_t128", 64, 128), ("e2m1", 64, 128), ("bf16", 64, 16), ("bf16", 32, 16),
+                                          ("bf16", 16, 128), ("e2m1", 32, 16)])
+def test_block_decode_step_over_other_caches(dev, fmt, page, H):
+    """The chained step against its three calls, over every row format and over pages of other sizes; eagerly, and captured and
+    replayed with other queries."""
+    g = torch.Generator(device=dev).manual_seed(page + H)
+    lens, per, N = [900, 333], 2, 6
+    B, T, ctx = len(lens), len(lens) * per, max(lens)
+    pages = (ctx + page - 1) // page
+    rows = B * pages * page
+    table = torch.randperm(B * pages, generator=g, device=dev).to(torch.int32).view(B, pages)
+    seq = dsa.Seq(q_seq=torch.arange(B, dtype=torch.int32, device=dev).repeat_interleave(per), block_table=table, max_ctx=ctx, cache_rows=rows,
+                  q_pos=torch.cat([torch.arange(n - per, n) for n in lens]).to(torch.int32).to(dev), page_size=page, q_per_seq=per)
+    every = dsa.Seq(q_seq=torch.arange(B, dtype=torch.int32, device=dev).repeat_interleave(ctx), block_table=table, max_ctx=ctx, cache_rows=rows,
+                    q_pos=torch.arange(ctx, dtype=torch.int32, device=dev).repeat(B), page_size=page)
+    code, width = {"bf16": (None, None), "e4m3": (dsa.DSA_E4M3, 656), "e4m3_t128": (dsa.DSA_E4M3_T128, 656), "e2m1": (dsa.DSA_E2M1, 432)}[fmt]
+    cache = torch.zeros((rows, D_ROW), dtype=torch.bfloat16, device=dev) if width is None else torch.zeros((rows, width), dtype=torch.uint8, device=dev)
+    rnd = lambda *n: torch.randn(n, generator=g, device=dev).to(torch.bfloat16)
+    mla = dsa.Mla(q=rnd(T, H, D_ROW), kv_cache=cache, d_latent=D_V, d_rope=64, softmax_scale=SCALE, dtype=code)
+    dsa.latent_cache_append(every, mla, rnd(B * ctx, D_ROW))
+    codes, exps = torch.zeros((rows, 64), dtype=torch.uint8, device=dev), torch.zeros((rows, 4), dtype=torch.uint8, device=dev)
+    dsa.index_cache_append(every, rnd(B * ctx, 128), codes, exps, dtype=dsa.DSA_MXFP4_E2M1)
+    qc, qs = torch.empty((T, 64, 64), dtype=torch.uint8, device=dev), torch.empty((T, 64, 4), dtype=torch.uint8, device=dev)
+    idx = dsa.Indexer(q=qc, w=torch.randn((T, 64), generator=g, device=dev), k_cache=codes, q_scale=qs, k_scale=exps, dtype=dsa.DSA_MXFP4_E2M1)
+    q_new = rnd(T, 64, 128)
+    out, lse = torch.empty((T, H, D_V), dtype=torch.bfloat16, device=dev), torch.empty((T, H), device=dev)
+    sel = torch.full((T, N), -7, dtype=torch.int32, device=dev)
+    ws = torch.empty(dsa.block_decode_workspace_size(seq, mla, N), dtype=torch.uint8, device=dev)
+
+    def step():
+        dsa.index_query_quantize(q_new, qc, qs, dtype=dsa.DSA_MXFP4_E2M1)
+        dsa.block_decode_step(seq, idx, mla, N, out, ws, first=1, last=1, lse=lse, block_idx_out=sel)
+
+    def check():
+        dsa.check_status()
+        scores = torch.zeros((T, (ctx + 3) // 4 * 4), device=dev)
+        dsa.indexer_scores(seq, idx, scores)
+        assert np.array_equal(sel.cpu().numpy(), _choice(scores.cpu().numpy(), seq.q_pos.cpu().numpy(), page, N, 1, 1))
+        o2, l2 = torch.empty_like(out), torch.empty_like(lse)
+        dsa.block_mla_attn(seq, mla, sel, o2, lse=l2, workspace=torch.empty(
+            max(16, dsa.block_mla_attn_workspace_size(seq, mla, N)), dtype=torch.uint8, device=dev))
+        dsa.check_status()
+        assert torch.equal(out, o2) and torch.equal(lse, l2) and bool(torch.isfinite(lse).all())
+
+    step()
+    assert ("expand_blocks" in dsa.last_plan()) == ((fmt, page) != ("bf16", 64))
+    check()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            step()
+        for x in (q_new, mla.q):
+            x.copy_(torch.randn(x.shape, generator=g, device=dev).to(torch.bfloat16))
+        graph.replay()
+    side.synchronize()
+    check()

@@ -511,3 +511,40 @@ def test_e4m3_vectors_whose_scale_would_be_zero(dev):
     kc, turned = kc[:n].cpu().numpy(), (np.arange(128) >= 80) & (np.arange(128) < 112)
     assert np.array_equal(kc[:, ~turned], c[:, ~turned]) and np.all((kc[:, turned] & 127) == 0)
     assert np.array_equal(ks[:n].cpu().numpy(), s)
+
+
+@pytest.mark.parametrize("H, D, per", [(64, 128, 1), (64, 128, 4), (3, 128, 2)])
+def test_keys_beyond_32_bit_offsets(dev, H, D, per):
+    """Keys in the last pages of a pool whose codes and scales both pass 2^31 bytes: written, with and without rotation, read and
+    scored as in a small pool, bit for bit."""
+    if torch.cuda.mem_get_info()[0] < (60 << 30):
+        pytest.skip("needs 36 GB and room")
+    g = torch.Generator().manual_seed(H + per)
+    ctx, pages = 500, 8
+    far = (2 ** 29 + 64 * 64) // 64              # 2^29 rows of 64 and of 4 bytes
+    byte = lambda *n: torch.randint(0, 256, n, generator=g).to(torch.uint8).to(dev)
+    q, qe = byte(per, H, D // 2), torch.randint(121, 134, (per, H, D // 32), generator=g).to(torch.uint8).to(dev)
+    w, new = torch.randn((per, H), generator=g).to(dev), torch.randn((ctx, D), generator=g).to(dev)
+    order = torch.randperm(pages, generator=g).to(torch.int32)
+    results = []
+    for n in (pages, far):
+        codes, exps = (torch.empty((n * 64, b), dtype=torch.uint8, device=dev) for b in (D // 2, D // 32))
+        table = (order + (n - pages)).view(1, pages).to(dev)
+        every = dsa.Seq(q_seq=torch.zeros(ctx, dtype=torch.int32, device=dev), q_pos=torch.arange(ctx, dtype=torch.int32, device=dev),
+                        block_table=table, max_ctx=ctx, cache_rows=n * 64)
+        seq = dsa.Seq(q_seq=torch.zeros(per, dtype=torch.int32, device=dev), q_pos=torch.arange(ctx - per, ctx, dtype=torch.int32, device=dev),
+                      block_table=table, max_ctx=ctx, cache_rows=n * 64, q_per_seq=per)
+        for rotated in (False, True):
+            if rotated:
+                dsa.index_cache_append_rope(every, dsa.Rope.make(64), new, codes, exps, offset=0, dtype=dsa.DSA_MXFP4_E2M1)
+            else:
+                dsa.index_cache_append(every, new, codes, exps, dtype=dsa.DSA_MXFP4_E2M1)
+            read = dsa.index_cache_read(every, codes, exps, torch.empty((ctx, D), device=dev), dtype=dsa.DSA_MXFP4_E2M1)
+            out = torch.full((per, 500), -77.0, device=dev)
+            dsa.indexer_scores(seq, dsa.Indexer(q=q, w=w, k_cache=codes, q_scale=qe, k_scale=exps, dtype=dsa.DSA_MXFP4_E2M1), out)
+            results.append((read, out))
+        dsa.check_status()
+    for near, away in zip(results[:2], results[2:]):
+        assert torch.equal(near[0], away[0]) and torch.equal(near[1], away[1])
+    v = O.dequantize_mx_e2m1(*O.quantize_mx_e2m1(new.cpu().numpy()))
+    assert np.array_equal(results[2][0].cpu().numpy().astype(np.float64), v)

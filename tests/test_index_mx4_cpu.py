@@ -115,3 +115,12 @@ def test_binding_refuses_shapes(dsa):
                  lambda: dsa.index_cache_read(seq, z(256, 64), z(256, 4), z(2, 128, d=torch.float32), dtype=M4)):   # not on a GPU
         with pytest.raises(ValueError):
             call()
+
+
+def test_mx4_value_beyond_the_border_at_five():
+    """0.01 = 5.12 * 2^-9 lies beyond 5, the border between 4 and 6: code 7 in the low nibble, nothing in the high one."""
+    x = np.zeros((1, 32))
+    x[0, 0] = 0.01
+    codes, e = O.quantize_mx_e2m1(x)
+    assert e.tolist() == [[118]] and codes[0].tolist() == [7] + [0] * 15
+    assert O.dequantize_mx_e2m1(codes, e)[0, 0] == 6 * 2.0 ** -9
