@@ -465,9 +465,9 @@ __device__ __forceinline__ float e4m3_scale(float amax) {
   return s > 0.f ? s : 1.f;
 }
 
-// An E8M0 scale byte: 2^(e - 127); 255 stands for no number.
+// An E8M0 scale byte: 2^(e - 127) (the maximum: 2^-127 for 0); 255 stands for no number.
 __device__ __forceinline__ float e8m0_to_float(uint32_t e) {
-  return __uint_as_float(e == 0u ? 0x00400000u : (e == 255u ? 0x7FC00000u : e << 23));
+  return __uint_as_float(e == 255u ? 0x7FC00000u : max(e << 23, 0x00400000u));
 }
 
 // Page-table translation: logical position s of the sequence whose table row
