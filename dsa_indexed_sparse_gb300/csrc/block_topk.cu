@@ -121,9 +121,11 @@ __global__ void __launch_bounds__(kMaxThreads, 2) block_topk_kernel(BlockTopkArg
   } else {
     for (int blk = lo + warp; blk < hi; blk += nt >> 5) {
       float best = -INFINITY;
-      // unsigned: the step behind the last position may pass 2^31
-      const uint32_t end = blk == n - 1 ? n_tok : (blk + 1) * a.page_size;
-      for (uint32_t pos = blk * a.page_size + lane; pos < end; pos += 32) best = fmaxf(best, __ldg(row + pos));
+      const int start = blk * a.page_size;
+      // what is left is counted, not positions: the one a step behind the last may pass 2^31
+      const float* at = row + start + lane;
+#pragma unroll 4
+      for (int left = (blk == n - 1 ? n_tok - start : a.page_size) - lane; left > 0; left -= 32, at += 32) best = fmaxf(best, __ldg(at));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
       if (lane == 0) put(blk, best);
