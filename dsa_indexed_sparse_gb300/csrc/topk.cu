@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kThreads) topk_kernel(TopkArgs a) {
   }
   select_prepare<kThreads>(&sel, CL);
   // this CTA's slice [lo, hi) of the history (slice starts are multiples of 4)
-  const uint32_t slice = (static_cast<uint32_t>(div_up(n, CL)) + 3u) & ~3u;
+  const uint32_t slice = (static_cast<uint32_t>((n - 1) / CL) + 4u) & ~3u;
   const int lo = static_cast<int>(min(static_cast<uint32_t>(n), rank * slice));
   const int len = static_cast<int>(min(static_cast<uint32_t>(n - lo), slice));
   const float* row = a.scores + static_cast<int64_t>(t) * a.ld + lo;
