@@ -33,8 +33,8 @@
 //
 // P goes to bf16, the type of V: at most 2^-8 of a weight, half a step; what normalises the output is
 // the sum of the unrounded weights, the one the log-sum-exp takes.  m, a running bound of the
-// logits, moves only when it grows by more than 2^64: bf16 and fp32 have the exponents for it,
-// and O is rescaled for the first tile and hardly ever after.
+// logits, is set by the first tile and moves only when it grows by more than 2^64: bf16 and fp32
+// have the exponents for it, and O is hardly ever rescaled.
 //
 // Work.  An item is a slice of the blocks (few queries: joined by attn_combine) of 128 heads
 // of a query; the clusters that fit the GPU at once share the items out, and tiles, buffers and
@@ -46,8 +46,8 @@
 // K^T, 3 P V (rank 0 for both CTAs).  What both CTAs load for an MMA is counted on a barrier of the
 // leader's (passing on an arrival took 500 clocks).  4-19 are softmax and output, a thread 16 logits.
 //
-// Measured (32 blocks a query, 128 heads): 775 us for a chunk of 2048 queries, 1500 TFLOP/s of the
-// 1926 measured (86 % of what the card holds over seconds: clocks fall to 1.8 GHz); 37.5 us for 64
+// Measured (32 blocks a query, 128 heads): 785 us for a chunk of 2048 queries, 1490 TFLOP/s of the
+// 1926 measured (85 % of what the card holds over seconds: clocks fall to 1.8 GHz); 37.5 us for 64
 // queries, 10.2 for one (16 slices and their merge).  A tile takes 2900 clocks in the middle of a chunk
 // where its MMAs need 2176: shared memory moves 360 KB for it (240 for operands, 104 from the TMA, 16
 // of P), 2880 clocks of its 128 bytes a clock.  64 queries read their 151 MB at 6 TB/s once under way
@@ -94,7 +94,8 @@ constexpr int kOffInfo = kOffMax + 2 * 2 * kParts * 32 * 4;   // int4 [4]: what 
 constexpr int kOffOk = kOffInfo + 4 * 16;                 // int [kSoftWarps]
 constexpr int kOffBar = kOffOk + kSoftWarps * 4;
 // What a tile is, in info: x flags, y the other block's first cache row, z and w how many rows of
-// blocks 0 and 1 count.  Written before the tile's loads, that is after P V of the tile two before.
+// blocks 0 and 1 count.  Written before the tile's loads, that is when the first half of P V of the
+// tile two before is complete; the tile four before, whose place it takes, has long been passed.
 constexpr int kFirst = 1, kLast = 2, kEnd = 4;            // of its item; last of all
 constexpr int kNumBars = 24;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;
@@ -114,7 +115,10 @@ struct BlockParams {
   int32_t per_split;        // entries per slice, an even number
   int32_t head_blocks;      // blocks of 128 heads
   int32_t items;            // T * head_blocks * n_split, shared out among the clusters
-  uint16_t* ws_o;           // [n_split, T, H, 512] (n_split > 1)
+  // [n_split, T, H, 512] (n_split > 1), bf16 as attn.cu's for the same merge: 2^-8 of a partial at most.  Of the
+  // output, root of the mean square: 0.0021 of it off without slices (P and the output's own rounding, which
+  // alone is 0.0017), 0.0022 (one query of 32 blocks) to 0.0025 (7 of 13) with them.
+  uint16_t* ws_o;
   float* ws_lse;            // [n_split, T, H]
   uint64_t wait_limit_ns;
   uint32_t dbg_withhold;

@@ -33,7 +33,7 @@ DSA_DEFINE_STATUS_WORD(index_keys)
 namespace dsa {
 namespace {
 
-constexpr int kBlockThreads = 128;   // at least; a block holds whole vectors
+constexpr int kBlockThreads = 128;   // at most, in whole vectors (the E4M3 reader: up to twice that for the longest)
 constexpr int kVals = 16;            // values a thread
 
 // Cache row of token t, or -1 (flagged) when its position or page is invalid.

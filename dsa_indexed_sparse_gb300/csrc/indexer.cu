@@ -10,8 +10,9 @@
 //     I[t, s] = k_scale[s] * sum_h (w[t,h] * q_scale[t,h]) * ReLU(q_code . k_code)
 //
 // Two kernels:
-//  * indexer_tc_kernel<G> -- the tensor-core path (FP8 e4m3, H_I = 64, D_I = 128,
-//    64-token pages).  Swap-AB tcgen05 GEMM: the 128 keys of a tile are the M
+//  * indexer_tc_kernel<G> -- the tensor-core path (E4M3, MXFP8 and MXFP4 codes, H_I =
+//    64, D_I = 128, 64-token pages; what the two MX formats do differently stands
+//    beside TcCfg).  Swap-AB tcgen05 GEMM: the 128 keys of a tile are the M
 //    rows (TMEM lanes), the G queries x 64 heads of a query group are the N
 //    columns, K = 128.  Keys arrive page by page through TMA (128-byte swizzle)
 //    and their per-key scales through one warp-wide cp.async per tile (a TMA op
@@ -21,7 +22,7 @@
 //    dot products of a query into its score with an in-thread head sum.
 //    Persistent: every CTA takes an equal contiguous share of the (group, key
 //    tile) list, computed on the device from q_pos.
-//  * indexer_generic_kernel -- CUDA cores, any H_I/D_I, fp32 or e4m3.
+//  * indexer_generic_kernel -- CUDA cores, any H_I, D_I and page size, every format.
 #include <algorithm>
 #include <cstdio>
 #include <mutex>
@@ -513,7 +514,7 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
     // ------------------------------------------------ TMA producers (warps 0 .. kProd - 1)
     // Producer pw issues the copies of the tiles it with it % kProd == pw (and so
     // of the stages st with st % kProd == pw).  It keeps the page ids of its next
-    // 16 tiles in registers (lane l: tile l / 2, page l % 2, loaded in parallel);
+    // kWindow tiles in registers (lane l: tile l / kPages, page l % kPages, loaded in parallel);
     // lane 0 issues the TMA tile loads, every lane one 16-byte copy of key
     // scales.  The TMA loads into query buffer pw go with producer pw too,
     // whichever of them has the group's first tile, so that a buffer's releases are
@@ -1097,7 +1098,12 @@ cudaError_t launch_decode_fused(const SeqArgs& seq, const IndexerArgs& a, int32_
   // queries) the fused kernel beats the chained indexer + Top-K (decode batch 64:
   // 81.0 vs 83.7 us a step); with more CTAs per query the selection's exchanges
   // between them cost more than the chained plan's score round trip (decode
-  // batch 1: 25.9 vs 25.7 us; batch 4 at 131072 positions: 61.1 vs 55.8 us).
+  // batch 1: 25.9 vs 25.7 us; batch 4 at 131072 positions: 61.1 vs 55.8 us).  With MXFP4
+  // keys it is the same (us a step, fused and chained; bf16 rows): 64 queries of 4096
+  // positions 68.8 and 71.6, 8192 73.0 and 75.7, 16384 82.8 and 85.1, 32768 101.7 and
+  // 101.9; 152 queries of 8192 141.5 and 146.9.  Where one or two CTAs a query leave half
+  // of the SMs without one the chained plan is ahead for long histories: 40 queries of 8192
+  // 70.6 and 72.5, 16384 80.7 and 77.8, 32768 100.3 and 88.9 (E4M3 112.3 and 98.3).
   if (cl < 1 || cl > kFusedMaxCluster) return cudaSuccess;
   *unsupported = false;
   return a.kind == IndexKind::kMx4   ? launch_fused<IndexKind::kMx4>(seq, a, K, idx, cl, env, plan, why, unsupported)
