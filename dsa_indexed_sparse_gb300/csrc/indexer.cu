@@ -417,7 +417,12 @@ __global__ void __launch_bounds__(TcWarps<G, kKind>::kThreads, 1)
   }
   begin = static_cast<int64_t>(blockIdx.x) * total / gridDim.x;
   end = static_cast<int64_t>(blockIdx.x + 1) * total / gridDim.x;
-  if (begin >= end) return;  // block-uniform
+  if (begin >= end) {  // block-uniform
+    // With no tile at all (every position invalid) no CTA of this grid would wait for the kernel
+    // before, and the kernel after, which waits for this grid alone, would write beside it.
+    if (total == 0) grid_dep_wait();
+    return;
+  }
   {
     int run = 0;
     for (int g0 = 0; g0 < p.n_groups; g0 += kTcThreads) {
