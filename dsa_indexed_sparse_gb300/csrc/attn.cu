@@ -127,12 +127,12 @@ __global__ void __launch_bounds__(kGenThreads)
   const float m = block_reduce_max(mloc, red);
   float lsum = 0.f;
   for (int r = threadIdx.x; r < K; r += blockDim.x) {
-    const float p = (m == -INFINITY || ps[r] == -INFINITY) ? 0.f : __expf(ps[r] - m);
+    const float p = ps[r] == -INFINITY ? 0.f : __expf(ps[r] - m);   // NaN logits leave m alone and stay NaN
     ps[r] = p;
     lsum += p;
   }
   const float l = block_reduce_sum(lsum, red);  // includes a __syncthreads
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;   // l may be NaN
   const int64_t ooff = (static_cast<int64_t>(t) * a.H + h) * dv;
   for (int d = threadIdx.x; d < dv; d += blockDim.x) {
     float acc = 0.f;
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kGenThreads)
       static_cast<__nv_bfloat16*>(a.out)[ooff + d] = __float2bfloat16_rn(acc);
   }
   if (threadIdx.x == 0 && a.lse)
-    a.lse[static_cast<int64_t>(t) * a.H + h] = l > 0.f ? m + logf(l) : -INFINITY;
+    a.lse[static_cast<int64_t>(t) * a.H + h] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
 // =============================================================== tcgen05 kernel
@@ -869,8 +869,8 @@ __global__ void __launch_bounds__(kT48Threads, 1) attn_tc48_kernel(TcAttnParams 
     }
     if (ok) {
       tc_fence_after();
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const float lse = l32 > 0.f ? (m + log2f(l32)) * kLn2 : -INFINITY;
+      const float inv = l == 0.f ? 0.f : 1.f / l;   // l and l32 may be NaN
+      const float lse = l32 == 0.f ? -INFINITY : (m + log2f(l32)) * kLn2;
       const int64_t th = static_cast<int64_t>(t) * kH + h;
       // all MMAs are complete (ofull), so the stage buffers are idle: 4 KB per warp
       const uint32_t stg = smem_u32(sm + C::kOffKV) + quarter * 4096;
@@ -1006,7 +1006,7 @@ __global__ void __launch_bounds__(32 * SW * HPC)
     ll = fmaf(fw[w], s_l[w0 + w], ll);
   }
   const int i0 = threadIdx.x - w0 * 32;   // thread within the head's warps
-  // ll is NaN where a slice's LSE is (the 4-bit rows' kernel)
+  // ll is NaN where a slice's LSE is
   if (i0 == 0 && lse_out) lse_out[th] = ll == 0.f ? -INFINITY : mm + logf(ll);
   const float inv = ll == 0.f ? 0.f : 1.f / ll;
   uint2* dst = reinterpret_cast<uint2*>(out + th * kDv);
